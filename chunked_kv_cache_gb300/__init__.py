@@ -16,7 +16,10 @@ from ._native import (SrConfig, SrBuffers, SrError, sr_session_init, sr_session_
                       sr_chunk_attention_batch, sr_device_error_status, sr_debug_wait_timeout,
                       sr_workspace_bytes, sr_plan_chunk, sr_rope3d_qk_frames, sr_chunk_attention_frames,
                       sr_cache_commit_frames, SrChunkPlan, sr_window_attention, sr_rope3d_qk_at,
-                      sr_rope3d_qk_dev, sr_chunk_attention_dev, sr_cache_commit_dev, SR_MAX_BATCH)
+                      sr_rope3d_qk_dev, sr_chunk_attention_dev, sr_cache_commit_dev, SR_MAX_BATCH,
+                      SrPagedConfig, SrPagedBuffers, sr_paged_workspace_bytes, sr_paged_init, sr_paged_free,
+                      sr_paged_reset, sr_paged_append, sr_paged_attention, sr_paged_evict, sr_paged_locate)
+from .paged import PagedCache
 
 __all__ = [
     "Session", "chunk_attention_batch", "SrConfig", "SrBuffers", "SrError",
@@ -25,7 +28,9 @@ __all__ = [
     "sr_debug_wait_timeout", "sr_workspace_bytes", "sr_plan_chunk", "sr_rope3d_qk_frames",
     "sr_chunk_attention_frames", "sr_cache_commit_frames", "SrChunkPlan", "plan_chunk",
     "sr_window_attention", "sr_rope3d_qk_at", "sr_rope3d_qk_dev", "sr_chunk_attention_dev",
-    "sr_cache_commit_dev",
+    "sr_cache_commit_dev", "PagedCache", "SrPagedConfig", "SrPagedBuffers", "sr_paged_workspace_bytes",
+    "sr_paged_init", "sr_paged_free", "sr_paged_reset", "sr_paged_append", "sr_paged_attention",
+    "sr_paged_evict", "sr_paged_locate",
 ]
 
 _BF16 = torch.bfloat16

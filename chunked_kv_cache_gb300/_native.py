@@ -20,8 +20,15 @@ SR_ERR_STATE = -4
 SR_ERR_CUDA = -5
 SR_ERR_TIMEOUT = -6
 SR_DEVERR_WAIT_TIMEOUT = 1
+SR_DEVERR_BAD_PAGE = 2
+SR_DEVERR_CACHE_FULL = 3
+SR_DEVERR_WORKSPACE = 4
 SR_MAX_BATCH = 24
 SR_MAX_LAYER_WINDOWS = 96
+SR_MAX_PAGED_SEQS = 256
+SR_MAX_PAGED_GROUP = 16
+SR_PAGE_BF16 = 0
+SR_PAGE_E4M3 = 1
 
 # every extern "C" symbol that include/sr.h declares
 EXPORTS = (
@@ -32,6 +39,8 @@ EXPORTS = (
     "sr_cache_commit_frames", "sr_window_attention", "sr_rope3d_qk_at", "sr_rope3d_qk_dev",
     "sr_chunk_attention_dev", "sr_cache_commit_dev", "sr_window_count", "sr_plan_window",
     "sr_plan_attention", "sr_rope_angle", "sr_layer_rope_gather", "sr_layer_commit",
+    "sr_paged_workspace_bytes", "sr_paged_init", "sr_paged_free", "sr_paged_reset", "sr_paged_append",
+    "sr_paged_attention", "sr_paged_evict", "sr_paged_locate",
 )
 
 
@@ -66,6 +75,23 @@ class SrChunkPlan(ctypes.Structure):
 class SrWindow(ctypes.Structure):
     _fields_ = [("row0", ctypes.c_int32), ("col0", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("cols", ctypes.c_int32)]
+
+
+class SrPagedConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("page_type", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class SrPagedBuffers(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p), ("seq_pos", ctypes.c_void_p), ("token_pos", ctypes.c_void_p),
+        ("token_mass", ctypes.c_void_p), ("kv_exp", ctypes.c_void_p), ("err_word", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+    ]
 
 
 class SrError(RuntimeError):
@@ -114,6 +140,16 @@ def lib() -> ctypes.CDLL:
         L.sr_layer_rope_gather.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(SrWindow), i32, i32, i32, vp, vp, vp,
                                            vp, vp, vp, vp]
         L.sr_layer_commit.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(SrWindow), i32, i32, i32, vp, vp, vp]
+        pi32 = ctypes.POINTER(i32)
+        L.sr_paged_workspace_bytes.argtypes = [ctypes.POINTER(SrPagedConfig), i32, ctypes.POINTER(u64)]
+        L.sr_paged_init.argtypes = [ctypes.POINTER(SrPagedConfig), ctypes.POINTER(SrPagedBuffers), vp,
+                                    ctypes.POINTER(vp)]
+        L.sr_paged_free.argtypes = [vp]
+        L.sr_paged_reset.argtypes = [vp, pi32, i32, vp]
+        L.sr_paged_append.argtypes = [vp, pi32, pi32, i32, vp, vp, vp]
+        L.sr_paged_attention.argtypes = [vp, pi32, i32, vp, vp, vp, ctypes.c_float, vp]
+        L.sr_paged_evict.argtypes = [vp, pi32, i32, i32, i32, i32, vp]
+        L.sr_paged_locate.argtypes = [ctypes.POINTER(SrPagedConfig), pi32, i64, ctypes.POINTER(i64)]
         L.sr_device_error_status.argtypes = [i32]
         L.sr_debug_wait_timeout.argtypes = [vp, u64, vp]
         L.sr_workspace_bytes.argtypes = [ctypes.POINTER(SrConfig), ctypes.POINTER(ctypes.c_uint64)]
@@ -300,3 +336,49 @@ def sr_device_error_status(value: int) -> int:
 
 def sr_debug_wait_timeout(err_word: int, timeout_ns: int, stream: int) -> None:
     _check(lib().sr_debug_wait_timeout(err_word, int(timeout_ns), stream or None), "sr_debug_wait_timeout")
+
+
+# ---------------------------------------------------------------- the paged token cache
+# seqs and n_tokens are arrays of c_int32, or None
+def sr_paged_workspace_bytes(cfg: SrPagedConfig, with_mass: bool) -> int:
+    n = ctypes.c_uint64()
+    _check(lib().sr_paged_workspace_bytes(ctypes.byref(cfg), 1 if with_mass else 0, ctypes.byref(n)),
+           "sr_paged_workspace_bytes")
+    return n.value
+
+
+def sr_paged_init(cfg: SrPagedConfig, bufs: SrPagedBuffers, stream: int) -> int:
+    out = ctypes.c_void_p()
+    _check(lib().sr_paged_init(ctypes.byref(cfg), ctypes.byref(bufs), stream or None, ctypes.byref(out)),
+           "sr_paged_init")
+    return out.value
+
+
+def sr_paged_free(handle: int) -> None:
+    _check(lib().sr_paged_free(handle), "sr_paged_free")
+
+
+def sr_paged_reset(handle: int, seqs, n: int, stream: int) -> None:
+    _check(lib().sr_paged_reset(handle, seqs, n, stream or None), "sr_paged_reset")
+
+
+def sr_paged_append(handle: int, seqs, n_tokens, n: int, k: int, v: int, stream: int) -> None:
+    _check(lib().sr_paged_append(handle, seqs, n_tokens, n, k, v, stream or None), "sr_paged_append")
+
+
+def sr_paged_attention(handle: int, seqs, n: int, q: int, o: int, lse: int, mass_decay: float, stream: int) -> None:
+    _check(lib().sr_paged_attention(handle, seqs, n, q, o, lse or None, mass_decay, stream or None),
+           "sr_paged_attention")
+
+
+def sr_paged_evict(handle: int, seqs, n: int, budget: int, n_sink: int, n_recent: int, stream: int) -> None:
+    _check(lib().sr_paged_evict(handle, seqs, n, int(budget), int(n_sink), int(n_recent), stream or None),
+           "sr_paged_evict")
+
+
+def sr_paged_locate(cfg: SrPagedConfig, table_row, index: int) -> int:
+    """The pool row of a logical index through one row of the block table, -1 if it has none (host arithmetic)."""
+    row = ctypes.c_int64()
+    t = (ctypes.c_int32 * len(table_row))(*[int(x) for x in table_row])
+    _check(lib().sr_paged_locate(ctypes.byref(cfg), t, int(index), ctypes.byref(row)), "sr_paged_locate")
+    return row.value

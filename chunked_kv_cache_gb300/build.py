@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsr.so")
-SOURCES = ["attention.cu", "rope_commit.cu", "rope_phase.cu", "sr_api.cu", "sr_noalloc.cu"]
+SOURCES = ["attention.cu", "rope_commit.cu", "rope_phase.cu", "sr_api.cu", "sr_noalloc.cu",
+           "paged_api.cu", "paged_attention.cu", "paged_cache.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

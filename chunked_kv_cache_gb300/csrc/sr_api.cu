@@ -570,7 +570,15 @@ const char* sr_status_string(sr_status st) {
   return "unknown status";
 }
 
-sr_status sr_device_error_status(int32_t v) { return v == SR_DEVERR_NONE ? SR_OK : SR_ERR_TIMEOUT; }
+sr_status sr_device_error_status(int32_t v) {
+  if (v == SR_DEVERR_NONE) return SR_OK;
+  switch (v & 0xff) {
+    case SR_DEVERR_BAD_PAGE: return SR_ERR_INVALID_ARG;
+    case SR_DEVERR_CACHE_FULL:
+    case SR_DEVERR_WORKSPACE: return SR_ERR_STATE;
+  }
+  return SR_ERR_TIMEOUT;
+}
 
 sr_status sr_plan_attention(int32_t n_heads, int64_t lq, int64_t key_tiles, int32_t has_workspace,
                             int32_t tail_split, int32_t sm_count, int32_t* parts, int32_t* whole_as_tiles,

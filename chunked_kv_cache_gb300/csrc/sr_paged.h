@@ -1,0 +1,103 @@
+// sr_paged.h -- parameter blocks and launchers of the paged token cache, shared
+// by its host API (paged_api.cu) and kernels. Internal to libsr.so.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "sr.h"
+
+namespace sr {
+
+constexpr int kMaxPagedSeqs = SR_MAX_PAGED_SEQS;
+constexpr int kMaxPagedCtas = 1024;   // most CTAs an attention launch may have (partial result slots)
+
+// The pool row of logical index `idx` of a sequence whose block table row is
+// `table`: -1 when the entry is no page of the pool. 0 <= idx < cap.
+__host__ __device__ __forceinline__ int64_t paged_row(const int32_t* table, int32_t idx, int32_t page_tokens,
+                                                      int32_t n_pages) {
+  const int32_t p = idx / page_tokens;
+  const int32_t page = table[p];
+  if (page < 0 || page >= n_pages) return -1;
+  return static_cast<int64_t>(page) * page_tokens + (idx - p * page_tokens);
+}
+
+struct PagedView {
+  void* k_pages;
+  void* v_pages;
+  const int32_t* table;
+  int32_t* seq_len;
+  int32_t* seq_pos;
+  int32_t* token_pos;
+  float* token_mass;
+  const int32_t* kv_exp;
+  int32_t* err_word;
+  int32_t n_heads, n_kv, group, head_dim;
+  int32_t page_tokens, n_pages, max_pages;
+  int32_t cap;             // max_pages * page_tokens
+  int32_t page_type;
+  float scale_log2;        // softmax scale * log2(e)
+};
+
+// Workspace: counters, partial results, move lists, scores (see paged_layout).
+struct PagedLayout {
+  size_t counters;         // int32[kPagedCounters]
+  size_t plan;             // EvictPlan[kMaxPagedSeqs]
+  size_t moves;            // int2[move_cap]: (from, to) logical indices
+  int64_t move_cap;
+  size_t lse;              // float[kMaxPagedSeqs][n_heads]
+  size_t bytes;
+};
+constexpr int kPagedCounters = 1024;
+
+// What an eviction does to one sequence of the batch.
+struct EvictPlan {
+  int64_t list0;           // its first entry in the list of moves
+  int32_t moves;
+  int32_t new_len;         // -1: left as it is
+};
+
+struct PagedBatch {
+  int32_t n;
+  int32_t id[kMaxPagedSeqs];
+};
+
+struct AppendParams {
+  PagedView c;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int32_t* arrivals;               // [n] CTAs of each sequence that are done; left at zero
+  int32_t n;
+  int32_t rows_per_cta;
+  int32_t id[kMaxPagedSeqs];
+  int32_t row0[kMaxPagedSeqs + 1]; // first row of each sequence
+  int32_t cta0[kMaxPagedSeqs + 1]; // first CTA of each sequence
+};
+
+struct PagedAttnParams {
+  PagedView c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  float* ws_lse;
+  float mass_decay;
+  PagedBatch b;
+};
+
+struct EvictParams {
+  PagedView c;
+  int32_t budget, n_sink, n_recent;
+  EvictPlan* plan;
+  int2* moves;
+  int64_t move_cap;
+  PagedBatch b;
+};
+
+cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st);
+cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
+cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
+int paged_append_rows_per_cta(int n_kv, int head_dim);
+
+}  // namespace sr

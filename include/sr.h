@@ -67,7 +67,10 @@ typedef enum {
 /* Device error codes written into err_word (0 = no error). */
 enum {
   SR_DEVERR_NONE = 0,
-  SR_DEVERR_WAIT_TIMEOUT = 1  /* low 8 bits; bits 8..15 name the wait site */
+  SR_DEVERR_WAIT_TIMEOUT = 1, /* low 8 bits; bits 8..15 name the wait site */
+  SR_DEVERR_BAD_PAGE = 2,     /* paged cache: a token's block table entry is not a page of the pool */
+  SR_DEVERR_CACHE_FULL = 3,   /* paged cache: new tokens do not fit into their sequence */
+  SR_DEVERR_WORKSPACE = 4     /* paged cache: a batch longer than the pool (pages shared by its sequences) */
 };
 
 /* Session shape and constants. */
@@ -414,7 +417,143 @@ SR_API sr_status sr_layer_rope_gather(sr_session* const* sessions, const sr_wind
 SR_API sr_status sr_layer_commit(sr_session* const* sessions, const sr_window* windows, int32_t n,
                                  int32_t frame_h, int32_t frame_w, const void* k_raw, const void* v, void* stream);
 
-/* Map a value read from err_word to SR_OK or SR_ERR_TIMEOUT. */
+/* ------------------------------------------------------------------------------
+ * The paged token cache: serving sequences token by token.
+ *
+ * The calls above keep a dense ring of latent frames per session and evict by age.
+ * A token-by-token model that runs beside the renderer (its history is tokens, not
+ * frames) keeps its keys and values in pages of a pool that all sequences share, and
+ * may evict by the attention that a token has drawn: the sinks and the most recent
+ * tokens stay, as above, and the budget's other places go to the tokens with the
+ * largest accumulated attention weight.
+ *
+ * Layout. A token of sequence s has a logical index i, 0 <= i < seq_len[s]. Its keys
+ * and values are row  block_table[s][i / page_tokens] * page_tokens + i % page_tokens
+ * of k_pages and v_pages, [n_pages * page_tokens][n_kv_heads][head_dim]: token-major,
+ * as everywhere in this library. Its position in the stream (token_pos) and the
+ * attention weight it has drawn (token_mass) are kept by logical index. Attention
+ * treats a sequence's tokens as a set, so that an evicted token's index can be taken
+ * by any other token: keys keep the positions they were computed with, and token_pos
+ * tells which position an index holds (the slot table of the ring).
+ *
+ * Pages hold bf16, or e4m3 with one power-of-two scale per key/value head:
+ * value = e4m3 * 2^e. A power of two makes the scaling exact, so that the one rounding
+ * of a stored value is the conversion (to nearest even, saturating at +-448 * 2^e).
+ *
+ * The state that changes per token (lengths, positions, weights) lives on the device,
+ * and no call reads it on the host: a captured sequence of these calls serves every
+ * later token. What cannot be known on the host is checked on the device: a token
+ * whose block table entry is not a page of the pool is not read or written, and
+ * err_word receives SR_DEVERR_BAD_PAGE. All calls are asynchronous on the stream and
+ * use the current device, which must be the one sr_paged_init ran on (SR_ERR_STATE).
+ * Calls of one cache share its workspace: two that overlap on the GPU (two streams, or
+ * two captured graphs replayed at once) race on it, as calls of a session do.
+ * Caches that share pages need a workspace each and may run at the same time as long as
+ * none writes what another reads.
+ *
+ * Every call takes its sequences as a HOST array seqs[n] of distinct rows of the
+ * block table; NULL stands for 0 .. n-1. 1 <= n <= SR_MAX_PAGED_SEQS.
+ */
+typedef struct sr_paged_cache sr_paged_cache;   /* opaque host handle */
+
+#define SR_MAX_PAGED_SEQS 256
+#define SR_MAX_PAGED_GROUP 16
+
+enum { SR_PAGE_BF16 = 0, SR_PAGE_E4M3 = 1 };
+
+typedef struct {
+  int32_t n_heads;         /* query heads; a multiple of n_kv_heads, at most SR_MAX_PAGED_GROUP times it */
+  int32_t n_kv_heads;      /* key/value heads >= 1; query head h reads head h / (n_heads / n_kv_heads) */
+  int32_t head_dim;        /* 64 or 128 */
+  int32_t page_tokens;     /* tokens per page: a multiple of 16, at most 1024 */
+  int32_t n_pages;         /* pages of the pool >= 1 */
+  int32_t max_seqs;        /* rows of the block table, 1 .. 65536 */
+  int32_t max_pages;       /* pages a sequence may have >= 1; max_pages * page_tokens <= 2^24 */
+  int32_t page_type;       /* SR_PAGE_BF16 or SR_PAGE_E4M3 */
+  float softmax_scale;     /* <= 0 selects 1/sqrt(head_dim) */
+} sr_paged_config;
+
+/* Caller-owned device buffers. cap = max_pages * page_tokens. */
+typedef struct {
+  void* k_pages;            /* [n_pages * page_tokens][n_kv_heads][head_dim], 16-byte aligned */
+  void* v_pages;
+  int32_t* block_table;     /* [max_seqs][max_pages]: pages of each sequence (negative: none); the caller's to change */
+  int32_t* seq_len;         /* [max_seqs] tokens held */
+  int32_t* seq_pos;         /* [max_seqs] position the next token gets */
+  int32_t* token_pos;       /* [max_seqs][cap] position of each token */
+  float* token_mass;        /* [max_seqs][cap] accumulated attention weight, or NULL (no weights, no eviction) */
+  const int32_t* kv_exp;    /* [2][n_kv_heads] exponents e of the keys' and the values' scales, each -64..64;
+                               e4m3 pages only, NULL: all zero */
+  int32_t* err_word;        /* [1] device error word (see SR_DEVERR_*) */
+  void* workspace;          /* sr_paged_workspace_bytes() long, 256-byte aligned */
+} sr_paged_buffers;
+
+/* Bytes of workspace a cache of this shape needs; with_mass: it has a token_mass buffer. */
+SR_API sr_status sr_paged_workspace_bytes(const sr_paged_config* cfg, int32_t with_mass, uint64_t* bytes);
+
+/*
+ * Create a cache over the caller's buffers. Clears err_word and the workspace's counters;
+ * the sequences' state is used as found (resume), sr_paged_reset makes it empty.
+ * On failure *out is left NULL.
+ */
+SR_API sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs, void* stream,
+                               sr_paged_cache** out);
+SR_API sr_status sr_paged_free(sr_paged_cache* c);
+
+/* Empty sequences: length 0, next position 0. Their pages, positions and weights are left as they are. */
+SR_API sr_status sr_paged_reset(sr_paged_cache* c, const int32_t* seqs, int32_t n, void* stream);
+
+/*
+ * Append new tokens, one per sequence or whole prompts. k, v: [rows][n_kv_heads][head_dim]
+ * bf16, the sequences' rows back to back in the order of seqs (final: no rotary position is
+ * applied here). n_tokens: HOST array of n counts >= 0, NULL for one each. Token j of
+ * sequence s goes to index seq_len[s] + j with position seq_pos[s] + j and weight 0; then
+ * both grow by the count. A sequence whose new tokens do not all fit (past cap, onto an
+ * entry that is no page of the pool, or past position 2^31 - 1) is left as it was and
+ * err_word receives SR_DEVERR_CACHE_FULL or SR_DEVERR_BAD_PAGE; the others are not affected.
+ */
+SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const int32_t* n_tokens, int32_t n,
+                                 const void* k, const void* v, void* stream);
+
+/*
+ * Attention of one new token per sequence over the sequence's cached tokens (its own
+ * among them, once appended):
+ *   o[i][h] = softmax(scale * q[i][h] . K) V   over the seq_len tokens of seqs[i].
+ * q, o: [n][n_heads][head_dim] bf16. lse: optional [n][n_heads] fp32, natural-log sum-exp of
+ * the scaled scores. A sequence of length 0 gets o = 0 and lse = -inf. Indices at or past
+ * seq_len are never read as values: what the pages hold there does not matter.
+ * fp32 scores, softmax and sums; the weights are rounded to bf16 for their product with V.
+ * mass_decay >= 0 (finite; needs token_mass): also
+ *   token_mass[s][t] = mass_decay * token_mass[s][t] + sum over heads of the token's weight.
+ * mass_decay < 0: weights are not accumulated. The work is split over the length of the
+ * sequences and joined, whatever their number; results do not depend on timing.
+ */
+SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, const void* q, void* o,
+                                    float* lse, float mass_decay, void* stream);
+
+/*
+ * Evict down to `budget` tokens per sequence. A sequence with more keeps its sinks
+ * (position < n_sink), its recent tokens (position >= seq_pos - n_recent) and, of the
+ * others, those with the largest token_mass (a tie goes to the lower index; NaN counts as
+ * larger than every number). Then the j-th evicted index below the new length takes over
+ * the j-th kept token at or behind it: only these tokens move, with their positions and
+ * weights, the others stay in place, and what lies behind the new length is left as it was.
+ * budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget. Needs token_mass
+ * (SR_ERR_STATE). Pages of an evicted sequence must not be shared with another one.
+ */
+SR_API sr_status sr_paged_evict(sr_paged_cache* c, const int32_t* seqs, int32_t n, int32_t budget, int32_t n_sink,
+                                int32_t n_recent, void* stream);
+
+/*
+ * The pool row of logical index `index` through a HOST copy of one block table row, as the
+ * kernels look it up (host arithmetic, no GPU call). *row = -1 when the index is outside
+ * [0, cap) or its entry is not a page of the pool.
+ */
+SR_API sr_status sr_paged_locate(const sr_paged_config* cfg, const int32_t* block_table_row, int64_t index,
+                                 int64_t* row);
+
+/* Map a value read from err_word to SR_OK or SR_ERR_TIMEOUT (a wait), SR_ERR_INVALID_ARG (SR_DEVERR_BAD_PAGE),
+   SR_ERR_STATE (SR_DEVERR_CACHE_FULL, SR_DEVERR_WORKSPACE). */
 SR_API sr_status sr_device_error_status(int32_t err_word_value);
 
 /*

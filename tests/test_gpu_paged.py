@@ -1,0 +1,404 @@
+"""The paged token cache on the GPU against its float64 oracle.
+
+Tolerances, from the arithmetic (u = 2^-24, e = 2^-8 the half step of bf16):
+* an output is rounded to bf16 (e |o|), and each weight is rounded to bf16 before its
+  product with V (e sum w|v|); fp32 scores, exponentials and sums add
+  (2 dx + L u + 2^-20) sum w|v|, with dx the error of a scaled score:
+  (d + 8) u * scale * max_t sum_i |q_i k_i(t)|, and 2^-22 for the exponential.
+* the log-sum-exp is off by dx + L u + 2^-20 + 4 u |lse|.
+* a weight is off by (2 dx + L u + 2^-20) of itself, and the accumulated weight by
+  that and 4 u of itself.
+Copies (pages, positions), lengths and the choice of what to evict are exact; the
+choice is made by the oracle from the weights that the GPU holds.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle.paged import OraclePagedCache
+from tests.gpu_common import device
+
+pytestmark = pytest.mark.gpu
+
+U, E = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from chunked_kv_cache_gb300 import build
+    build.build()
+    device()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy() if t.dtype != torch.float8_e4m3fn else t.float().double().cpu().numpy()
+
+
+class Pair:
+    """A GPU cache and its oracle; stale pages are filled with `junk`."""
+
+    def __init__(self, heads, kv, d, page, max_seqs, max_pages, e4m3=False, seed=0, spare=3, junk=float("nan"),
+                 mass=True, scale=0.0):
+        import chunked_kv_cache_gb300 as sr
+        self.dev = device()
+        self.rng = np.random.default_rng(seed)
+        self.g = torch.Generator(device=self.dev).manual_seed(seed)
+        self.page, self.kv, self.d, self.heads = page, kv, d, heads
+        n_pages = max_seqs * max_pages + spare
+        exps = torch.from_numpy(self.rng.integers(-5, 3, (2, kv)).astype(np.int32)).to(self.dev)
+        dtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        pool = [torch.full((n_pages, page, kv, d), junk, device=self.dev).to(dtype) for _ in range(2)]
+        self.table = self.rng.permutation(n_pages)[: max_seqs * max_pages].reshape(max_seqs, max_pages)
+        self.cache = sr.PagedCache(heads, kv, d, page_tokens=page, n_pages=n_pages, max_seqs=max_seqs,
+                                   max_pages=max_pages, page_dtype=dtype, device=self.dev, mass=mass,
+                                   softmax_scale=scale,
+                                   buffers=dict(k_pages=pool[0], v_pages=pool[1], kv_exp=exps, block_table=torch.from_numpy(
+                                       self.table.astype(np.int32)).to(self.dev)))
+        self.ora = OraclePagedCache(heads, kv, d, max_seqs, max_pages * page, e4m3, exps.cpu().numpy(),
+                                    scale if scale > 0 else None)
+        self.exps = exps.cpu().numpy()
+
+    def randn(self, *shape, s=1.0):
+        return (torch.randn(shape, generator=self.g, device=self.dev) * s).to(torch.bfloat16)
+
+    def append(self, seqs, counts):
+        rows = int(sum(counts))
+        k, v = self.randn(rows, self.kv, self.d), self.randn(rows, self.kv, self.d)
+        self.cache.append(k, v, seqs=seqs, counts=counts)
+        self.ora.append(seqs, counts, f64(k), f64(v))
+
+    def check_state(self, seqs):
+        torch.cuda.synchronize()
+        length, nxt = self.cache.seq_len.cpu().numpy(), self.cache.seq_pos.cpu().numpy()
+        pos = self.cache.token_pos.cpu().numpy()
+        k, v = f64(self.cache.k_pages), f64(self.cache.v_pages)
+        if self.ora.e4m3:
+            k, v = k * (2.0 ** self.exps[0])[:, None], v * (2.0 ** self.exps[1])[:, None]
+        for s in seqs:
+            n = int(self.ora.length[s])
+            assert length[s] == n and nxt[s] == self.ora.next_pos[s], s
+            assert np.array_equal(pos[s, :n], self.ora.pos[s, :n]), s
+            t = np.arange(n)
+            pg = self.table[s][t // self.page]
+            assert np.array_equal(k[pg, t % self.page], self.ora.k[s, :n], equal_nan=True), s
+            assert np.array_equal(v[pg, t % self.page], self.ora.v[s, :n], equal_nan=True), s
+
+    def attend(self, seqs, decay=None, qs=1.5, visible=None):
+        n = len(seqs)
+        q = self.randn(n, self.heads, self.d, s=qs)
+        out = torch.full_like(q, float("nan"))
+        o, lse = self.cache.attention(q, seqs=seqs, out=out, lse=True, mass_decay=decay)
+        torch.cuda.synchronize()
+        q64, g = f64(q), self.heads // self.kv
+        ref, ref_lse, wv = self.ora.attention(seqs, q64, decay, visible)
+        o, lse = f64(o), f64(lse)
+        mass = f64(self.cache.token_mass) if decay is not None else None
+        for i, s in enumerate(seqs):
+            L = int(self.ora.length[s])
+            qa = np.abs(q64[i]).reshape(self.kv, g, self.d)
+            ka = np.abs(self.ora.k[s, :L])
+            if visible is not None:
+                ka = ka[visible[i]]
+            dot = np.einsum("hgd,thd->hgt", qa, ka).max(2, initial=0.0).reshape(self.heads)
+            dx = (self.d + 8) * U * self.ora.scale * dot
+            rel = 2 * dx + L * U + 2.0 ** -20
+            bound = E * np.abs(ref[i]) + (E + rel[:, None]) * wv[i] + 1e-30
+            err = np.abs(o[i] - ref[i])
+            assert np.all(err <= bound), (s, L, float((err / bound).max()))
+            if L == 0 or (visible is not None and not visible[i].any()):
+                assert np.all(lse[i] == -np.inf)
+            else:
+                tol = dx + L * U + 2.0 ** -20 + 4 * U * np.abs(ref_lse[i])
+                assert np.all(np.abs(lse[i] - ref_lse[i]) <= tol), (s, L, float((np.abs(lse[i] - ref_lse[i]) / tol).max()))
+            if decay is not None:
+                m = self.ora.mass[s, :L]
+                tol = (float(rel.max()) + 4 * U) * np.abs(m) + 1e-30
+                assert np.all(np.abs(mass[s, :L] - m) <= tol), (s, L)
+        if mass is not None:      # what the oracle chooses by from here on
+            for s in seqs:
+                L = int(self.ora.length[s])
+                self.ora.mass[s, :L] = mass[s, :L]
+        return o, lse
+
+    def ok(self):
+        assert self.cache.error_status() == 0
+
+
+SHAPES = [  # heads, kv heads, d, page tokens
+    (4, 4, 64, 16), (8, 1, 128, 64), (40, 8, 128, 64), (16, 1, 64, 48), (10, 5, 64, 32), (32, 2, 128, 16),
+    (6, 2, 128, 128), (1, 1, 128, 16),
+]
+LENGTHS = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 255, 300, 511]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_append_and_attend_every_length(shape, e4m3):
+    heads, kv, d, page = shape
+    n = len(LENGTHS)
+    p = Pair(heads, kv, d, page, n, -(-512 // page), e4m3, seed=heads * 7 + d)
+    seqs = p.rng.permutation(n).tolist()
+    p.append(seqs, [LENGTHS[s] for s in seqs])
+    p.check_state(range(n))
+    p.attend(seqs)
+    p.attend(seqs[::-1][:5], decay=1.0)
+    p.append(seqs[:7], [1] * 7)                 # token by token
+    p.attend(seqs[:7], decay=0.5)
+    p.check_state(range(n))
+    p.ok()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,kv,d,length", [(5, 1, 128, 20011), (16, 2, 64, 9001), (4, 4, 128, 4097)])
+def test_one_long_sequence_is_split_and_joined(heads, kv, d, length, e4m3):
+    p = Pair(heads, kv, d, 64, 2, -(-length // 64), e4m3, seed=5)
+    p.append([1], [length])
+    p.attend([1], decay=1.0)
+    p.attend([1], decay=0.25)
+    p.ok()
+
+
+def test_many_sequences_of_unequal_length():
+    n = 256
+    p = Pair(8, 2, 64, 16, n, 20, seed=6)
+    counts = [int(x) for x in p.rng.integers(0, 320, n)]
+    counts[:6] = [0, 320, 1, 0, 0, 319]
+    p.append(list(range(n)), counts)
+    p.check_state(range(n))
+    p.attend(list(range(n)), decay=1.0)
+    p.ok()
+
+
+def test_large_scores_and_scale():
+    """Scores of several hundred: one token holds nearly all weight."""
+    p = Pair(4, 2, 128, 32, 3, 8, seed=7, scale=0.7)
+    p.append([0, 1, 2], [200, 1, 77])
+    p.attend([0, 1, 2], decay=1.0, qs=8.0)
+    p.ok()
+
+
+def test_results_do_not_depend_on_the_run():
+    p = Pair(40, 8, 128, 64, 5, 40, seed=8)
+    p.append([0, 1, 2, 3, 4], [2500, 0, 3, 64, 1111])
+    q = p.randn(5, 40, 128)
+    first = None
+    for _ in range(6):
+        p.cache.token_mass.zero_()
+        o, lse = p.cache.attention(q, lse=True, mass_decay=1.0)
+        got = (o.clone(), lse.clone(), p.cache.token_mass.clone())
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+    o2 = p.cache.attention(q)
+    assert torch.equal(o2, first[0])
+
+
+def test_empty_batch_of_empty_sequences():
+    p = Pair(4, 1, 64, 16, 3, 2, seed=9)
+    o, lse = p.attend([0, 1, 2], decay=1.0)
+    assert not o.any() and np.all(lse == -np.inf)
+    p.cache.evict(4)
+    p.check_state(range(3))
+    p.ok()
+
+
+def test_values_in_unused_rows_do_not_matter():
+    for junk in (float("inf"), float("-inf"), float("nan"), torch.finfo(torch.bfloat16).min):
+        p = Pair(8, 2, 128, 64, 2, 3, seed=10, junk=junk)
+        p.append([0, 1], [65, 130])
+        p.attend([0, 1], decay=1.0)
+        p.ok()
+
+
+def test_bad_pages_are_left_out_and_reported():
+    """Entries that are no page of the pool: their tokens are not seen, err_word says so."""
+    p = Pair(4, 2, 64, 16, 2, 6, seed=11)
+    p.append([0, 1], [90, 40])
+    p.cache.block_table[0, 1] = -1
+    p.cache.block_table[0, 4] = p.cache.n_pages
+    vis0 = np.ones(90, bool)
+    vis0[16:32] = vis0[64:80] = False
+    p.attend([0, 1], visible=[vis0, np.ones(40, bool)])
+    from chunked_kv_cache_gb300 import _native as N
+    assert p.cache.error_status() == N.SR_ERR_INVALID_ARG
+    assert int(p.cache.err_word.item()) == N.SR_DEVERR_BAD_PAGE
+    # nothing but bad pages: an empty row
+    p.cache.block_table[1, :] = -7
+    p.attend([1], visible=[np.zeros(40, bool)])
+
+
+def test_append_is_all_or_nothing():
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 2, 64, 16, 3, 4, seed=12)
+    p.append([0, 1, 2], [60, 10, 63])
+    before = [t.clone() for t in (p.cache.k_pages, p.cache.v_pages)]
+    k, v = p.randn(8, 2, 64), p.randn(8, 2, 64)
+    p.cache.append(k, v, seqs=[0, 2], counts=[5, 3])       # 65 of 64; 66 of 64
+    assert p.cache.error_status() == N.SR_ERR_STATE and int(p.cache.err_word.item()) == N.SR_DEVERR_CACHE_FULL
+    assert p.cache.seq_len.tolist() == [60, 10, 63] and p.cache.seq_pos.tolist() == [60, 10, 63]
+    for a, b in zip(before, (p.cache.k_pages, p.cache.v_pages)):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    p.cache.err_word.zero_()
+    p.cache.block_table[1, 2] = -1
+    p.cache.append(k, v, seqs=[1, 0], counts=[6, 2])       # tokens 10..15 fit, 60 and 61 do
+    assert p.cache.error_status() == 0 and p.cache.seq_len.tolist() == [62, 16, 63]
+    k, v = p.randn(40, 2, 64), p.randn(40, 2, 64)
+    p.cache.append(k, v, seqs=[1], counts=[40])            # 16 .. 55 touches the unmapped page 2
+    assert int(p.cache.err_word.item()) == N.SR_DEVERR_BAD_PAGE and p.cache.seq_len.tolist() == [62, 16, 63]
+
+
+@pytest.mark.parametrize("n,budget,sink,recent", [
+    (300, 128, 4, 32), (300, 299, 0, 0), (300, 1, 0, 1), (300, 1, 0, 0), (65, 64, 8, 56), (1500, 1024, 100, 300),
+    (5000, 17, 3, 5), (2049, 2048, 0, 2048), (33, 32, 32, 0),
+])
+@pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
+def test_evict_is_exact(n, budget, sink, recent, kind):
+    p = Pair(2, 1, 64, 16, 3, -(-n // 16), seed=n + budget)
+    p.append([0, 2], [n, budget])               # sequence 2 is already within the budget, 1 is empty
+    m = p.rng.lognormal(0, 2, (3, p.cache.capacity)).astype(np.float32)
+    if kind == "ties":
+        m = np.floor(p.rng.random(m.shape) * 4).astype(np.float32)
+        m[m == 0] = np.where(p.rng.random((m == 0).sum()) < 0.5, 0.0, -0.0)
+    if kind == "odd":
+        pick = p.rng.integers(0, 9, m.shape)
+        m[pick == 0], m[pick == 1], m[pick == 2], m[pick == 3] = np.nan, np.inf, -np.inf, -3.0
+        m[pick == 4], m[pick == 5] = -np.nan, 1e-42
+    p.cache.token_mass.copy_(torch.from_numpy(m))
+    p.ora.mass[:] = m
+    behind = p.cache.token_pos.clone()
+    p.cache.evict(budget, sink, recent)
+    p.ora.evict(range(3), budget, sink, recent)
+    p.check_state(range(3))
+    got = p.cache.token_mass.cpu().numpy()
+    new = int(p.ora.length[0])
+    assert np.array_equal(got[0, :new], p.ora.mass[0, :new].astype(np.float32), equal_nan=True)
+    # nothing behind the new length was touched
+    assert np.array_equal(got[0, new:], m[0, new:], equal_nan=True) and np.array_equal(got[1:], m[1:], equal_nan=True)
+    assert torch.equal(p.cache.token_pos[:, new:], behind[:, new:])
+    p.ok()
+
+
+def test_evict_long_sequences():
+    p = Pair(1, 1, 64, 64, 2, 1100, seed=13, spare=0)
+    p.append([0, 1], [70000, 66001])
+    m = p.rng.exponential(1.0, (2, p.cache.capacity)).astype(np.float32)
+    p.cache.token_mass.copy_(torch.from_numpy(m))
+    p.ora.mass[:] = m
+    p.cache.evict(60000, 16, 1000, seqs=[1, 0])
+    p.ora.evict([1, 0], 60000, 16, 1000)
+    p.check_state([0, 1])
+    p.ok()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_serving_loop_at_a_budget(e4m3):
+    """Prompts, then token by token with weights and eviction, two budgets; lengths never exceed them."""
+    p = Pair(8, 2, 64, 16, 4, 8, e4m3, seed=14)
+    p.append([0, 1, 2, 3], [70, 5, 0, 100])
+    for step in range(40):
+        seqs = [3, 0, 1, 2] if step % 3 else [1, 3]
+        p.append(seqs, [1] * len(seqs))
+        p.attend(seqs, decay=0.9)
+        p.cache.evict(64, n_sink=4, n_recent=16, seqs=seqs)
+        p.ora.evict(seqs, 64, 4, 16)
+        if step % 8 == 7:
+            p.check_state(range(4))
+    assert p.ora.length.max() == 64
+    p.ok()
+
+
+def test_captured_step_serves_later_tokens():
+    p = Pair(8, 2, 128, 16, 3, 8, seed=15)
+    p.append([0, 1, 2], [60, 63, 3])
+    k, v, q = (torch.zeros(3, h, 128, dtype=torch.bfloat16, device=p.dev) for h in (2, 2, 8))
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device=p.dev)
+
+    def step():
+        p.cache.append(k, v)
+        p.cache.attention(q, out=out, lse=lse, mass_decay=1.0)
+        p.cache.evict(64, 2, 8)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    twin = Pair(8, 2, 128, 16, 3, 8, seed=15)
+    twin.append([0, 1, 2], [60, 63, 3])
+    for t in range(10):
+        kk, vv, qq = p.randn(3, 2, 128), p.randn(3, 2, 128), p.randn(3, 8, 128)
+        for dst, src in ((k, kk), (v, vv), (q, qq)):
+            dst.copy_(src)
+        graph.replay()
+        twin.cache.append(kk, vv)
+        o, l = twin.cache.attention(qq, lse=True, mass_decay=1.0)
+        twin.cache.evict(64, 2, 8)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(lse, l)
+        for name in ("seq_len", "seq_pos", "token_pos", "token_mass"):
+            assert torch.equal(getattr(p.cache, name), getattr(twin.cache, name)), (t, name)
+    assert p.cache.seq_len.tolist() == [64, 64, 13]
+    p.ok()
+
+
+def test_other_stream_and_reserved_pages():
+    import chunked_kv_cache_gb300 as sr
+    dev = device()
+    c = sr.PagedCache(4, 4, 64, page_tokens=16, n_pages=6, max_seqs=4, max_pages=4, device=dev)
+    st = torch.cuda.Stream(dev)
+    st.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(st):
+        c.reserve(2, 33)
+        c.reserve(0, 16)
+        with pytest.raises(RuntimeError):
+            c.reserve(1, 48)
+        with pytest.raises(ValueError):
+            c.reserve(1, 80)
+        g = torch.Generator(device=dev).manual_seed(1)
+        k = torch.randn(33, 4, 64, device=dev, generator=g).to(torch.bfloat16)
+        c.append(k, k, seqs=[2], counts=[33])
+        o = c.attention(torch.zeros(2, 4, 64, dtype=torch.bfloat16, device=dev), seqs=[2, 0])
+    st.synchronize()
+    assert c.error_status() == 0
+    want = k.double().mean(0)
+    assert (o[0].double() - want).abs().max() <= 2 * E * k.double().abs().mean(0).max()
+    assert not o[1].any()
+    c.release(2)
+    c.reserve(1, 48)                            # the pages came back
+    assert c.seq_len.tolist() == [0, 0, 0, 0]
+
+
+def test_refusals():
+    import chunked_kv_cache_gb300 as sr
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 2, 64, 16, 3, 4, seed=16, mass=False)
+    q, k = p.randn(3, 4, 64), p.randn(3, 2, 64)
+
+    def refused(status, f, *a, **kw):
+        with pytest.raises(sr.SrError) as e:
+            f(*a, **kw)
+        assert e.value.status == status
+
+    refused(N.SR_ERR_STATE, p.cache.attention, q, mass_decay=1.0)
+    refused(N.SR_ERR_STATE, p.cache.evict, 8)
+    p = Pair(4, 2, 64, 16, 3, 4, seed=16)
+    refused(N.SR_ERR_INVALID_ARG, p.cache.attention, q, seqs=[0, 1, 1])      # the same row twice
+    refused(N.SR_ERR_INVALID_ARG, p.cache.append, k, k, seqs=[0, 1, 0])
+    refused(N.SR_ERR_INVALID_ARG, p.cache.attention, q, seqs=[0, 1, 3])
+    refused(N.SR_ERR_INVALID_ARG, p.cache.attention, q, seqs=[0, -1, 2])
+    refused(N.SR_ERR_INVALID_ARG, p.cache.append, k, k, counts=[4, -2, 1])
+    refused(N.SR_ERR_INVALID_ARG, p.cache.attention, q, mass_decay=float("nan"))
+    refused(N.SR_ERR_INVALID_ARG, p.cache.evict, 0)
+    refused(N.SR_ERR_INVALID_ARG, p.cache.evict, 8, 5, 4)
+    refused(N.SR_ERR_INVALID_ARG, p.cache.evict, 8, -1, 4)
+    refused(N.SR_ERR_INVALID_ARG, p.cache.evict, 8, seqs=[])
+    for bad in (q.float(), q[:, :2], q.transpose(0, 1).contiguous().transpose(0, 1), q.cpu()):
+        with pytest.raises(ValueError):
+            p.cache.attention(bad)
+    with pytest.raises(ValueError):
+        p.cache.attention(q, seqs=[0, 1])
+    with pytest.raises(ValueError):
+        p.cache.append(k, k, counts=[1, 1])
+    with pytest.raises(ValueError):
+        p.cache.attention(q, mass_decay=-1.0)
+    p.cache.append(k[:0], k[:0], counts=[0, 0, 0])            # nothing to do
+    p.cache.evict(1 << 20)                                     # above every length
+    assert p.cache.seq_len.tolist() == [0, 0, 0]
+    p.ok()
