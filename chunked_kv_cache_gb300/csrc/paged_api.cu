@@ -55,7 +55,15 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   // a sequence of length n moves at most n / 2 tokens
   l.move_cap = with_mass ? static_cast<int64_t>(c.n_pages) * c.page_tokens / 2 + sr::kMaxPagedSeqs : 0;
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
-  l.lse = take(static_cast<size_t>(sr::kMaxPagedSeqs) * c.n_heads * 4);
+  const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
+  l.items = take(seqs * c.n_kv_heads * sizeof(sr::PagedItem));
+  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.head_dim) * 4);
+  l.lse2 = take(seqs * c.n_heads * 4);
+  // every token of the pool once, the sequences' lengths rounded up to tiles
+  const int64_t tile = sr::paged_tile_tokens(c.head_dim, c.page_type);
+  l.score_tiles = with_mass ? (static_cast<int64_t>(c.n_pages) * c.page_tokens / tile + static_cast<int64_t>(seqs)) *
+                                  c.n_kv_heads : 0;
+  l.scores = take(static_cast<size_t>(l.score_tiles) * (c.n_heads / c.n_kv_heads) * tile * 4);
   l.bytes = at;
   return l;
 }
@@ -226,7 +234,11 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.ws_lse = ws_at<float>(c, c->layout.lse);
+  p.items = ws_at<sr::PagedItem>(c, c->layout.items);
+  p.parts = ws_at<float>(c, c->layout.parts);
+  p.lse2 = ws_at<float>(c, c->layout.lse2);
+  p.scores = ws_at<float>(c, c->layout.scores);
+  p.score_tiles = c->layout.score_tiles;
   p.mass_decay = mass_decay;
   return sr::launch_paged_attention(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
 }

@@ -4,11 +4,39 @@
 //   x_h(t) = scale * q_h . k(t),  o_h = sum_t e^(x_h(t) - lse_h) v(t),
 //   lse_h = ln sum_t e^x_h(t),    mass(t) <- decay * mass(t) + sum_h e^(x_h(t) - lse_h).
 //
-// The simplest form: one warp per sequence and query head walks the tokens, its
-// lanes across the head dimension; a second launch forms each token's weight from
-// the log-sum-exps, one warp per token.
+// Bound by the one read of the cache: a token's 2 D values per key/value head meet at
+// most 16 query heads. Every choice below serves that stream.
+//
+// Work split. A sequence and key/value head (an item) is cut into tiles of CT
+// tokens; the launch's tiles, item after item, form one line, and every CTA takes an
+// equal stretch of it, whatever the lengths: a batch of unequal sequences and a
+// single long one both occupy the whole GPU, and the lengths, which only the device
+// knows, never reach the host. A CTA that covers an item whole writes its output; of an
+// item cut between CTAs each writes its partial result (fp32 sums, maximum and sum of
+// the softmax), and a second launch joins them in the order of the line, so that
+// results do not depend on timing.
+//
+// Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
+// copies its tokens' keys and values into its own three shared-memory stages
+// (cp.async, 16-byte chunks, rows past the length filled with zeros) and computes on
+// the oldest stage, with no barrier but its own. The copies run ahead across items,
+// so that the stream does not pause where one item ends. Scores are the matrix product of the
+// group's query heads (16 rows, the unused ones zero) with 16 keys at a time; the
+// accumulators' layout is the left operand's of the product with the values, so weights
+// never leave registers. Warp-level products fit here: the rows that a tcgen05 tile
+// would need (128) are not there, and the tensor pipe has room to spare.
+//
+// Precision. Scores, softmax statistics and sums are fp32. bf16 pages: the weights
+// are rounded to bf16 (relative 2^-9 each, unbiased) for their product with the
+// values. e4m3 pages: keys and values become fp16 exactly, the weights are scaled by
+// 2^10 and rounded to fp16, and a query row is scaled by a power of two to a largest
+// element in [1, 2), which leaves fp16's ten fraction bits more than bf16's seven over
+// 2^24 of range.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "sr_device.cuh"
 #include "sr_kernels.h"
@@ -18,113 +46,652 @@ namespace sr {
 
 namespace {
 
-__device__ __forceinline__ int32_t live_len(const PagedView& c, int32_t seq) {
-  return min(max(c.seq_len[seq], 0), c.cap);
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;
+constexpr int kRows = SR_MAX_PAGED_GROUP;   // query rows of an item's matrix product
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D, int TYPE>
+struct Geo {
+  static constexpr int kRowBytes = D * (TYPE == SR_PAGE_BF16 ? 2 : 1);   // a token's keys (or values) of one head
+  static constexpr int kChunks = kRowBytes / 16;
+  static constexpr int KT = 4096 / kRowBytes;      // tokens per warp and tile: 4 KB of keys, 4 KB of values
+  static constexpr int CT = kWarps * KT;           // tokens per tile
+  static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
+  static constexpr int kStageBytes = 8192;
+  static constexpr int kStageArea = kWarps * kStages * kStageBytes;
+  static constexpr int kMergeFloats = (kWarps - 1) * 8 * D;
+};
+
+// Shared-memory position of 16-byte chunk c of row r, permuted so that eight rows'
+// equal chunks (what one matrix load reads) lie in different banks.
+template <int CHUNKS>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (CHUNKS >= 8) return static_cast<uint32_t>(r * CHUNKS + (c ^ (r & 7))) * 16u;
+  return static_cast<uint32_t>(r * CHUNKS + (c ^ ((r >> 1) & 3))) * 16u;
 }
 
-template <int D>
-__device__ __forceinline__ void load_row(const PagedView& c, const void* pages, int64_t row, int head, float (&x)[D / 32],
-                                         int lane) {
-  const int64_t at = (row * c.n_kv + head) * D;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    if (c.page_type == SR_PAGE_BF16)
-      x[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(pages)[at + lane + 32 * i]);
-    else
-      x[i] = static_cast<float>(static_cast<const __nv_fp8_e4m3*>(pages)[at + lane + 32 * i]);
-  }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  return x;
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <int TYPE>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (TYPE == SR_PAGE_BF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+// two e4m3 values (the low 16 bits) as fp16, exactly
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
+  return y;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn_simple(const __grid_constant__ PagedAttnParams p) {
+struct SharedHead {
+  int64_t cum[kMaxPagedSeqs + 1];       // tiles before each sequence of the batch
+  int32_t len[kMaxPagedSeqs];
+  float ml[kWarps][kRows][2];           // each warp's maximum and sum, while warps merge
+};
+
+// A place on the line of tiles.
+struct Cursor {
+  int i, h;            // sequence of the batch, key/value head
+  int32_t tile, tiles; // tile of the item, tiles it has
+  int32_t len;
+};
+
+template <int CT>
+__device__ __forceinline__ void cursor_seq(Cursor& c, const SharedHead& s) {
+  while (s.len[c.i] == 0) ++c.i;        // the line holds a tile here: some sequence has one
+  c.len = s.len[c.i];
+  c.tiles = (c.len + CT - 1) / CT;
+}
+template <int CT>
+__device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int n_kv, bool more) {
+  if (++c.tile < c.tiles || !more) return;
+  c.tile = 0;
+  if (++c.h < n_kv) return;
+  c.h = 0;
+  ++c.i;
+  cursor_seq<CT>(c, s);
+}
+
+template <int D, int TYPE, bool MASS>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+  using G = Geo<D, TYPE>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea + G::kMergeFloats * 4);
+  float* merge = reinterpret_cast<float*>(smem + G::kStageArea);
+  grid_dep_launch_dependents();
   grid_dep_wait();
   const PagedView& c = p.c;
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
-  if (warp >= p.b.n * c.n_heads) return;
-  const int i = warp / c.n_heads, h = warp % c.n_heads, kv = h / c.group;
-  const int32_t seq = p.b.id[i];
-  const int32_t len = live_len(c, seq);
-  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  const float ks = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f;
-  const float vs = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[c.n_kv + kv])) : 1.f;
-  float q[D / 32], o[D / 32] = {};
-  for (int k = 0; k < D / 32; ++k)
-    q[k] = __bfloat162float(p.q[(static_cast<int64_t>(i) * c.n_heads + h) * D + lane + 32 * k]);
-  float m = -INFINITY, l = 0.f;
-  for (int32_t t = 0; t < len; ++t) {
-    const int64_t row = paged_row(table, t, c.page_tokens, c.n_pages);
-    if (row < 0) {
-      if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
-      continue;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = p.b.n, n_kv = c.n_kv, group = c.group;
+
+  // ---- the line of tiles
+  if (warp == 0) {
+    int64_t mine = 0;
+    int32_t len[kMaxPagedSeqs / 32];
+#pragma unroll
+    for (int k = 0; k < kMaxPagedSeqs / 32; ++k) {
+      const int i = lane * (kMaxPagedSeqs / 32) + k;
+      len[k] = i < n ? min(max(c.seq_len[p.b.id[i]], 0), c.cap) : 0;
+      mine += static_cast<int64_t>((len[k] + G::CT - 1) / G::CT) * n_kv;
     }
-    float k[D / 32], v[D / 32];
-    load_row<D>(c, c.k_pages, row, kv, k, lane);
-    load_row<D>(c, c.v_pages, row, kv, v, lane);
-    float s = 0.f;
-    for (int j = 0; j < D / 32; ++j) s = fmaf(q[j], k[j], s);
-    s = warp_sum(s) * ks * c.scale_log2;
-    const float m1 = fmaxf(m, s);
-    const float f = exp2f(m - m1), w = exp2f(s - m1);
-    l = l * f + w;
-    for (int j = 0; j < D / 32; ++j) o[j] = o[j] * f + w * v[j];
-    m = m1;
+    int64_t incl = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += y;
+    }
+    int64_t at = incl - mine;
+#pragma unroll
+    for (int k = 0; k < kMaxPagedSeqs / 32; ++k) {
+      const int i = lane * (kMaxPagedSeqs / 32) + k;
+      sh.len[i] = len[k];
+      sh.cum[i] = at;
+      at += static_cast<int64_t>((len[k] + G::CT - 1) / G::CT) * n_kv;
+    }
+    if (lane == 31) sh.cum[kMaxPagedSeqs] = at;
   }
-  const float inv = l > 0.f ? vs / l : (l == 0.f ? 0.f : l);
-  const int64_t out = static_cast<int64_t>(i) * c.n_heads + h;
-  for (int j = 0; j < D / 32; ++j) p.o[out * D + lane + 32 * j] = __float2bfloat16(o[j] * inv);
-  const float lse = m == -INFINITY ? m : (m + log2f(l)) * 0.69314718055994531f;
-  if (lane == 0) {
-    if (p.lse) p.lse[out] = lse;
-    p.ws_lse[out] = lse;
+  __syncthreads();
+  // sequences without a token: nothing to attend to
+  for (int i = blockIdx.x; i < n; i += gridDim.x)
+    if (sh.len[i] == 0) {
+      for (int x = threadIdx.x; x < c.n_heads * D / 8; x += kThreads)
+        reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * c.n_heads * D)[x] = make_uint4(0, 0, 0, 0);
+      for (int h = threadIdx.x; h < c.n_heads; h += kThreads)
+        if (p.lse) p.lse[static_cast<int64_t>(i) * c.n_heads + h] = -INFINITY;
+      for (int h = threadIdx.x; h < n_kv; h += kThreads) p.items[i * n_kv + h] = PagedItem{0, 0, 0};
+    }
+  const int64_t T = sh.cum[n];
+  // CTAs that work: each gets one tile at least, so that all between an item's first and last have a part of it
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), T);
+  if (blockIdx.x >= ctas) return;
+  const int64_t t0 = blockIdx.x * T / ctas, t1 = (blockIdx.x + 1) * T / ctas;
+  Cursor comp;
+  {
+    int lo = 0, hi = n - 1;   // the last sequence that starts at or before t0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (sh.cum[mid] <= t0) lo = mid; else hi = mid - 1;
+    }
+    comp.i = lo;
+    cursor_seq<G::CT>(comp, sh);
+    const int64_t within = t0 - sh.cum[lo];
+    comp.h = static_cast<int>(within / comp.tiles);
+    comp.tile = static_cast<int32_t>(within - static_cast<int64_t>(comp.h) * comp.tiles);
   }
-}
+  Cursor load = comp;
+  int64_t t_load = t0;
+  const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
+  uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
+  const int64_t row_pitch = static_cast<int64_t>(n_kv) * G::kRowBytes;
 
-template <int D>
-__global__ void __launch_bounds__(128) paged_mass_simple(const __grid_constant__ PagedAttnParams p) {
-  grid_dep_wait();
-  const PagedView& c = p.c;
-  const int lane = threadIdx.x % 32;
-  const int i = blockIdx.x % p.b.n;
-  const int32_t seq = p.b.id[i];
-  const int32_t len = live_len(c, seq);
-  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  for (int32_t t = (blockIdx.x / p.b.n) * 4 + threadIdx.x / 32; t < len; t += gridDim.x / p.b.n * 4) {
-    const int64_t row = paged_row(table, t, c.page_tokens, c.n_pages);
-    if (row < 0) continue;
-    float w = 0.f;
-    for (int kv = 0; kv < c.n_kv; ++kv) {
-      const float ks = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f;
-      float k[D / 32];
-      load_row<D>(c, c.k_pages, row, kv, k, lane);
-      for (int g = 0; g < c.group; ++g) {
-        const int64_t out = static_cast<int64_t>(i) * c.n_heads + kv * c.group + g;
-        float s = 0.f;
-        for (int j = 0; j < D / 32; ++j) s = fmaf(__bfloat162float(p.q[out * D + lane + 32 * j]), k[j], s);
-        w += exp2f(warp_sum(s) * ks * c.scale_log2 - p.ws_lse[out] * 1.4426950408889634f);
+  // ---- copy this warp's tokens of one tile into a stage
+  auto issue = [&](int stage) {
+    if (t_load < t1) {
+      const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
+      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
+      constexpr int kRowsPer = 32 / G::kChunks;   // rows per instruction
+      const int r0 = lane / G::kChunks, ch = lane % G::kChunks;
+#pragma unroll
+      for (int g = 0; g < G::kGroups; ++g) {
+        const int32_t tok = load.tile * G::CT + warp * G::KT + g * 16;
+        int32_t live = load.len - tok;
+        int64_t row = 0;
+        if (live > 0) {
+          row = paged_row(table, tok, c.page_tokens, c.n_pages);
+          const uint32_t bit = 1u << (stage * G::kGroups + g);
+          bad &= ~bit;
+          if (row < 0) {
+            if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
+            bad |= bit;
+            row = 0;
+            live = 0;
+          }
+        }
+        const int64_t at = row * row_pitch + load.h * G::kRowBytes + ch * 16;
+        const char* kp = static_cast<const char*>(c.k_pages) + at;
+        const char* vp = static_cast<const char*>(c.v_pages) + at;
+#pragma unroll
+        for (int x = 0; x < 16 / kRowsPer; ++x) {
+          const int r = x * kRowsPer + r0;
+          const bool in = r < live;
+          const int64_t off = in ? r * row_pitch : 0;
+          copy16(ks + chunk_at<G::kChunks>(g * 16 + r, ch), kp + off, in);
+          copy16(vs + chunk_at<G::kChunks>(g * 16 + r, ch), vp + off, in);
+        }
+      }
+      ++t_load;
+      cursor_next<G::CT>(load, sh, n_kv, t_load < t1);
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
+
+  // ---- the items of this stretch, one after the other
+  int stage = 0;
+  int64_t t = t0;
+  const int j4 = lane % 4, r8 = lane / 4;
+  while (t < t1) {
+    const int item_i = comp.i, item_h = comp.h;
+    const int32_t first_tile = comp.tile;
+    const int64_t item_tile0 = t - first_tile;       // the item's first tile on the line
+    const int64_t seg_end = min(t1, item_tile0 + comp.tiles);
+    const int32_t len = comp.len;
+    // the group's query rows as left operands; e4m3: rows scaled to a largest element in [1, 2)
+    uint32_t qa[D / 16][4];
+    float xs[2];                                      // log2-scaled scores = product * xs, rows r8 and r8 + 8
+    {
+      const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(item_i) * c.n_heads + item_h * group) * D;
+      const float ks = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f;
+      xs[0] = xs[1] = c.scale_log2 * ks;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = r8 + 8 * half;
+        if constexpr (TYPE == SR_PAGE_BF16) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              qa[kk][half + 2 * x] =
+                  r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
+        } else {
+          uint2 raw[D / 16];
+          float top = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            raw[kk] = r < group ? *reinterpret_cast<const uint2*>(qp + r * D + kk * 16 + 4 * j4) : make_uint2(0u, 0u);
+            const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].x));
+            const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].y));
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
+          const float down = ldexpf(1.f, -e);
+          xs[half] *= ldexpf(1.f, e);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].x));
+            const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].y));
+            qa[kk][half] = pack_half2(a.x * down, a.y * down);
+            qa[kk][half + 2] = pack_half2(b.x * down, b.y * down);
+          }
+        }
       }
     }
+    float o[D / 8][4];
+#pragma unroll
+    for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // of rows r8, r8 + 8; l: this lane's share
+
+    for (; t < seg_end; ++t) {
+      issue((stage + kStages - 1) % kStages);
+      copy_wait<kStages - 1>();
+      __syncwarp();
+      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
+      const int32_t tok = comp.tile * G::CT + warp * G::KT;
+      uint32_t live[G::kGroups], any = 0;
+#pragma unroll
+      for (int g = 0; g < G::kGroups; ++g) {
+        live[g] = (bad >> (stage * G::kGroups + g)) & 1u ? 0u : static_cast<uint32_t>(min(max(len - tok - g * 16, 0), 16));
+        any |= live[g];
+      }
+      if (any) {
+        float s[G::KT / 8][4];
+#pragma unroll
+        for (int k = 0; k < G::KT / 8; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[k][x] = 0.f;
+        // scores: matrices of 8 keys x 16 bytes; lane -> (key, chunk) of the four that one load brings
+#pragma unroll
+        for (int g = 0; g < G::kGroups; ++g) {
+          const int kr = g * 16 + (lane % 8) + 8 * (lane / 16), kc = (lane / 8) % 2;
+          if constexpr (TYPE == SR_PAGE_BF16) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              uint32_t b[4];
+              ldsm4(b, ks + chunk_at<G::kChunks>(kr, 2 * kk + kc));
+              mma16816<TYPE>(s[2 * g], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
+              mma16816<TYPE>(s[2 * g + 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+              uint32_t b[4];
+              ldsm4(b, ks + chunk_at<G::kChunks>(kr, kk + kc));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                mma16816<TYPE>(s[2 * g], qa[kk + x][0], qa[kk + x][1], qa[kk + x][2], qa[kk + x][3], half2_of_e4m3(b[x]),
+                               half2_of_e4m3(b[x] >> 16));
+                mma16816<TYPE>(s[2 * g + 1], qa[kk + x][0], qa[kk + x][1], qa[kk + x][2], qa[kk + x][3],
+                               half2_of_e4m3(b[2 + x]), half2_of_e4m3(b[2 + x] >> 16));
+              }
+            }
+          }
+        }
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < G::KT / 8; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t key = (k % 2) * 8 + 2 * j4 + (x & 1);
+            s[k][x] = key < live[k / 2] ? s[k][x] * xs[x / 2] : -INFINITY;
+            top[x / 2] = fmaxf(top[x / 2], s[k][x]);
+          }
+        if constexpr (MASS) {
+          // the scaled scores, for the weights that the second launch forms
+          if (t < p.score_tiles) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int r = r8 + 8 * half;
+              if (r < group) {
+                float* dst = p.scores + (t * group + r) * G::CT + warp * G::KT + 2 * j4;
+#pragma unroll
+                for (int k = 0; k < G::KT / 8; ++k)
+                  *reinterpret_cast<float2*>(dst + k * 8) = make_float2(s[k][2 * half], s[k][2 * half + 1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
+          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+          float f[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float m1 = fmaxf(m[half], top[half]);
+            f[half] = m[half] == -INFINITY ? 0.f : ex2_approx(m[half] - m1);
+            m[half] = m1;
+            l[half] *= f[half];
+          }
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[k][x] *= f[x / 2];
+        }
+        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+#pragma unroll
+        for (int k = 0; k < G::KT / 8; ++k)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            s[k][x] = ex2_approx(s[k][x] - (x < 2 ? m0 : m1));
+            l[x / 2] += s[k][x];
+          }
+#pragma unroll
+        for (int g = 0; g < G::kGroups; ++g) {
+          uint32_t a[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float lo = s[2 * g + x / 2][2 * (x % 2)], hi = s[2 * g + x / 2][2 * (x % 2) + 1];
+            a[x] = TYPE == SR_PAGE_BF16 ? pack_bf16x2(lo, hi) : pack_half2(lo * 1024.f, hi * 1024.f);
+          }
+          const int vr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
+          if constexpr (TYPE == SR_PAGE_BF16) {
+#pragma unroll
+            for (int k = 0; k < D / 8; k += 2) {
+              uint32_t b[4];
+              ldsm4t(b, vs + chunk_at<G::kChunks>(vr, k + vc));
+              mma16816<TYPE>(o[k], a[0], a[1], a[2], a[3], b[0], b[1]);
+              mma16816<TYPE>(o[k + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+            }
+          } else {
+            // a transposed 16-bit element is two neighbouring head dims of one key: the even ones
+            // form one operand, the odd ones the next
+#pragma unroll
+            for (int k = 0; k < D / 8; k += 4) {
+              uint32_t b[4];
+              ldsm4t(b, vs + chunk_at<G::kChunks>(vr, k / 2 + vc));
+#pragma unroll
+              for (int x = 0; x < 4; ++x) b[x] = __byte_perm(b[x], 0, 0x3120);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                mma16816<TYPE>(o[k + 2 * x], a[0], a[1], a[2], a[3], half2_of_e4m3(b[2 * x]), half2_of_e4m3(b[2 * x + 1]));
+                mma16816<TYPE>(o[k + 2 * x + 1], a[0], a[1], a[2], a[3], half2_of_e4m3(b[2 * x] >> 16),
+                               half2_of_e4m3(b[2 * x + 1] >> 16));
+              }
+            }
+          }
+        }
+      } else if constexpr (MASS) {
+        // no token here, or none with a page: weights of zero
+        if (t < p.score_tiles) {
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            if (r8 + 8 * half < group) {
+              float* dst = p.scores + (t * group + r8 + 8 * half) * G::CT + warp * G::KT + 2 * j4;
+#pragma unroll
+              for (int k = 0; k < G::KT / 8; ++k) *reinterpret_cast<float2*>(dst + k * 8) = make_float2(-INFINITY, -INFINITY);
+            }
+        }
+      }
+      __syncwarp();
+      stage = (stage + 1) % kStages;
+      cursor_next<G::CT>(comp, sh, n_kv, t + 1 < t1);
+    }
+
+    // ---- merge the four warps' results; warp 0 writes them
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], 1);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], 2);
+    if (j4 == 0) {
+      sh.ml[warp][r8][0] = m[0];
+      sh.ml[warp][r8][1] = l[0];
+      sh.ml[warp][r8 + 8][0] = m[1];
+      sh.ml[warp][r8 + 8][1] = l[1];
+    }
+    __syncthreads();
+    const bool whole = first_tile == 0 && seg_end == item_tile0 + (len + G::CT - 1) / G::CT;
+    const int slot = static_cast<int>(blockIdx.x) * 2 + (first_tile == 0 ? 1 : 0);
+    float* part = p.parts + static_cast<int64_t>(slot) * kRows * (D + 2);
+    const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[n_kv + item_h])) : 1.f;
+    const float vs1 = TYPE == SR_PAGE_BF16 ? vscale : vscale * 0x1p-10f;
+    float mine[2], top[2], sum[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = r8 + 8 * half;
+      top[half] = sh.ml[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top[half] = fmaxf(top[half], sh.ml[w][r][0]);
+      sum[half] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = sh.ml[w][r][0];
+        sum[half] = fmaf(mw == -INFINITY ? 0.f : ex2_approx(mw - top[half]), sh.ml[w][r][1], sum[half]);
+      }
+      mine[half] = m[half] == -INFINITY ? 0.f : ex2_approx(m[half] - top[half]);
+    }
+    if constexpr (TYPE != SR_PAGE_BF16) {
+      // (even dims, odd dims) back to neighbours: o[k] holds dims 16 b + 4 j4 + {0, 1}, o[k + 1] + {2, 3}
+#pragma unroll
+      for (int k = 0; k < D / 8; k += 2)
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          const float y = o[k][x + 1];
+          o[k][x + 1] = o[k + 1][x];
+          o[k + 1][x] = y;
+        }
+    }
+    auto col = [&](int k) { return TYPE == SR_PAGE_BF16 ? 8 * k + 2 * j4 : 8 * (k & ~1) + 4 * j4 + 2 * (k & 1); };
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half * 8 >= group) break;
+      if (half == 1) __syncthreads();         // warp 0 has read the first eight rows
+      if (warp > 0) {
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k)
+          *reinterpret_cast<float2*>(merge + ((warp - 1) * 8 + r8) * D + col(k)) =
+              make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
+      }
+      __syncthreads();
+      const int r = r8 + 8 * half;
+      if (warp == 0 && r < group) {
+        const int64_t out = static_cast<int64_t>(item_i) * c.n_heads + item_h * group + r;
+        const float scale = whole ? (sum[half] == 0.f ? 0.f : vs1 / sum[half]) : vs1;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          float2 y = make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
+#pragma unroll
+          for (int w = 0; w < kWarps - 1; ++w) {
+            const float2 z = *reinterpret_cast<const float2*>(merge + (w * 8 + r8) * D + col(k));
+            y.x += z.x;
+            y.y += z.y;
+          }
+          y.x *= scale;
+          y.y *= scale;
+          if (whole)
+            *reinterpret_cast<uint32_t*>(p.o + out * D + col(k)) = pack_bf16x2(y.x, y.y);
+          else
+            *reinterpret_cast<float2*>(part + r * D + col(k)) = y;
+        }
+        if (j4 == 0) {
+          if (whole) {
+            const float lse2 = sum[half] == 0.f ? -INFINITY : top[half] + log2f(sum[half]);
+            if (p.lse) p.lse[out] = lse2 * kLn2;
+            if (MASS) p.lse2[out] = lse2;
+          } else {
+            part[kRows * D + 2 * r] = top[half];
+            part[kRows * D + 2 * r + 1] = sum[half];
+          }
+        }
+      }
+    }
+    if (first_tile == 0 && threadIdx.x == 0) {
+      // the CTA of the item's last tile, for the join
+      const int64_t last = item_tile0 + (len + G::CT - 1) / G::CT - 1;
+      const int c1 = static_cast<int>(((last + 1) * ctas - 1) / T);
+      p.items[item_i * n_kv + item_h] = PagedItem{item_tile0, static_cast<int32_t>(blockIdx.x), c1};
+      if (MASS && last >= p.score_tiles) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
+    }
+    __syncthreads();   // sh.ml and merge are free for the next item
+  }
+}
+
+// Join the partial results of the items that several CTAs share: one CTA per
+// item, a warp per query row, the lanes across the head dimension.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const PagedView& c = p.c;
+  const PagedItem it = p.items[blockIdx.x];
+  if (it.c0 == it.c1) return;
+  const int i = blockIdx.x / c.n_kv, h = blockIdx.x % c.n_kv;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n_parts = it.c1 - it.c0 + 1;
+  constexpr int kPart = kRows * (D + 2);
+  constexpr int kCols = D / 32;
+  auto part = [&](int k) { return p.parts + static_cast<int64_t>((it.c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPart; };
+  for (int r = warp; r < c.group; r += kJoinThreads / 32) {
+    float top = -INFINITY;
+    for (int k = lane; k < n_parts; k += 32) top = fmaxf(top, part(k)[kRows * D + 2 * r]);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    float sum = 0.f, a[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) a[x] = 0.f;
+    for (int k0 = 0; k0 < n_parts; k0 += 32) {
+      float w = 0.f;
+      if (k0 + lane < n_parts) {
+        const float mk = part(k0 + lane)[kRows * D + 2 * r];
+        w = mk == -INFINITY ? 0.f : ex2_approx(mk - top);
+        sum = fmaf(w, part(k0 + lane)[kRows * D + 2 * r + 1], sum);
+      }
+      const int m = min(32, n_parts - k0);
+#pragma unroll 4
+      for (int k = 0; k < m; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const float* src = part(k0 + k) + r * D + lane * kCols;
+        if constexpr (kCols == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]); a[2] = fmaf(wk, v.z, a[2]); a[3] = fmaf(wk, v.w, a[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t out = static_cast<int64_t>(i) * c.n_heads + h * c.group + r;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + out * D + lane * kCols);
+    dst[0] = pack_bf16x2(a[0] * inv, a[1] * inv);
+    if constexpr (kCols == 4) dst[1] = pack_bf16x2(a[2] * inv, a[3] * inv);
     if (lane == 0) {
-      float* m = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
-      *m = fmaf(p.mass_decay, *m, w);
+      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+      if (p.lse) p.lse[out] = lse2 * kLn2;
+      p.lse2[out] = lse2;
     }
   }
+}
+
+// The weights: mass(t) <- decay * mass(t) + sum over heads of 2^(x_h(t) - lse2_h).
+// `per` CTAs per sequence, a thread per token; a token's scores of one head lie next
+// to its neighbours', so that loads are contiguous.
+constexpr int kMassThreads = 256;
+template <int CT>
+__global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_constant__ PagedAttnParams p, int per) {
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const PagedView& c = p.c;
+  const int i = blockIdx.x / per;
+  const int32_t seq = p.b.id[i];
+  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
+  if (len == 0) return;
+  const int32_t tiles = (len + CT - 1) / CT;
+  const float* lse2 = p.lse2 + static_cast<int64_t>(i) * c.n_heads;
+  const int64_t tile0 = p.items[i * c.n_kv].tile0;       // the other heads' items follow
+  if (tile0 + static_cast<int64_t>(tiles) * c.n_kv > p.score_tiles) return;
+  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  for (int32_t t = (blockIdx.x % per) * kMassThreads + threadIdx.x; t < len; t += per * kMassThreads) {
+    if (paged_row(table, t, c.page_tokens, c.n_pages) < 0) continue;   // not seen: left as it is
+    const float* x = p.scores + (tile0 + t / CT) * c.group * CT + t % CT;
+    const int64_t pitch = static_cast<int64_t>(tiles) * c.group * CT;
+    float w = 0.f;
+    for (int h = 0; h < c.n_kv; ++h)
+#pragma unroll 4
+      for (int g = 0; g < c.group; ++g) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
+    float* m = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
+    *m = fmaf(p.mass_decay, *m, w);
+  }
+}
+
+template <int D, int TYPE, bool MASS>
+cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
+  using G = Geo<D, TYPE>;
+  constexpr int smem = G::kStageArea + G::kMergeFloats * 4 + static_cast<int>(sizeof(SharedHead));
+  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
+  // per device, and cheap next to a launch
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(paged_attn_ctas());
+  e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, smem, st, p);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(paged_join_kernel<D>, static_cast<unsigned>(p.b.n) * p.c.n_kv, kJoinThreads, 0, st, p);
+  if (e != cudaSuccess || !MASS) return e;
+  const int per = std::max(1, 4 * sm_count() / p.b.n);
+  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads, 0, st, p, per);
+}
+
+template <int D, int TYPE>
+cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
+  return p.mass_decay >= 0.f ? launch<D, TYPE, true>(p, st) : launch<D, TYPE, false>(p, st);
 }
 
 }  // namespace
 
+int paged_attn_ctas() { return std::min(2 * sm_count(), kMaxPagedCtas); }
+
+size_t paged_part_floats(int head_dim) { return static_cast<size_t>(kRows) * (head_dim + 2); }
+int paged_tile_tokens(int head_dim, int page_type) {
+  if (head_dim == 128) return page_type == SR_PAGE_BF16 ? Geo<128, SR_PAGE_BF16>::CT : Geo<128, SR_PAGE_E4M3>::CT;
+  return page_type == SR_PAGE_BF16 ? Geo<64, SR_PAGE_BF16>::CT : Geo<64, SR_PAGE_E4M3>::CT;
+}
+
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st) {
-  const unsigned grid = (p.b.n * p.c.n_heads + 3) / 4;
-  auto k = p.c.head_dim == 128 ? paged_attn_simple<128> : paged_attn_simple<64>;
-  cudaError_t e = launch_dependent(k, grid, 128, 0, st, p);
-  if (e != cudaSuccess || p.mass_decay < 0.f) return e;
-  auto m = p.c.head_dim == 128 ? paged_mass_simple<128> : paged_mass_simple<64>;
-  return launch_dependent(m, static_cast<unsigned>(p.b.n) * 64, 128, 0, st, p);
+  if (p.c.head_dim == 128)
+    return p.c.page_type == SR_PAGE_BF16 ? launch<128, SR_PAGE_BF16>(p, st) : launch<128, SR_PAGE_E4M3>(p, st);
+  return p.c.page_type == SR_PAGE_BF16 ? launch<64, SR_PAGE_BF16>(p, st) : launch<64, SR_PAGE_E4M3>(p, st);
 }
 
 }  // namespace sr

@@ -46,7 +46,11 @@ struct PagedLayout {
   size_t plan;             // EvictPlan[kMaxPagedSeqs]
   size_t moves;            // int2[move_cap]: (from, to) logical indices
   int64_t move_cap;
-  size_t lse;              // float[kMaxPagedSeqs][n_heads]
+  size_t items;            // PagedItem[kMaxPagedSeqs][n_kv]
+  size_t parts;            // [kMaxPagedCtas][2] partial results
+  size_t lse2;             // float[kMaxPagedSeqs][n_heads], log2 units
+  size_t scores;           // float[score_tiles][group][tile tokens]
+  int64_t score_tiles;
   size_t bytes;
 };
 constexpr int kPagedCounters = 1024;
@@ -56,6 +60,13 @@ struct EvictPlan {
   int64_t list0;           // its first entry in the list of moves
   int32_t moves;
   int32_t new_len;         // -1: left as it is
+};
+
+// A sequence and key/value head of an attention call: its first tile on the line
+// of all tiles, and the CTAs that hold its first and last ones.
+struct PagedItem {
+  int64_t tile0;
+  int32_t c0, c1;
 };
 
 struct PagedBatch {
@@ -80,7 +91,11 @@ struct PagedAttnParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
-  float* ws_lse;
+  PagedItem* items;
+  float* parts;
+  float* lse2;
+  float* scores;
+  int64_t score_tiles;
   float mass_decay;
   PagedBatch b;
 };
@@ -98,6 +113,9 @@ cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStre
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
+int paged_attn_ctas();                                    // CTAs of an attention launch
+int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
+size_t paged_part_floats(int head_dim);                   // floats of one partial result
 int paged_append_rows_per_cta(int n_kv, int head_dim);
 
 }  // namespace sr
