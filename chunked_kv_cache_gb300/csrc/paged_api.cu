@@ -56,13 +56,13 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   l.move_cap = with_mass ? static_cast<int64_t>(c.n_pages) * c.page_tokens / 2 + sr::kMaxPagedSeqs : 0;
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
-  l.items = take(seqs * c.n_kv_heads * sizeof(sr::PagedItem));
+  l.unit0 = take(sr::kMaxPagedSeqs * sizeof(int64_t));
   l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.head_dim) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
   // every token of the pool once, the sequences' lengths rounded up to tiles
   const int64_t tile = sr::paged_tile_tokens(c.head_dim, c.page_type);
-  l.score_tiles = with_mass ? (static_cast<int64_t>(c.n_pages) * c.page_tokens / tile + static_cast<int64_t>(seqs)) *
-                                  c.n_kv_heads : 0;
+  l.score_tiles = with_mass ? sr::paged_score_tiles(static_cast<int64_t>(c.n_pages) * c.page_tokens, static_cast<int>(seqs),
+                                                    c.n_kv_heads, static_cast<int>(tile)) : 0;
   l.scores = take(static_cast<size_t>(l.score_tiles) * (c.n_heads / c.n_kv_heads) * tile * 4);
   l.bytes = at;
   return l;
@@ -158,6 +158,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
+  if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);
   if (e != cudaSuccess) {
@@ -234,7 +235,9 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  p.items = ws_at<sr::PagedItem>(c, c->layout.items);
+  p.unit0 = ws_at<int64_t>(c, c->layout.unit0);
+  p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
+  p.group_arrivals = p.arrivals + sr::kMaxPagedCtas;
   p.parts = ws_at<float>(c, c->layout.parts);
   p.lse2 = ws_at<float>(c, c->layout.lse2);
   p.scores = ws_at<float>(c, c->layout.scores);

@@ -13,8 +13,9 @@
 // single long one both occupy the whole GPU, and the lengths, which only the device
 // knows, never reach the host. A CTA that covers an item whole writes its output; of an
 // item cut between CTAs each writes its partial result (fp32 sums, maximum and sum of
-// the softmax), and a second launch joins them in the order of the line, so that
-// results do not depend on timing.
+// the softmax), and the last of them to arrive joins the parts in the order of the line,
+// so that results do not depend on timing. More than kJoin parts are joined in two
+// levels (kJoin neighbours first), so that no CTA reads many of them by itself.
 //
 // Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
 // copies its tokens' keys and values into its own three shared-memory stages
@@ -117,12 +118,15 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
 }
 
 struct SharedHead {
-  int64_t cum[kMaxPagedSeqs + 1];       // tiles before each sequence of the batch
+  int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
   float ml[kWarps][kRows][2];           // each warp's maximum and sum, while warps merge
+  int last;                             // this CTA is the last of its item's to arrive
 };
 
-// A place on the line of tiles.
+// A place on the line of tiles. Each item takes kItemCost units before its tiles:
+// what changing items costs a CTA, in tiles.
+constexpr int kItemCost = 1;
 struct Cursor {
   int i, h;            // sequence of the batch, key/value head
   int32_t tile, tiles; // tile of the item, tiles it has
@@ -130,19 +134,93 @@ struct Cursor {
 };
 
 template <int CT>
+__device__ __forceinline__ int64_t seq_units(int32_t len, int n_kv) {
+  return len > 0 ? static_cast<int64_t>((len + CT - 1) / CT + kItemCost) * n_kv : 0;
+}
+template <int CT>
 __device__ __forceinline__ void cursor_seq(Cursor& c, const SharedHead& s) {
   while (s.len[c.i] == 0) ++c.i;        // the line holds a tile here: some sequence has one
   c.len = s.len[c.i];
   c.tiles = (c.len + CT - 1) / CT;
 }
 template <int CT>
-__device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int n_kv, bool more) {
-  if (++c.tile < c.tiles || !more) return;
+__device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int n_kv, int64_t& left) {
+  // left: units of this CTA's stretch from the cursor's tile on
+  --left;
+  if (++c.tile < c.tiles) return;
   c.tile = 0;
-  if (++c.h < n_kv) return;
+  left -= kItemCost;
+  if (left <= 0 || ++c.h < n_kv) return;
   c.h = 0;
   ++c.i;
   cursor_seq<CT>(c, s);
+}
+
+// ---- joining partial results
+constexpr int kJoin = 16;
+
+// Partial result of a CTA: slot 0 for an item that began before its stretch, 1 for one
+// that begins in it. [kRows][D] sums, then (maximum, sum) per row.
+template <int D>
+__device__ __forceinline__ float* part_at(const PagedAttnParams& p, int cta, int slot) {
+  return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * kRows * (D + 2);
+}
+
+// Joins `n` <= 32 parts: the one at first, slot s0, and those of every step-th CTA after it, slot 0. The
+// result is another part (dst) or the output. Each warp takes query rows, its lanes the
+// head dimension; the loads of four parts are in flight together.
+template <int D>
+__device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int s0, int step, int n, float* dst,
+                                        int64_t out0, int warp, int lane) {
+  __threadfence();
+  constexpr int kCols = D / 32;
+  for (int r = warp; r < p.c.group; r += kWarps) {
+    float mk = -INFINITY, lk = 0.f;
+    if (lane < n) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(part_at<D>(p, first + lane * step, lane == 0 ? s0 : 0) +
+                                                              kRows * D) + r);
+      mk = v.x;
+      lk = v.y;
+    }
+    float top = mk;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float w = mk == -INFINITY ? 0.f : ex2_approx(mk - top);
+    float sum = w * lk;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    float a[kCols];
+#pragma unroll
+    for (int x = 0; x < kCols; ++x) a[x] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* src = part_at<D>(p, first + k * step, k == 0 ? s0 : 0) + r * D + lane * kCols;
+      if constexpr (kCols == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]); a[2] = fmaf(wk, v.z, a[2]); a[3] = fmaf(wk, v.w, a[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+        a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]);
+      }
+    }
+    if (dst) {
+      // in place over its own first part: this warp alone reads and writes row r
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) dst[r * D + lane * kCols + x] = a[x];
+      if (lane == 0) reinterpret_cast<float2*>(dst + kRows * D)[r] = make_float2(top, sum);
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint32_t* o = reinterpret_cast<uint32_t*>(p.o + (out0 + r) * D + lane * kCols);
+      o[0] = pack_bf16x2(a[0] * inv, a[1] * inv);
+      if constexpr (kCols == 4) o[1] = pack_bf16x2(a[2] * inv, a[3] * inv);
+      if (lane == 0) {
+        const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+        if (p.lse) p.lse[out0 + r] = lse2 * kLn2;
+        p.lse2[out0 + r] = lse2;
+      }
+    }
+  }
 }
 
 template <int D, int TYPE, bool MASS>
@@ -165,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     for (int k = 0; k < kMaxPagedSeqs / 32; ++k) {
       const int i = lane * (kMaxPagedSeqs / 32) + k;
       len[k] = i < n ? min(max(c.seq_len[p.b.id[i]], 0), c.cap) : 0;
-      mine += static_cast<int64_t>((len[k] + G::CT - 1) / G::CT) * n_kv;
+      mine += seq_units<G::CT>(len[k], n_kv);
     }
     int64_t incl = mine;
 #pragma unroll
@@ -179,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       const int i = lane * (kMaxPagedSeqs / 32) + k;
       sh.len[i] = len[k];
       sh.cum[i] = at;
-      at += static_cast<int64_t>((len[k] + G::CT - 1) / G::CT) * n_kv;
+      at += seq_units<G::CT>(len[k], n_kv);
     }
     if (lane == 31) sh.cum[kMaxPagedSeqs] = at;
   }
@@ -191,35 +269,41 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         reinterpret_cast<uint4*>(p.o + static_cast<int64_t>(i) * c.n_heads * D)[x] = make_uint4(0, 0, 0, 0);
       for (int h = threadIdx.x; h < c.n_heads; h += kThreads)
         if (p.lse) p.lse[static_cast<int64_t>(i) * c.n_heads + h] = -INFINITY;
-      for (int h = threadIdx.x; h < n_kv; h += kThreads) p.items[i * n_kv + h] = PagedItem{0, 0, 0};
     }
   const int64_t T = sh.cum[n];
-  // CTAs that work: each gets one tile at least, so that all between an item's first and last have a part of it
+  if (MASS && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < n; i += kThreads) p.unit0[i] = sh.cum[i];
+  // CTAs that work: each gets one unit at least, so that all between an item's first and last have a part of it
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), T);
   if (blockIdx.x >= ctas) return;
-  const int64_t t0 = blockIdx.x * T / ctas, t1 = (blockIdx.x + 1) * T / ctas;
+  const int64_t u0 = blockIdx.x * T / ctas, u1 = (blockIdx.x + 1) * T / ctas;
   Cursor comp;
+  int64_t left = u1 - u0;   // units of the stretch from comp on
   {
-    int lo = 0, hi = n - 1;   // the last sequence that starts at or before t0
+    int lo = 0, hi = n - 1;   // the last sequence that starts at or before u0
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (sh.cum[mid] <= t0) lo = mid; else hi = mid - 1;
+      if (sh.cum[mid] <= u0) lo = mid; else hi = mid - 1;
     }
     comp.i = lo;
     cursor_seq<G::CT>(comp, sh);
-    const int64_t within = t0 - sh.cum[lo];
-    comp.h = static_cast<int>(within / comp.tiles);
-    comp.tile = static_cast<int32_t>(within - static_cast<int64_t>(comp.h) * comp.tiles);
+    const int64_t within = u0 - sh.cum[comp.i];
+    const int32_t units = comp.tiles + kItemCost;
+    comp.h = static_cast<int>(within / units);
+    const int32_t unit = static_cast<int32_t>(within - static_cast<int64_t>(comp.h) * units);
+    comp.tile = max(unit - kItemCost, 0);
+    left -= max(kItemCost - unit, 0);
   }
+  if (left <= 0) return;    // nothing but the units before an item
   Cursor load = comp;
-  int64_t t_load = t0;
+  int64_t left_load = left;
   const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
   const int64_t row_pitch = static_cast<int64_t>(n_kv) * G::kRowBytes;
 
   // ---- copy this warp's tokens of one tile into a stage
   auto issue = [&](int stage) {
-    if (t_load < t1) {
+    if (left_load > 0) {
       const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
       constexpr int kRowsPer = 32 / G::kChunks;   // rows per instruction
@@ -252,8 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           copy16(vs + chunk_at<G::kChunks>(g * 16 + r, ch), vp + off, in);
         }
       }
-      ++t_load;
-      cursor_next<G::CT>(load, sh, n_kv, t_load < t1);
+      cursor_next<G::CT>(load, sh, n_kv, left_load);
     }
     copy_commit();
   };
@@ -262,56 +345,62 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
   // ---- the items of this stretch, one after the other
   int stage = 0;
-  int64_t t = t0;
   const int j4 = lane % 4, r8 = lane / 4;
-  while (t < t1) {
-    const int item_i = comp.i, item_h = comp.h;
-    const int32_t first_tile = comp.tile;
-    const int64_t item_tile0 = t - first_tile;       // the item's first tile on the line
-    const int64_t seg_end = min(t1, item_tile0 + comp.tiles);
-    const int32_t len = comp.len;
-    // the group's query rows as left operands; e4m3: rows scaled to a largest element in [1, 2)
-    uint32_t qa[D / 16][4];
-    float xs[2];                                      // log2-scaled scores = product * xs, rows r8 and r8 + 8
-    {
-      const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(item_i) * c.n_heads + item_h * group) * D;
-      const float ks = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f;
-      xs[0] = xs[1] = c.scale_log2 * ks;
+  // The group's query rows as left operands. Those of the next item are fetched before
+  // the current one's results are merged, so that their latency hides behind that.
+  uint32_t qa[D / 16][4];
+  auto fetch_q = [&](int i, int h) {
+    const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(i) * c.n_heads + h * group) * D;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int r = r8 + 8 * half;
+    for (int half = 0; half < 2; ++half) {
+      const int r = r8 + 8 * half;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
         if constexpr (TYPE == SR_PAGE_BF16) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              qa[kk][half + 2 * x] =
-                  r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
+          for (int x = 0; x < 2; ++x)
+            qa[kk][half + 2 * x] = r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
         } else {
-          uint2 raw[D / 16];
-          float top = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            raw[kk] = r < group ? *reinterpret_cast<const uint2*>(qp + r * D + kk * 16 + 4 * j4) : make_uint2(0u, 0u);
-            const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].x));
-            const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].y));
-            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-          }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
-          const float down = ldexpf(1.f, -e);
-          xs[half] *= ldexpf(1.f, e);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const float2 a = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].x));
-            const float2 b = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&raw[kk].y));
-            qa[kk][half] = pack_half2(a.x * down, a.y * down);
-            qa[kk][half + 2] = pack_half2(b.x * down, b.y * down);
-          }
+          const uint2 raw = r < group ? *reinterpret_cast<const uint2*>(qp + r * D + kk * 16 + 4 * j4) : make_uint2(0u, 0u);
+          qa[kk][half] = raw.x;
+          qa[kk][half + 2] = raw.y;
         }
       }
     }
+  };
+  fetch_q(comp.i, comp.h);
+  while (left > 0) {
+    const int item_i = comp.i, item_h = comp.h;
+    const int32_t first_tile = comp.tile, tiles = comp.tiles;
+    const int32_t end_tile = static_cast<int32_t>(min(static_cast<int64_t>(tiles), first_tile + left));
+    const int32_t len = comp.len;
+    // e4m3: rows scaled to a largest element in [1, 2), in fp16
+    float xs[2];                                      // log2-scaled scores = product * xs, rows r8 and r8 + 8
+    xs[0] = xs[1] = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f);
+    if constexpr (TYPE != SR_PAGE_BF16) {
+      auto pair = [](uint32_t x) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x)); };
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float top = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const float2 a = pair(qa[kk][half]), b = pair(qa[kk][half + 2]);
+          top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
+        const float down = ldexpf(1.f, -e);
+        xs[half] *= ldexpf(1.f, e);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const float2 a = pair(qa[kk][half]), b = pair(qa[kk][half + 2]);
+          qa[kk][half] = pack_half2(a.x * down, a.y * down);
+          qa[kk][half + 2] = pack_half2(b.x * down, b.y * down);
+        }
+      }
+    }
+    const int64_t item_u = sh.cum[item_i] + static_cast<int64_t>(item_h) * (tiles + kItemCost) + kItemCost;   // its first tile
     float o[D / 8][4];
 #pragma unroll
     for (int k = 0; k < D / 8; ++k)
@@ -319,12 +408,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // of rows r8, r8 + 8; l: this lane's share
 
-    for (; t < seg_end; ++t) {
+    for (int32_t tile = first_tile; tile < end_tile; ++tile) {
       issue((stage + kStages - 1) % kStages);
       copy_wait<kStages - 1>();
       __syncwarp();
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
-      const int32_t tok = comp.tile * G::CT + warp * G::KT;
+      const int32_t tok = tile * G::CT + warp * G::KT;
       uint32_t live[G::kGroups], any = 0;
 #pragma unroll
       for (int g = 0; g < G::kGroups; ++g) {
@@ -375,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           }
         if constexpr (MASS) {
           // the scaled scores, for the weights that the second launch forms
-          if (t < p.score_tiles) {
+          if (item_u + tile < p.score_tiles) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               const int r = r8 + 8 * half;
               if (r < group) {
-                float* dst = p.scores + (t * group + r) * G::CT + warp * G::KT + 2 * j4;
+                float* dst = p.scores + ((item_u + tile) * group + r) * G::CT + warp * G::KT + 2 * j4;
 #pragma unroll
                 for (int k = 0; k < G::KT / 8; ++k)
                   *reinterpret_cast<float2*>(dst + k * 8) = make_float2(s[k][2 * half], s[k][2 * half + 1]);
@@ -452,11 +541,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       } else if constexpr (MASS) {
         // no token here, or none with a page: weights of zero
-        if (t < p.score_tiles) {
+        if (item_u + tile < p.score_tiles) {
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             if (r8 + 8 * half < group) {
-              float* dst = p.scores + (t * group + r8 + 8 * half) * G::CT + warp * G::KT + 2 * j4;
+              float* dst = p.scores + ((item_u + tile) * group + r8 + 8 * half) * G::CT + warp * G::KT + 2 * j4;
 #pragma unroll
               for (int k = 0; k < G::KT / 8; ++k) *reinterpret_cast<float2*>(dst + k * 8) = make_float2(-INFINITY, -INFINITY);
             }
@@ -464,8 +553,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       }
       __syncwarp();
       stage = (stage + 1) % kStages;
-      cursor_next<G::CT>(comp, sh, n_kv, t + 1 < t1);
+      cursor_next<G::CT>(comp, sh, n_kv, left);
     }
+    if (left > 0) fetch_q(comp.i, comp.h);
 
     // ---- merge the four warps' results; warp 0 writes them
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
@@ -479,9 +569,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       sh.ml[warp][r8 + 8][1] = l[1];
     }
     __syncthreads();
-    const bool whole = first_tile == 0 && seg_end == item_tile0 + (len + G::CT - 1) / G::CT;
-    const int slot = static_cast<int>(blockIdx.x) * 2 + (first_tile == 0 ? 1 : 0);
-    float* part = p.parts + static_cast<int64_t>(slot) * kRows * (D + 2);
+    const bool whole = first_tile == 0 && end_tile == tiles;
+    float* part = part_at<D>(p, blockIdx.x, first_tile == 0 ? 1 : 0);
     const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[n_kv + item_h])) : 1.f;
     const float vs1 = TYPE == SR_PAGE_BF16 ? vscale : vscale * 0x1p-10f;
     float mine[2], top[2], sum[2];
@@ -554,123 +643,121 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
-    if (first_tile == 0 && threadIdx.x == 0) {
-      // the CTA of the item's last tile, for the join
-      const int64_t last = item_tile0 + (len + G::CT - 1) / G::CT - 1;
-      const int c1 = static_cast<int>(((last + 1) * ctas - 1) / T);
-      p.items[item_i * n_kv + item_h] = PagedItem{item_tile0, static_cast<int32_t>(blockIdx.x), c1};
-      if (MASS && last >= p.score_tiles) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
-    }
-    __syncthreads();   // sh.ml and merge are free for the next item
-  }
-}
-
-// Join the partial results of the items that several CTAs share: one CTA per
-// item, a warp per query row, the lanes across the head dimension.
-constexpr int kJoinThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  grid_dep_launch_dependents();
-  grid_dep_wait();
-  const PagedView& c = p.c;
-  const PagedItem it = p.items[blockIdx.x];
-  if (it.c0 == it.c1) return;
-  const int i = blockIdx.x / c.n_kv, h = blockIdx.x % c.n_kv;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int n_parts = it.c1 - it.c0 + 1;
-  constexpr int kPart = kRows * (D + 2);
-  constexpr int kCols = D / 32;
-  auto part = [&](int k) { return p.parts + static_cast<int64_t>((it.c0 + k) * 2 + (k == 0 ? 1 : 0)) * kPart; };
-  for (int r = warp; r < c.group; r += kJoinThreads / 32) {
-    float top = -INFINITY;
-    for (int k = lane; k < n_parts; k += 32) top = fmaxf(top, part(k)[kRows * D + 2 * r]);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    float sum = 0.f, a[kCols];
-#pragma unroll
-    for (int x = 0; x < kCols; ++x) a[x] = 0.f;
-    for (int k0 = 0; k0 < n_parts; k0 += 32) {
-      float w = 0.f;
-      if (k0 + lane < n_parts) {
-        const float mk = part(k0 + lane)[kRows * D + 2 * r];
-        w = mk == -INFINITY ? 0.f : ex2_approx(mk - top);
-        sum = fmaf(w, part(k0 + lane)[kRows * D + 2 * r + 1], sum);
-      }
-      const int m = min(32, n_parts - k0);
-#pragma unroll 4
-      for (int k = 0; k < m; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const float* src = part(k0 + k) + r * D + lane * kCols;
-        if constexpr (kCols == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]); a[2] = fmaf(wk, v.z, a[2]); a[3] = fmaf(wk, v.w, a[3]);
-        } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]);
+    if (!whole) {
+      // The parts of this item lie with CTAs c0 .. c1. The last of a group of kJoin to
+      // arrive joins the group, the last group to be joined the item.
+      const int me = static_cast<int>(blockIdx.x);
+      const int c0 = static_cast<int>(((item_u + 1) * ctas - 1) / T);
+      const int n_parts = static_cast<int>(((item_u + tiles) * ctas - 1) / T) - c0 + 1;
+      const int64_t out0 = static_cast<int64_t>(item_i) * c.n_heads + item_h * group;
+      auto arrive = [&](int32_t* ctr, int need) -> bool {   // warp 0 wrote; true for the whole CTA in the last one
+        if (warp == 0) {
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            const bool all = atomicAdd(ctr, 1) == need - 1;
+            if (all) *ctr = 0;
+            sh.last = all;
+          }
+        }
+        __syncthreads();
+        const bool all = sh.last;
+        __syncthreads();
+        return all;
+      };
+      if (n_parts <= kJoin) {
+        if (arrive(p.arrivals + c0, n_parts)) join_parts<D>(p, c0, 1, 1, n_parts, nullptr, out0, warp, lane);
+      } else {
+        const int g = (me - c0) / kJoin, lead = c0 + g * kJoin, s0 = g == 0 ? 1 : 0;
+        const int size = min(kJoin, n_parts - g * kJoin);
+        if (arrive(p.group_arrivals + 2 * lead + s0, size)) {
+          join_parts<D>(p, lead, s0, 1, size, part_at<D>(p, lead, s0), 0, warp, lane);
+          __threadfence();
+          __syncthreads();
+          if (arrive(p.arrivals + c0, (n_parts + kJoin - 1) / kJoin))
+            join_parts<D>(p, c0, 1, kJoin, (n_parts + kJoin - 1) / kJoin, nullptr, out0, warp, lane);
         }
       }
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t out = static_cast<int64_t>(i) * c.n_heads + h * c.group + r;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + out * D + lane * kCols);
-    dst[0] = pack_bf16x2(a[0] * inv, a[1] * inv);
-    if constexpr (kCols == 4) dst[1] = pack_bf16x2(a[2] * inv, a[3] * inv);
-    if (lane == 0) {
-      const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-      if (p.lse) p.lse[out] = lse2 * kLn2;
-      p.lse2[out] = lse2;
     }
   }
 }
 
 // The weights: mass(t) <- decay * mass(t) + sum over heads of 2^(x_h(t) - lse2_h).
-// `per` CTAs per sequence, a thread per token; a token's scores of one head lie next
-// to its neighbours', so that loads are contiguous.
+// `per` CTAs per sequence walk its tokens 64 at a time; four threads share a token's
+// heads and add up in a fixed order.
 constexpr int kMassThreads = 256;
+constexpr int kMassTokens = 64;
+constexpr int kMassShare = kMassThreads / kMassTokens;
 template <int CT>
 __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_constant__ PagedAttnParams p, int per) {
+  extern __shared__ float lse2[];                         // [n_heads]
+  __shared__ float sums[kMassShare][kMassTokens];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const PagedView& c = p.c;
   const int i = blockIdx.x / per;
   const int32_t seq = p.b.id[i];
   const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
-  if (len == 0) return;
+  int32_t t0 = (blockIdx.x % per) * kMassTokens;
+  if (t0 >= len) return;
   const int32_t tiles = (len + CT - 1) / CT;
-  const float* lse2 = p.lse2 + static_cast<int64_t>(i) * c.n_heads;
-  const int64_t tile0 = p.items[i * c.n_kv].tile0;       // the other heads' items follow
-  if (tile0 + static_cast<int64_t>(tiles) * c.n_kv > p.score_tiles) return;
-  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  for (int32_t t = (blockIdx.x % per) * kMassThreads + threadIdx.x; t < len; t += per * kMassThreads) {
-    if (paged_row(table, t, c.page_tokens, c.n_pages) < 0) continue;   // not seen: left as it is
-    const float* x = p.scores + (tile0 + t / CT) * c.group * CT + t % CT;
-    const int64_t pitch = static_cast<int64_t>(tiles) * c.group * CT;
-    float w = 0.f;
-    for (int h = 0; h < c.n_kv; ++h)
-#pragma unroll 4
-      for (int g = 0; g < c.group; ++g) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
-    float* m = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
-    *m = fmaf(p.mass_decay, *m, w);
+  const int64_t unit0 = p.unit0[i];
+  if (unit0 + static_cast<int64_t>(tiles + kItemCost) * c.n_kv > p.score_tiles) {   // not stored
+    if (threadIdx.x == 0) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
+    return;
   }
+  for (int h = threadIdx.x; h < c.n_heads; h += kMassThreads) lse2[h] = p.lse2[static_cast<int64_t>(i) * c.n_heads + h];
+  __syncthreads();
+  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  const int tok = threadIdx.x % kMassTokens, share = threadIdx.x / kMassTokens;
+  const int64_t pitch = static_cast<int64_t>(tiles + kItemCost) * c.group * CT;   // from one head's item to the next
+  for (; t0 < len; t0 += per * kMassTokens) {
+    const int32_t t = t0 + tok;
+    float w = 0.f;
+    if (t < len) {
+      const float* x = p.scores + (unit0 + kItemCost + t / CT) * c.group * CT + t % CT;
+      if (c.n_kv >= kMassShare) {
+        for (int h = share; h < c.n_kv; h += kMassShare)
+#pragma unroll 8
+          for (int g = 0; g < c.group; ++g) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
+      } else {
+        for (int h = 0; h < c.n_kv; ++h)
+#pragma unroll 4
+          for (int g = share; g < c.group; g += kMassShare) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
+      }
+    }
+    sums[share][tok] = w;
+    __syncthreads();
+    if (share == 0 && t < len && paged_row(table, t, c.page_tokens, c.n_pages) >= 0) {   // else not seen: left as it is
+      float* m = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
+      *m = fmaf(p.mass_decay, *m, (sums[0][tok] + sums[1][tok]) + (sums[2][tok] + sums[3][tok]));
+    }
+    __syncthreads();
+  }
+}
+
+template <int D, int TYPE>
+constexpr int kSmem = Geo<D, TYPE>::kStageArea + Geo<D, TYPE>::kMergeFloats * 4 + static_cast<int>(sizeof(SharedHead));
+
+template <int D, int TYPE>
+cudaError_t prepare() {
+  static_assert(2 * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
+  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, false>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, TYPE>);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSmem<D, TYPE>);
 }
 
 template <int D, int TYPE, bool MASS>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   using G = Geo<D, TYPE>;
-  constexpr int smem = G::kStageArea + G::kMergeFloats * 4 + static_cast<int>(sizeof(SharedHead));
-  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
-  // per device, and cheap next to a launch
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(paged_attn_ctas());
-  e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, smem, st, p);
-  if (e != cudaSuccess) return e;
-  e = launch_dependent(paged_join_kernel<D>, static_cast<unsigned>(p.b.n) * p.c.n_kv, kJoinThreads, 0, st, p);
+  const cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess || !MASS) return e;
-  const int per = std::max(1, 4 * sm_count() / p.b.n);
-  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads, 0, st, p, per);
+  const int per = std::max(1, 8 * sm_count() / p.b.n);
+  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads,
+                          static_cast<size_t>(p.c.n_heads) * 4, st, p, per);
 }
 
 template <int D, int TYPE>
@@ -686,6 +773,15 @@ size_t paged_part_floats(int head_dim) { return static_cast<size_t>(kRows) * (he
 int paged_tile_tokens(int head_dim, int page_type) {
   if (head_dim == 128) return page_type == SR_PAGE_BF16 ? Geo<128, SR_PAGE_BF16>::CT : Geo<128, SR_PAGE_E4M3>::CT;
   return page_type == SR_PAGE_BF16 ? Geo<64, SR_PAGE_BF16>::CT : Geo<64, SR_PAGE_E4M3>::CT;
+}
+
+cudaError_t paged_attn_prepare(int head_dim, int page_type) {
+  if (head_dim == 128) return page_type == SR_PAGE_BF16 ? prepare<128, SR_PAGE_BF16>() : prepare<128, SR_PAGE_E4M3>();
+  return page_type == SR_PAGE_BF16 ? prepare<64, SR_PAGE_BF16>() : prepare<64, SR_PAGE_E4M3>();
+}
+
+int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens) {
+  return (pool_tokens / tile_tokens + static_cast<int64_t>(n_seqs) * (1 + kItemCost)) * n_kv;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st) {

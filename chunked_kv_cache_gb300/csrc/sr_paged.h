@@ -11,7 +11,7 @@
 namespace sr {
 
 constexpr int kMaxPagedSeqs = SR_MAX_PAGED_SEQS;
-constexpr int kMaxPagedCtas = 1024;   // most CTAs an attention launch may have (partial result slots)
+constexpr int kMaxPagedCtas = 512;   // most CTAs an attention launch may have (partial result slots)
 
 // The pool row of logical index `idx` of a sequence whose block table row is
 // `table`: -1 when the entry is no page of the pool. 0 <= idx < cap.
@@ -46,27 +46,21 @@ struct PagedLayout {
   size_t plan;             // EvictPlan[kMaxPagedSeqs]
   size_t moves;            // int2[move_cap]: (from, to) logical indices
   int64_t move_cap;
-  size_t items;            // PagedItem[kMaxPagedSeqs][n_kv]
+  size_t unit0;            // int64[kMaxPagedSeqs]
   size_t parts;            // [kMaxPagedCtas][2] partial results
   size_t lse2;             // float[kMaxPagedSeqs][n_heads], log2 units
   size_t scores;           // float[score_tiles][group][tile tokens]
   int64_t score_tiles;
   size_t bytes;
 };
-constexpr int kPagedCounters = 1024;
+// arrivals of an append's CTAs, then of an attention's parts and groups of parts
+constexpr int kPagedCounters = kMaxPagedSeqs + 3 * kMaxPagedCtas;
 
 // What an eviction does to one sequence of the batch.
 struct EvictPlan {
   int64_t list0;           // its first entry in the list of moves
   int32_t moves;
   int32_t new_len;         // -1: left as it is
-};
-
-// A sequence and key/value head of an attention call: its first tile on the line
-// of all tiles, and the CTAs that hold its first and last ones.
-struct PagedItem {
-  int64_t tile0;
-  int32_t c0, c1;
 };
 
 struct PagedBatch {
@@ -91,7 +85,9 @@ struct PagedAttnParams {
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
   float* lse;
-  PagedItem* items;
+  int64_t* unit0;          // [n] first unit of each sequence on the line (see paged_attention.cu)
+  int32_t* arrivals;       // [kMaxPagedCtas] parts, or groups of parts, of an item that are done; left at zero
+  int32_t* group_arrivals; // [2 * kMaxPagedCtas]
   float* parts;
   float* lse2;
   float* scores;
@@ -115,6 +111,8 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_attn_ctas();                                    // CTAs of an attention launch
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
+cudaError_t paged_attn_prepare(int head_dim, int page_type);
+int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int head_dim);                   // floats of one partial result
 int paged_append_rows_per_cta(int n_kv, int head_dim);
 
