@@ -51,7 +51,7 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
     return here;
   };
   l.counters = take(sr::kPagedCounters * 4);
-  l.plan = take(sr::kMaxPagedSeqs * sizeof(sr::EvictPlan));
+  l.alloc = l.counters + sr::kPagedCounters * 4 - 16;   // the last four counters
   // a sequence of length n moves at most n / 2 tokens
   l.move_cap = with_mass ? static_cast<int64_t>(c.n_pages) * c.page_tokens / 2 + sr::kMaxPagedSeqs : 0;
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
@@ -159,6 +159,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type);
+  if (e == cudaSuccess) e = sr::paged_evict_prepare();
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);
   if (e != cudaSuccess) {
@@ -262,7 +263,7 @@ sr_status sr_paged_evict(sr_paged_cache* c, const int32_t* seqs, int32_t n, int3
   p.budget = budget;
   p.n_sink = n_sink;
   p.n_recent = n_recent;
-  p.plan = ws_at<sr::EvictPlan>(c, c->layout.plan);
+  p.alloc = ws_at<unsigned long long>(c, c->layout.alloc);
   p.moves = ws_at<int2>(c, c->layout.moves);
   p.move_cap = c->layout.move_cap;
   return sr::launch_paged_evict(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;

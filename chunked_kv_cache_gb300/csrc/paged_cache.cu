@@ -123,11 +123,18 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ evict
-// Two launches. The first picks, one CTA per sequence: a radix select over the
-// weights' bits finds the weight below which tokens go, then three ordered passes
-// (ties, counts, lists) write the moves. The second moves the rows.
-constexpr int kPickThreads = 1024;
-constexpr int kPickWarps = kPickThreads / 32;
+// One cluster of CTAs per sequence and one launch. The weights' bits, mapped to
+// unsigned integers in the weights' order, are read once into shared memory (each
+// CTA a stretch of indices). A radix select over 11, 11 and 10 bits, the CTAs' counts
+// added through distributed shared memory, finds the key at and below which tokens
+// go; ordered counts turn the choice into a list of moves (from, to); then all warps
+// move rows, a warp per token. A move reads at or behind the new length and writes below
+// it, so that no move sees another. Latency bound until the moves, which are HBM bound.
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+constexpr int kKeyLimit = 40960;      // keys a CTA can hold; longer stretches are read again from global memory
 
 // The order of the weights as unsigned integers; protected tokens come last.
 __device__ __forceinline__ uint32_t weight_key(float m) {
@@ -145,171 +152,271 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t x, int lane) {
   return x;
 }
 
-__global__ void __launch_bounds__(kPickThreads) paged_pick_kernel(const __grid_constant__ EvictParams p) {
-  grid_dep_wait();
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// the address of another CTA's copy of a shared variable, and loads from it
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint32_t peer_load(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 peer_load4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __grid_constant__ EvictParams p, int key_cap) {
+  extern __shared__ uint32_t keys[];              // [key_cap]
+  __shared__ __align__(16) uint32_t hist[2][kBins];
+  __shared__ uint32_t sums[kEvictWarps];
+  __shared__ uint32_t found[3];                   // digit, rank left, keys counted
+  __shared__ uint32_t pub[4];                     // what the other CTAs read: ties, holes, kept tokens behind; first move (low half)
+  __shared__ uint32_t pub_hi;
+  const uint32_t C = cluster_size(), rank_c = cluster_rank();
+  const int i = blockIdx.x / C, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  for (int x = tid; x < 2 * kBins; x += kEvictThreads) (&hist[0][0])[x] = 0;
   grid_dep_launch_dependents();
+  grid_dep_wait();
   const PagedView& c = p.c;
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t sums[3][kPickWarps];
-  __shared__ uint32_t pick[2];          // digit found, rank left
-  __shared__ uint32_t n_free;
-  __shared__ int64_t list0;
-  const int i = blockIdx.x, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int32_t seq = p.b.id[i];
   const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
-  const int32_t pos_next = c.seq_pos[seq];
-  if (len <= p.budget) {
-    if (tid == 0) p.plan[i] = EvictPlan{0, 0, -1};
-    return;
-  }
-  const int32_t* tpos = c.token_pos + static_cast<int64_t>(seq) * c.cap;
-  const float* mass = c.token_mass + static_cast<int64_t>(seq) * c.cap;
-  const int32_t recent0 = pos_next - p.n_recent;   // both >= 0
-  auto key = [&](int32_t t) -> uint32_t {
-    const int32_t q = tpos[t];
-    return q < p.n_sink || q >= recent0 ? 0xFFFFFFFFu : weight_key(mass[t]);
+  // the last sequence to be done clears the list's counters for the next call
+  auto done = [&] {
+    if (rank_c == 0 && tid == 0 && atomicAdd(p.alloc + 1, 1ull) == static_cast<unsigned long long>(p.b.n) - 1) {
+      p.alloc[0] = 0;
+      p.alloc[1] = 0;
+    }
   };
-  // where this sequence's moves go: behind those of the sequences before it
-  if (warp == 0) {
-    int64_t s = 0;
-    for (int j = lane; j < i; j += 32) s += min(max(c.seq_len[p.b.id[j]], 0), c.cap) / 2;
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    if (lane == 0) {
-      list0 = s;
-      n_free = 0;
-    }
-  }
-  __syncthreads();
-  uint32_t mine = 0;
-  for (int32_t t = tid; t < len; t += kPickThreads) mine += key(t) != 0xFFFFFFFFu;
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) atomicAdd(&n_free, mine);
-  __syncthreads();
-  uint32_t gone = min(static_cast<uint32_t>(len - p.budget), n_free);
-  if (gone > 0 && list0 + len / 2 > p.move_cap) {
-    if (tid == 0) note_error(c, SR_DEVERR_WORKSPACE);
-    gone = 0;
-  }
-  if (gone == 0) {
-    if (tid == 0) p.plan[i] = EvictPlan{0, 0, -1};
+  if (len <= p.budget) {
+    done();
     return;
   }
-  const int32_t kept = len - static_cast<int32_t>(gone);   // the new length
-  // the key of rank `gone` (from 1): eight bits at a time
-  uint32_t prefix = 0, rank = gone;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int32_t t = tid; t < len; t += kPickThreads) {
-      const uint32_t k = key(t);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+  int32_t* tpos = c.token_pos + static_cast<int64_t>(seq) * c.cap;
+  float* mass = c.token_mass + static_cast<int64_t>(seq) * c.cap;
+  const int64_t recent0 = static_cast<int64_t>(c.seq_pos[seq]) - p.n_recent;
+  auto key_of = [&](int32_t q, float m) { return q < p.n_sink || q >= recent0 ? 0xFFFFFFFFu : weight_key(m); };
+  // this CTA's stretch of indices: a multiple of 32 for each of its warps
+  const int32_t chunk = static_cast<int32_t>((len + C * kEvictThreads - 1) / (C * kEvictThreads)) * kEvictThreads;
+  const int32_t first = min(static_cast<int32_t>(rank_c) * chunk, len), count = min(chunk, len - first);
+  const bool held = chunk <= key_cap;
+  if (held) {
+#pragma unroll 4
+    for (int32_t x = tid; x < count; x += kEvictThreads) keys[x] = key_of(tpos[first + x], mass[first + x]);
+  }
+  __syncthreads();
+  auto key = [&](int32_t x) { return held ? keys[x] : key_of(tpos[first + x], mass[first + x]); };
+
+  // ---- the key of rank `gone` (from 1) among those that may go
+  uint32_t prefix = 0, rank = 0;
+  int32_t gone = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t bins = pass == 2 ? 1024 : 2048;
+    uint32_t* h = hist[pass & 1];
+    for (int32_t x0 = warp * 32; x0 < count; x0 += kEvictThreads) {
+      const int32_t x = x0 + lane;
+      const uint32_t k = x < count ? key(x) : 0xFFFFFFFFu;
+      const bool in = k != 0xFFFFFFFFu && (pass == 0 || k >> (pass == 1 ? 21 : 10) == prefix >> (pass == 1 ? 21 : 10));
+      const uint32_t digit = (k >> shift) & (bins - 1);
+      const uint32_t act = __ballot_sync(0xffffffffu, in);
+      if (act == 0) continue;
+      // equal weights would queue on one counter: the warp adds them at once
+      const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(act) - 1);
+      if (__all_sync(0xffffffffu, !in || digit == d0)) {
+        if (lane == 0) atomicAdd(&h[d0], __popc(act));
+      } else if (in) {
+        atomicAdd(&h[digit], 1u);
+      }
     }
     __syncthreads();
-    if (warp == 0) {
-      uint32_t h[8], s = 0;
-      for (int j = 0; j < 8; ++j) {
-        h[j] = hist[lane * 8 + j];
-        s += h[j];
-      }
-      uint32_t before = warp_incl_scan(s, lane) - s;
-      for (int j = 0; j < 8; ++j) {
-        if (before < rank && rank <= before + h[j]) {
-          pick[0] = lane * 8 + j;
-          pick[1] = rank - before;
-        }
-        before += h[j];
+    if (C > 1) cluster_sync();
+    // every CTA adds all counts, four digits per thread, and finds the same digit
+    uint4 s = make_uint4(0, 0, 0, 0);
+    if (tid * 4 < static_cast<int>(bins)) {
+      if (C == 1) {
+        s = *reinterpret_cast<const uint4*>(h + tid * 4);
+      } else {
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r)
+          if (r < C) {
+            const uint4 v = peer_load4(peer_addr(h + tid * 4, r));
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+          }
       }
     }
+    const uint32_t mine = s.x + s.y + s.z + s.w;
+    const uint32_t incl = warp_incl_scan(mine, lane);
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    prefix |= pick[0] << shift;
-    rank = pick[1];
+    const uint32_t ws = lane < kEvictWarps ? sums[lane] : 0;
+    const uint32_t wi = warp_incl_scan(ws, lane);
+    uint32_t before = incl - mine + __shfl_sync(0xffffffffu, wi - ws, warp);
+    if (pass == 0) {
+      const uint32_t total = __shfl_sync(0xffffffffu, wi, 31);   // tokens that may go
+      gone = static_cast<int32_t>(min(static_cast<uint32_t>(len - p.budget), total));
+      rank = static_cast<uint32_t>(gone);
+    }
+    const uint32_t v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (before < rank && rank <= before + v[j]) {
+        found[0] = tid * 4 + j;
+        found[1] = rank - before;
+      }
+      before += v[j];
+    }
+    __syncthreads();
+    if (gone == 0) break;
+    prefix |= found[0] << shift;
+    rank = found[1];
+    // the other buffer was read before this pass's barrier: clear it for the pass after the next
+    uint32_t* other = hist[(pass + 1) & 1];
+    if (pass == 1)
+      for (int x = tid; x < kBins; x += kEvictThreads) other[x] = 0;
     __syncthreads();
   }
-  // every key below `prefix` goes, and of those equal to it the last `rank` by index
-  const int32_t chunk = (len + kPickThreads - 1) / kPickThreads * 32;   // a warp's stretch of indices
-  const int32_t t0 = warp * chunk, t1 = min(t0 + chunk, len);
-  auto block_scan = [&](uint32_t x, uint32_t* buf, uint32_t& total) -> uint32_t {   // x: a per-warp count
-    if (lane == 0) buf[warp] = x;
+  if (gone == 0) {            // every token is protected; as in all CTAs of the cluster
+    if (C > 1) cluster_sync();   // the others may still be reading this CTA's counts
+    done();
+    return;
+  }
+  const int32_t kept = len - gone;   // the new length
+
+  // ---- every key below `prefix` goes, and of those equal to it the last `rank` by index
+  const int32_t w0 = min(warp * (chunk / kEvictWarps), count), w1 = min(w0 + chunk / kEvictWarps, count);
+  auto block_scan = [&](uint32_t x, uint32_t& total) -> uint32_t {   // x: a per-warp count
     __syncthreads();
-    const uint32_t v = buf[lane];
+    if (lane == 0) sums[warp] = x;
+    __syncthreads();
+    const uint32_t v = lane < kEvictWarps ? sums[lane] : 0;
     const uint32_t incl = warp_incl_scan(v, lane);
     total = __shfl_sync(0xffffffffu, incl, 31);
     return __shfl_sync(0xffffffffu, incl - v, warp);
   };
-  uint32_t ties = 0;
-  for (int32_t b = t0; b < t1; b += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, b + lane < t1 && key(b + lane) == prefix));
-  uint32_t n_ties;
-  const uint32_t tie0 = block_scan(ties, sums[0], n_ties);
+  // counts of the CTAs before this one, and of all
+  auto across = [&](int which, uint32_t& all) -> uint32_t {
+    const uint32_t v = lane < static_cast<int>(C) ? (C == 1 ? pub[which] : peer_load(peer_addr(&pub[which], lane))) : 0;
+    const uint32_t incl = warp_incl_scan(v, lane);
+    all = __shfl_sync(0xffffffffu, incl, 31);
+    return __shfl_sync(0xffffffffu, incl - v, static_cast<int>(rank_c));
+  };
+  uint32_t ties = 0, cta_total, n_ties;
+  for (int32_t b = w0; b < w1; b += 32) ties += __popc(__ballot_sync(0xffffffffu, b + lane < w1 && key(b + lane) == prefix));
+  uint32_t tie0 = block_scan(ties, cta_total);
+  if (tid == 0) {
+    pub[0] = cta_total;
+    if (rank_c == 0) {        // room in the list for as many moves as there can be
+      const unsigned long long at = atomicAdd(p.alloc, static_cast<unsigned long long>(min(gone, kept)));
+      pub[3] = static_cast<uint32_t>(at);
+      pub_hi = static_cast<uint32_t>(at >> 32);
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_sync();
+  tie0 += across(0, n_ties);
   const uint32_t tie_keep = n_ties - rank;   // ties that stay: the first ones
+  const int64_t list0 = C == 1 ? static_cast<int64_t>(pub_hi) << 32 | pub[3]
+                               : static_cast<int64_t>(peer_load(peer_addr(&pub_hi, 0))) << 32 | peer_load(peer_addr(&pub[3], 0));
+  const bool room = list0 + min(gone, kept) <= p.move_cap;
   auto walk = [&](auto&& f) {
     uint32_t tie = tie0;
-    for (int32_t b = t0; b < t1; b += 32) {
-      const int32_t t = b + lane;
-      const uint32_t k = t < t1 ? key(t) : 0xFFFFFFFFu;
-      const uint32_t eq = __ballot_sync(0xffffffffu, t < t1 && k == prefix);
+    for (int32_t b = w0; b < w1; b += 32) {
+      const int32_t x = b + lane, t = first + x;
+      const uint32_t k = x < w1 ? key(x) : 0xFFFFFFFFu;
+      const uint32_t eq = __ballot_sync(0xffffffffu, x < w1 && k == prefix);
       const uint32_t below = __popc(eq & ((1u << lane) - 1u));
-      const bool go = t < t1 && (k < prefix || (k == prefix && tie + below >= tie_keep));
+      const bool go = x < w1 && (k < prefix || (k == prefix && tie + below >= tie_keep));
       tie += __popc(eq);
       const uint32_t holes = __ballot_sync(0xffffffffu, go && t < kept);
-      const uint32_t backs = __ballot_sync(0xffffffffu, t < t1 && !go && t >= kept);
+      const uint32_t backs = __ballot_sync(0xffffffffu, x < w1 && !go && t >= kept);
       f(t, holes, backs);
     }
   };
-  uint32_t nh = 0, nb = 0, n_holes, n_backs;
+  uint32_t nh = 0, nb = 0;
   walk([&](int32_t, uint32_t holes, uint32_t backs) {
     nh += __popc(holes);
     nb += __popc(backs);
   });
-  uint32_t h0 = block_scan(nh, sums[1], n_holes), b0 = block_scan(nb, sums[2], n_backs);
+  uint32_t h0 = block_scan(nh, cta_total);
+  if (tid == 0) pub[1] = cta_total;
+  uint32_t b0 = block_scan(nb, cta_total);
+  if (tid == 0) pub[2] = cta_total;
+  __syncthreads();
+  if (C > 1) cluster_sync();
+  uint32_t moves, n_backs;
+  h0 += across(1, moves);
+  b0 += across(2, n_backs);
   int2* list = p.moves + list0;
-  walk([&](int32_t t, uint32_t holes, uint32_t backs) {
-    const uint32_t lt = (1u << lane) - 1u;
-    if (holes >> lane & 1u) list[h0 + __popc(holes & lt)].y = t;
-    if (backs >> lane & 1u) list[b0 + __popc(backs & lt)].x = t;
-    h0 += __popc(holes);
-    b0 += __popc(backs);
-  });
-  // the second launch lowers the length: by then every CTA of this one has read the lengths
-  if (tid == 0) p.plan[i] = EvictPlan{list0, static_cast<int32_t>(n_holes), kept};
-}
+  if (room)
+    walk([&](int32_t t, uint32_t holes, uint32_t backs) {
+      const uint32_t lt = (1u << lane) - 1u;
+      if (holes >> lane & 1u) list[h0 + __popc(holes & lt)].y = t;
+      if (backs >> lane & 1u) list[b0 + __popc(backs & lt)].x = t;
+      h0 += __popc(holes);
+      b0 += __popc(backs);
+    });
+  __syncthreads();
+  if (C > 1) cluster_sync();   // the list is whole, and nobody reads another CTA's shared memory any more
+  done();
+  if (!room) {                 // sequences that share pages: more tokens than the pool has
+    if (tid == 0) note_error(c, SR_DEVERR_WORKSPACE);
+    return;
+  }
 
-// The second launch: `per` CTAs per sequence, a warp per moved token. A move reads
-// at or behind the new length and writes below it, so that no move sees another.
-constexpr int kMoveThreads = 256;
-__global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ EvictParams p, int per) {
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  const PagedView& c = p.c;
-  const int i = blockIdx.x / per, part = blockIdx.x % per;
-  const EvictPlan plan = p.plan[i];
-  if (plan.new_len < 0) return;
-  const int32_t seq = p.b.id[i];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // ---- move
+  if (rank_c == 0 && tid == 0) c.seq_len[seq] = kept;
   const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  const int64_t t0 = static_cast<int64_t>(seq) * c.cap;
   const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
-  for (int32_t j = part * (kMoveThreads / 32) + warp; j < plan.moves; j += per * (kMoveThreads / 32)) {
-    const int2 m = p.moves[plan.list0 + j];
+  for (uint32_t j = warp * C + rank_c; j < moves; j += C * kEvictWarps) {
+    const int2 m = __ldcg(list + j);
     const int64_t from = paged_row(table, m.x, c.page_tokens, c.n_pages);
     const int64_t to = paged_row(table, m.y, c.page_tokens, c.n_pages);
     if (from < 0 || to < 0) {
       if (lane == 0) note_error(c, SR_DEVERR_BAD_PAGE);
       continue;
     }
-    for (int x = lane; x < 2 * vpr; x += 32) {
-      uint4* pages = static_cast<uint4*>(x < vpr ? c.k_pages : c.v_pages);
-      const int col = x < vpr ? x : x - vpr;
-      pages[to * vpr + col] = pages[from * vpr + col];
+    const uint4* ks = static_cast<const uint4*>(c.k_pages) + from * vpr;
+    const uint4* vs = static_cast<const uint4*>(c.v_pages) + from * vpr;
+    uint4* kd = static_cast<uint4*>(c.k_pages) + to * vpr;
+    uint4* vd = static_cast<uint4*>(c.v_pages) + to * vpr;
+    for (int x0 = lane; x0 < vpr; x0 += 128) {      // eight loads in flight per lane
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x0 + 32 * k < vpr) {
+          a[k] = __ldcs(ks + x0 + 32 * k);
+          b[k] = __ldcs(vs + x0 + 32 * k);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (x0 + 32 * k < vpr) {
+          kd[x0 + 32 * k] = a[k];
+          vd[x0 + 32 * k] = b[k];
+        }
     }
     if (lane == 0) {
-      c.token_pos[t0 + m.y] = c.token_pos[t0 + m.x];
-      c.token_mass[t0 + m.y] = c.token_mass[t0 + m.x];
+      tpos[m.y] = tpos[m.x];
+      mass[m.y] = mass[m.x];
     }
   }
-  if (part == 0 && threadIdx.x == 0) c.seq_len[seq] = plan.new_len;
 }
 
 }  // namespace
@@ -328,11 +435,32 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st) {
   return launch_dependent(paged_append_kernel<SR_PAGE_E4M3>, grid, kAppendThreads, 0, st, p);
 }
 
+cudaError_t paged_evict_prepare() {
+  return cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
+}
+
+// CTAs per sequence: one where there is little to read and to move (no barrier across
+// CTAs then), else a whole cluster.
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
-  cudaError_t e = launch_dependent(paged_pick_kernel, p.b.n, kPickThreads, 0, st, p);
-  if (e != cudaSuccess) return e;
-  const int per = std::max(1, 2 * sm_count() / p.b.n);
-  return launch_dependent(paged_move_kernel, static_cast<unsigned>(p.b.n) * per, kMoveThreads, 0, st, p, per);
+  const int32_t most = std::min(p.budget, p.c.cap - p.budget);   // moves
+  const unsigned C = p.c.cap <= 8192 && most <= 64 ? 1 : kMaxCluster;
+  const int32_t chunk = (p.c.cap + static_cast<int32_t>(C) * kEvictThreads - 1) / (static_cast<int32_t>(C) * kEvictThreads) * kEvictThreads;
+  const int key_cap = std::min(chunk, kKeyLimit);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.b.n) * C);
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p, key_cap);
 }
 
 }  // namespace sr

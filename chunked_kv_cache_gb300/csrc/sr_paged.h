@@ -43,7 +43,7 @@ struct PagedView {
 // Workspace: counters, partial results, move lists, scores (see paged_layout).
 struct PagedLayout {
   size_t counters;         // int32[kPagedCounters]
-  size_t plan;             // EvictPlan[kMaxPagedSeqs]
+  size_t alloc;            // uint64[2]: entries of `moves` taken, sequences done
   size_t moves;            // int2[move_cap]: (from, to) logical indices
   int64_t move_cap;
   size_t unit0;            // int64[kMaxPagedSeqs]
@@ -53,15 +53,8 @@ struct PagedLayout {
   int64_t score_tiles;
   size_t bytes;
 };
-// arrivals of an append's CTAs, then of an attention's parts and groups of parts
-constexpr int kPagedCounters = kMaxPagedSeqs + 3 * kMaxPagedCtas;
-
-// What an eviction does to one sequence of the batch.
-struct EvictPlan {
-  int64_t list0;           // its first entry in the list of moves
-  int32_t moves;
-  int32_t new_len;         // -1: left as it is
-};
+// arrivals of an append's CTAs, then of an attention's parts and groups of parts, then an eviction's two 64-bit counters
+constexpr int kPagedCounters = kMaxPagedSeqs + 3 * kMaxPagedCtas + 4;
 
 struct PagedBatch {
   int32_t n;
@@ -99,7 +92,7 @@ struct PagedAttnParams {
 struct EvictParams {
   PagedView c;
   int32_t budget, n_sink, n_recent;
-  EvictPlan* plan;
+  unsigned long long* alloc;
   int2* moves;
   int64_t move_cap;
   PagedBatch b;
@@ -111,6 +104,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_attn_ctas();                                    // CTAs of an attention launch
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
+cudaError_t paged_evict_prepare();
 cudaError_t paged_attn_prepare(int head_dim, int page_type);
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int head_dim);                   // floats of one partial result

@@ -289,6 +289,33 @@ def test_evict_long_sequences():
     p.ok()
 
 
+def test_evict_from_a_sequence_longer_than_shared_memory_holds():
+    """Half a million tokens: their keys are read again from global memory. Copies are checked by position."""
+    import chunked_kv_cache_gb300 as sr
+    dev = device()
+    n, budget, sink, recent = 400_003, 300_000, 10, 5000
+    c = sr.PagedCache(1, 1, 64, page_tokens=1024, n_pages=400, max_seqs=1, max_pages=400, device=dev)
+    c.reserve(0, n)
+    g = torch.Generator(device=dev).manual_seed(2)
+    k = torch.randn(n, 1, 64, device=dev, generator=g).to(torch.bfloat16)
+    c.append(k, -k, counts=[n])
+    m = torch.floor(torch.rand(c.capacity, device=dev, generator=g) * 50000)     # ties among them
+    c.token_mass[0] = m
+    c.evict(budget, sink, recent)
+    assert c.seq_len.tolist() == [budget] and c.error_status() == 0
+    t = torch.arange(n, device=dev)
+    free = (t >= sink) & (t < n - recent)
+    key = torch.where(free, m[:n].double(), torch.inf)
+    order = torch.sort(key, descending=True, stable=True).indices          # a tie: the lower index stays
+    keep = torch.zeros(n, dtype=torch.bool, device=dev).index_fill_(0, order[:budget], True)
+    want = t[:budget].clone()
+    want[~keep[:budget]] = t[budget:][keep[budget:]]
+    got = c.token_pos[0, :budget].long()
+    assert torch.equal(got, want) and torch.equal(c.token_mass[0, :budget], m[want])
+    rows = c.block_table[0].long()[t[:budget] // 1024] * 1024 + t[:budget] % 1024
+    assert torch.equal(c.k_pages.view(-1, 1, 64)[rows], k[want]) and torch.equal(c.v_pages.view(-1, 1, 64)[rows], -k[want])
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_serving_loop_at_a_budget(e4m3):
     """Prompts, then token by token with weights and eviction, two budgets; lengths never exceed them."""
