@@ -123,13 +123,17 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ evict
-// One cluster of CTAs per sequence and one launch. The weights' bits, mapped to
-// unsigned integers in the weights' order, are read once into shared memory (each
-// CTA a stretch of indices). A radix select over 11, 11 and 10 bits, the CTAs' counts
-// added through distributed shared memory, finds the key at and below which tokens
-// go; ordered counts turn the choice into a list of moves (from, to); then all warps
-// move rows, a warp per token. A move reads at or behind the new length and writes below
-// it, so that no move sees another. Latency bound until the moves, which are HBM bound.
+// One launch. The weights' bits, mapped to unsigned integers in the weights' order,
+// are read once into shared memory. A radix select over 11, 11 and 10 bits finds the
+// key at and below which tokens go; ordered counts turn the choice into moves (from,
+// to); then all warps move rows, a warp per token. A move reads at or behind the new
+// length and writes below it, so that no move sees another. Latency bound until the
+// moves, which are HBM bound.
+//
+// Two kernels. paged_evict_kernel: every CTA of a sequence's cluster holds all keys and
+// makes the whole choice for itself, so that they meet at one barrier only, before the
+// first move. paged_evict_long_kernel: for sequences whose keys one CTA cannot hold;
+// each CTA holds a stretch and the counts are added through distributed shared memory.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
@@ -182,7 +186,186 @@ __device__ __forceinline__ uint4 peer_load4(uint32_t a) {
   return v;
 }
 
-__global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __grid_constant__ EvictParams p, int key_cap) {
+
+// A warp moves one token: its rows, position and weight.
+__device__ __forceinline__ void move_token(const PagedView& c, const int32_t* table, int32_t* tpos, float* mass, int2 m,
+                                           int vpr, int lane) {
+  const int64_t from = paged_row(table, m.x, c.page_tokens, c.n_pages);
+  const int64_t to = paged_row(table, m.y, c.page_tokens, c.n_pages);
+  if (from < 0 || to < 0) {
+    if (lane == 0) note_error(c, SR_DEVERR_BAD_PAGE);
+    return;
+  }
+  if (lane == 0) {
+    tpos[m.y] = tpos[m.x];
+    mass[m.y] = mass[m.x];
+  }
+  const uint4* ks = static_cast<const uint4*>(c.k_pages) + from * vpr;
+  const uint4* vs = static_cast<const uint4*>(c.v_pages) + from * vpr;
+  uint4* kd = static_cast<uint4*>(c.k_pages) + to * vpr;
+  uint4* vd = static_cast<uint4*>(c.v_pages) + to * vpr;
+  for (int x0 = lane; x0 < vpr; x0 += 128) {      // eight loads in flight per lane
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x0 + 32 * k < vpr) {
+        a[k] = __ldcs(ks + x0 + 32 * k);
+        b[k] = __ldcs(vs + x0 + 32 * k);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x0 + 32 * k < vpr) {
+        kd[x0 + 32 * k] = a[k];
+        vd[x0 + 32 * k] = b[k];
+      }
+  }
+}
+
+// Scans over a block of WARPS warps of a per-warp count: those before this warp, and all.
+template <int WARPS>
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* buf, int warp, int lane, uint32_t& total) {
+  if (lane == 0) buf[warp] = x;
+  __syncthreads();
+  const uint32_t v = lane < WARPS ? buf[lane] : 0;
+  const uint32_t incl = warp_incl_scan(v, lane);
+  total = __shfl_sync(0xffffffffu, incl, 31);
+  return __shfl_sync(0xffffffffu, incl - v, warp);
+}
+
+constexpr int kPickThreads = 1024;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickLimit = 40960;     // keys a CTA holds
+
+__global__ void __launch_bounds__(kPickThreads, 1) paged_evict_kernel(const __grid_constant__ EvictParams p, int key_cap) {
+  extern __shared__ __align__(16) uint32_t keys[];   // [key_cap], then this CTA's moves
+  __shared__ uint32_t hist[3][kBins];
+  __shared__ uint32_t sums[4][kPickWarps];
+  __shared__ uint32_t found[3][3];                   // per pass: digit, rank in it, its keys
+  const uint32_t C = cluster_size(), me = cluster_rank();
+  const int i = blockIdx.x / C, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int2* list = reinterpret_cast<int2*>(keys + key_cap);
+  for (int x = tid; x < 3 * kBins; x += kPickThreads) (&hist[0][0])[x] = 0;
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  const PagedView& c = p.c;
+  const int32_t seq = p.b.id[i];
+  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
+  const int64_t recent0 = static_cast<int64_t>(c.seq_pos[seq]) - p.n_recent;
+  if (len <= p.budget) return;                       // as in every CTA of the cluster
+  int32_t* tpos = c.token_pos + static_cast<int64_t>(seq) * c.cap;
+  float* mass = c.token_mass + static_cast<int64_t>(seq) * c.cap;
+#pragma unroll 4
+  for (int32_t t = tid; t < len; t += kPickThreads) {
+    const int32_t q = tpos[t];
+    const float m = mass[t];
+    keys[t] = q < p.n_sink || q >= recent0 ? 0xFFFFFFFFu : weight_key(m);
+  }
+  __syncthreads();
+  // a warp's stretch of indices, a multiple of 32
+  const int32_t seg = (len + kPickThreads - 1) / kPickThreads * 32;
+  const int32_t w0 = min(warp * seg, len), w1 = min(w0 + seg, len);
+
+  // ---- the key of rank `gone` (from 1) among those that may go
+  uint32_t limit = 0, rank = 0, ties = 0;            // keys below `limit` go; of those equal to it the last `rank`
+  int32_t gone = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
+    const uint32_t digits = pass == 2 ? 1023 : 2047;
+#pragma unroll 4
+    for (int32_t x0 = w0; x0 < w1; x0 += 32) {
+      const uint32_t k = x0 + lane < w1 ? keys[x0 + lane] : 0xFFFFFFFFu;
+      const bool in = k != 0xFFFFFFFFu && (pass == 0 || k >> above == limit >> above);
+      const uint32_t digit = k >> shift & digits;
+      // equal weights would queue on one counter: the warp adds them at once
+      const uint32_t act = __ballot_sync(0xffffffffu, in);
+      const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(act) - 1 & 31);
+      if (__all_sync(0xffffffffu, !in || digit == d0)) {
+        if (lane == 0 && act) atomicAdd(&hist[pass][d0], __popc(act));
+      } else if (in) {
+        atomicAdd(&hist[pass][digit], 1u);
+      }
+    }
+    __syncthreads();
+    const uint2 h = reinterpret_cast<const uint2*>(hist[pass])[tid];   // two digits per thread
+    const uint32_t incl = warp_incl_scan(h.x + h.y, lane);
+    const uint32_t warp_all = __shfl_sync(0xffffffffu, incl, 31);
+    uint32_t total;
+    uint32_t before = block_scan<kPickWarps>(warp_all, sums[pass], warp, lane, total) + incl - h.x - h.y;
+    if (pass == 0) {
+      gone = static_cast<int32_t>(min(static_cast<uint32_t>(len - p.budget), total));
+      rank = static_cast<uint32_t>(gone);
+    }
+    if (before < rank && rank <= before + h.x + h.y) {
+      const bool second = rank > before + h.x;
+      found[pass][0] = tid * 2 + second;
+      found[pass][1] = rank - before - (second ? h.x : 0);
+      found[pass][2] = second ? h.y : h.x;
+    }
+    __syncthreads();
+    if (gone == 0) return;                           // every token is protected; as in every CTA of the cluster
+    limit |= found[pass][0] << shift;
+    rank = found[pass][1];
+    ties = found[pass][2];
+    if (rank == ties) {                              // all keys of this digit go: no need to look further
+      limit = min(limit | ((1u << shift) - 1u), 0xFFFFFFFEu);   // never the protected ones
+      break;
+    }
+  }
+  const int32_t kept = len - gone;                   // the new length
+
+  // ---- the moves: the j-th index below `kept` that goes, the j-th at or behind it that stays
+  uint32_t tie0 = 0, unused;
+  const bool split = rank != ties;                   // some of the keys equal to `limit` stay: the first ones
+  if (split) {
+    uint32_t eq = 0;
+    for (int32_t x0 = w0; x0 < w1; x0 += 32)
+      eq += __popc(__ballot_sync(0xffffffffu, x0 + lane < w1 && keys[x0 + lane] == limit));
+    tie0 = block_scan<kPickWarps>(eq, sums[3], warp, lane, unused);
+    __syncthreads();
+  }
+  const uint32_t tie_keep = ties - rank, lt = (1u << lane) - 1u;
+  auto walk = [&](auto&& f) {
+    uint32_t tie = tie0;
+#pragma unroll 4
+    for (int32_t x0 = w0; x0 < w1; x0 += 32) {
+      const int32_t t = x0 + lane;
+      const uint32_t k = t < w1 ? keys[t] : 0xFFFFFFFFu;
+      bool go = k <= limit;                          // never a protected one, nor one past the stretch
+      if (split) {
+        const uint32_t eq = __ballot_sync(0xffffffffu, k == limit);
+        if (k == limit && tie + __popc(eq & lt) < tie_keep) go = false;
+        tie += __popc(eq);
+      }
+      f(t, __ballot_sync(0xffffffffu, go && t < kept), __ballot_sync(0xffffffffu, t < w1 && !go && t >= kept));
+    }
+  };
+  uint32_t nh = 0, nb = 0, moves, n_backs;
+  walk([&](int32_t, uint32_t holes, uint32_t backs) {
+    nh += __popc(holes);
+    nb += __popc(backs);
+  });
+  // a count of each kind fits 16 bits: kPickLimit keys
+  const uint32_t both = block_scan<kPickWarps>(nh | nb << 16, sums[3], warp, lane, moves);
+  uint32_t h0 = both & 0xFFFFu, b0 = both >> 16;
+  n_backs = moves >> 16;
+  moves &= 0xFFFFu;
+  walk([&](int32_t t, uint32_t holes, uint32_t backs) {
+    const uint32_t h = h0 + __popc(holes & lt), b = b0 + __popc(backs & lt);
+    if ((holes >> lane & 1u) && h % C == me) list[h / C].y = t;
+    if ((backs >> lane & 1u) && b % C == me) list[b / C].x = t;
+    h0 += __popc(holes);
+    b0 += __popc(backs);
+  });
+  __syncthreads();
+  if (C > 1) cluster_sync();   // every CTA has read the weights and positions: they may change
+  if (me == 0 && tid == 0) c.seq_len[seq] = kept;
+  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
+  for (uint32_t j = warp; j * C + me < moves; j += kPickWarps) move_token(c, table, tpos, mass, list[j], vpr, lane);
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_long_kernel(const __grid_constant__ EvictParams p, int key_cap) {
   extern __shared__ uint32_t keys[];              // [key_cap]
   __shared__ __align__(16) uint32_t hist[2][kBins];
   __shared__ uint32_t sums[kEvictWarps];
@@ -302,14 +485,9 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __g
 
   // ---- every key below `prefix` goes, and of those equal to it the last `rank` by index
   const int32_t w0 = min(warp * (chunk / kEvictWarps), count), w1 = min(w0 + chunk / kEvictWarps, count);
-  auto block_scan = [&](uint32_t x, uint32_t& total) -> uint32_t {   // x: a per-warp count
+  auto scan = [&](uint32_t x, uint32_t& total) {
     __syncthreads();
-    if (lane == 0) sums[warp] = x;
-    __syncthreads();
-    const uint32_t v = lane < kEvictWarps ? sums[lane] : 0;
-    const uint32_t incl = warp_incl_scan(v, lane);
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    return __shfl_sync(0xffffffffu, incl - v, warp);
+    return block_scan<kEvictWarps>(x, sums, warp, lane, total);
   };
   // counts of the CTAs before this one, and of all
   auto across = [&](int which, uint32_t& all) -> uint32_t {
@@ -320,7 +498,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __g
   };
   uint32_t ties = 0, cta_total, n_ties;
   for (int32_t b = w0; b < w1; b += 32) ties += __popc(__ballot_sync(0xffffffffu, b + lane < w1 && key(b + lane) == prefix));
-  uint32_t tie0 = block_scan(ties, cta_total);
+  uint32_t tie0 = scan(ties, cta_total);
   if (tid == 0) {
     pub[0] = cta_total;
     if (rank_c == 0) {        // room in the list for as many moves as there can be
@@ -355,9 +533,9 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __g
     nh += __popc(holes);
     nb += __popc(backs);
   });
-  uint32_t h0 = block_scan(nh, cta_total);
+  uint32_t h0 = scan(nh, cta_total);
   if (tid == 0) pub[1] = cta_total;
-  uint32_t b0 = block_scan(nb, cta_total);
+  uint32_t b0 = scan(nb, cta_total);
   if (tid == 0) pub[2] = cta_total;
   __syncthreads();
   if (C > 1) cluster_sync();
@@ -387,35 +565,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1) paged_evict_kernel(const __g
   const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
   for (uint32_t j = warp * C + rank_c; j < moves; j += C * kEvictWarps) {
     const int2 m = __ldcg(list + j);
-    const int64_t from = paged_row(table, m.x, c.page_tokens, c.n_pages);
-    const int64_t to = paged_row(table, m.y, c.page_tokens, c.n_pages);
-    if (from < 0 || to < 0) {
-      if (lane == 0) note_error(c, SR_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const uint4* ks = static_cast<const uint4*>(c.k_pages) + from * vpr;
-    const uint4* vs = static_cast<const uint4*>(c.v_pages) + from * vpr;
-    uint4* kd = static_cast<uint4*>(c.k_pages) + to * vpr;
-    uint4* vd = static_cast<uint4*>(c.v_pages) + to * vpr;
-    for (int x0 = lane; x0 < vpr; x0 += 128) {      // eight loads in flight per lane
-      uint4 a[4], b[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (x0 + 32 * k < vpr) {
-          a[k] = __ldcs(ks + x0 + 32 * k);
-          b[k] = __ldcs(vs + x0 + 32 * k);
-        }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (x0 + 32 * k < vpr) {
-          kd[x0 + 32 * k] = a[k];
-          vd[x0 + 32 * k] = b[k];
-        }
-    }
-    if (lane == 0) {
-      tpos[m.y] = tpos[m.x];
-      mass[m.y] = mass[m.x];
-    }
+    move_token(c, table, tpos, mass, m, vpr, lane);
   }
 }
 
@@ -435,21 +585,28 @@ cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st) {
   return launch_dependent(paged_append_kernel<SR_PAGE_E4M3>, grid, kAppendThreads, 0, st, p);
 }
 
-cudaError_t paged_evict_prepare() {
-  return cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
+// Shared memory of the small form: the keys, and this CTA's share of the moves.
+static size_t pick_bytes(int32_t cap, int32_t most, unsigned C) {
+  return static_cast<size_t>((cap + 3) / 4 * 4) * 4 + (static_cast<size_t>(most) / C + 1) * sizeof(int2);
 }
 
-// CTAs per sequence: one where there is little to read and to move (no barrier across
-// CTAs then), else a whole cluster.
+cudaError_t paged_evict_prepare() {
+  const cudaError_t e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(pick_bytes(kPickLimit, kPickLimit / 2, kMaxCluster)));
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_evict_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
+}
+
+// CTAs per sequence: one where there are few tokens to move (no barrier across CTAs
+// then), else a whole cluster.
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
-  const int32_t most = std::min(p.budget, p.c.cap - p.budget);   // moves
-  const unsigned C = p.c.cap <= 8192 && most <= 64 ? 1 : kMaxCluster;
-  const int32_t chunk = (p.c.cap + static_cast<int32_t>(C) * kEvictThreads - 1) / (static_cast<int32_t>(C) * kEvictThreads) * kEvictThreads;
-  const int key_cap = std::min(chunk, kKeyLimit);
+  // a move fills an index that goes with a token that stays: at most so many
+  const int32_t cap = p.c.cap, most = std::min(cap / 2, cap - p.budget);
+  const bool small = cap <= kPickLimit;
+  const unsigned C = small && most <= 64 ? 1 : kMaxCluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.b.n) * C);
-  cfg.blockDim = dim3(kEvictThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
+  cfg.blockDim = dim3(small ? kPickThreads : kEvictThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -460,7 +617,14 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p, key_cap);
+  if (small) {
+    cfg.dynamicSmemBytes = pick_bytes(cap, most, C);
+    return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p, static_cast<int>((cap + 3) / 4 * 4));
+  }
+  const int32_t per = static_cast<int32_t>(C) * kEvictThreads;
+  const int key_cap = std::min((cap + per - 1) / per * kEvictThreads, kKeyLimit);
+  cfg.dynamicSmemBytes = static_cast<size_t>(key_cap) * 4;
+  return cudaLaunchKernelEx(&cfg, paged_evict_long_kernel, p, key_cap);
 }
 
 }  // namespace sr

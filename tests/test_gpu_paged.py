@@ -277,14 +277,18 @@ def test_evict_is_exact(n, budget, sink, recent, kind):
     p.ok()
 
 
-def test_evict_long_sequences():
-    p = Pair(1, 1, 64, 64, 2, 1100, seed=13, spare=0)
-    p.append([0, 1], [70000, 66001])
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("n0,n1,budget", [(70000, 66001, 60000), (40000, 33007, 32500), (9000, 8999, 8192)])
+def test_evict_long_sequences(n0, n1, budget, odd):
+    p = Pair(1, 1, 64, 64, 2, -(-n0 // 64), seed=13, spare=0)
+    p.append([0, 1], [n0, n1])
     m = p.rng.exponential(1.0, (2, p.cache.capacity)).astype(np.float32)
+    if odd:      # so few that may go below NaN that some of the NaN go too, and many ties
+        m[:] = np.where(p.rng.random(m.shape) < 0.99, np.nan, np.float32(2.0))
     p.cache.token_mass.copy_(torch.from_numpy(m))
     p.ora.mass[:] = m
-    p.cache.evict(60000, 16, 1000, seqs=[1, 0])
-    p.ora.evict([1, 0], 60000, 16, 1000)
+    p.cache.evict(budget, 16, 1000, seqs=[1, 0])
+    p.ora.evict([1, 0], budget, 16, 1000)
     p.check_state([0, 1])
     p.ok()
 
@@ -314,6 +318,34 @@ def test_evict_from_a_sequence_longer_than_shared_memory_holds():
     assert torch.equal(got, want) and torch.equal(c.token_mass[0, :budget], m[want])
     rows = c.block_table[0].long()[t[:budget] // 1024] * 1024 + t[:budget] % 1024
     assert torch.equal(c.k_pages.view(-1, 1, 64)[rows], k[want]) and torch.equal(c.v_pages.view(-1, 1, 64)[rows], -k[want])
+
+
+def test_all_that_may_go_goes():
+    """NaN weights only, and exactly the protected tokens stay."""
+    for n, budget, sink, recent in ((300, 100, 40, 60), (9000, 5000, 1000, 4000)):
+        p = Pair(1, 1, 64, 64, 1, -(-n // 64), seed=n)
+        p.append([0], [n])
+        p.cache.token_mass.fill_(float("nan"))
+        p.ora.mass[:] = np.nan
+        p.cache.evict(budget, sink, recent)
+        p.ora.evict([0], budget, sink, recent)
+        p.check_state([0])
+        p.ok()
+
+
+def test_positions_that_protect_more_than_the_budget():
+    """Positions a caller restored wrongly (all recent): nothing may go, and nothing is written."""
+    for n, budget in ((300, 290), (300, 20), (9000, 100)):
+        p = Pair(1, 1, 64, 64, 1, -(-n // 64), seed=n)
+        p.append([0], [n])
+        p.cache.token_pos.fill_(n - 1)
+        p.cache.token_pos[0, :5] = 1
+        p.ora.pos[:] = n - 1
+        p.ora.pos[0, :5] = 1
+        p.cache.evict(budget, 0, 1)
+        p.ora.evict([0], budget, 0, 1)
+        p.check_state([0])
+        p.ok()
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
