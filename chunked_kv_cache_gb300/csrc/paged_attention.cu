@@ -683,54 +683,59 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 }
 
 // The weights: mass(t) <- decay * mass(t) + sum over heads of 2^(x_h(t) - lse2_h).
-// `per` CTAs per sequence walk its tokens 64 at a time; four threads share a token's
-// heads and add up in a fixed order.
-constexpr int kMassThreads = 256;
+// Latency bound (the scores mostly still lie in L2): `per` CTAs per sequence walk its
+// tokens 64 at a time, eight threads share a token's heads, with all their loads in
+// flight at once, and add up in a fixed order.
 constexpr int kMassTokens = 64;
-constexpr int kMassShare = kMassThreads / kMassTokens;
+constexpr int kMassShare = 8;
+constexpr int kMassThreads = kMassTokens * kMassShare;
 template <int CT>
 __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_constant__ PagedAttnParams p, int per) {
-  extern __shared__ float lse2[];                         // [n_heads]
   __shared__ float sums[kMassShare][kMassTokens];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const PagedView& c = p.c;
   const int i = blockIdx.x / per;
   const int32_t seq = p.b.id[i];
-  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
-  int32_t t0 = (blockIdx.x % per) * kMassTokens;
-  if (t0 >= len) return;
-  const int32_t tiles = (len + CT - 1) / CT;
   const int64_t unit0 = p.unit0[i];
-  if (unit0 + static_cast<int64_t>(tiles + kItemCost) * c.n_kv > p.score_tiles) {   // not stored
+  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
+  const int32_t tiles = (len + CT - 1) / CT;
+  if (len > 0 && unit0 + static_cast<int64_t>(tiles + kItemCost) * c.n_kv > p.score_tiles) {   // not stored
     if (threadIdx.x == 0) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
     return;
   }
-  for (int h = threadIdx.x; h < c.n_heads; h += kMassThreads) lse2[h] = p.lse2[static_cast<int64_t>(i) * c.n_heads + h];
-  __syncthreads();
   const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  const float* lse2 = p.lse2 + static_cast<int64_t>(i) * c.n_heads;
   const int tok = threadIdx.x % kMassTokens, share = threadIdx.x / kMassTokens;
-  const int64_t pitch = static_cast<int64_t>(tiles + kItemCost) * c.group * CT;   // from one head's item to the next
-  for (; t0 < len; t0 += per * kMassTokens) {
+  const int64_t pitch = static_cast<int64_t>(tiles + kItemCost) * c.group * CT;   // from one key head's scores to the next
+  for (int32_t t0 = (blockIdx.x % per) * kMassTokens; t0 < len; t0 += per * kMassTokens) {
     const int32_t t = t0 + tok;
-    float w = 0.f;
+    float w = 0.f, old = 0.f;
+    bool seen = false;
     if (t < len) {
       const float* x = p.scores + (unit0 + kItemCost + t / CT) * c.group * CT + t % CT;
-      if (c.n_kv >= kMassShare) {
-        for (int h = share; h < c.n_kv; h += kMassShare)
+      if (share == 0) {
+        seen = paged_row(table, t, c.page_tokens, c.n_pages) >= 0;   // else left as it is
+        old = c.token_mass[static_cast<int64_t>(seq) * c.cap + t];
+      }
+      int kv = share / c.group, g = share - kv * c.group;
 #pragma unroll 8
-          for (int g = 0; g < c.group; ++g) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
-      } else {
-        for (int h = 0; h < c.n_kv; ++h)
-#pragma unroll 4
-          for (int g = share; g < c.group; g += kMassShare) w += ex2_approx(x[h * pitch + g * CT] - lse2[h * c.group + g]);
+      for (int h = share; h < c.n_heads; h += kMassShare) {
+        w += ex2_approx(__ldcg(x + kv * pitch + g * CT) - __ldcg(lse2 + h));
+        g += kMassShare;
+        while (g >= c.group) {
+          g -= c.group;
+          ++kv;
+        }
       }
     }
     sums[share][tok] = w;
     __syncthreads();
-    if (share == 0 && t < len && paged_row(table, t, c.page_tokens, c.n_pages) >= 0) {   // else not seen: left as it is
-      float* m = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
-      *m = fmaf(p.mass_decay, *m, (sums[0][tok] + sums[1][tok]) + (sums[2][tok] + sums[3][tok]));
+    if (seen) {
+      float all = 0.f;
+#pragma unroll
+      for (int k = 0; k < kMassShare; ++k) all += sums[k][tok];
+      c.token_mass[static_cast<int64_t>(seq) * c.cap + t] = fmaf(p.mass_decay, old, all);
     }
     __syncthreads();
   }
@@ -755,9 +760,8 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(paged_attn_ctas());
   const cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess || !MASS) return e;
-  const int per = std::max(1, 8 * sm_count() / p.b.n);
-  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads,
-                          static_cast<size_t>(p.c.n_heads) * 4, st, p, per);
+  const int per = std::max(1, std::min((p.c.cap + kMassTokens - 1) / kMassTokens, 16 * sm_count() / p.b.n));
+  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads, 0, st, p, per);
 }
 
 template <int D, int TYPE>
