@@ -85,6 +85,7 @@ struct PagedAttnParams {
   float* lse2;
   float* scores;
   int64_t score_tiles;
+  int32_t spread;          // neighbouring key/value heads that neighbouring CTAs take side by side; divides n_kv
   float mass_decay;
   PagedBatch b;
 };
