@@ -57,7 +57,7 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
   l.unit0 = take(sr::kMaxPagedSeqs * sizeof(int64_t));
-  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.head_dim) * 4);
+  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.n_heads / c.n_kv_heads, c.head_dim) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
   // every token of the pool once, the sequences' lengths rounded up to tiles
   const int64_t tile = sr::paged_tile_tokens(c.head_dim, c.page_type);

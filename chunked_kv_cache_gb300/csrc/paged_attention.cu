@@ -62,7 +62,8 @@ struct Geo {
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   static constexpr int kStageBytes = 8192;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
-  static constexpr int kMergeFloats = (kWarps - 1) * 8 * D;
+  static constexpr int kMergeRow = D + 8;          // a row's floats, padded off the other rows' banks
+  static constexpr int kMergeFloats = (kWarps - 1) * 8 * kMergeRow;
 };
 
 // Shared-memory position of 16-byte chunk c of row r, permuted so that eight rows'
@@ -161,29 +162,35 @@ __device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int 
   cursor_seq<CT>(c, s);
 }
 
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {   // a >= 0, b > 0; mostly short numbers
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // ---- joining partial results
 constexpr int kJoin = 16;
 
 // Partial result of a CTA: slot 0 for an item that began before its stretch, 1 for one
-// that begins in it. [kRows][D] sums, then (maximum, sum) per row.
+// that begins in it. [group][D] sums, then (maximum, sum) per row.
+__host__ __device__ __forceinline__ int64_t part_floats(int group, int D) { return (group * (D + 2) + 3) / 4 * 4; }
 template <int D>
 __device__ __forceinline__ float* part_at(const PagedAttnParams& p, int cta, int slot) {
-  return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * kRows * (D + 2);
+  return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * part_floats(p.c.group, D);
 }
 
 // Joins `n` <= 32 parts: the one at first, slot s0, and those of every step-th CTA after it, slot 0. The
 // result is another part (dst) or the output. Each warp takes query rows, its lanes the
-// head dimension; the loads of four parts are in flight together.
+// head dimension; the loads of eight parts are in flight together.
 template <int D>
 __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int s0, int step, int n, float* dst,
                                         int64_t out0, int warp, int lane) {
   __threadfence();
   constexpr int kCols = D / 32;
+  const int ml = p.c.group * D;
   for (int r = warp; r < p.c.group; r += kWarps) {
     float mk = -INFINITY, lk = 0.f;
     if (lane < n) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(part_at<D>(p, first + lane * step, lane == 0 ? s0 : 0) +
-                                                              kRows * D) + r);
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(part_at<D>(p, first + lane * step, lane == 0 ? s0 : 0) + ml) + r);
       mk = v.x;
       lk = v.y;
     }
@@ -197,7 +204,7 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
     float a[kCols];
 #pragma unroll
     for (int x = 0; x < kCols; ++x) a[x] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < n; ++k) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
       const float* src = part_at<D>(p, first + k * step, k == 0 ? s0 : 0) + r * D + lane * kCols;
@@ -213,7 +220,7 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
       // in place over its own first part: this warp alone reads and writes row r
 #pragma unroll
       for (int x = 0; x < kCols; ++x) dst[r * D + lane * kCols + x] = a[x];
-      if (lane == 0) reinterpret_cast<float2*>(dst + kRows * D)[r] = make_float2(top, sum);
+      if (lane == 0) reinterpret_cast<float2*>(dst + ml)[r] = make_float2(top, sum);
     } else {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       uint32_t* o = reinterpret_cast<uint32_t*>(p.o + (out0 + r) * D + lane * kCols);
@@ -284,9 +291,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   // CTAs that work: each gets one unit at least, so that all between an item's first and last have a part of it
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x / S), T);
   if (me >= ctas) return;
-  const int64_t u0 = me * T / ctas, u1 = (me + 1) * T / ctas;
+  // equal stretches, the first `rest` one unit longer
+  const int64_t share = div_pos(T, ctas), rest = T - share * ctas;
+  const int64_t u0 = me * share + min(static_cast<int64_t>(me), rest);
   Cursor comp;
-  int64_t left = u1 - u0;   // units of the stretch from comp on
+  int64_t left = share + (me < rest ? 1 : 0);   // units of the stretch from comp on
   {
     int lo = 0, hi = n - 1;   // the last sequence that starts at or before u0
     while (lo < hi) {
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     cursor_seq<G::CT>(comp, sh);
     const int64_t within = u0 - sh.cum[comp.i];
     const int32_t units = comp.tiles + kItemCost;
-    comp.h = static_cast<int>(within / units);
+    comp.h = static_cast<int>(div_pos(within, units));
     const int32_t unit = static_cast<int32_t>(within - static_cast<int64_t>(comp.h) * units);
     comp.tile = max(unit - kItemCost, 0);
     left -= max(kItemCost - unit, 0);
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       if (warp > 0) {
 #pragma unroll
         for (int k = 0; k < D / 8; ++k)
-          *reinterpret_cast<float2*>(merge + ((warp - 1) * 8 + r8) * D + col(k)) =
+          *reinterpret_cast<float2*>(merge + ((warp - 1) * 8 + r8) * G::kMergeRow + col(k)) =
               make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
       }
       __syncthreads();
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
           float2 y = make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
 #pragma unroll
           for (int w = 0; w < kWarps - 1; ++w) {
-            const float2 z = *reinterpret_cast<const float2*>(merge + (w * 8 + r8) * D + col(k));
+            const float2 z = *reinterpret_cast<const float2*>(merge + (w * 8 + r8) * G::kMergeRow + col(k));
             y.x += z.x;
             y.y += z.y;
           }
@@ -645,8 +654,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             if (p.lse) p.lse[out] = lse2 * kLn2;
             if (MASS) p.lse2[out] = lse2;
           } else {
-            part[kRows * D + 2 * r] = top[half];
-            part[kRows * D + 2 * r + 1] = sum[half];
+            part[group * D + 2 * r] = top[half];
+            part[group * D + 2 * r + 1] = sum[half];
           }
         }
       }
@@ -654,8 +663,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     if (!whole) {
       // The parts of this item lie with CTAs c0 .. c1. The last of a group of kJoin to
       // arrive joins the group, the last group to be joined the item.
-      const int c0 = static_cast<int>(((item_u + 1) * ctas - 1) / T);
-      const int n_parts = static_cast<int>(((item_u + tiles) * ctas - 1) / T) - c0 + 1;
+      auto owner = [&](int64_t u) {   // of unit u of the line
+        const int64_t longer = rest * (share + 1);
+        return static_cast<int>(u < longer ? div_pos(u, share + 1) : rest + div_pos(u - longer, share));
+      };
+      const int c0 = owner(item_u);
+      const int n_parts = owner(item_u + tiles - 1) - c0 + 1;
       const int64_t out0 = static_cast<int64_t>(item_i) * c.n_heads + item_h * group;
       auto arrive = [&](int32_t* ctr, int need) -> bool {   // warp 0 wrote; true for the whole CTA in the last one
         if (warp == 0) {
@@ -690,46 +703,56 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 }
 
 // The weights: mass(t) <- decay * mass(t) + sum over heads of 2^(x_h(t) - lse2_h).
-// Latency bound (the scores mostly still lie in L2): `per` CTAs per sequence walk its
-// tokens 64 at a time, eight threads share a token's heads, with all their loads in
-// flight at once, and add up in a fixed order.
-constexpr int kMassTokens = 64;
+// Latency bound (the scores mostly still lie in L2), so few dependent loads: a CTA takes
+// 128 tokens, four per thread in one 16-byte load per head; eight threads share a token's
+// heads, with their loads in flight together, and add up in a fixed order.
+constexpr int kMassTokens = 128;
 constexpr int kMassShare = 8;
-constexpr int kMassThreads = kMassTokens * kMassShare;
+constexpr int kMassQuads = kMassTokens / 4;
+constexpr int kMassThreads = kMassQuads * kMassShare;
 template <int CT>
 __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_constant__ PagedAttnParams p, int per) {
-  __shared__ float sums[kMassShare][kMassTokens];
+  __shared__ float4 sums[kMassShare][kMassQuads];
   grid_dep_launch_dependents();
   grid_dep_wait();
   const PagedView& c = p.c;
-  const int i = blockIdx.x / per;
+  const int i = blockIdx.x / per, S = p.spread;
   const int32_t seq = p.b.id[i];
   const int64_t unit0 = p.unit0[i];
   const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
   const int32_t tiles = (len + CT - 1) / CT;
-  if (len > 0 && (unit0 + static_cast<int64_t>(tiles + kItemCost) * (c.n_kv / p.spread)) * p.spread > p.score_tiles) {   // not stored
+  if (len > 0 && (unit0 + static_cast<int64_t>(tiles + kItemCost) * (c.n_kv / S)) * S > p.score_tiles) {   // not stored
     if (threadIdx.x == 0) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
     return;
   }
   const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
   const float* lse2 = p.lse2 + static_cast<int64_t>(i) * c.n_heads;
-  const int tok = threadIdx.x % kMassTokens, share = threadIdx.x / kMassTokens;
+  const int quad = threadIdx.x % kMassQuads, share = threadIdx.x / kMassQuads;
   // from a key head's scores to the next one's on the line; neighbours of one CTA group lie side by side
-  const int64_t pitch = static_cast<int64_t>(tiles + kItemCost) * p.spread * c.group * CT;
+  const int64_t pitch = static_cast<int64_t>(tiles + kItemCost) * S * c.group * CT;
   for (int32_t t0 = (blockIdx.x % per) * kMassTokens; t0 < len; t0 += per * kMassTokens) {
-    const int32_t t = t0 + tok;
-    float w = 0.f, old = 0.f;
+    const int32_t t = t0 + 4 * quad;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    float old[4];
     bool seen = false;
+    float* mass = c.token_mass + static_cast<int64_t>(seq) * c.cap + t;
     if (t < len) {
-      const float* x = p.scores + (unit0 + kItemCost + t / CT) * p.spread * c.group * CT + t % CT;
+      const float* x = p.scores + (unit0 + kItemCost + t / CT) * S * c.group * CT + t % CT;
       if (share == 0) {
-        seen = paged_row(table, t, c.page_tokens, c.n_pages) >= 0;   // else left as it is
-        old = c.token_mass[static_cast<int64_t>(seq) * c.cap + t];
+        seen = paged_row(table, t, c.page_tokens, c.n_pages) >= 0;   // else left as they are
+#pragma unroll
+        for (int k = 0; k < 4; ++k) old[k] = t + k < len ? mass[k] : 0.f;
       }
       int kv = share / c.group, g = share - kv * c.group;
 #pragma unroll 8
       for (int h = share; h < c.n_heads; h += kMassShare) {
-        w += ex2_approx(__ldcg(x + (kv / p.spread) * pitch + (kv % p.spread * c.group + g) * CT) - __ldcg(lse2 + h));
+        const int side = kv / S;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(x + side * pitch + ((kv - side * S) * c.group + g) * CT));
+        const float l = __ldcg(lse2 + h);
+        w.x += ex2_approx(v.x - l);
+        w.y += ex2_approx(v.y - l);
+        w.z += ex2_approx(v.z - l);
+        w.w += ex2_approx(v.w - l);
         g += kMassShare;
         while (g >= c.group) {
           g -= c.group;
@@ -737,13 +760,22 @@ __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_c
         }
       }
     }
-    sums[share][tok] = w;
+    sums[share][quad] = w;
     __syncthreads();
     if (seen) {
-      float all = 0.f;
+      float4 all = sums[0][quad];
 #pragma unroll
-      for (int k = 0; k < kMassShare; ++k) all += sums[k][tok];
-      c.token_mass[static_cast<int64_t>(seq) * c.cap + t] = fmaf(p.mass_decay, old, all);
+      for (int k = 1; k < kMassShare; ++k) {
+        const float4 y = sums[k][quad];
+        all.x += y.x;
+        all.y += y.y;
+        all.z += y.z;
+        all.w += y.w;
+      }
+      const float sum[4] = {all.x, all.y, all.z, all.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (t + k < len) mass[k] = fmaf(p.mass_decay, old[k], sum[k]);
     }
     __syncthreads();
   }
@@ -781,7 +813,7 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
 
 int paged_attn_ctas() { return std::min(2 * sm_count(), kMaxPagedCtas); }
 
-size_t paged_part_floats(int head_dim) { return static_cast<size_t>(kRows) * (head_dim + 2); }
+size_t paged_part_floats(int group, int head_dim) { return static_cast<size_t>(part_floats(group, head_dim)); }
 int paged_tile_tokens(int head_dim, int page_type) {
   if (head_dim == 128) return page_type == SR_PAGE_BF16 ? Geo<128, SR_PAGE_BF16>::CT : Geo<128, SR_PAGE_E4M3>::CT;
   return page_type == SR_PAGE_BF16 ? Geo<64, SR_PAGE_BF16>::CT : Geo<64, SR_PAGE_E4M3>::CT;
