@@ -154,6 +154,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.max_pages = cfg->max_pages;
   v.cap = cfg->max_pages * cfg->page_tokens;
   v.page_type = cfg->page_type;
+  v.magic = sr::page_magic(cfg->page_tokens);
   const float scale = cfg->softmax_scale > 0.f ? cfg->softmax_scale : 1.0f / std::sqrt(static_cast<float>(cfg->head_dim));
   v.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);

@@ -318,10 +318,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
   const int64_t row_pitch = static_cast<int64_t>(c.n_kv) * G::kRowBytes;
 
-  // ---- copy this warp's tokens of one tile into a stage
+  // ---- copy this warp's tokens of one tile into a stage. The block table's entries for the
+  // tile after it are fetched on the way, so that no copy waits for them.
+  int32_t page[G::kGroups];
+  auto fetch_pages = [&] {
+    const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
+#pragma unroll
+    for (int g = 0; g < G::kGroups; ++g) {
+      const int32_t tok = load.tile * G::CT + warp * G::KT + g * 16;
+      if (tok < load.len) page[g] = table[page_of_group(tok >> 4, c.magic)];
+    }
+  };
+  fetch_pages();
   auto issue = [&](int stage) {
     if (left_load > 0) {
-      const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
       constexpr int kRowsPer = 32 / G::kChunks;   // rows per instruction
       const int r0 = lane / G::kChunks, ch = lane % G::kChunks;
@@ -331,13 +341,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         int32_t live = load.len - tok;
         int64_t row = 0;
         if (live > 0) {
-          row = paged_row(table, tok, c.page_tokens, c.n_pages);
           const uint32_t bit = 1u << (stage * G::kGroups + g);
           bad &= ~bit;
-          if (row < 0) {
+          if (page[g] >= 0 && page[g] < c.n_pages) {
+            row = static_cast<int64_t>(page[g]) * c.page_tokens + (tok - page_of_group(tok >> 4, c.magic) * c.page_tokens);
+          } else {
             if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
             bad |= bit;
-            row = 0;
             live = 0;
           }
         }
@@ -354,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
       cursor_next<G::CT>(load, sh, n_kv, left_load);
+      if (left_load > 0) fetch_pages();
     }
     copy_commit();
   };

@@ -23,6 +23,16 @@ __host__ __device__ __forceinline__ int64_t paged_row(const int32_t* table, int3
   return static_cast<int64_t>(page) * page_tokens + (idx - p * page_tokens);
 }
 
+// Page of 16-token group g (0 <= g < 2^20) of a sequence: g / (page_tokens / 16) by
+// multiplication with ceil(2^32 / d), exact because g * d < 2^32. magic 0: pages of one group.
+__host__ __device__ __forceinline__ uint32_t page_magic(int32_t page_tokens) {
+  const uint32_t d = static_cast<uint32_t>(page_tokens) / 16;
+  return d == 1 ? 0u : 0xFFFFFFFFu / d + 1u;
+}
+__device__ __forceinline__ int32_t page_of_group(int32_t g, uint32_t magic) {
+  return magic == 0 ? g : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(g), magic));
+}
+
 struct PagedView {
   void* k_pages;
   void* v_pages;
@@ -37,6 +47,7 @@ struct PagedView {
   int32_t page_tokens, n_pages, max_pages;
   int32_t cap;             // max_pages * page_tokens
   int32_t page_type;
+  uint32_t magic;          // page_magic(page_tokens)
   float scale_log2;        // softmax scale * log2(e)
 };
 
