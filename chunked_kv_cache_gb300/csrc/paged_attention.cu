@@ -74,7 +74,10 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * CHUNKS + (c ^ ((r >> 1) & 3))) * 16u;
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -320,6 +323,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 
   // ---- copy this warp's tokens of one tile into a stage. The block table's entries for the
   // tile after it are fetched on the way, so that no copy waits for them.
+  constexpr int kRowsPer = 32 / G::kChunks;     // rows per instruction
+  const int r0 = lane / G::kChunks, ch = lane % G::kChunks;
+  const int64_t lane_off = r0 * row_pitch + ch * 16;
   int32_t page[G::kGroups];
   auto fetch_pages = [&] {
     const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
@@ -333,8 +339,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   auto issue = [&](int stage) {
     if (left_load > 0) {
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
-      constexpr int kRowsPer = 32 / G::kChunks;   // rows per instruction
-      const int r0 = lane / G::kChunks, ch = lane % G::kChunks;
 #pragma unroll
       for (int g = 0; g < G::kGroups; ++g) {
         const int32_t tok = load.tile * G::CT + warp * G::KT + g * 16;
@@ -351,16 +355,23 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             live = 0;
           }
         }
-        const int64_t at = row * row_pitch + (load.h * S + sub) * G::kRowBytes + ch * 16;
-        const char* kp = static_cast<const char*>(c.k_pages) + at;
-        const char* vp = static_cast<const char*>(c.v_pages) + at;
+        int64_t at = row * row_pitch + lane_off + (load.h * S + sub) * G::kRowBytes;
+        if (live >= 16) {
 #pragma unroll
-        for (int x = 0; x < 16 / kRowsPer; ++x) {
-          const int r = x * kRowsPer + r0;
-          const bool in = r < live;
-          const int64_t off = in ? r * row_pitch : 0;
-          copy16(ks + chunk_at<G::kChunks>(g * 16 + r, ch), kp + off, in);
-          copy16(vs + chunk_at<G::kChunks>(g * 16 + r, ch), vp + off, in);
+          for (int x = 0; x < 16 / kRowsPer; ++x, at += kRowsPer * row_pitch) {
+            const uint32_t to = chunk_at<G::kChunks>(g * 16 + x * kRowsPer + r0, ch);
+            copy16(ks + to, static_cast<const char*>(c.k_pages) + at);
+            copy16(vs + to, static_cast<const char*>(c.v_pages) + at);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 16 / kRowsPer; ++x, at += kRowsPer * row_pitch) {
+            const int r = x * kRowsPer + r0;
+            const uint32_t to = chunk_at<G::kChunks>(g * 16 + r, ch);
+            const int64_t from = r < live ? at : 0;       // past the length: zeros, nothing read
+            copy16_or_zero(ks + to, static_cast<const char*>(c.k_pages) + from, r < live);
+            copy16_or_zero(vs + to, static_cast<const char*>(c.v_pages) + from, r < live);
+          }
         }
       }
       cursor_next<G::CT>(load, sh, n_kv, left_load);
@@ -434,7 +445,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     for (int k = 0; k < D / 8; ++k)
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};   // of rows r8, r8 + 8; l: this lane's share
+    // m: the running maximum less kLift (fp16 weights then reach 2^10), the reference of the
+    // exponentials; l: this lane's share of their sum. Of rows r8 and r8 + 8.
+    constexpr float kLift = TYPE == SR_PAGE_BF16 ? 0.f : 10.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
       issue((stage + kStages - 1) % kStages);
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 #pragma unroll
       for (int g = 0; g < G::kGroups; ++g) {
         live[g] = (bad >> (stage * G::kGroups + g)) & 1u ? 0u : static_cast<uint32_t>(min(max(len - tok - g * 16, 0), 16));
-        any |= live[g];
+        any += live[g];
       }
       if (any) {
         float s[G::KT / 8][4];
@@ -481,15 +495,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
             }
           }
         }
+        if (any != 16 * G::kGroups) {                 // keys past the length, or without a page
+#pragma unroll
+          for (int k = 0; k < G::KT / 8; ++k)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if ((k % 2) * 8 + 2 * j4 + (x & 1) >= live[k / 2]) s[k][x] = -INFINITY;
+        }
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < G::KT / 8; ++k)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t key = (k % 2) * 8 + 2 * j4 + (x & 1);
-            s[k][x] = key < live[k / 2] ? s[k][x] * xs[x / 2] : -INFINITY;
-            top[x / 2] = fmaxf(top[x / 2], s[k][x]);
-          }
+        for (int k = 0; k < G::KT / 8; ++k) {
+          top[0] = fmax3(top[0], s[k][0], s[k][1]);
+          top[1] = fmax3(top[1], s[k][2], s[k][3]);
+        }
         if constexpr (MASS) {
           // the scaled scores, for the weights that the second launch forms
           if ((item_u + tile) * S + sub < p.score_tiles) {
@@ -500,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
                 float* dst = p.scores + (((item_u + tile) * S + sub) * group + r) * G::CT + warp * G::KT + 2 * j4;
 #pragma unroll
                 for (int k = 0; k < G::KT / 8; ++k)
-                  *reinterpret_cast<float2*>(dst + k * 8) = make_float2(s[k][2 * half], s[k][2 * half + 1]);
+                  *reinterpret_cast<float2*>(dst + k * 8) = make_float2(s[k][2 * half] * xs[half], s[k][2 * half + 1] * xs[half]);
               }
             }
           }
@@ -509,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         for (int half = 0; half < 2; ++half) {
           top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
           top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
+          top[half] = top[half] * xs[half] - kLift;      // xs > 0
         }
         if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
           float f[2];
@@ -529,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         for (int k = 0; k < G::KT / 8; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            s[k][x] = ex2_approx(s[k][x] - (x < 2 ? m0 : m1));
+            s[k][x] = ex2_approx(fmaf(s[k][x], xs[x / 2], x < 2 ? -m0 : -m1));
             l[x / 2] += s[k][x];
           }
 #pragma unroll
@@ -538,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const float lo = s[2 * g + x / 2][2 * (x % 2)], hi = s[2 * g + x / 2][2 * (x % 2) + 1];
-            a[x] = TYPE == SR_PAGE_BF16 ? pack_bf16x2(lo, hi) : pack_half2(lo * 1024.f, hi * 1024.f);
+            a[x] = TYPE == SR_PAGE_BF16 ? pack_bf16x2(lo, hi) : pack_half2(lo, hi);
           }
           const int vr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
           if constexpr (TYPE == SR_PAGE_BF16) {
@@ -600,7 +619,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     const bool whole = first_tile == 0 && end_tile == tiles;
     float* part = part_at<D>(p, blockIdx.x, first_tile == 0 ? 1 : 0);
     const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[c.n_kv + item_h])) : 1.f;
-    const float vs1 = TYPE == SR_PAGE_BF16 ? vscale : vscale * 0x1p-10f;
     float mine[2], top[2], sum[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -642,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       const int r = r8 + 8 * half;
       if (warp == 0 && r < group) {
         const int64_t out = static_cast<int64_t>(item_i) * c.n_heads + item_h * group + r;
-        const float scale = whole ? (sum[half] == 0.f ? 0.f : vs1 / sum[half]) : vs1;
+        const float scale = whole ? (sum[half] == 0.f ? 0.f : vscale / sum[half]) : vscale;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
           float2 y = make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
