@@ -121,6 +121,13 @@ __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
   return y;
 }
 
+// Releases what this thread has seen written, and acquires what earlier such additions released.
+__device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
+  int32_t old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(x) : "memory");
+  return old;
+}
+
 struct SharedHead {
   int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
@@ -171,7 +178,7 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {   // a >= 0, 
 }
 
 // ---- joining partial results
-constexpr int kJoin = 16;
+constexpr int kJoin = 48;
 
 // Partial result of a CTA: slot 0 for an item that began before its stretch, 1 for one
 // that begins in it. [group][D] sums, then (maximum, sum) per row.
@@ -181,42 +188,61 @@ __device__ __forceinline__ float* part_at(const PagedAttnParams& p, int cta, int
   return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * part_floats(p.c.group, D);
 }
 
-// Joins `n` <= 32 parts: the one at first, slot s0, and those of every step-th CTA after it, slot 0. The
-// result is another part (dst) or the output. Each warp takes query rows, its lanes the
-// head dimension; the loads of eight parts are in flight together.
+// Joins n parts: the one at first, slot s0, and those of every step-th CTA after it, slot
+// 0. The result is another part (dst) or the output. Each warp takes query rows, its lanes
+// the head dimension; sixteen parts at a time, all their loads in flight together.
+constexpr int kJoinBatch = 16;
 template <int D>
 __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int s0, int step, int n, float* dst,
                                         int64_t out0, int warp, int lane) {
-  __threadfence();
   constexpr int kCols = D / 32;
   const int ml = p.c.group * D;
   for (int r = warp; r < p.c.group; r += kWarps) {
-    float mk = -INFINITY, lk = 0.f;
-    if (lane < n) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(part_at<D>(p, first + lane * step, lane == 0 ? s0 : 0) + ml) + r);
-      mk = v.x;
-      lk = v.y;
-    }
-    float top = mk;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float w = mk == -INFINITY ? 0.f : ex2_approx(mk - top);
-    float sum = w * lk;
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    float a[kCols];
+    float top = -INFINITY, sum = 0.f, a[kCols];
 #pragma unroll
     for (int x = 0; x < kCols; ++x) a[x] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const float* src = part_at<D>(p, first + k * step, k == 0 ? s0 : 0) + r * D + lane * kCols;
-      if constexpr (kCols == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-        a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]); a[2] = fmaf(wk, v.z, a[2]); a[3] = fmaf(wk, v.w, a[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-        a[0] = fmaf(wk, v.x, a[0]); a[1] = fmaf(wk, v.y, a[1]);
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
+      float v[kJoinBatch][kCols];
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int kk = min(k0 + k, n - 1);     // one past the end repeats the last, with no weight
+        const float* src = part_at<D>(p, first + kk * step, kk == 0 ? s0 : 0) + r * D + lane * kCols;
+        if constexpr (kCols == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(src));
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(src));
+          v[k][0] = x.x; v[k][1] = x.y;
+        }
+      }
+      float mk = -INFINITY, lk = 0.f;
+      if (lane < kJoinBatch && k0 + lane < n) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(
+                                    part_at<D>(p, first + (k0 + lane) * step, k0 + lane == 0 ? s0 : 0) + ml) + r);
+        mk = x.x;
+        lk = x.y;
+      }
+      float t = mk;
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, s));
+      t = fmaxf(__shfl_sync(0xffffffffu, t, 0), top);
+      // a first batch has nothing to rescale; a maximum of -inf stands for no token, or NaN alone
+      const float f = top == -INFINITY ? 1.f : ex2_approx(top - t);
+      const float w = mk == -INFINITY ? 0.f : ex2_approx(mk - t);
+      top = t;
+      float s1 = w * lk;
+#pragma unroll
+      for (int s = 8; s > 0; s >>= 1) s1 += __shfl_xor_sync(0xffffffffu, s1, s);
+      sum = sum * f + __shfl_sync(0xffffffffu, s1, 0);
+#pragma unroll
+      for (int x = 0; x < kCols; ++x) a[x] *= f;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        if (k0 + k < n)
+#pragma unroll
+          for (int x = 0; x < kCols; ++x) a[x] = fmaf(wk, v[k][x], a[x]);
       }
     }
     if (dst) {
@@ -701,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
       const int64_t out0 = static_cast<int64_t>(item_i) * c.n_heads + item_h * group;
       auto arrive = [&](int32_t* ctr, int need) -> bool {   // warp 0 wrote; true for the whole CTA in the last one
         if (warp == 0) {
-          __threadfence();
-          __syncwarp();
+          __syncwarp();         // the lanes' stores come before lane 0's release
           if (lane == 0) {
-            const bool all = atomicAdd(ctr, 1) == need - 1;
+            const bool all = add_acq_rel(ctr, 1) == need - 1;
             if (all) *ctr = 0;
             sh.last = all;
           }
@@ -721,7 +746,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         const int size = min(kJoin, n_parts - g * kJoin);
         if (arrive(p.group_arrivals + 2 * lead + s0, size)) {
           join_parts<D>(p, lead, s0, S, size, part_at<D>(p, lead, s0), 0, warp, lane);
-          __threadfence();
           __syncthreads();
           if (arrive(p.arrivals + c0 * S + sub, (n_parts + kJoin - 1) / kJoin))
             join_parts<D>(p, c0 * S + sub, 1, kJoin * S, (n_parts + kJoin - 1) / kJoin, nullptr, out0, warp, lane);
