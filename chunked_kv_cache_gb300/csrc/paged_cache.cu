@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // weights' bits, mapped to unsigned integers in the weights' order, are read once into
 // shared memory. A radix select (11, 11 and 10 bits, the CTAs' counts added through
 // distributed shared memory) narrows the keys down to those that share the digits of
-// the last key to go; as soon as these are few they are gathered and ranked against one
-// another, which settles ties by index as well. The result is a cut: a token goes if its
+// the last key to go; as soon as these are few they are gathered, one per thread, and the
+// cut is found among them bit by bit, first of the key, then of the index, which settles ties. The result is a cut: a token goes if its
 // key lies below the cut's, or equals it at an index at or behind the cut's. Ordered
 // counts turn that into moves (from, to), and all warps move rows, a warp per token. A
 // move reads at or behind the new length and writes below it, so that no move sees
@@ -137,9 +137,9 @@ constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kCandidates = 512;      // keys that are ranked against one another: one per thread
+constexpr int kCandidates = 512;      // keys gathered to find the cut among them
 constexpr int kKeyLimit = 45056;      // keys a CTA can hold; longer stretches are read again from global memory
-static_assert(kCandidates <= kEvictThreads, "a thread ranks one candidate");
+static_assert(kCandidates <= kEvictThreads, "a thread holds one candidate");
 
 // The order of the weights as unsigned integers; protected tokens come last.
 constexpr uint32_t kProtected = 0xFFFFFFFFu;
@@ -203,13 +203,36 @@ struct EvictShared {
   uint2 cand[kCandidates];          // (key, index) of this CTA's candidates
   uint32_t n_cand, n_ties, n_holes, n_backs, cut_index;
   unsigned long long list0;         // rank 0: the sequence's first entry in the list of moves
+  unsigned long long lightest;      // one token to go: the smallest (key, complement of the index)
 };
+
+// A warp moves one token's rows.
+__device__ __forceinline__ void move_rows(const PagedView& c, int64_t from, int64_t to, int vpr, int lane) {
+  const uint4* ks = static_cast<const uint4*>(c.k_pages) + from * vpr;
+  const uint4* vs = static_cast<const uint4*>(c.v_pages) + from * vpr;
+  uint4* kd = static_cast<uint4*>(c.k_pages) + to * vpr;
+  uint4* vd = static_cast<uint4*>(c.v_pages) + to * vpr;
+  for (int x0 = lane; x0 < vpr; x0 += 128) {     // eight loads in flight per lane
+    uint4 a[4], b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x0 + 32 * k < vpr) {
+        a[k] = __ldcs(ks + x0 + 32 * k);
+        b[k] = __ldcs(vs + x0 + 32 * k);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (x0 + 32 * k < vpr) {
+        kd[x0 + 32 * k] = a[k];
+        vd[x0 + 32 * k] = b[k];
+      }
+  }
+}
 
 __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __grid_constant__ EvictParams p, int key_cap) {
   extern __shared__ uint32_t keys[];              // [key_cap]
   __shared__ __align__(16) EvictShared sh;
   __shared__ uint32_t sums[2][kEvictWarps];
-  __shared__ uint2 all[kCandidates];              // every CTA's candidates
   __shared__ uint32_t found[3];                   // digit, rank in it, its keys
   __shared__ uint2 cut_at;
   const uint32_t C = cluster_size(), me = cluster_rank();
@@ -242,12 +265,70 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   const int32_t w0 = min(warp * (chunk / kEvictWarps), count), w1 = min(w0 + chunk / kEvictWarps, count);
   const bool held = chunk <= key_cap;
   if (held) {
-#pragma unroll 4
+#pragma unroll 8
     for (int32_t x = w0 + lane; x < w1; x += 32) keys[x] = key_of(tpos[first + x], mass[first + x]);
     __syncwarp();                                 // a warp reads the keys that it wrote
   }
   auto key = [&](int32_t x) { return x >= w1 ? kProtected : held ? keys[x] : key_of(tpos[first + x], mass[first + x]); };
   __syncthreads();
+
+  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
+  if (len - p.budget == 1) {
+    // ---- one token too many, as in serving token by token: the lightest goes, and the last
+    // index's token takes its place
+    unsigned long long best = ~0ull;
+    for (int32_t x = w0 + lane; x < w1; x += 32) {
+      const uint32_t k = key(x);
+      if (k != kProtected)
+        best = min(best, static_cast<unsigned long long>(k) << 32 | static_cast<uint32_t>(~(first + x)));
+    }
+    auto warp_min = [](unsigned long long v) {
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, s));
+      return v;
+    };
+    best = warp_min(best);
+    unsigned long long* mins = reinterpret_cast<unsigned long long*>(sh.cand);
+    if (lane == 0) mins[warp] = best;
+    __syncthreads();
+    if (warp == 0) {
+      best = warp_min(lane < kEvictWarps ? mins[lane] : ~0ull);
+      if (lane == 0) sh.lightest = best;
+    }
+    cluster_sync(C);
+    if (me == 0 && warp == 0) {
+      if (C > 1) {
+        best = ~0ull;
+        if (lane < static_cast<int>(C)) {
+          const uint2 v = peer_load2(peer_addr(&sh.lightest, lane));
+          best = static_cast<unsigned long long>(v.y) << 32 | v.x;
+        }
+        best = warp_min(best);
+      }
+      best = __shfl_sync(0xffffffffu, best, 0);
+      const int32_t at = static_cast<int32_t>(~static_cast<uint32_t>(best)), last = len - 1;
+      if (best != ~0ull) {
+        if (at != last) {
+          const int64_t from = paged_row(table, last, c.page_tokens, c.n_pages);
+          const int64_t to = paged_row(table, at, c.page_tokens, c.n_pages);
+          if (from >= 0 && to >= 0) {
+            if (lane == 0) {
+              tpos[at] = tpos[last];
+              mass[at] = mass[last];
+            }
+            move_rows(c, from, to, vpr, lane);
+          } else if (lane == 0) {
+            note_error(c, SR_DEVERR_BAD_PAGE);
+          }
+        }
+        if (lane == 0) c.seq_len[seq] = last;
+      }
+    }
+    if (C > 1) cluster_sync(C);   // this CTA's lightest has been read
+    done();
+    return;
+  }
 
   // ---- the key of rank `rank` (from 1) among those that may go
   uint32_t prefix = 0, rank = 0;
@@ -341,14 +422,18 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
           if (at < m) my = C == 1 ? sh.cand[at] : peer_load2(peer_addr(&sh.cand[at], r));
           from += m;                               // n in the end
         }
-      if (tid < kCandidates) all[tid] = my;
-      __syncthreads();
-      if (static_cast<uint32_t>(tid) < n) {
-        uint32_t order = 0;
-#pragma unroll 4
-        for (uint32_t x = 0; x < n; ++x) order += all[x].x < my.x || (all[x].x == my.x && all[x].y > my.y);
-        if (order == rank - 1) cut_at = my;
+      // The rank-th of n <= 512 distinct values, one per thread, bit by bit: the block counts those
+      // that have agreed with it so far and have a zero next.
+      const unsigned long long v = static_cast<unsigned long long>(my.x & ((1u << shift) - 1u)) << 24 | (~my.y & 0xFFFFFFu);
+      bool alive = static_cast<uint32_t>(tid) < n;
+      for (int bit = shift + 23; bit >= 0; --bit) {
+        const bool one = v >> bit & 1ull;
+        const uint32_t zeros = static_cast<uint32_t>(__syncthreads_count(alive && !one));
+        const bool go_one = rank > zeros;
+        if (go_one) rank -= zeros;
+        alive = alive && one == go_one;
       }
+      if (alive) cut_at = my;
       __syncthreads();
       cut_key = cut_at.x;
       cut_index = cut_at.y;
@@ -447,8 +532,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
 
   // ---- move: a warp looks up 32 of its moves at once, then takes them one by one
   if (me == 0 && tid == 0) c.seq_len[seq] = kept;
-  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
   const uint32_t step = C * kEvictWarps;
   for (uint32_t j0 = warp * C + me; j0 < moves; j0 += 32 * step) {
     const uint32_t j = j0 + lane * step;
@@ -469,25 +552,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     for (int q = 0; q < n; ++q) {
       const int64_t f = __shfl_sync(0xffffffffu, from, q), g = __shfl_sync(0xffffffffu, to, q);
       if (f < 0) continue;
-      const uint4* ks = static_cast<const uint4*>(c.k_pages) + f * vpr;
-      const uint4* vs = static_cast<const uint4*>(c.v_pages) + f * vpr;
-      uint4* kd = static_cast<uint4*>(c.k_pages) + g * vpr;
-      uint4* vd = static_cast<uint4*>(c.v_pages) + g * vpr;
-      for (int x0 = lane; x0 < vpr; x0 += 64) {      // four loads in flight per lane
-        uint4 a[2], b[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (x0 + 32 * k < vpr) {
-            a[k] = __ldcs(ks + x0 + 32 * k);
-            b[k] = __ldcs(vs + x0 + 32 * k);
-          }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (x0 + 32 * k < vpr) {
-            kd[x0 + 32 * k] = a[k];
-            vd[x0 + 32 * k] = b[k];
-          }
-      }
+      move_rows(c, f, g, vpr, lane);
     }
   }
 }
