@@ -49,7 +49,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
 constexpr int kRows = SR_MAX_PAGED_GROUP;   // query rows of an item's matrix product
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -61,6 +60,11 @@ struct Geo {
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   static constexpr int kStageBytes = 8192;
+  // CTAs per SM, and stages per warp that fit them: head dim 64 leaves registers for a third CTA, which
+  // its shorter rows need (more tokens, so more arithmetic, per byte): 64 sequences of 8192 tokens, 8
+  // heads, e4m3: 110 us with two CTAs of three stages, 99 us with three of two; bf16, 4096: 94 us, 93 us.
+  static constexpr int kCtas = D == 64 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 2 : 3;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
   static constexpr int kMergeRow = D + 8;          // a row's floats, padded off the other rows' banks
   static constexpr int kMergeFloats = (kWarps - 1) * 8 * kMergeRow;
@@ -265,7 +269,7 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
 }
 
 template <int D, int TYPE, bool MASS>
-__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using G = Geo<D, TYPE>;
   extern __shared__ __align__(128) uint8_t smem[];
   SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea + G::kMergeFloats * 4);
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
   if (left <= 0) return;    // nothing but the units before an item
   Cursor load = comp;
   int64_t left_load = left;
-  const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
+  const uint32_t stage0 = smem_u32(smem) + warp * G::kStages * G::kStageBytes;
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
   const int64_t row_pitch = static_cast<int64_t>(c.n_kv) * G::kRowBytes;
 
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     copy_commit();
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
+  for (int s = 0; s < G::kStages - 1; ++s) issue(s);
 
   // ---- the items of this stretch, one after the other
   int stage = 0;
@@ -465,6 +469,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
     }
+    // a scale so small that it underflows: the scores are zero as well as with this one, and masked ones stay -inf
+    xs[0] = fmaxf(xs[0], 0x1p-126f);
+    xs[1] = fmaxf(xs[1], 0x1p-126f);
     const int64_t item_u = sh.cum[item_i] + static_cast<int64_t>(comp.h) * (tiles + kItemCost) + kItemCost;   // its first tile
     float o[D / 8][4];
 #pragma unroll
@@ -477,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
-      issue((stage + kStages - 1) % kStages);
-      copy_wait<kStages - 1>();
+      issue((stage + G::kStages - 1) % G::kStages);
+      copy_wait<G::kStages - 1>();
       __syncwarp();
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
       const int32_t tok = tile * G::CT + warp * G::KT;
@@ -625,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(const __grid_co
         }
       }
       __syncwarp();
-      stage = (stage + 1) % kStages;
+      stage = (stage + 1) % G::kStages;
       cursor_next<G::CT>(comp, sh, n_kv, left);
     }
     if (left > 0) fetch_q(comp.i, comp.h);
@@ -839,7 +846,7 @@ constexpr int kSmem = Geo<D, TYPE>::kStageArea + Geo<D, TYPE>::kMergeFloats * 4 
 
 template <int D, int TYPE>
 cudaError_t prepare() {
-  static_assert(2 * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "two CTAs per SM do not fit");
+  static_assert(Geo<D, TYPE>::kCtas * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "the CTAs of an SM do not fit");
   const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, TYPE>);
   if (e != cudaSuccess) return e;
@@ -850,7 +857,7 @@ cudaError_t prepare() {
 template <int D, int TYPE, bool MASS>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
   using G = Geo<D, TYPE>;
-  const unsigned grid = static_cast<unsigned>(paged_attn_ctas() / p.spread * p.spread);
+  const unsigned grid = static_cast<unsigned>(std::min(G::kCtas * sm_count(), kMaxPagedCtas) / p.spread * p.spread);
   const cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess || !MASS) return e;
   const int per = std::max(1, std::min((p.c.cap + kMassTokens - 1) / kMassTokens, 16 * sm_count() / p.b.n));
@@ -863,8 +870,6 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
 }
 
 }  // namespace
-
-int paged_attn_ctas() { return std::min(2 * sm_count(), kMaxPagedCtas); }
 
 size_t paged_part_floats(int group, int head_dim) { return static_cast<size_t>(part_floats(group, head_dim)); }
 int paged_tile_tokens(int head_dim, int page_type) {

@@ -114,7 +114,6 @@ cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStre
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
-int paged_attn_ctas();                                    // CTAs of an attention launch
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
 cudaError_t paged_evict_prepare();
 cudaError_t paged_attn_prepare(int head_dim, int page_type);

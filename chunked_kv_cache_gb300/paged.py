@@ -113,6 +113,8 @@ class PagedCache:
         """Give sequence `seq` the pages it needs to hold n_tokens tokens (those it has stay)."""
         if self._free is None:
             raise RuntimeError("the caller's block table is the caller's to fill")
+        if not 0 <= seq < self.max_seqs:
+            raise ValueError(f"sequence {seq} of {self.max_seqs}")
         have = self._pages[seq]
         need = -(-n_tokens // self.page_tokens)
         if need > self.max_pages:

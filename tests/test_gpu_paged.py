@@ -424,6 +424,131 @@ def test_other_stream_and_reserved_pages():
     assert c.seq_len.tolist() == [0, 0, 0, 0]
 
 
+def test_pages_past_4_gigabytes():
+    """Rows whose offsets pass 32 bits, in elements and in bytes, on every path."""
+    import chunked_kv_cache_gb300 as sr
+    dev = device()
+    kv, d, page, n_pages = 32, 128, 64, 10240          # 5.4 GB of keys, as much of values
+    k_pages = torch.empty(n_pages, page, kv, d, dtype=torch.bfloat16, device=dev)
+    v_pages = torch.empty_like(k_pages)
+    table = torch.tensor([[n_pages - 1, 0, n_pages - 7], [n_pages - 2, n_pages - 3, 5]], dtype=torch.int32, device=dev)
+    c = sr.PagedCache(kv, kv, d, page_tokens=page, n_pages=n_pages, max_seqs=2, max_pages=3, device=dev,
+                      buffers=dict(k_pages=k_pages, v_pages=v_pages, block_table=table))
+    o = OraclePagedCache(kv, kv, d, 2, 192)
+    g = torch.Generator(device=dev).manual_seed(3)
+    k, v = (torch.randn(300, kv, d, device=dev, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(2, kv, d, device=dev, generator=g).to(torch.bfloat16)
+    c.append(k, v, counts=[180, 120])
+    o.append([0, 1], [180, 120], f64(k), f64(v))
+    out = f64(c.attention(q, mass_decay=1.0))
+    ref, _, wv = o.attention([0, 1], f64(q), 1.0)
+    assert np.all(np.abs(out - ref) <= E * np.abs(ref) + (E + 1e-4) * wv)
+    o.mass = f64(c.token_mass)
+    c.evict(100, 2, 30)
+    o.evict([0, 1], 100, 2, 30)
+    assert c.seq_len.tolist() == [100, 100] and c.error_status() == 0
+    for s in range(2):
+        t = torch.arange(100, device=dev)
+        rows = table[s].long()[t // page], t % page
+        assert np.array_equal(f64(k_pages[rows]), o.k[s, :100]) and np.array_equal(f64(v_pages[rows]), o.v[s, :100])
+
+
+def test_sequences_that_share_pages():
+    """Reading shared pages is fine; weights and eviction need room for every token once, and say so."""
+    import chunked_kv_cache_gb300 as sr
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 1, 64, 16, 1, 64, seed=17, spare=0)
+    p.append([0], [1024])
+    n = 8
+    table = torch.from_numpy(np.repeat(p.table, n, 0).astype(np.int32)).to(p.dev)
+    i32 = dict(dtype=torch.int32, device=p.dev)
+    shared = sr.PagedCache(4, 1, 64, page_tokens=16, n_pages=64, max_seqs=n, max_pages=64, device=p.dev,
+                           buffers=dict(k_pages=p.cache.k_pages, v_pages=p.cache.v_pages, block_table=table,
+                                        seq_len=torch.full((n,), 1024, **i32), seq_pos=torch.full((n,), 1024, **i32),
+                                        token_pos=torch.arange(1024, **i32).repeat(n, 1)))
+    q = p.randn(n, 4, 64)
+    want = torch.cat([p.cache.attention(q[i:i + 1]) for i in range(n)])
+    got = shared.attention(q)
+    assert (got.double() - want.double()).abs().max() <= 4 * E * want.double().abs().max()
+    assert shared.error_status() == 0
+    got = shared.attention(q, mass_decay=1.0)
+    assert int(shared.err_word.item()) == N.SR_DEVERR_WORKSPACE and shared.error_status() == N.SR_ERR_STATE
+    assert (got.double() - want.double()).abs().max() <= 4 * E * want.double().abs().max()
+    shared.err_word.zero_()
+    shared.token_mass.uniform_()
+    shared.evict(512)
+    assert int(shared.err_word.item()) == N.SR_DEVERR_WORKSPACE
+    shared.err_word.zero_()
+    shared.seq_len.fill_(100)                  # the counters are whole again
+    o = shared.attention(q, mass_decay=1.0)
+    assert shared.error_status() == 0 and torch.isfinite(o.float()).all()
+
+
+def test_two_caches_read_the_same_pages_at_once():
+    import chunked_kv_cache_gb300 as sr
+    p = Pair(8, 2, 128, 64, 4, 40, seed=18)
+    p.append([0, 1, 2, 3], [2500, 700, 64, 1999])
+    q = p.randn(4, 8, 128)
+    want = p.cache.attention(q)
+    bufs = {k: getattr(p.cache, k) for k in ("k_pages", "v_pages", "block_table", "seq_len", "seq_pos", "token_pos")}
+    others = [sr.PagedCache(8, 2, 128, page_tokens=64, n_pages=p.cache.n_pages, max_seqs=4, max_pages=40, mass=False,
+                            buffers=bufs, device=p.dev) for _ in range(2)]
+    streams = [torch.cuda.Stream(p.dev) for _ in others]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(others[i].attention(q))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for both in outs for o in both)
+
+
+def test_lengths_the_caller_spoilt_stay_in_bounds():
+    """Lengths outside [0, cap] are read as the nearest end; an append to them is refused."""
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 2, 64, 16, 3, 4, seed=19)
+    p.append([0, 1, 2], [64, 64, 10])
+    p.cache.seq_len[0] = 1 << 30
+    p.cache.seq_len[2] = -5
+    p.ora.length[2] = 0
+    p.attend([0, 1, 2], decay=1.0)
+    k = p.randn(2, 2, 64)
+    p.cache.append(k, k, seqs=[0, 2])
+    assert int(p.cache.err_word.item()) == N.SR_DEVERR_CACHE_FULL
+    assert p.cache.seq_len.tolist() == [1 << 30, 64, -5]
+    p.cache.seq_len[1] = 20
+    p.cache.seq_pos[1] = 2 ** 31 - 2
+    p.cache.err_word.zero_()
+    p.cache.append(k, k, seqs=[1], counts=[2])               # positions would pass 2^31 - 1
+    assert int(p.cache.err_word.item()) == N.SR_DEVERR_CACHE_FULL and int(p.cache.seq_len[1]) == 20
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_infinities_and_nan_of_live_tokens_are_not_hidden(e4m3):
+    p = Pair(4, 2, 64, 16, 3, 4, e4m3, seed=20)
+    k, v = p.randn(120, 2, 64), p.randn(120, 2, 64)
+    k[5, 0, 3] = float("nan")                                 # sequence 0, head 0
+    v[45, 1, 7] = float("nan")                                # sequence 1, head 1, one output column
+    p.cache.append(k, v, counts=[40, 40, 40])
+    p.ora.append([0, 1, 2], [40, 40, 40], f64(k), f64(v))
+    o, lse = p.cache.attention(p.randn(3, 4, 64), lse=True)
+    o, lse = f64(o), f64(lse)
+    assert np.isnan(o[0, :2]).all() and np.isnan(lse[0, :2]).all() and np.isfinite(o[0, 2:]).all()
+    assert np.isnan(o[1, 2:, 7]).all() and np.isnan(o[1]).sum() == 2 and np.isfinite(lse[1]).all()
+    assert np.isfinite(o[2]).all()
+
+
+def test_a_scale_that_underflows():
+    p = Pair(4, 2, 64, 16, 2, 4, True, seed=21, scale=1e-38)
+    p.append([0, 1], [37, 64])
+    q = p.randn(2, 4, 64, s=1e-30)
+    o = f64(p.cache.attention(q))
+    for i in range(2):
+        want = np.repeat(p.ora.v[i, : p.ora.length[i]].mean(0), 2, 0)
+        assert np.abs(o[i] - want).max() <= 2 * E * np.abs(p.ora.v[i]).max()
+
+
 def test_refusals():
     import chunked_kv_cache_gb300 as sr
     from chunked_kv_cache_gb300 import _native as N
