@@ -197,23 +197,25 @@ sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const int32_t*
   sr_status st = take_seqs(c, seqs, n, p.id);
   if (st != SR_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16)) return SR_ERR_ALIGN;
-  p.rows_per_cta = sr::paged_append_rows_per_cta(c->cfg.n_kv_heads, c->cfg.head_dim);
   int64_t rows = 0, ctas = 0;
   for (int i = 0; i < n; ++i) {
     const int32_t count = n_tokens ? n_tokens[i] : 1;
     if (count < 0) return SR_ERR_INVALID_ARG;
     p.row0[i] = static_cast<int32_t>(rows);
-    p.cta0[i] = static_cast<int32_t>(ctas);
     rows += count;
-    ctas += (static_cast<int64_t>(count) + p.rows_per_cta - 1) / p.rows_per_cta;
     if (rows > (int64_t(1) << 28)) return SR_ERR_INVALID_ARG;
   }
   p.row0[n] = static_cast<int32_t>(rows);
-  p.cta0[n] = static_cast<int32_t>(ctas);
   st = on_device(c);
   if (st != SR_OK) return st;
   if (rows == 0) return SR_OK;
   if (!k || !v) return SR_ERR_INVALID_ARG;
+  p.rows_per_cta = sr::paged_append_rows_per_cta(c->cfg.n_kv_heads, c->cfg.head_dim, rows);
+  for (int i = 0; i < n; ++i) {
+    p.cta0[i] = static_cast<int32_t>(ctas);
+    ctas += (static_cast<int64_t>(p.row0[i + 1]) - p.row0[i] + p.rows_per_cta - 1) / p.rows_per_cta;
+  }
+  p.cta0[n] = static_cast<int32_t>(ctas);
   p.c = c->view;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
