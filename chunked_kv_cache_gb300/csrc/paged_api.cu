@@ -56,6 +56,7 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   l.move_cap = with_mass ? static_cast<int64_t>(c.n_pages) * c.page_tokens / 2 + sr::kMaxPagedSeqs : 0;
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
+  l.items = take(seqs * c.n_kv_heads * sizeof(int2));
   l.unit0 = take(sr::kMaxPagedSeqs * sizeof(int64_t));
   l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.n_heads / c.n_kv_heads, c.head_dim) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
@@ -239,6 +240,7 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  p.items = ws_at<int2>(c, c->layout.items);
   p.unit0 = ws_at<int64_t>(c, c->layout.unit0);
   p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
   p.group_arrivals = p.arrivals + sr::kMaxPagedCtas;

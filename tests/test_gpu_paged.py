@@ -158,6 +158,20 @@ def test_one_long_sequence_is_split_and_joined(heads, kv, d, length, e4m3):
     p.ok()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,kv,d", [(4, 1, 128), (8, 1, 64), (16, 1, 64), (6, 3, 64)])
+def test_one_long_sequence_among_many_short_ones(heads, kv, d, e4m3):
+    """The long one is cut into far more parts than the batch's size lets expect."""
+    n, long = 48, 20011
+    p = Pair(heads, kv, d, 64, n, -(-long // 64), e4m3, seed=22)
+    counts = [s % 4 for s in range(n)]
+    counts[17] = long
+    p.append(list(range(n)), counts)
+    p.attend(list(range(n)), decay=1.0)
+    p.attend(list(range(n)), decay=0.5)
+    p.ok()
+
+
 def test_many_sequences_of_unequal_length():
     n = 256
     p = Pair(8, 2, 64, 16, n, 20, seed=6)
