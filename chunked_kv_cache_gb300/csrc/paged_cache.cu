@@ -82,24 +82,28 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
   if (!bad) {
     const int32_t r0 = (static_cast<int32_t>(blockIdx.x) - p.cta0[i]) * p.rows_per_cta;
     const int32_t rows = min(p.rows_per_cta, count - r0);
-    const int vph = c.head_dim / 8;             // vectors per head
-    const int vpr = c.n_kv * vph;               // vectors per row
+    const int vpr = c.n_kv * c.head_dim / 8;    // vectors per row
     const uint4* ksrc = reinterpret_cast<const uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
     const uint4* vsrc = reinterpret_cast<const uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
-    auto put = [&](int x, const uint4& kx, const uint4& vx) {
-      const int r = x / vpr, col = x - r * vpr;
-      const int64_t at = paged_row(table, len + r0 + r, c.page_tokens, c.n_pages) * vpr + col;
+    const int head_shift = c.head_dim == 128 ? 4 : 3;
+    auto put = [&](int r, int col, const uint4& kx, const uint4& vx) {
+      const int32_t t = len + r0 + r;
+      const int32_t pg = page_of_group(t >> 4, c.magic);
+      const int64_t at = (static_cast<int64_t>(table[pg]) * c.page_tokens + (t - pg * c.page_tokens)) * vpr + col;
       if constexpr (TYPE == SR_PAGE_BF16) {
         static_cast<uint4*>(c.k_pages)[at] = kx;
         static_cast<uint4*>(c.v_pages)[at] = vx;
       } else {
-        const int head = col / vph;
+        const int head = col >> head_shift;
         const float ki = c.kv_exp ? exp2f(-static_cast<float>(c.kv_exp[head])) : 1.f;
         const float vi = c.kv_exp ? exp2f(-static_cast<float>(c.kv_exp[c.n_kv + head])) : 1.f;
         static_cast<uint2*>(c.k_pages)[at] = to_e4m3(kx, ki);
         static_cast<uint2*>(c.v_pages)[at] = to_e4m3(vx, vi);
       }
     };
+    // row and vector of it, advanced by the block's size without a division
+    const int step_r = kAppendThreads / vpr, step_c = kAppendThreads - step_r * vpr;
+    int r = static_cast<int>(threadIdx.x) / vpr, col = static_cast<int>(threadIdx.x) - r * vpr;
     for (int x0 = threadIdx.x; x0 < rows * vpr; x0 += kAppendUnroll * kAppendThreads) {
       uint4 kx[kAppendUnroll], vx[kAppendUnroll];
 #pragma unroll
@@ -109,8 +113,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
           vx[u] = __ldcs(vsrc + x0 + u * kAppendThreads);
         }
 #pragma unroll
-      for (int u = 0; u < kAppendUnroll; ++u)
-        if (x0 + u * kAppendThreads < rows * vpr) put(x0 + u * kAppendThreads, kx[u], vx[u]);
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        if (x0 + u * kAppendThreads < rows * vpr) put(r, col, kx[u], vx[u]);
+        r += step_r;
+        col += step_c;
+        if (col >= vpr) {
+          col -= vpr;
+          ++r;
+        }
+      }
     }
     const int64_t t0 = static_cast<int64_t>(seq) * c.cap + len + r0;
     for (int r = threadIdx.x; r < rows; r += kAppendThreads) {
