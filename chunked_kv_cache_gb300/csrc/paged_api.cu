@@ -160,7 +160,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
-  if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type);
+  if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type, v.group);
   if (e == cudaSuccess) e = sr::paged_evict_prepare();
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);

@@ -17,22 +17,33 @@
 // so that results do not depend on timing. More than kJoin parts are joined in two
 // levels (kJoin neighbours first), so that no CTA reads many of them by itself.
 //
+// Many rows of many parts are joined by a launch of their own (the rule stands at the launch).
+//
 // Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
 // copies its tokens' keys and values into its own three shared-memory stages
 // (cp.async, 16-byte chunks, rows past the length filled with zeros) and computes on
 // the oldest stage, with no barrier but its own. The copies run ahead across items,
-// so that the stream does not pause where one item ends. Scores are the matrix product of the
-// group's query heads (16 rows, the unused ones zero) with 16 keys at a time; the
-// accumulators' layout is the left operand's of the product with the values, so weights
-// never leave registers. Warp-level products fit here: the rows that a tcgen05 tile
-// would need (128) are not there, and the tensor pipe has room to spare.
+// so that the stream does not pause where one item ends.
 //
-// Precision. Scores, softmax statistics and sums are fp32. bf16 pages: the weights
-// are rounded to bf16 (relative 2^-9 each, unbiased) for their product with the
-// values. e4m3 pages: keys and values become fp16 exactly, the weights are scaled by
-// 2^10 and rounded to fp16, and a query row is scaled by a power of two to a largest
-// element in [1, 2), which leaves fp16's ten fraction bits more than bf16's seven over
-// 2^24 of range.
+// The products are transposed: scores = keys (16 rows) x queries (8 columns), sums =
+// values^T (16 dims) x weights (8 columns), so that a group of up to 8 query heads wastes
+// nothing that 16 rows of queries would (e4m3: 97 us with queries as rows, 94 us so). The
+// weights turn from the one product's result into the other's operand by an 8x8
+// transposition between registers and never leave them. Warp-level products fit here: the
+// rows that a tcgen05 tile would need (128) are not there, and the tensor pipe is idle for
+// more than half of the time. The merge of the four warps' sums uses the stages just read.
+//
+// What bounds it: the stream, at 6.4 - 6.9 TB/s once it runs, and about 9 us per call before and after it (lengths, the first
+// copies, merge, join); with e4m3 pages the instructions' latency too, since a scheduler has two
+// warps. 8 sessions of 2072 .. 11432 tokens with 40 heads of 128: 150 us for 963 MB; one of
+// 131071, 8 heads: 88 us for 537 MB; 32 of 4001 .. 32768, e4m3: 149 us for 935 MB.
+//
+// Precision. Scores, softmax statistics and sums are fp32. bf16 pages: the weights are
+// rounded to bf16 (by 2^-8 of themselves at most, to either side) for their product with
+// the values. e4m3 pages: keys and values become fp16 exactly, the weights are scaled by
+// 2^10 and rounded to fp16, and a head's query is scaled by a power of two to a largest
+// element in [1, 2), so that fp16's ten fraction bits hold bf16's seven exactly over 2^14 of
+// range and to 2^-24 of the largest element below that.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -49,7 +60,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = SR_MAX_PAGED_GROUP;   // query rows of an item's matrix product
+// Two CTAs of three stages per warp fill an SM's shared memory with 128 KB of copies in flight; three
+// CTAs of two stages have 96 KB and were slower (one sequence of 131071 tokens: 87 us, 100 us) or no faster.
+constexpr int kCtasPerSm = 2;
+constexpr int kStages = 3;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D, int TYPE>
@@ -60,14 +74,11 @@ struct Geo {
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   static constexpr int kStageBytes = 8192;
-  // CTAs per SM, and stages per warp that fit them: head dim 64 leaves registers for a third CTA, which
-  // its shorter rows need (more tokens, so more arithmetic, per byte): 64 sequences of 8192 tokens, 8
-  // heads, e4m3: 110 us with two CTAs of three stages, 99 us with three of two; bf16, 4096: 94 us, 93 us.
-  static constexpr int kCtas = D == 64 ? 3 : 2;
-  static constexpr int kStages = D == 64 ? 2 : 3;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
-  static constexpr int kMergeRow = D + 8;          // a row's floats, padded off the other rows' banks
-  static constexpr int kMergeFloats = (kWarps - 1) * 8 * kMergeRow;
+  // A warp's 8 rows of D sums while the warps merge, in its free stage: rows four floats apart in
+  // banks beyond a multiple of 32, so that stores and loads spread over all of them.
+  static constexpr int kMergeRow = D + 4;
+  static_assert(8 * kMergeRow * 4 <= kStageBytes, "the merge does not fit a stage");
 };
 
 // Shared-memory position of 16-byte chunk c of row r, permuted so that eight rows'
@@ -102,6 +113,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// transposes an 8x8 matrix of 16-bit elements spread over the warp
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
 template <int TYPE>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -135,7 +152,7 @@ __device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
 struct SharedHead {
   int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
-  float ml[kWarps][kRows][2];           // each warp's maximum and sum, while warps merge
+  float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
 };
 
@@ -268,12 +285,11 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
   }
 }
 
-template <int D, int TYPE, bool MASS>
-__global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+template <int D, int TYPE, int NT, bool MASS>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using G = Geo<D, TYPE>;
   extern __shared__ __align__(128) uint8_t smem[];
-  SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea + G::kMergeFloats * 4);
-  float* merge = reinterpret_cast<float*>(smem + G::kStageArea);
+  SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea);
   grid_dep_launch_dependents();
   grid_dep_wait();
   const PagedView& c = p.c;
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kern
   if (left <= 0) return;    // nothing but the units before an item
   Cursor load = comp;
   int64_t left_load = left;
-  const uint32_t stage0 = smem_u32(smem) + warp * G::kStages * G::kStageBytes;
+  const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
   const int64_t row_pitch = static_cast<int64_t>(c.n_kv) * G::kRowBytes;
 
@@ -412,29 +428,30 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kern
     copy_commit();
   };
 #pragma unroll
-  for (int s = 0; s < G::kStages - 1; ++s) issue(s);
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
 
   // ---- the items of this stretch, one after the other
   int stage = 0;
   const int j4 = lane % 4, r8 = lane / 4;
-  // The group's query rows as left operands. Those of the next item are fetched before
-  // the current one's results are merged, so that their latency hides behind that.
-  uint32_t qa[D / 16][4];
+  // The group's queries as right operands, [head tile][16 dims]. Those of the next item are
+  // fetched before the current one's results are merged, so that their latency hides behind that.
+  uint32_t qb[NT][D / 16][2];
   auto fetch_q = [&](int i, int h) {
     const __nv_bfloat16* qp = p.q + (static_cast<int64_t>(i) * c.n_heads + (h * S + sub) * group) * D;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = r8 + 8 * half;
+    for (int t = 0; t < NT; ++t) {
+      const int r = 8 * t + r8;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         if constexpr (TYPE == SR_PAGE_BF16) {
 #pragma unroll
           for (int x = 0; x < 2; ++x)
-            qa[kk][half + 2 * x] = r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
+            qb[t][kk][x] = r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
         } else {
+          // the order of the dims in which a 16-byte row of keys arrives: four neighbours per lane
           const uint2 raw = r < group ? *reinterpret_cast<const uint2*>(qp + r * D + kk * 16 + 4 * j4) : make_uint2(0u, 0u);
-          qa[kk][half] = raw.x;
-          qa[kk][half + 2] = raw.y;
+          qb[t][kk][0] = raw.x;
+          qb[t][kk][1] = raw.y;
         }
       }
     }
@@ -445,284 +462,301 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kern
     const int32_t first_tile = comp.tile, tiles = comp.tiles;
     const int32_t end_tile = static_cast<int32_t>(min(static_cast<int64_t>(tiles), first_tile + left));
     const int32_t len = comp.len;
-    // e4m3: rows scaled to a largest element in [1, 2), in fp16
-    float xs[2];                                      // log2-scaled scores = product * xs, rows r8 and r8 + 8
-    xs[0] = xs[1] = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f);
-    if constexpr (TYPE != SR_PAGE_BF16) {
-      auto pair = [](uint32_t x) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&x)); };
+    const int64_t item_u = sh.cum[item_i] + static_cast<int64_t>(comp.h) * (tiles + kItemCost) + kItemCost;   // its first tile
+    // log2-scaled scores = product * xs, of this lane's heads 8 t + 2 j4 and the next
+    float xs[NT][2];
+    {
+      const float scale = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float top = 0.f;
+      for (int t = 0; t < NT; ++t) {
+        float x = scale;
+        if constexpr (TYPE != SR_PAGE_BF16) {
+          // queries to fp16, scaled by a power of two to a largest element in [1, 2)
+          auto pair = [](uint32_t y) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&y)); };
+          float top = 0.f;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const float2 a = pair(qa[kk][half]), b = pair(qa[kk][half + 2]);
-          top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const float2 a = pair(qb[t][kk][0]), b = pair(qb[t][kk][1]);
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
+          }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
+          const float down = ldexpf(1.f, -e);
+          x *= ldexpf(1.f, e);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const float2 a = pair(qb[t][kk][0]), b = pair(qb[t][kk][1]);
+            qb[t][kk][0] = pack_half2(a.x * down, a.y * down);
+            qb[t][kk][1] = pack_half2(b.x * down, b.y * down);
+          }
         }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
-        const float down = ldexpf(1.f, -e);
-        xs[half] *= ldexpf(1.f, e);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const float2 a = pair(qa[kk][half]), b = pair(qa[kk][half + 2]);
-          qa[kk][half] = pack_half2(a.x * down, a.y * down);
-          qa[kk][half + 2] = pack_half2(b.x * down, b.y * down);
-        }
+        // a scale so small that it underflows: the scores are zero as well as with this one, and masked ones stay -inf
+        x = fmaxf(x, 0x1p-126f);
+        xs[t][0] = __shfl_sync(0xffffffffu, x, 8 * j4);       // lanes of head 2 j4, then of the next
+        xs[t][1] = __shfl_sync(0xffffffffu, x, 8 * j4 + 4);
       }
     }
-    // a scale so small that it underflows: the scores are zero as well as with this one, and masked ones stay -inf
-    xs[0] = fmaxf(xs[0], 0x1p-126f);
-    xs[1] = fmaxf(xs[1], 0x1p-126f);
-    const int64_t item_u = sh.cum[item_i] + static_cast<int64_t>(comp.h) * (tiles + kItemCost) + kItemCost;   // its first tile
-    float o[D / 8][4];
-#pragma unroll
-    for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[k][x] = 0.f;
-    // m: the running maximum less kLift (fp16 weights then reach 2^10), the reference of the
-    // exponentials; l: this lane's share of their sum. Of rows r8 and r8 + 8.
+    // o: [head tile][16 dims]: rows are dims, columns heads. m: the running maximum less kLift (fp16
+    // weights then reach 2^10), the reference of the exponentials; l: this lane's share of their sum.
     constexpr float kLift = TYPE == SR_PAGE_BF16 ? 0.f : 10.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NT][D / 16][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[t][k][x] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
 
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
-      issue((stage + G::kStages - 1) % G::kStages);
-      copy_wait<G::kStages - 1>();
+      issue((stage + kStages - 1) % kStages);
+      copy_wait<kStages - 1>();
       __syncwarp();
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
       const int32_t tok = tile * G::CT + warp * G::KT;
-      uint32_t live[G::kGroups], any = 0;
+      int32_t live[G::kGroups], any = 0;
 #pragma unroll
       for (int g = 0; g < G::kGroups; ++g) {
-        live[g] = (bad >> (stage * G::kGroups + g)) & 1u ? 0u : static_cast<uint32_t>(min(max(len - tok - g * 16, 0), 16));
+        live[g] = (bad >> (stage * G::kGroups + g)) & 1u ? 0 : min(max(len - tok - g * 16, 0), 16);
         any += live[g];
       }
+      // where this lane's scores go for the second launch: [head][tokens of the tile]
+      [[maybe_unused]] float* score = nullptr;
+      if constexpr (MASS)
+        if ((item_u + tile) * S + sub < p.score_tiles)
+          score = p.scores + (((item_u + tile) * S + sub) * group + 2 * j4) * G::CT + warp * G::KT + r8;
       if (any) {
-        float s[G::KT / 8][4];
-#pragma unroll
-        for (int k = 0; k < G::KT / 8; ++k)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) s[k][x] = 0.f;
-        // scores: matrices of 8 keys x 16 bytes; lane -> (key, chunk) of the four that one load brings
+        // scores: rows are keys, columns heads
+        float s[G::kGroups][NT][4];
 #pragma unroll
         for (int g = 0; g < G::kGroups; ++g) {
-          const int kr = g * 16 + (lane % 8) + 8 * (lane / 16), kc = (lane / 8) % 2;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[g][t][x] = 0.f;
+          // lane -> (key, chunk) of the four matrices of 8 keys x 16 bytes that one load brings
+          const int kr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), kc = lane / 16;
           if constexpr (TYPE == SR_PAGE_BF16) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              uint32_t b[4];
-              ldsm4(b, ks + chunk_at<G::kChunks>(kr, 2 * kk + kc));
-              mma16816<TYPE>(s[2 * g], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
-              mma16816<TYPE>(s[2 * g + 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
+              uint32_t a[4];
+              ldsm4(a, ks + chunk_at<G::kChunks>(kr, 2 * kk + kc));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816<TYPE>(s[g][t], a[0], a[1], a[2], a[3], qb[t][kk][0], qb[t][kk][1]);
             }
           } else {
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk += 2) {
-              uint32_t b[4];
-              ldsm4(b, ks + chunk_at<G::kChunks>(kr, kk + kc));
+              uint32_t a[4];
+              ldsm4(a, ks + chunk_at<G::kChunks>(kr, kk + kc));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                mma16816<TYPE>(s[2 * g], qa[kk + x][0], qa[kk + x][1], qa[kk + x][2], qa[kk + x][3], half2_of_e4m3(b[x]),
-                               half2_of_e4m3(b[x] >> 16));
-                mma16816<TYPE>(s[2 * g + 1], qa[kk + x][0], qa[kk + x][1], qa[kk + x][2], qa[kk + x][3],
-                               half2_of_e4m3(b[2 + x]), half2_of_e4m3(b[2 + x] >> 16));
+                const uint32_t lo0 = half2_of_e4m3(a[2 * x]), lo1 = half2_of_e4m3(a[2 * x + 1]);
+                const uint32_t hi0 = half2_of_e4m3(a[2 * x] >> 16), hi1 = half2_of_e4m3(a[2 * x + 1] >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816<TYPE>(s[g][t], lo0, lo1, hi0, hi1, qb[t][kk + x][0], qb[t][kk + x][1]);
               }
             }
           }
         }
         if (any != 16 * G::kGroups) {                 // keys past the length, or without a page
 #pragma unroll
-          for (int k = 0; k < G::KT / 8; ++k)
+          for (int g = 0; g < G::kGroups; ++g)
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if ((k % 2) * 8 + 2 * j4 + (x & 1) >= live[k / 2]) s[k][x] = -INFINITY;
-        }
-        float top[2] = {-INFINITY, -INFINITY};
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int k = 0; k < G::KT / 8; ++k) {
-          top[0] = fmax3(top[0], s[k][0], s[k][1]);
-          top[1] = fmax3(top[1], s[k][2], s[k][3]);
+              for (int x = 0; x < 4; ++x)
+                if (r8 + 8 * (x / 2) >= live[g]) s[g][t][x] = -INFINITY;
         }
+        bool raise = false;
+        float top[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float y = fmaxf(s[0][t][x], s[0][t][x + 2]);
+#pragma unroll
+            for (int g = 1; g < G::kGroups; ++g) y = fmax3(y, s[g][t][x], s[g][t][x + 2]);
+#pragma unroll
+            for (int k = 4; k < 32; k *= 2) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, k));
+            top[t][x] = y * xs[t][x] - kLift;      // xs > 0
+            raise |= top[t][x] > m[t][x];
+          }
         if constexpr (MASS) {
-          // the scaled scores, for the weights that the second launch forms
-          if ((item_u + tile) * S + sub < p.score_tiles) {
+          if (score) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int r = r8 + 8 * half;
-              if (r < group) {
-                float* dst = p.scores + (((item_u + tile) * S + sub) * group + r) * G::CT + warp * G::KT + 2 * j4;
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int k = 0; k < G::KT / 8; ++k)
-                  *reinterpret_cast<float2*>(dst + k * 8) = make_float2(s[k][2 * half] * xs[half], s[k][2 * half + 1] * xs[half]);
-              }
+              for (int x = 0; x < 4; ++x)
+                if (8 * t + 2 * j4 + x % 2 < group)
+#pragma unroll
+                  for (int g = 0; g < G::kGroups; ++g)
+                    score[(8 * t + x % 2) * G::CT + g * 16 + 8 * (x / 2)] = s[g][t][x] * xs[t][x % 2];
+          }
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float f[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float m1 = fmaxf(m[t][x], top[t][x]);
+              f[x] = m[t][x] == -INFINITY ? 0.f : ex2_approx(m[t][x] - m1);
+              m[t][x] = m1;
+              l[t][x] *= f[x];
             }
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[t][k][x] *= f[x % 2];
           }
         }
+        uint32_t w[G::kGroups][NT][2];                // the weights as right operands
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 1));
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xffffffffu, top[half], 2));
-          top[half] = top[half] * xs[half] - kLift;      // xs > 0
-        }
-        if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
-          float f[2];
+        for (int t = 0; t < NT; ++t) {
+          const float n0 = m[t][0] == -INFINITY ? 0.f : -m[t][0], n1 = m[t][1] == -INFINITY ? 0.f : -m[t][1];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float m1 = fmaxf(m[half], top[half]);
-            f[half] = m[half] == -INFINITY ? 0.f : ex2_approx(m[half] - m1);
-            m[half] = m1;
-            l[half] *= f[half];
+          for (int g = 0; g < G::kGroups; ++g) {
+            float e[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e[x] = ex2_approx(fmaf(s[g][t][x], xs[t][x % 2], x % 2 ? n1 : n0));
+              l[t][x % 2] += e[x];
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              w[g][t][x] = transpose8x8(TYPE == SR_PAGE_BF16 ? pack_bf16x2(e[2 * x], e[2 * x + 1])
+                                                             : pack_half2(e[2 * x], e[2 * x + 1]));
           }
-#pragma unroll
-          for (int k = 0; k < D / 8; ++k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) o[k][x] *= f[x / 2];
         }
-        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
-#pragma unroll
-        for (int k = 0; k < G::KT / 8; ++k)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            s[k][x] = ex2_approx(fmaf(s[k][x], xs[x / 2], x < 2 ? -m0 : -m1));
-            l[x / 2] += s[k][x];
-          }
 #pragma unroll
         for (int g = 0; g < G::kGroups; ++g) {
-          uint32_t a[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float lo = s[2 * g + x / 2][2 * (x % 2)], hi = s[2 * g + x / 2][2 * (x % 2) + 1];
-            a[x] = TYPE == SR_PAGE_BF16 ? pack_bf16x2(lo, hi) : pack_half2(lo, hi);
-          }
-          const int vr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
           if constexpr (TYPE == SR_PAGE_BF16) {
+            const int vr = g * 16 + (lane % 8) + 8 * (lane / 16), vc = (lane / 8) % 2;
 #pragma unroll
-            for (int k = 0; k < D / 8; k += 2) {
-              uint32_t b[4];
-              ldsm4t(b, vs + chunk_at<G::kChunks>(vr, k + vc));
-              mma16816<TYPE>(o[k], a[0], a[1], a[2], a[3], b[0], b[1]);
-              mma16816<TYPE>(o[k + 1], a[0], a[1], a[2], a[3], b[2], b[3]);
+            for (int k = 0; k < D / 16; ++k) {
+              uint32_t a[4];
+              ldsm4t(a, vs + chunk_at<G::kChunks>(vr, 2 * k + vc));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816<TYPE>(o[t][k], a[0], a[1], a[2], a[3], w[g][t][0], w[g][t][1]);
             }
           } else {
-            // a transposed 16-bit element is two neighbouring head dims of one key: the even ones
-            // form one operand, the odd ones the next
+            // a transposed 16-bit element is two neighbouring dims of one key: rows 0-7 of the
+            // product are the even dims, rows 8-15 the odd ones
+            const int vr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
 #pragma unroll
-            for (int k = 0; k < D / 8; k += 4) {
-              uint32_t b[4];
-              ldsm4t(b, vs + chunk_at<G::kChunks>(vr, k / 2 + vc));
-#pragma unroll
-              for (int x = 0; x < 4; ++x) b[x] = __byte_perm(b[x], 0, 0x3120);
+            for (int k = 0; k < D / 16; k += 2) {
+              uint32_t a[4];
+              ldsm4t(a, vs + chunk_at<G::kChunks>(vr, k + vc));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                mma16816<TYPE>(o[k + 2 * x], a[0], a[1], a[2], a[3], half2_of_e4m3(b[2 * x]), half2_of_e4m3(b[2 * x + 1]));
-                mma16816<TYPE>(o[k + 2 * x + 1], a[0], a[1], a[2], a[3], half2_of_e4m3(b[2 * x] >> 16),
-                               half2_of_e4m3(b[2 * x + 1] >> 16));
+                const uint32_t y0 = __byte_perm(a[2 * x], 0, 0x3120), y1 = __byte_perm(a[2 * x + 1], 0, 0x3120);
+                const uint32_t a0 = half2_of_e4m3(y0), a1 = half2_of_e4m3(y0 >> 16);
+                const uint32_t a2 = half2_of_e4m3(y1), a3 = half2_of_e4m3(y1 >> 16);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma16816<TYPE>(o[t][k + x], a0, a1, a2, a3, w[g][t][0], w[g][t][1]);
               }
             }
           }
         }
       } else if constexpr (MASS) {
         // no token here, or none with a page: weights of zero
-        if ((item_u + tile) * S + sub < p.score_tiles) {
+        if (score) {
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if (r8 + 8 * half < group) {
-              float* dst = p.scores + (((item_u + tile) * S + sub) * group + r8 + 8 * half) * G::CT + warp * G::KT + 2 * j4;
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int k = 0; k < G::KT / 8; ++k) *reinterpret_cast<float2*>(dst + k * 8) = make_float2(-INFINITY, -INFINITY);
-            }
+            for (int x = 0; x < 4; ++x)
+              if (8 * t + 2 * j4 + x % 2 < group)
+#pragma unroll
+                for (int g = 0; g < G::kGroups; ++g) score[(8 * t + x % 2) * G::CT + g * 16 + 8 * (x / 2)] = -INFINITY;
         }
       }
       __syncwarp();
-      stage = (stage + 1) % G::kStages;
+      stage = (stage + 1) % kStages;
       cursor_next<G::CT>(comp, sh, n_kv, left);
     }
     if (left > 0) fetch_q(comp.i, comp.h);
 
-    // ---- merge the four warps' results; warp 0 writes them
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);
-    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 2);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], 1);
-    l[1] += __shfl_xor_sync(0xffffffffu, l[1], 2);
-    if (j4 == 0) {
-      sh.ml[warp][r8][0] = m[0];
-      sh.ml[warp][r8][1] = l[0];
-      sh.ml[warp][r8 + 8][0] = m[1];
-      sh.ml[warp][r8 + 8][1] = l[1];
-    }
-    __syncthreads();
+    // ---- merge the four warps' results: each puts its sums into the stage that it has just
+    // read, which the next copy fills, then all threads add them up and write
     const bool whole = first_tile == 0 && end_tile == tiles;
     float* part = part_at<D>(p, blockIdx.x, first_tile == 0 ? 1 : 0);
+    const int free_stage = (stage + kStages - 1) % kStages;
     const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[c.n_kv + item_h])) : 1.f;
-    float mine[2], top[2], sum[2];
+    constexpr int kQuads = D / 4;                 // of a row
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int r = r8 + 8 * half;
-      top[half] = sh.ml[0][r][0];
+    for (int t = 0; t < NT; ++t) {
+      if (8 * t >= group) break;
+      float* mine = reinterpret_cast<float*>(smem + (warp * kStages + free_stage) * G::kStageBytes);
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) top[half] = fmaxf(top[half], sh.ml[w][r][0]);
-      sum[half] = 0.f;
+      for (int x = 0; x < 2; ++x) {
+        float y = l[t][x];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = sh.ml[w][r][0];
-        sum[half] = fmaf(mw == -INFINITY ? 0.f : ex2_approx(mw - top[half]), sh.ml[w][r][1], sum[half]);
-      }
-      mine[half] = m[half] == -INFINITY ? 0.f : ex2_approx(m[half] - top[half]);
-    }
-    if constexpr (TYPE != SR_PAGE_BF16) {
-      // (even dims, odd dims) back to neighbours: o[k] holds dims 16 b + 4 j4 + {0, 1}, o[k + 1] + {2, 3}
-#pragma unroll
-      for (int k = 0; k < D / 8; k += 2)
-#pragma unroll
-        for (int x = 0; x < 4; x += 2) {
-          const float y = o[k][x + 1];
-          o[k][x + 1] = o[k + 1][x];
-          o[k + 1][x] = y;
+        for (int k = 4; k < 32; k *= 2) y += __shfl_xor_sync(0xffffffffu, y, k);
+        if (r8 == 0) {
+          sh.ml[warp][2 * j4 + x][0] = m[t][x];
+          sh.ml[warp][2 * j4 + x][1] = y;
         }
-    }
-    auto col = [&](int k) { return TYPE == SR_PAGE_BF16 ? 8 * k + 2 * j4 : 8 * (k & ~1) + 4 * j4 + 2 * (k & 1); };
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half * 8 >= group) break;
-      if (half == 1) __syncthreads();         // warp 0 has read the first eight rows
-      if (warp > 0) {
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k)
-          *reinterpret_cast<float2*>(merge + ((warp - 1) * 8 + r8) * G::kMergeRow + col(k)) =
-              make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
       }
-      __syncthreads();
-      const int r = r8 + 8 * half;
-      if (warp == 0 && r < group) {
-        const int64_t out = static_cast<int64_t>(item_i) * c.n_heads + item_h * group + r;
-        const float scale = whole ? (sum[half] == 0.f ? 0.f : vscale / sum[half]) : vscale;
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          float2 y = make_float2(o[k][2 * half] * mine[half], o[k][2 * half + 1] * mine[half]);
+      for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-          for (int w = 0; w < kWarps - 1; ++w) {
-            const float2 z = *reinterpret_cast<const float2*>(merge + (w * 8 + r8) * G::kMergeRow + col(k));
-            y.x += z.x;
-            y.y += z.y;
+        for (int x = 0; x < 2; ++x) {
+          float* row = mine + (2 * j4 + x) * G::kMergeRow + 16 * k;
+          if constexpr (TYPE == SR_PAGE_BF16) {
+            row[r8] = o[t][k][x];
+            row[r8 + 8] = o[t][k][x + 2];
+          } else {
+            *reinterpret_cast<float2*>(row + 2 * r8) = make_float2(o[t][k][x], o[t][k][x + 2]);
           }
-          y.x *= scale;
-          y.y *= scale;
-          if (whole)
-            *reinterpret_cast<uint32_t*>(p.o + out * D + col(k)) = pack_bf16x2(y.x, y.y);
-          else
-            *reinterpret_cast<float2*>(part + r * D + col(k)) = y;
         }
-        if (j4 == 0) {
-          if (whole) {
-            const float lse2 = sum[half] == 0.f ? -INFINITY : top[half] + log2f(sum[half]);
+      __syncthreads();
+#pragma unroll 1
+      for (int y = threadIdx.x; y < 8 * kQuads; y += kThreads) {
+        const int r = y / kQuads, quad = y - r * kQuads, row = 8 * t + r;
+        if (row >= group) break;
+        float top = sh.ml[0][r][0];
+#pragma unroll
+        for (int v = 1; v < kWarps; ++v) top = fmaxf(top, sh.ml[v][r][0]);
+        float sum = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          const float mv = sh.ml[v][r][0];
+          const float f = mv == -INFINITY ? 0.f : ex2_approx(mv - top);
+          sum = fmaf(f, sh.ml[v][r][1], sum);
+          const float4 z = *reinterpret_cast<const float4*>(smem + (v * kStages + free_stage) * G::kStageBytes +
+                                                            (r * G::kMergeRow + 4 * quad) * 4);
+          a.x = fmaf(f, z.x, a.x);
+          a.y = fmaf(f, z.y, a.y);
+          a.z = fmaf(f, z.z, a.z);
+          a.w = fmaf(f, z.w, a.w);
+        }
+        const float scale = whole ? (sum == 0.f ? 0.f : vscale / sum) : vscale;
+        a.x *= scale;
+        a.y *= scale;
+        a.z *= scale;
+        a.w *= scale;
+        if (whole) {
+          const int64_t out = static_cast<int64_t>(item_i) * c.n_heads + item_h * group + row;
+          *reinterpret_cast<uint2*>(p.o + out * D + 4 * quad) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+          if (quad == 0) {
+            const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
             if (p.lse) p.lse[out] = lse2 * kLn2;
             if (MASS) p.lse2[out] = lse2;
-          } else {
-            part[group * D + 2 * r] = top[half];
-            part[group * D + 2 * r + 1] = sum[half];
+          }
+        } else {
+          *reinterpret_cast<float4*>(part + row * D + 4 * quad) = a;
+          if (quad == 0) {
+            part[group * D + 2 * row] = top;
+            part[group * D + 2 * row + 1] = sum;
           }
         }
       }
+      __syncthreads();   // the stages may be filled again
     }
     if (whole) {
       if (p.items && threadIdx.x == 0) p.items[item_i * c.n_kv + item_h] = make_int2(0, 1);
@@ -736,14 +770,11 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtas) paged_attn_kern
       const int c0 = owner(item_u);
       const int n_parts = owner(item_u + tiles - 1) - c0 + 1;
       const int64_t out0 = static_cast<int64_t>(item_i) * c.n_heads + item_h * group;
-      auto arrive = [&](int32_t* ctr, int need) -> bool {   // warp 0 wrote; true for the whole CTA in the last one
-        if (warp == 0) {
-          __syncwarp();         // the lanes' stores come before lane 0's release
-          if (lane == 0) {
-            const bool all = add_acq_rel(ctr, 1) == need - 1;
-            if (all) *ctr = 0;
-            sh.last = all;
-          }
+      auto arrive = [&](int32_t* ctr, int need) -> bool {   // behind a barrier; true for the whole CTA in the last one
+        if (threadIdx.x == 0) {
+          const bool all = add_acq_rel(ctr, 1) == need - 1;
+          if (all) *ctr = 0;
+          sh.last = all;
         }
         __syncthreads();
         const bool all = sh.last;
@@ -931,23 +962,34 @@ __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_c
 }
 
 template <int D, int TYPE>
-constexpr int kSmem = Geo<D, TYPE>::kStageArea + Geo<D, TYPE>::kMergeFloats * 4 + static_cast<int>(sizeof(SharedHead));
+constexpr int kSmem = Geo<D, TYPE>::kStageArea + static_cast<int>(sizeof(SharedHead));
 
-template <int D, int TYPE>
+template <int D, int TYPE, int NT>
 cudaError_t prepare() {
-  static_assert(Geo<D, TYPE>::kCtas * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "the CTAs of an SM do not fit");
-  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, false>,
+  static_assert(kCtasPerSm * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "the CTAs of an SM do not fit");
+  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, NT, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, TYPE>);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSmem<D, TYPE>);
 }
 
-template <int D, int TYPE, bool MASS>
-cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
+template <int D, int TYPE, int NT, bool MASS>
+cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   using G = Geo<D, TYPE>;
-  const unsigned grid = static_cast<unsigned>(std::min(G::kCtas * sm_count(), kMaxPagedCtas) / p.spread * p.spread);
-  cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, MASS>, grid, kThreads, kSmem<D, TYPE>, st, p);
+  PagedAttnParams p = p0;
+  p.spread = kSpread;
+  while (p.c.n_kv % p.spread) p.spread /= 2;
+  const int ctas = std::min(kCtasPerSm * sm_count(), kMaxPagedCtas) / p.spread * p.spread;
+  // Who joins: the last CTA to arrive (its four warps take rows in turn, sixteen parts at a time, about 1.6 us
+  // a turn), or a launch of its own (about 2 us of the GPU and as much of the host, more CTAs than it can use
+  // in large batches). One sequence of 4096 tokens, 4 query heads per key head (39 parts): 12.6 us and 9.0 us;
+  // 4 of 5000, 16 heads: 28.8 us and 10.5 us; 1 of 16 tokens: 4.1 us and 5.1 us; 256 of 16: 19 us and 29 us.
+  const int parts = std::min(ctas / (p.b.n * p.c.n_kv) + 1, p.c.cap / G::CT + 1);
+  const int turns = (p.c.group + 3) / 4 * ((parts + kJoinBatch - 1) / kJoinBatch);
+  if (turns <= 2 + p.b.n * p.c.n_heads / 2048) p.items = nullptr;
+  cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, NT, MASS>, static_cast<unsigned>(ctas), kThreads,
+                                   kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess) return e;
   if (p.items) {
     e = launch_dependent(paged_join_kernel<D>, static_cast<unsigned>(p.b.n) * p.c.n_heads, kJoinWarps * 32, 0, st, p);
@@ -960,7 +1002,14 @@ cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
 
 template <int D, int TYPE>
 cudaError_t launch(const PagedAttnParams& p, cudaStream_t st) {
-  return p.mass_decay >= 0.f ? launch<D, TYPE, true>(p, st) : launch<D, TYPE, false>(p, st);
+  const bool mass = p.mass_decay >= 0.f;
+  if (p.c.group <= 8) return mass ? launch<D, TYPE, 1, true>(p, st) : launch<D, TYPE, 1, false>(p, st);
+  return mass ? launch<D, TYPE, 2, true>(p, st) : launch<D, TYPE, 2, false>(p, st);
+}
+
+template <int D, int TYPE>
+cudaError_t prepare(int group) {
+  return group <= 8 ? prepare<D, TYPE, 1>() : prepare<D, TYPE, 2>();
 }
 
 }  // namespace
@@ -971,28 +1020,17 @@ int paged_tile_tokens(int head_dim, int page_type) {
   return page_type == SR_PAGE_BF16 ? Geo<64, SR_PAGE_BF16>::CT : Geo<64, SR_PAGE_E4M3>::CT;
 }
 
-cudaError_t paged_attn_prepare(int head_dim, int page_type) {
-  if (head_dim == 128) return page_type == SR_PAGE_BF16 ? prepare<128, SR_PAGE_BF16>() : prepare<128, SR_PAGE_E4M3>();
-  return page_type == SR_PAGE_BF16 ? prepare<64, SR_PAGE_BF16>() : prepare<64, SR_PAGE_E4M3>();
+cudaError_t paged_attn_prepare(int head_dim, int page_type, int group) {
+  if (head_dim == 128)
+    return page_type == SR_PAGE_BF16 ? prepare<128, SR_PAGE_BF16>(group) : prepare<128, SR_PAGE_E4M3>(group);
+  return page_type == SR_PAGE_BF16 ? prepare<64, SR_PAGE_BF16>(group) : prepare<64, SR_PAGE_E4M3>(group);
 }
 
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens) {
   return (pool_tokens / tile_tokens + static_cast<int64_t>(n_seqs) * (1 + kItemCost)) * n_kv;
 }
 
-cudaError_t launch_paged_attention(const PagedAttnParams& p0, cudaStream_t st) {
-  PagedAttnParams p = p0;
-  p.spread = kSpread;
-  while (p.c.n_kv % p.spread) p.spread /= 2;
-  // Who joins: the last CTA to arrive (its four warps take rows in turn, sixteen parts at a time, about 1.6 us
-  // a turn), or a launch of its own (about 2 us of the GPU and as much of the host, more CTAs than it can use
-  // in large batches). One sequence of 4096 tokens, 4 query heads per key head (39 parts): 12.6 us and 9.0 us;
-  // 4 of 5000, 16 heads: 28.8 us and 10.5 us; 1 of 16 tokens: 4.1 us and 5.1 us; 256 of 16: 19 us and 29 us.
-  const int ctas = std::min((p.c.head_dim == 64 ? Geo<64, SR_PAGE_BF16>::kCtas : Geo<128, SR_PAGE_BF16>::kCtas) * sm_count(),
-                            kMaxPagedCtas);
-  const int parts = std::min(ctas / (p.b.n * p.c.n_kv) + 1, p.c.cap / paged_tile_tokens(p.c.head_dim, p.c.page_type) + 1);
-  const int turns = (p.c.group + 3) / 4 * ((parts + kJoinBatch - 1) / kJoinBatch);
-  if (turns <= 2 + p.b.n * p.c.n_heads / 2048) p.items = nullptr;
+cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st) {
   if (p.c.head_dim == 128)
     return p.c.page_type == SR_PAGE_BF16 ? launch<128, SR_PAGE_BF16>(p, st) : launch<128, SR_PAGE_E4M3>(p, st);
   return p.c.page_type == SR_PAGE_BF16 ? launch<64, SR_PAGE_BF16>(p, st) : launch<64, SR_PAGE_E4M3>(p, st);

@@ -118,7 +118,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
 cudaError_t paged_evict_prepare();
-cudaError_t paged_attn_prepare(int head_dim, int page_type);
+cudaError_t paged_attn_prepare(int head_dim, int page_type, int group);
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int group, int head_dim);                   // floats of one partial result
 int paged_append_rows_per_cta(int n_kv, int head_dim, int64_t rows);
