@@ -529,39 +529,54 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         if ((item_u + tile) * S + sub < p.score_tiles)
           score = p.scores + (((item_u + tile) * S + sub) * group + 2 * j4) * G::CT + warp * G::KT + r8;
       if (any) {
-        // scores: rows are keys, columns heads
-        float s[G::kGroups][NT][4];
+        // scores: rows are keys, columns heads. Two accumulators each, so that no product waits for the
+        // one before it; groups inside steps for the same reason.
+        float s[G::kGroups][NT][4], s2[G::kGroups][NT][4];
 #pragma unroll
-        for (int g = 0; g < G::kGroups; ++g) {
+        for (int g = 0; g < G::kGroups; ++g)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) s[g][t][x] = 0.f;
-          // lane -> (key, chunk) of the four matrices of 8 keys x 16 bytes that one load brings
-          const int kr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), kc = lane / 16;
-          if constexpr (TYPE == SR_PAGE_BF16) {
+            for (int x = 0; x < 4; ++x) s[g][t][x] = s2[g][t][x] = 0.f;
+        // lane -> (key, chunk) of the four matrices of 8 keys x 16 bytes that one load brings
+        const int kr = (lane % 8) + 8 * ((lane / 8) % 2), kc = lane / 16;
+        if constexpr (TYPE == SR_PAGE_BF16) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              uint32_t a[4];
-              ldsm4(a, ks + chunk_at<G::kChunks>(kr, 2 * kk + kc));
+          for (int kk = 0; kk < D / 16; kk += 2)
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16816<TYPE>(s[g][t], a[0], a[1], a[2], a[3], qb[t][kk][0], qb[t][kk][1]);
+            for (int g = 0; g < G::kGroups; ++g) {
+              uint32_t a[4], b[4];
+              ldsm4(a, ks + chunk_at<G::kChunks>(g * 16 + kr, 2 * kk + kc));
+              ldsm4(b, ks + chunk_at<G::kChunks>(g * 16 + kr, 2 * kk + 2 + kc));
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                mma16816<TYPE>(s[g][t], a[0], a[1], a[2], a[3], qb[t][kk][0], qb[t][kk][1]);
+                mma16816<TYPE>(s2[g][t], b[0], b[1], b[2], b[3], qb[t][kk + 1][0], qb[t][kk + 1][1]);
+              }
             }
-          } else {
+        } else {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk += 2) {
+          for (int kk = 0; kk < D / 16; kk += 2)
+#pragma unroll
+            for (int g = 0; g < G::kGroups; ++g) {
               uint32_t a[4];
-              ldsm4(a, ks + chunk_at<G::kChunks>(kr, kk + kc));
+              ldsm4(a, ks + chunk_at<G::kChunks>(g * 16 + kr, kk + kc));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint32_t lo0 = half2_of_e4m3(a[2 * x]), lo1 = half2_of_e4m3(a[2 * x + 1]);
                 const uint32_t hi0 = half2_of_e4m3(a[2 * x] >> 16), hi1 = half2_of_e4m3(a[2 * x + 1] >> 16);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma16816<TYPE>(s[g][t], lo0, lo1, hi0, hi1, qb[t][kk + x][0], qb[t][kk + x][1]);
+                for (int t = 0; t < NT; ++t)
+                  mma16816<TYPE>(x ? s2[g][t] : s[g][t], lo0, lo1, hi0, hi1, qb[t][kk + x][0], qb[t][kk + x][1]);
               }
             }
-          }
         }
+#pragma unroll
+        for (int g = 0; g < G::kGroups; ++g)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[g][t][x] += s2[g][t][x];
         if (any != 16 * G::kGroups) {                 // keys past the length, or without a page
 #pragma unroll
           for (int g = 0; g < G::kGroups; ++g)
@@ -632,25 +647,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
                                                              : pack_half2(e[2 * x], e[2 * x + 1]));
           }
         }
+        if constexpr (TYPE == SR_PAGE_BF16) {
+          const int vr = (lane % 8) + 8 * (lane / 16), vc = (lane / 8) % 2;
 #pragma unroll
-        for (int g = 0; g < G::kGroups; ++g) {
-          if constexpr (TYPE == SR_PAGE_BF16) {
-            const int vr = g * 16 + (lane % 8) + 8 * (lane / 16), vc = (lane / 8) % 2;
+          for (int g = 0; g < G::kGroups; ++g)
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               uint32_t a[4];
-              ldsm4t(a, vs + chunk_at<G::kChunks>(vr, 2 * k + vc));
+              ldsm4t(a, vs + chunk_at<G::kChunks>(g * 16 + vr, 2 * k + vc));
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma16816<TYPE>(o[t][k], a[0], a[1], a[2], a[3], w[g][t][0], w[g][t][1]);
             }
-          } else {
-            // a transposed 16-bit element is two neighbouring dims of one key: rows 0-7 of the
-            // product are the even dims, rows 8-15 the odd ones
-            const int vr = g * 16 + (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
+        } else {
+          // a transposed 16-bit element is two neighbouring dims of one key: rows 0-7 of the
+          // product are the even dims, rows 8-15 the odd ones
+          const int vr = (lane % 8) + 8 * ((lane / 8) % 2), vc = lane / 16;
+#pragma unroll
+          for (int g = 0; g < G::kGroups; ++g)
 #pragma unroll
             for (int k = 0; k < D / 16; k += 2) {
               uint32_t a[4];
-              ldsm4t(a, vs + chunk_at<G::kChunks>(vr, k + vc));
+              ldsm4t(a, vs + chunk_at<G::kChunks>(g * 16 + vr, k + vc));
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 const uint32_t y0 = __byte_perm(a[2 * x], 0, 0x3120), y1 = __byte_perm(a[2 * x + 1], 0, 0x3120);
@@ -660,7 +677,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
                 for (int t = 0; t < NT; ++t) mma16816<TYPE>(o[t][k + x], a0, a1, a2, a3, w[g][t][0], w[g][t][1]);
               }
             }
-          }
         }
       } else if constexpr (MASS) {
         // no token here, or none with a page: weights of zero
