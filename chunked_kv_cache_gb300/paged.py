@@ -88,6 +88,7 @@ class PagedCache:
                                 self.seq_len.data_ptr(), self.seq_pos.data_ptr(), self.token_pos.data_ptr(),
                                 self.token_mass.data_ptr() if mass else None, self.kv_exp.data_ptr(),
                                 self.err_word.data_ptr(), self.workspace.data_ptr())
+        self._lib = N.lib()
         with torch.cuda.device(dev):
             self.handle = N.sr_paged_init(self.cfg, bufs, self._stream())
 
@@ -96,10 +97,15 @@ class PagedCache:
         # the handle itself: a Stream object costs two microseconds, as much as a launch
         return torch._C._cuda_getCurrentRawStream(self.device.index)
 
-    def _ids(self, seqs: Sequence[int] | None):
-        if seqs is None:
-            return None
-        return (ctypes.c_int32 * len(seqs))(*seqs)
+    @staticmethod
+    def _ids(seqs: Sequence[int] | None):
+        return None if seqs is None else (ctypes.c_int32 * len(seqs))(*seqs)
+
+    # The calls below go to the library without N's wrappers: a call is a few microseconds on the host.
+    @staticmethod
+    def _done(status: int, what: str) -> None:
+        if status != N.SR_OK:
+            raise N.SrError(status, what)
 
     def _check(self, name: str, t: torch.Tensor, shape, dtype=_BF16) -> None:
         if not isinstance(t, torch.Tensor):
@@ -141,7 +147,7 @@ class PagedCache:
     def reset(self, seqs: Sequence[int] | None = None) -> None:
         """Empty sequences (None: the first SR_MAX_PAGED_SEQS rows, or all where there are fewer)."""
         n = min(self.max_seqs, N.SR_MAX_PAGED_SEQS) if seqs is None else len(seqs)
-        N.sr_paged_reset(self.handle, self._ids(seqs), n, self._stream())
+        self._done(self._lib.sr_paged_reset(self.handle, self._ids(seqs), n, self._stream()), "sr_paged_reset")
 
     def append(self, k: torch.Tensor, v: torch.Tensor, seqs: Sequence[int] | None = None,
                counts: Sequence[int] | None = None) -> None:
@@ -153,11 +159,11 @@ class PagedCache:
         n = len(seqs) if seqs is not None else len(counts) if counts is not None else rows
         if counts is not None and len(counts) != n:
             raise ValueError(f"{len(counts)} counts for {n} sequences")
-        if (n if counts is None else sum(counts)) != rows:
-            raise ValueError(f"k and v have {rows} rows, the sequences take "
-                             f"{n if counts is None else sum(counts)}")
-        N.sr_paged_append(self.handle, self._ids(seqs), self._ids(counts), n, k.data_ptr(), v.data_ptr(),
-                          self._stream())
+        takes = n if counts is None else sum(counts)
+        if takes != rows:
+            raise ValueError(f"k and v have {rows} rows, the sequences take {takes}")
+        self._done(self._lib.sr_paged_append(self.handle, self._ids(seqs), self._ids(counts), n, k.data_ptr(),
+                                             v.data_ptr(), self._stream()), "sr_paged_append")
 
     def attention(self, q: torch.Tensor, seqs: Sequence[int] | None = None, out: torch.Tensor | None = None,
                   lse: torch.Tensor | bool | None = None, mass_decay: float | None = None):
@@ -181,9 +187,10 @@ class PagedCache:
             self._check("lse", lse, (n, self.n_heads), torch.float32)
         else:
             lse = None
-        N.sr_paged_attention(self.handle, self._ids(seqs), n, q.data_ptr(), out.data_ptr(),
-                             0 if lse is None else lse.data_ptr(), -1.0 if mass_decay is None else mass_decay,
-                             self._stream())
+        self._done(self._lib.sr_paged_attention(self.handle, self._ids(seqs), n, q.data_ptr(), out.data_ptr(),
+                                                None if lse is None else lse.data_ptr(),
+                                                -1.0 if mass_decay is None else mass_decay, self._stream()),
+                   "sr_paged_attention")
         return out if lse is None else (out, lse)
 
     def evict(self, budget: int, n_sink: int = 0, n_recent: int = 0, seqs: Sequence[int] | None = None) -> None:
@@ -191,7 +198,8 @@ class PagedCache:
         positions, and the tokens with the largest token_mass (None: the first
         SR_MAX_PAGED_SEQS rows, or all where there are fewer)."""
         n = min(self.max_seqs, N.SR_MAX_PAGED_SEQS) if seqs is None else len(seqs)
-        N.sr_paged_evict(self.handle, self._ids(seqs), n, budget, n_sink, n_recent, self._stream())
+        self._done(self._lib.sr_paged_evict(self.handle, self._ids(seqs), n, budget, n_sink, n_recent, self._stream()),
+                   "sr_paged_evict")
 
     # ---------------------------------------------------------------- state
     def error_status(self) -> int:
