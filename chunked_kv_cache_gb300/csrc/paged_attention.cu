@@ -22,8 +22,8 @@
 // Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
 // copies its tokens' keys and values into its own three shared-memory stages
 // (cp.async, 16-byte chunks, rows past the length filled with zeros) and computes on
-// the oldest stage, with no barrier but its own. The copies run ahead across items,
-// so that the stream does not pause where one item ends.
+// the oldest stage. The copies run ahead across items, so that the stream does not pause
+// where one item ends.
 //
 // The products are transposed: scores = keys (16 rows) x queries (8 columns), sums =
 // values^T (16 dims) x weights (8 columns), so that a group of up to 8 query heads wastes
@@ -33,15 +33,16 @@
 // rows that a tcgen05 tile would need (128) are not there, and the tensor pipe is idle for
 // more than half of the time. The merge of the four warps' sums uses the stages just read.
 //
-// What bounds it: the stream, at 6.4 - 6.9 TB/s once it runs, and about 9 us per call before and after it (lengths, the first
-// copies, merge, join); with e4m3 pages the instructions' latency too, since a scheduler has two
-// warps. 8 sessions of 2072 .. 11432 tokens with 40 heads of 128: 150 us for 963 MB; one of
-// 131071, 8 heads: 88 us for 537 MB; 32 of 4001 .. 32768, e4m3: 149 us for 935 MB.
+// What bounds it: the stream, at 6.5 - 6.9 TB/s once it runs, and about 7 us per call before
+// and after it (lengths, the first copies, merge, join); with e4m3 pages and head dim 64 the
+// arithmetic too, since a scheduler has two warps. 8 sessions of 2072 .. 11432 tokens with 40
+// heads of 128: 148 us for 963 MB; one of 131071, 8 heads: 85 us for 537 MB; 32 of 4001 ..
+// 32768, e4m3: 152 us for 935 MB.
 //
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: the weights are
 // rounded to bf16 (by 2^-8 of themselves at most, to either side) for their product with
 // the values. e4m3 pages: keys and values become fp16 exactly, the weights are scaled by
-// 2^10 and rounded to fp16, and a head's query is scaled by a power of two to a largest
+// 2^6 and rounded to fp16, and a head's query is scaled by a power of two to a largest
 // element in [1, 2), so that fp16's ten fraction bits hold bf16's seven exactly over 2^14 of
 // range and to 2^-24 of the largest element below that.
 #include <cuda_bf16.h>
@@ -73,6 +74,11 @@ struct Geo {
   static constexpr int KT = 4096 / kRowBytes;      // tokens per warp and tile: 4 KB of keys, 4 KB of values
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
+  // Whether the warps take their tiles in step. Nothing in them depends on it, but warps that drift apart
+  // read DRAM in shorter runs: 32 sequences of 4001 .. 32768 tokens, e4m3: 160 us without, 152 us in
+  // step; 8 sessions, bf16: 152 us, 148 us. Rows of 64 bytes have more arithmetic than that gains
+  // (64 sequences of 8192: 95 us, 98 us in step).
+  static constexpr bool kInStep = kRowBytes > 64;
   static constexpr int kStageBytes = 8192;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
   // A warp's 8 rows of D sums while the warps merge, in its free stage: rows four floats apart in
@@ -497,9 +503,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         xs[t][1] = __shfl_sync(0xffffffffu, x, 8 * j4 + 4);
       }
     }
-    // o: [head tile][16 dims]: rows are dims, columns heads. m: the running maximum less kLift (fp16
-    // weights then reach 2^10), the reference of the exponentials; l: this lane's share of their sum.
-    constexpr float kLift = TYPE == SR_PAGE_BF16 ? 0.f : 10.f;
+    // o: [head tile][16 dims]: rows are dims, columns heads. m: the reference of the exponentials, an
+    // earlier maximum less kLift, raised only when a score passes it by 2^kSlack, so that most
+    // tiles need no maximum across lanes; l: this lane's share of the weights' sum. Weights reach
+    // 2^8 (bf16), 2^14 (fp16), and what rounds to fp16's smallest is 2^-30 of the largest or less.
+    constexpr float kLift = TYPE == SR_PAGE_BF16 ? 0.f : 6.f, kSlack = 8.f;
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -514,7 +522,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
       issue((stage + kStages - 1) % kStages);
       copy_wait<kStages - 1>();
-      __syncwarp();
+      if constexpr (G::kInStep)
+        __syncthreads();
+      else
+        __syncwarp();
       const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
       const int32_t tok = tile * G::CT + warp * G::KT;
       int32_t live[G::kGroups], any = 0;
@@ -595,10 +606,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
             float y = fmaxf(s[0][t][x], s[0][t][x + 2]);
 #pragma unroll
             for (int g = 1; g < G::kGroups; ++g) y = fmax3(y, s[g][t][x], s[g][t][x + 2]);
-#pragma unroll
-            for (int k = 4; k < 32; k *= 2) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, k));
-            top[t][x] = y * xs[t][x] - kLift;      // xs > 0
-            raise |= top[t][x] > m[t][x];
+            top[t][x] = y * xs[t][x] - kLift;      // of this lane's keys; xs > 0
+            raise |= top[t][x] > m[t][x] + kSlack;
           }
         if constexpr (MASS) {
           if (score) {
@@ -618,6 +627,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
             float f[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+#pragma unroll
+              for (int k = 4; k < 32; k *= 2) top[t][x] = fmaxf(top[t][x], __shfl_xor_sync(0xffffffffu, top[t][x], k));
               const float m1 = fmaxf(m[t][x], top[t][x]);
               f[x] = m[t][x] == -INFINITY ? 0.f : ex2_approx(m[t][x] - m1);
               m[t][x] = m1;
