@@ -99,7 +99,11 @@ class PagedCache:
 
     @staticmethod
     def _ids(seqs: Sequence[int] | None):
-        return None if seqs is None else (ctypes.c_int32 * len(seqs))(*seqs)
+        if seqs is None:
+            return None
+        if seqs and (min(seqs) < 0 or max(seqs) >= 1 << 31):     # ctypes would cut them to 32 bits
+            raise N.SrError(N.SR_ERR_INVALID_ARG, "sequence or count")
+        return (ctypes.c_int32 * len(seqs))(*seqs)
 
     # The calls below go to the library without N's wrappers: a call is a few microseconds on the host.
     @staticmethod
@@ -197,6 +201,9 @@ class PagedCache:
         """Keep at most `budget` tokens per sequence: positions below n_sink, the last n_recent
         positions, and the tokens with the largest token_mass (None: the first
         SR_MAX_PAGED_SEQS rows, or all where there are fewer)."""
+        if not (0 <= n_sink < 1 << 31 and 0 <= n_recent < 1 << 31 and budget >= 0):
+            raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_evict")
+        budget = min(budget, (1 << 31) - 1)                      # no sequence is longer
         n = min(self.max_seqs, N.SR_MAX_PAGED_SEQS) if seqs is None else len(seqs)
         self._done(self._lib.sr_paged_evict(self.handle, self._ids(seqs), n, budget, n_sink, n_recent, self._stream()),
                    "sr_paged_evict")

@@ -449,7 +449,9 @@ SR_API sr_status sr_layer_commit(sr_session* const* sessions, const sr_window* w
  * Calls of one cache share its workspace: two that overlap on the GPU (two streams, or
  * two captured graphs replayed at once) race on it, as calls of a session do.
  * Caches that share pages need a workspace each and may run at the same time as long as
- * none writes what another reads.
+ * none writes what another reads. Sequences may share pages that are only read: the pages
+ * that new tokens go to, and every page of a sequence that is evicted from, must be its own.
+ * A cache is not thread-safe; distinct caches are independent.
  *
  * Every call takes its sequences as a HOST array seqs[n] of distinct rows of the
  * block table; NULL stands for 0 .. n-1. 1 <= n <= SR_MAX_PAGED_SEQS.

@@ -563,6 +563,68 @@ def test_a_scale_that_underflows():
         assert np.abs(o[i] - want).max() <= 2 * E * np.abs(p.ora.v[i]).max()
 
 
+def test_nothing_is_written_outside_the_buffers():
+    """Every buffer between canary bands, through prompts, single tokens, weights, both joins and evictions."""
+    import chunked_kv_cache_gb300 as sr
+    from chunked_kv_cache_gb300 import _native as N
+    from tests.test_gpu_guards import Guarded
+    dev = device()
+    for heads, kv, d, page, e4m3 in ((8, 2, 64, 16, False), (16, 1, 128, 48, True), (5, 5, 128, 64, False)):
+        n, pages_each = 3, -(-4200 // page)
+        n_pages, cap = n * pages_each, pages_each * page
+        cfg = N.SrPagedConfig(heads, kv, d, page, n_pages, n, pages_each, 1 if e4m3 else 0, 0.0)
+        row = n_pages * page * kv * d * (1 if e4m3 else 2)
+        g = {name: Guarded(size, dev) for name, size in dict(
+            k=row, v=row, table=n * pages_each * 4, length=n * 4, pos=n * 4, tpos=n * cap * 4, mass=n * cap * 4,
+            exp=2 * kv * 4, err=4, ws=N.sr_paged_workspace_bytes(cfg, True), q=n * heads * d * 2, o=n * heads * d * 2,
+            lse=n * heads * 4).items()}
+        for name in ("length", "pos", "exp", "mass"):
+            g[name].inner.zero_()
+        g["table"].view(torch.int32, (n, pages_each)).copy_(
+            torch.randperm(n_pages, device=dev).to(torch.int32).view(n, pages_each))
+        ptr = {name: x.inner.data_ptr() for name, x in g.items()}
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        h = N.sr_paged_init(cfg, N.SrPagedBuffers(ptr["k"], ptr["v"], ptr["table"], ptr["length"], ptr["pos"], ptr["tpos"],
+                                                  ptr["mass"], ptr["exp"], ptr["err"], ptr["ws"]), stream)
+        try:
+            import ctypes
+            for counts in ([4100, 0, 77], [1, 1, 1], [1, 130, 1]):
+                rows = sum(counts)
+                x = torch.randn(rows, kv, d, device=dev).to(torch.bfloat16)
+                N.sr_paged_append(h, None, (ctypes.c_int32 * n)(*counts), n, x.data_ptr(), x.data_ptr(), stream)
+                g["q"].view(torch.bfloat16, (n, heads, d)).normal_()
+                N.sr_paged_attention(h, None, n, ptr["q"], ptr["o"], ptr["lse"], 1.0, stream)
+                N.sr_paged_attention(h, (ctypes.c_int32 * 1)(0), 1, ptr["q"], ptr["o"], ptr["lse"], 0.5, stream)
+            N.sr_paged_evict(h, None, n, 4101, 4, 100, stream)      # one token too many
+            N.sr_paged_evict(h, None, n, 3000, 4, 100, stream)
+            N.sr_paged_evict(h, None, n, 60, 4, 10, stream)
+            N.sr_paged_attention(h, None, n, ptr["q"], ptr["o"], 0, -1.0, stream)
+            torch.cuda.synchronize()
+            assert int(g["err"].view(torch.int32, (1,)).item()) == 0
+            assert g["length"].view(torch.int32, (n,)).tolist() == [60, 60, 60]
+            assert torch.isfinite(g["o"].view(torch.bfloat16, (n, heads, d)).float()).all()
+            assert {name: x.intact() for name, x in g.items()} == {name: True for name in g}
+        finally:
+            N.sr_paged_free(h)
+
+
+def test_numbers_past_32_bits_are_not_cut():
+    import chunked_kv_cache_gb300 as sr
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 2, 64, 16, 2, 4, seed=23)
+    p.append([0, 1], [40, 40])
+    q = p.randn(1, 4, 64)
+    for call in (lambda: p.cache.attention(q, seqs=[1 << 32]), lambda: p.cache.reset([1 << 32]),
+                 lambda: p.cache.evict(10, n_sink=1 << 32), lambda: p.cache.evict(10, n_recent=(1 << 32) + 3),
+                 lambda: p.cache.evict(-((1 << 32) - 5))):
+        with pytest.raises(sr.SrError) as e:
+            call()
+        assert e.value.status == N.SR_ERR_INVALID_ARG
+    p.cache.evict((1 << 32) + 5)                              # above every length: nothing to do
+    p.check_state([0, 1])
+    p.ok()
+
+
 def test_refusals():
     import chunked_kv_cache_gb300 as sr
     from chunked_kv_cache_gb300 import _native as N
