@@ -1,8 +1,10 @@
 """The paged token cache on the GPU against its float64 oracle.
 
 Tolerances, from the arithmetic (u = 2^-24, e = 2^-8 the half step of bf16):
-* an output is rounded to bf16 (e |o|), and each weight is rounded to bf16 before its
-  product with V (e sum w|v|); fp32 scores, exponentials and sums add
+* an output is rounded to bf16 (e |o|). A weight meets V as two bf16 numbers that hold it to
+  2^-16 of itself (bf16 pages), or as fp16, which rounds it by 2^-11 of itself or, below
+  fp16's normal numbers, by 2^-31 of the largest weight (e4m3 pages): W sum w|v| and
+  L 2^-31 max|v|. fp32 scores, exponentials and sums add
   (2 dx + L u + 2^-20) sum w|v|, with dx the error of a scaled score:
   (d + 8) u * scale * max_t sum_i |q_i k_i(t)|, and 2^-22 for the exponential.
 * the log-sum-exp is off by dx + L u + 2^-20 + 4 u |lse|.
@@ -102,7 +104,9 @@ class Pair:
             dot = np.einsum("hgd,thd->hgt", qa, ka).max(2, initial=0.0).reshape(self.heads)
             dx = (self.d + 8) * U * self.ora.scale * dot
             rel = 2 * dx + L * U + 2.0 ** -20
-            bound = E * np.abs(ref[i]) + (E + rel[:, None]) * wv[i] + 1e-30
+            W = 2.0 ** -11 if self.ora.e4m3 else 2.0 ** -16
+            top_v = np.abs(self.ora.v[s, :L]).max(initial=0.0) if visible is None else np.abs(self.ora.v[s, :L][visible[i]]).max(initial=0.0)
+            bound = E * np.abs(ref[i]) + (W + rel[:, None]) * wv[i] + L * 2.0 ** -31 * top_v + 1e-30
             err = np.abs(o[i] - ref[i])
             assert np.all(err <= bound), (s, L, float((err / bound).max()))
             if L == 0 or (visible is not None and not visible[i].any()):
