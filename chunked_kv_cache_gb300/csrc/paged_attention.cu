@@ -36,11 +36,12 @@
 // What bounds it: the stream, at 6.5 - 6.9 TB/s once it runs, and about 7 us per call before
 // and after it (lengths, the first copies, merge, join); with e4m3 pages and head dim 64 the
 // arithmetic too, since a scheduler has two warps. 8 sessions of 2072 .. 11432 tokens with 40
-// heads of 128: 148 us for 963 MB; one of 131071, 8 heads: 85 us for 537 MB; 32 of 4001 ..
-// 32768, e4m3: 152 us for 935 MB.
+// heads of 128: 147 us for 963 MB (6.5 TB/s, 97 % of the copy rate); one of 131071, 8 heads: 85 us for
+// 537 MB (93 %); 32 of 4001 .. 32768, e4m3: 148 us for 935 MB (93 %); 64 of 1 .. 16384: 86 us for
+// 522 MB (89 %); 16 of 1000 .. 8192 with weights: 53 us for 232 MB (64 %).
 //
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: a weight meets the
-// values as two bf16 numbers, itself rounded and what that leaves (2^-16 of it at most is lost):
+// values as two bf16 numbers, itself rounded and what that leaves (2^-15 of it at most is lost):
 // the second product costs under 1 % of the time (85.4 us and 84.8 us for 16 sequences of 8192
 // tokens), and without it outputs were 0.0023 off in the mean instead of 0.0017, of which 0.0017
 // is the rounding of the output itself. e4m3 pages: keys and values become fp16 exactly, the
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     // earlier maximum less kLift, raised only when a score passes it by 2^kSlack, so that most
     // tiles need no maximum across lanes; l: this lane's share of the weights' sum. Weights reach
     // 2^8 (bf16), 2^14 (fp16), and what rounds to fp16's smallest is 2^-30 of the largest or less.
+    constexpr float kLess = 1.f - 0x1p-8f;
     constexpr float kLift = TYPE == SR_PAGE_BF16 ? 0.f : 6.f, kSlack = 8.f;
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -646,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
               for (int x = 0; x < 4; ++x) o[t][k][x] *= f[x % 2];
           }
         }
-        // the weights as right operands; bf16: what their rounding leaves as well
+        // the weights as right operands; bf16: as two numbers, the first rounded from a little less
+        // than the weight, so that the second is positive as well and an infinite value stays infinite
         uint32_t w[G::kGroups][NT][2];
         [[maybe_unused]] uint32_t w_low[G::kGroups][NT][2];
 #pragma unroll
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               if constexpr (TYPE == SR_PAGE_BF16) {
-                const uint32_t hi = pack_bf16x2(e[2 * x], e[2 * x + 1]);
+                const uint32_t hi = pack_bf16x2(e[2 * x] * kLess, e[2 * x + 1] * kLess);
                 w[g][t][x] = transpose8x8(hi);
                 w_low[g][t][x] = transpose8x8(pack_bf16x2(e[2 * x] - __uint_as_float(hi << 16),
                                                           e[2 * x + 1] - __uint_as_float(hi & 0xFFFF0000u)));
@@ -936,7 +939,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
 // The weights: mass(t) <- decay * mass(t) + sum over heads of 2^(x_h(t) - lse2_h).
 // Latency bound (the scores mostly still lie in L2), so few dependent loads: a CTA takes
 // 128 tokens, four per thread in one 16-byte load per head; eight threads share a token's
-// heads, with their loads in flight together, and add up in a fixed order.
+// heads, with their loads in flight together, and add up in a fixed order. It adds 6 us to a
+// call with 73,000 tokens and 40 heads and 6.5 us with 131,000 and 32 (64 tokens per CTA, and
+// half as many CTAs, measured the same); storing the scores costs the first launch 2 .. 4 us.
 constexpr int kMassTokens = 128;
 constexpr int kMassShare = 8;
 constexpr int kMassQuads = kMassTokens / 4;

@@ -523,8 +523,8 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  *   o[i][h] = softmax(scale * q[i][h] . K) V   over the seq_len tokens of seqs[i].
  * q, o: [n][n_heads][head_dim] bf16. lse: optional [n][n_heads] fp32, natural-log sum-exp of
  * the scaled scores. A sequence of length 0 gets o = 0 and lse = -inf. Indices at or past
- * seq_len are never read as values: what the pages hold there does not matter.
- * fp32 scores, softmax and sums; the weights are held to 2^-16 of themselves (bf16 pages) or
+ * seq_len are never read as values: what the pages hold there does not matter. o may be q.
+ * fp32 scores, softmax and sums; the weights are held to 2^-15 of themselves (bf16 pages) or
  * 2^-11 (e4m3 pages) for their product with V.
  * mass_decay >= 0 (finite; needs token_mass): also
  *   token_mass[s][t] = mass_decay * token_mass[s][t] + sum over heads of the token's weight.

@@ -1,8 +1,9 @@
 """The paged token cache on the GPU against its float64 oracle.
 
 Tolerances, from the arithmetic (u = 2^-24, e = 2^-8 the half step of bf16):
-* an output is rounded to bf16 (e |o|). A weight meets V as two bf16 numbers that hold it to
-  2^-16 of itself (bf16 pages), or as fp16, which rounds it by 2^-11 of itself or, below
+* an output is rounded to bf16 (e |o|). A weight meets V as two bf16 numbers, the first
+  rounded from (1 - 2^-8) of it, so that at most 2^-8 + 2^-8 of it is left for the second, whose
+  rounding loses 2^-8 of that: 2^-15 of the weight (bf16 pages); or as fp16, which rounds it by 2^-11 of itself or, below
   fp16's normal numbers, by 2^-31 of the largest weight (e4m3 pages): W sum w|v| and
   L 2^-31 max|v|. fp32 scores, exponentials and sums add
   (2 dx + L u + 2^-20) sum w|v|, with dx the error of a scaled score:
@@ -104,7 +105,7 @@ class Pair:
             dot = np.einsum("hgd,thd->hgt", qa, ka).max(2, initial=0.0).reshape(self.heads)
             dx = (self.d + 8) * U * self.ora.scale * dot
             rel = 2 * dx + L * U + 2.0 ** -20
-            W = 2.0 ** -11 if self.ora.e4m3 else 2.0 ** -16
+            W = 2.0 ** -11 if self.ora.e4m3 else 2.0 ** -15
             top_v = np.abs(self.ora.v[s, :L]).max(initial=0.0) if visible is None else np.abs(self.ora.v[s, :L][visible[i]]).max(initial=0.0)
             bound = E * np.abs(ref[i]) + (W + rel[:, None]) * wv[i] + L * 2.0 ** -31 * top_v + 1e-30
             err = np.abs(o[i] - ref[i])
@@ -555,6 +556,34 @@ def test_infinities_and_nan_of_live_tokens_are_not_hidden(e4m3):
     assert np.isnan(o[0, :2]).all() and np.isnan(lse[0, :2]).all() and np.isfinite(o[0, 2:]).all()
     assert np.isnan(o[1, 2:, 7]).all() and np.isnan(o[1]).sum() == 2 and np.isfinite(lse[1]).all()
     assert np.isfinite(o[2]).all()
+
+
+@pytest.mark.parametrize("length", [1, 40, 2000])
+def test_infinite_values_stay_infinite(length):
+    """softmax weights are positive, so an infinite value of one sign is the output; of both, NaN."""
+    p = Pair(4, 2, 64, 16, 1, 128, seed=22)
+    k, v = p.randn(length, 2, 64), p.randn(length, 2, 64)
+    v[length // 2, 0, 3] = float("inf")
+    v[length - 1, 1, 9] = -float("inf")
+    v[0, 1, 11], v[length - 1, 1, 11] = float("inf"), -float("inf")
+    p.cache.append(k, v, counts=[length])
+    o, lse = p.cache.attention(p.randn(1, 4, 64, s=0.25), lse=True)
+    o = f64(o)[0]
+    assert (o[:2, 3] == np.inf).all() and (o[2:, 9] == -np.inf).all() and np.isfinite(f64(lse)).all()
+    if length > 1:
+        assert np.isnan(o[2:, 11]).all()
+    assert np.isfinite(np.delete(o, [3, 9, 11], 1)).all()
+
+
+@pytest.mark.parametrize("heads,kv,n,length", [(8, 8, 3, 70), (16, 1, 2, 5000), (32, 8, 60, 900)])
+def test_the_output_may_take_the_place_of_the_queries(heads, kv, n, length):
+    p = Pair(heads, kv, 128, 64, n, -(-length // 64), seed=23)
+    p.append(list(range(n)), [length - i for i in range(n)])
+    q = p.randn(n, heads, 128)
+    want, lse = p.cache.attention(q, lse=True, mass_decay=0.0)
+    mass = p.cache.token_mass.clone()
+    same, lse2 = p.cache.attention(q, out=q, lse=True, mass_decay=0.0)
+    assert same is q and torch.equal(q, want) and torch.equal(lse, lse2) and torch.equal(mass, p.cache.token_mass)
 
 
 def test_a_scale_that_underflows():
