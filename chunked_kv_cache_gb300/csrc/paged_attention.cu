@@ -11,13 +11,13 @@
 // tokens; the launch's tiles, item after item, form one line, and every CTA takes an
 // equal stretch of it, whatever the lengths: a batch of unequal sequences and a
 // single long one both occupy the whole GPU, and the lengths, which only the device
-// knows, never reach the host. A CTA that covers an item whole writes its output; of an
-// item cut between CTAs each writes its partial result (fp32 sums, maximum and sum of
-// the softmax), and the last of them to arrive joins the parts in the order of the line,
-// so that results do not depend on timing. More than kJoin parts are joined in two
-// levels (kJoin neighbours first), so that no CTA reads many of them by itself.
-//
-// Many rows of many parts are joined by a launch of their own (the rule stands at the launch).
+// knows, never reach the host. Where items are nearly equal, or small, the stretches end
+// where items end (the rule stands at kWhole). A CTA that covers an item whole writes its
+// output; of an item cut between CTAs each writes its partial result (fp32 sums, maximum and
+// sum of the softmax), and the last of them to arrive joins the parts in the order of the
+// line, so that results do not depend on timing. More than kJoin parts are joined in two
+// levels (kJoin neighbours first), so that no CTA reads many of them by itself. Many rows of
+// many parts are joined by a launch of their own (the rule stands at the launch).
 //
 // Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
 // copies its tokens' keys and values into its own three shared-memory stages
@@ -82,6 +82,17 @@ struct Geo {
   // step; 8 sessions, bf16: 152 us, 148 us. Rows of 64 bytes have more arithmetic than that gains
   // (64 sequences of 8192: 95 us, 98 us in step).
   static constexpr bool kInStep = kRowBytes > 64;
+  // Stretches end where items end (so many whole items each, or an item in so many pieces), where the largest
+  // is not above kWhole / 16 of an even one or kWholeExtra units more: fewer parts to join, and none twice.
+  // The first bound: DRAM serves the CTAs that are left faster (even stretches, whole items: 32 sequences of
+  // 4096 tokens, 1.19 times an even one, 82.9 us, 78.8 us; 32 of 3500 .. 4096, 1.28, 77.5 us, 76.5 us; 32 of
+  // 3000 .. 4096, 1.37, 73.1 us, 74.1 us), but arithmetic does not get faster (64 of 8192, rows of 64 bytes,
+  // 1.19: 92.3 us, 99.0 us). The second: a join costs as much as a few tiles (16 of 256, 3 more: 11.1 us,
+  // 7.3 us; 16 of 512, 6 more: 12.5 us, 10.8 us; 8 of 512, 8 more: 9.2 us, 10.6 us; rows of 64 bytes, 16 of
+  // 100 .. 1000, 5 more: 8.3 us, 8.8 us). Pieces: 16 of 768 in two 15.5 us, 13.4 us, 8 of 2048 in four
+  // 18.8 us, 17.4 us; where the rule tries them in vain the trial costs 0.1 us.
+  static constexpr int kWhole = kInStep ? 21 : 18;
+  static constexpr int kWholeExtra = kInStep ? 6 : 4;
   static constexpr int kStageBytes = 8192;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
   // A warp's 8 rows of D sums while the warps merge, in its free stage: rows four floats apart in
@@ -161,6 +172,7 @@ __device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
 struct SharedHead {
   int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
+  int32_t longest;                      // units of the longest item
   float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
 };
@@ -172,7 +184,7 @@ constexpr int kItemCost = 1;
 // token's row, whole in memory, is read at about one time. Rows of 64 bytes per head need
 // it, because DRAM delivers twice that (8 heads, 64 sequences of 8192 tokens, head dim 64,
 // e4m3: 178 us one by one, 127 us side by side); longer ones gain up to 10 %.
-constexpr int kSpread = 8;
+constexpr int kSpreadLog2 = 3, kSpread = 1 << kSpreadLog2;
 struct Cursor {
   int i, h;            // sequence of the batch, key/value head
   int32_t tile, tiles; // tile of the item, tiles it has
@@ -300,13 +312,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   extern __shared__ __align__(128) uint8_t smem[];
   SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea);
   grid_dep_launch_dependents();
-  grid_dep_wait();
   const PagedView& c = p.c;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n = p.b.n, group = c.group;
+  // this lane's sequences, read from the parameters ahead of the wait (32 addresses of them at a
+  // time are slow: 256 sequences of 16 tokens 18.3 us behind it, 16.9 us so)
+  int32_t id[kMaxPagedSeqs / 32];
+  if (warp == 0) {
+#pragma unroll
+    for (int k = 0; k < kMaxPagedSeqs / 32; ++k) {
+      id[k] = p.b.id[lane * (kMaxPagedSeqs / 32) + k];
+      asm volatile("" : "+r"(id[k]));
+    }
+  }
+  grid_dep_wait();
   // S neighbouring CTAs take the same stretch for S neighbouring key/value heads
-  const int S = p.spread, sub = static_cast<int>(blockIdx.x) % S, me = static_cast<int>(blockIdx.x) / S;
-  const int n_kv = c.n_kv / S;        // heads on the line
+  const int S = p.spread, sub = static_cast<int>(blockIdx.x) & (S - 1), me = static_cast<int>(blockIdx.x) >> p.spread_log2;
+  const int n_kv = c.n_kv >> p.spread_log2;        // heads on the line
 
   // ---- the line of tiles
   if (warp == 0) {
@@ -315,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
     for (int k = 0; k < kMaxPagedSeqs / 32; ++k) {
       const int i = lane * (kMaxPagedSeqs / 32) + k;
-      len[k] = i < n ? min(max(c.seq_len[p.b.id[i]], 0), c.cap) : 0;
+      len[k] = i < n ? min(max(c.seq_len[id[k]], 0), c.cap) : 0;
       mine += seq_units<G::CT>(len[k], n_kv);
     }
     int64_t incl = mine;
@@ -333,6 +355,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
       at += seq_units<G::CT>(len[k], n_kv);
     }
     if (lane == 31) sh.cum[kMaxPagedSeqs] = at;
+    int32_t longest = len[0];
+#pragma unroll
+    for (int k = 1; k < kMaxPagedSeqs / 32; ++k) longest = max(longest, len[k]);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) sh.longest = (longest + G::CT - 1) / G::CT + kItemCost;
   }
   __syncthreads();
   // sequences without a token: nothing to attend to
@@ -348,14 +375,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   const int64_t T = sh.cum[n];
   if (MASS && blockIdx.x == 0)
     for (int i = threadIdx.x; i < n; i += kThreads) p.unit0[i] = sh.cum[i];
-  // CTAs that work: each gets one unit at least, so that all between an item's first and last have a part of it
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x / S), T);
-  if (me >= ctas) return;
-  // equal stretches, the first `rest` one unit longer
-  const int64_t share = div_pos(T, ctas), rest = T - share * ctas;
-  const int64_t u0 = me * share + min(static_cast<int64_t>(me), rest);
+  if (T == 0) return;
+  int64_t u0, left, share = 0, rest = 0;   // first unit and units of the stretch
+  int cut = 0;                             // pieces of each item of the stretch, where all have as many
+  const int64_t bound = max(T * G::kWhole, T * 16 + p.whole_extra);
+  if (sh.longest * p.whole_cost <= bound) {
+    // whole items; left == 0: none but empty ones
+    auto start = [&](int item) {
+      const int i = item / n_kv;
+      return i < n ? sh.cum[i] + (item - i * n_kv) * seq_units<G::CT>(sh.len[i], 1) : T;
+    };
+    u0 = start(me * p.each);
+    left = start((me + 1) * p.each) - u0;
+    if (left == 0) return;
+  } else if (p.pieces > 1 && (sh.longest + 2 * p.pieces) * p.cut_cost <= bound) {
+    // one of `pieces` equal pieces of an item, as far as it has tiles
+    const int item = me / p.pieces, i = item / n_kv;
+    if (i >= n) return;
+    const int32_t tiles = (sh.len[i] + G::CT - 1) / G::CT;
+    cut = min(p.pieces, tiles);
+    const int x = me - item * p.pieces;
+    if (x >= cut) return;
+    const int32_t t0 = x * tiles / cut;
+    u0 = sh.cum[i] + (item - i * n_kv) * static_cast<int64_t>(tiles + kItemCost) + kItemCost + t0;
+    left = (x + 1) * tiles / cut - t0;
+  } else {
+    // CTAs that work: each gets one unit at least, so that all between an item's first and last have a part of it
+    const int64_t ctas = min(static_cast<int64_t>(gridDim.x >> p.spread_log2), T);
+    if (me >= ctas) return;
+    // equal stretches, the first `rest` one unit longer
+    share = div_pos(T, ctas);
+    rest = T - share * ctas;
+    u0 = me * share + min(static_cast<int64_t>(me), rest);
+    left = share + (me < rest ? 1 : 0);
+  }
   Cursor comp;
-  int64_t left = share + (me < rest ? 1 : 0);   // units of the stretch from comp on
   {
     int lo = 0, hi = n - 1;   // the last sequence that starts at or before u0
     while (lo < hi) {
@@ -471,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   };
   fetch_q(comp.i, comp.h);
   while (left > 0) {
-    const int item_i = comp.i, item_h = comp.h * S + sub;
+    const int item_i = comp.i, comp_h = comp.h, item_h = comp_h * S + sub;
     const int32_t first_tile = comp.tile, tiles = comp.tiles;
     const int32_t end_tile = static_cast<int32_t>(min(static_cast<int64_t>(tiles), first_tile + left));
     const int32_t len = comp.len;
@@ -821,8 +875,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         const int64_t longer = rest * (share + 1);
         return static_cast<int>(u < longer ? div_pos(u, share + 1) : rest + div_pos(u - longer, share));
       };
-      const int c0 = owner(item_u);
-      const int n_parts = owner(item_u + tiles - 1) - c0 + 1;
+      const int c0 = cut ? (item_i * n_kv + comp_h) * p.pieces : owner(item_u);
+      const int n_parts = cut ? cut : owner(item_u + tiles - 1) - c0 + 1;
       const int64_t out0 = static_cast<int64_t>(item_i) * c.n_heads + item_h * group;
       auto arrive = [&](int32_t* ctr, int need) -> bool {   // behind a barrier; true for the whole CTA in the last one
         if (threadIdx.x == 0) {
@@ -1035,8 +1089,15 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   using G = Geo<D, TYPE>;
   PagedAttnParams p = p0;
   p.spread = kSpread;
-  while (p.c.n_kv % p.spread) p.spread /= 2;
+  p.spread_log2 = kSpreadLog2;
+  while (p.c.n_kv % p.spread) p.spread /= 2, --p.spread_log2;
   const int ctas = std::min(kCtasPerSm * sm_count(), kMaxPagedCtas) / p.spread * p.spread;
+  const int slots = ctas >> p.spread_log2, items = p.b.n * (p.c.n_kv >> p.spread_log2);
+  p.each = (items + slots - 1) / slots;
+  p.whole_cost = 16ll * p.each * slots;
+  p.pieces = slots / items;
+  p.cut_cost = p.pieces > 1 ? 16ll * slots / p.pieces : 0;
+  p.whole_extra = 16ll * slots * G::kWholeExtra;
   // Who joins: the last CTA to arrive (its four warps take rows in turn, sixteen parts at a time, about 1.6 us
   // a turn), or a launch of its own (about 2 us of the GPU and as much of the host, more CTAs than it can use
   // in large batches). One sequence of 4096 tokens, 4 query heads per key head (39 parts): 12.6 us and 9.0 us;

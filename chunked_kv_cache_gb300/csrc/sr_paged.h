@@ -99,6 +99,13 @@ struct PagedAttnParams {
   float* scores;
   int64_t score_tiles;
   int32_t spread;          // neighbouring key/value heads that neighbouring CTAs take side by side; divides n_kv
+  int32_t spread_log2;
+  // Stretches that end where items end (the rule stands at Geo::kWhole); all in 16ths of a unit, times the stretches
+  int32_t each;            // whole items for each CTA, or
+  int32_t pieces;          // pieces that an item is cut into (below 2: none)
+  int64_t whole_cost;      // 16 * each * stretches
+  int64_t cut_cost;        // 16 * stretches / pieces
+  int64_t whole_extra;     // 16 * kWholeExtra * stretches
   float mass_decay;
   PagedBatch b;
 };

@@ -188,6 +188,31 @@ def test_many_sequences_of_unequal_length():
     p.ok()
 
 
+@pytest.mark.parametrize("e4m3,d", [(False, 128), (True, 128), (False, 64), (True, 64)])
+@pytest.mark.parametrize("heads,kv,lengths", [
+    (32, 8, [512] * 32),                             # one item for each CTA
+    (32, 8, [512] * 20 + [0] * 3 + [1, 500] + [0] * 7),
+    (8, 8, [70] * 100 + [0, 0, 71, 1] * 3),          # several items for each
+    (4, 1, [33] * 256),
+    (3, 3, [40] * 251 + [0] * 5),
+    (8, 2, [2500] * 12),                             # items in equal pieces
+    (8, 2, [2500] * 9 + [0, 1, 130]),                # and some that have fewer tiles than pieces
+    (40, 8, [768, 0, 767, 500, 700, 768] * 2),
+    (5, 1, [6000]), (5, 1, [6000, 5990]), (16, 1, [0, 9000, 0]),
+    (12, 4, [1200, 1, 1199, 64, 0, 1000, 650]),      # neither
+])
+def test_batches_of_nearly_equal_sequences(heads, kv, lengths, e4m3, d):
+    n = len(lengths)
+    p = Pair(heads, kv, d, 64, n, -(-max(lengths) // 64) + 1, e4m3, seed=sum(lengths) % 97)
+    seqs = list(range(n))
+    p.append(seqs, lengths)
+    p.attend(seqs, decay=1.0)
+    p.append(seqs, [1] * n)                          # lengths of one tile more, empty ones that have a token now
+    p.attend(seqs)
+    p.attend(seqs[::-1], decay=0.5)
+    p.ok()
+
+
 def test_large_scores_and_scale():
     """Scores of several hundred: one token holds nearly all weight."""
     p = Pair(4, 2, 128, 32, 3, 8, seed=7, scale=0.7)
