@@ -115,6 +115,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t p
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void store_hinted(float* dst, float x, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(dst), "f"(x), "l"(policy) : "memory");
+}
+// Drops 128 bytes from L2 without writing them to memory: they hold nothing until they are written again.
+__device__ __forceinline__ void discard_line(const void* line) {
+  asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -441,6 +448,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   const int r0 = lane / G::kChunks, ch = lane % G::kChunks;
   const int64_t lane_off = r0 * row_pitch + ch * 16;
   const uint64_t policy = l2_policy_evict_first();
+  [[maybe_unused]] uint64_t keep;      // for the scores
+  if constexpr (MASS) keep = p.drop_scores ? l2_policy_evict_last() : l2_policy_evict_normal();
   int32_t page[G::kGroups];
   auto fetch_pages = [&] {
     const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
                 if (8 * t + 2 * j4 + x % 2 < group)
 #pragma unroll
                   for (int g = 0; g < G::kGroups; ++g)
-                    score[(8 * t + x % 2) * G::CT + g * 16 + 8 * (x / 2)] = s[g][t][x] * xs[t][x % 2];
+                    store_hinted(score + (8 * t + x % 2) * G::CT + g * 16 + 8 * (x / 2), s[g][t][x] * xs[t][x % 2], keep);
           }
         }
         if (__any_sync(0xffffffffu, raise)) {
@@ -995,12 +1004,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
 // 128 tokens, four per thread in one 16-byte load per head; eight threads share a token's
 // heads, with their loads in flight together, and add up in a fixed order. It adds 6 us to a
 // call with 73,000 tokens and 40 heads and 6.5 us with 131,000 and 32 (64 tokens per CTA, and
-// half as many CTAs, measured the same); storing the scores costs the first launch 2 .. 4 us.
+// half as many CTAs, measured the same). The first launch pays for what L2 writes back of the
+// scores meanwhile (8 us for the 17 MB of 32 sequences of 4096 tokens; 1 us if all go to one small
+// place). So in large batches they are stored to leave L2 last and dropped from it once read (DROP):
+// 94.5 us in all without that, 91.2 us with it; 8 of 16384 101.3 us, 98.1 us; 32 of 2048, at
+// kDropScores, 50.5 us, 49.7 us; below, 32 of 512, 19.6 us, 20.4 us.
+constexpr int64_t kDropScores = 1ll << 21;
 constexpr int kMassTokens = 128;
 constexpr int kMassShare = 8;
 constexpr int kMassQuads = kMassTokens / 4;
 constexpr int kMassThreads = kMassQuads * kMassShare;
-template <int CT>
+template <int CT, bool DROP>
 __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_constant__ PagedAttnParams p, int per) {
   __shared__ float4 sums[kMassShare][kMassQuads];
   grid_dep_launch_dependents();
@@ -1052,6 +1066,15 @@ __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_c
     }
     sums[share][quad] = w;
     __syncthreads();
+    if (DROP && t0 + kMassTokens <= len) {         // read by this CTA alone, and read now
+      constexpr int kLines = kMassTokens / 32;     // of a head's scores
+      for (int y = threadIdx.x; y < c.n_heads * kLines; y += kMassThreads) {
+        const int h = y / kLines, kv = h / c.group, g = h - kv * c.group, side = kv >> p.spread_log2;
+        const int32_t first = t0 + (y - h * kLines) * 32;
+        discard_line(p.scores + (unit0 + kItemCost + first / CT) * S * c.group * CT + first % CT + side * pitch +
+                     ((kv - side * S) * c.group + g) * CT);
+      }
+    }
     if (seen) {
       float4 all = sums[0][quad];
 #pragma unroll
@@ -1098,6 +1121,7 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   p.pieces = slots / items;
   p.cut_cost = p.pieces > 1 ? 16ll * slots / p.pieces : 0;
   p.whole_extra = 16ll * slots * G::kWholeExtra;
+  p.drop_scores = static_cast<int64_t>(p.b.n) * p.c.cap * p.c.n_heads >= kDropScores;
   // Who joins: the last CTA to arrive (its four warps take rows in turn, sixteen parts at a time, about 1.6 us
   // a turn), or a launch of its own (about 2 us of the GPU and as much of the host, more CTAs than it can use
   // in large batches). One sequence of 4096 tokens, 4 query heads per key head (39 parts): 12.6 us and 9.0 us;
@@ -1114,7 +1138,8 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   }
   if (!MASS) return e;
   const int per = std::max(1, std::min((p.c.cap + kMassTokens - 1) / kMassTokens, 16 * sm_count() / p.b.n));
-  return launch_dependent(paged_mass_kernel<G::CT>, static_cast<unsigned>(p.b.n) * per, kMassThreads, 0, st, p, per);
+  return launch_dependent(p.drop_scores ? paged_mass_kernel<G::CT, true> : paged_mass_kernel<G::CT, false>,
+                          static_cast<unsigned>(p.b.n) * per, kMassThreads, 0, st, p, per);
 }
 
 template <int D, int TYPE>

@@ -106,6 +106,7 @@ struct PagedAttnParams {
   int64_t whole_cost;      // 16 * each * stretches
   int64_t cut_cost;        // 16 * stretches / pieces
   int64_t whole_extra;     // 16 * kWholeExtra * stretches
+  bool drop_scores;        // the weights' launch drops the scores from L2
   float mass_decay;
   PagedBatch b;
 };

@@ -213,6 +213,25 @@ def test_batches_of_nearly_equal_sequences(heads, kv, lengths, e4m3, d):
     p.ok()
 
 
+@pytest.mark.parametrize("e4m3,d,heads,kv,n,pages", [(False, 128, 8, 8, 16, 256), (False, 64, 16, 1, 40, 52), (True, 128, 5, 1, 48, 144),
+                                                      (True, 64, 12, 4, 64, 44)])
+def test_weights_of_large_batches(e4m3, d, heads, kv, n, pages):
+    """Batches from 2^21 scores on drop them from the cache once read: every later call stores them anew."""
+    cap = 64 * pages
+    assert n * cap * heads >= 1 << 21
+    p = Pair(heads, kv, d, 64, n, pages, e4m3, seed=d + n)
+    lengths = [int(x) for x in p.rng.integers(1, 400, n)]
+    lengths[:4] = [cap - 3, 0, 128, 1000]
+    seqs = list(range(n))
+    p.append(seqs, lengths)
+    p.attend(seqs, decay=1.0)
+    p.attend(seqs[::-1], decay=0.5)
+    p.append(seqs[:4], [1, 1, 1, 129])
+    p.attend(seqs[:n // 2], decay=1.0)
+    p.attend(seqs, decay=0.75)
+    p.ok()
+
+
 def test_large_scores_and_scale():
     """Scores of several hundred: one token holds nearly all weight."""
     p = Pair(4, 2, 128, 32, 3, 8, seed=7, scale=0.7)
