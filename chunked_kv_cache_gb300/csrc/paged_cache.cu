@@ -152,19 +152,23 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // weights' bits, mapped to unsigned integers in the weights' order, are read once into
 // shared memory. A radix select (11, 11 and 10 bits, the CTAs' counts added through
 // distributed shared memory) narrows the keys down to those that share the digits of
-// the last key to go; as soon as these are few they are gathered, one per thread, and the
-// cut is found among them bit by bit, first of the key, then of the index, which settles
-// ties. The result is a cut: a token goes if its key lies below the cut's, or equals it at an
-// index at or behind the cut's. Ordered counts turn that into moves (from, to), and all warps
-// move rows, a warp per token. A move reads at or behind the new length and writes below it,
-// so that no move sees another. Latency bound (barriers, dependent loads) until the moves,
-// which are HBM bound: 512 of 16896 tokens go from each of 16 sequences, 1024 values to a row,
-// in 33 us, where the 70 MB alone would take 10 us. One token of a sequence (the least weight,
-// no digits) goes in 4 us of the GPU from 4 sequences of 157 tokens, 6 us from 32 of 4097.
+// the last key to go; as soon as these are few every CTA gathers them, one per thread, and
+// goes on by itself with digits of the key, then of the index, which settles ties (bit by
+// bit with a count of the block each: twice the time). The result is a cut: a token goes if
+// its key lies below the cut's, or equals it at an index at or behind the cut's. Ordered
+// counts turn that into moves (from, to), and all warps move rows, a warp per token. A
+// move reads at or behind the new length and writes below it, so that no move sees another.
+// Latency bound (barriers, dependent loads, code that runs once) until the moves, which are
+// HBM bound: 512 of 16896 tokens go from each of 16 sequences, 1024 values to a row, in
+// 28 us, where the 70 MB alone would take 10 us. One token of a sequence (the least weight, no
+// digits) goes in 4 us of the GPU from 8 sequences of 1025 tokens, 5 us from 32 of 4097.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
+// Up to here the first CTA of a cluster looks for the one lightest token by itself (8 sequences of 1025 tokens:
+// 6.2 us with an append where the clusters did, 5.9 us so; 16 of 8001: 7.3 us, 8.0 us).
+constexpr int32_t kAlone = 4608;
 constexpr int kCandidates = 512;      // keys gathered to find the cut among them
 constexpr int kKeyLimit = 45056;      // keys a CTA can hold; longer stretches are read again from global memory
 static_assert(kCandidates <= kEvictThreads, "a thread holds one candidate");
@@ -263,7 +267,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   __shared__ uint32_t sums[2][kEvictWarps];
   __shared__ uint32_t found[3];                   // digit, rank in it, its keys
   __shared__ uint2 cut_at;
-  const uint32_t C = cluster_size(), me = cluster_rank();
+  uint32_t C = cluster_size();
+  const uint32_t me = cluster_rank();
   const int i = blockIdx.x / C, tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   for (int x = tid; x < 2 * kBins; x += kEvictThreads) (&sh.hist[0][0])[x] = 0;
   if (tid == 0) sh.n_cand = 0;
@@ -284,6 +289,11 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     done();
     return;
   }
+  const bool one = len - p.budget == 1;           // token too many
+  if (one && len <= kAlone) {
+    if (me != 0) return;
+    C = 1;
+  }
   int32_t* tpos = c.token_pos + static_cast<int64_t>(seq) * c.cap;
   float* mass = c.token_mass + static_cast<int64_t>(seq) * c.cap;
   auto key_of = [&](int32_t q, float m) { return q < p.n_sink || q >= recent0 ? kProtected : weight_key(m); };
@@ -291,26 +301,35 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   const int32_t chunk = static_cast<int32_t>((len + C * kEvictThreads - 1) / (C * kEvictThreads)) * kEvictThreads;
   const int32_t first = min(static_cast<int32_t>(me) * chunk, len), count = min(chunk, len - first);
   const int32_t w0 = min(warp * (chunk / kEvictWarps), count), w1 = min(w0 + chunk / kEvictWarps, count);
-  const bool held = chunk <= key_cap;
-  if (held) {
-#pragma unroll 8
-    for (int32_t x = w0 + lane; x < w1; x += 32) keys[x] = key_of(tpos[first + x], mass[first + x]);
-    __syncwarp();                                 // a warp reads the keys that it wrote
-  }
-  auto key = [&](int32_t x) { return x >= w1 ? kProtected : held ? keys[x] : key_of(tpos[first + x], mass[first + x]); };
-  __syncthreads();
-
+  // f(x, key) for this warp's indices, eight loads of each array in flight, short stretches' as well
+  auto load_keys = [&](auto&& f) {
+    constexpr int kBatch = 8;
+    for (int32_t x0 = w0 + lane; x0 < w1; x0 += 32 * kBatch) {
+      int32_t q[kBatch];
+      float m[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (x0 + 32 * k < w1) {
+          q[k] = tpos[first + x0 + 32 * k];
+          m[k] = mass[first + x0 + 32 * k];
+        }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (x0 + 32 * k < w1) f(x0 + 32 * k, key_of(q[k], m[k]));
+    }
+  };
+  const bool held = !one && chunk <= key_cap;
+  if (held) load_keys([&](int32_t x, uint32_t k) { keys[x] = k; });   // a warp reads the keys that it wrote
   const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
   const int vpr = c.n_kv * c.head_dim * (c.page_type == SR_PAGE_BF16 ? 2 : 1) / 16;
-  if (len - p.budget == 1) {
+  if (one) {
     // ---- one token too many, as in serving token by token: the lightest goes, and the last
     // index's token takes its place
     unsigned long long best = ~0ull;
-    for (int32_t x = w0 + lane; x < w1; x += 32) {
-      const uint32_t k = key(x);
+    load_keys([&](int32_t x, uint32_t k) {
       if (k != kProtected)
         best = min(best, static_cast<unsigned long long>(k) << 32 | static_cast<uint32_t>(~(first + x)));
-    }
+    });
     auto warp_min = [](unsigned long long v) {
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, s));
@@ -358,51 +377,40 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     return;
   }
 
+  auto key = [&](int32_t x) { return x >= w1 ? kProtected : held ? keys[x] : key_of(tpos[first + x], mass[first + x]); };
+  __syncthreads();
+
+
   // ---- the key of rank `rank` (from 1) among those that may go
   uint32_t prefix = 0, rank = 0;
   uint32_t cut_key = 0, cut_index = 0;
   int32_t gone = 0;
   int pass = 0;
-#pragma unroll 1
-  for (;; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
-    const uint32_t digits = pass == 2 ? 1023 : 2047;
-    uint32_t* h = sh.hist[pass & 1];
-    for (int32_t x0 = w0; x0 < w1; x0 += 32) {
-      const uint32_t k = key(x0 + lane);
-      const bool in = k != kProtected && (pass == 0 || k >> above == prefix >> above);
-      const uint32_t act = __ballot_sync(0xffffffffu, in);
-      if (act == 0) continue;
-      const uint32_t digit = k >> shift & digits;
-      // equal weights would queue on one counter: the warp adds them at once
-      const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(act) - 1);
-      if (__all_sync(0xffffffffu, !in || digit == d0)) {
-        if (lane == 0) atomicAdd(&h[d0], __popc(act));
-      } else if (in) {
-        atomicAdd(&h[digit], 1u);
-      }
-    }
-    cluster_sync(C);
-    // every CTA adds all counts, four digits per thread, and finds the same digit
-    uint4 s = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (uint32_t r = 0; r < kMaxCluster; ++r)
-      if (r < C) {
-        const uint4 v = C == 1 ? *reinterpret_cast<const uint4*>(h + tid * 4) : peer_load4(peer_addr(h + tid * 4, r));
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
-      }
+  unsigned long long list_at = 0;
+  // Equal digits queue on one counter (weights share their leading bits): a warp adds those of its first lane
+  // at once. 2 sequences of 105000 tokens, 5000 to go: 40.8 us where it did so only if all were equal, 34.4 us
+  // so, 44.5 us with up to four rounds of it, 46.5 us with the warp's lanes matched among each other.
+  auto tally = [&](uint32_t* h, bool in, uint32_t digit) {
+    const uint32_t act = __ballot_sync(0xffffffffu, in);
+    if (act == 0) return;
+    const uint32_t d0 = __shfl_sync(0xffffffffu, digit, __ffs(act) - 1);
+    const uint32_t same = __ballot_sync(0xffffffffu, in && digit == d0);
+    if (lane == 0) atomicAdd(&h[d0], __popc(same));
+    if (in && digit != d0) atomicAdd(&h[digit], 1u);
+  };
+  // the keys before this thread's four digits, of which it has s; all of them in `total`
+  auto keys_before = [&](const uint4& s, uint32_t& total) {
     const uint32_t mine = s.x + s.y + s.z + s.w;
     const uint32_t incl = warp_incl_scan(mine, lane);
     if (lane == 31) sums[0][warp] = incl;
     __syncthreads();
     const uint32_t ws = lane < kEvictWarps ? sums[0][lane] : 0;
     const uint32_t wi = warp_incl_scan(ws, lane);
-    uint32_t before = incl - mine + __shfl_sync(0xffffffffu, wi - ws, warp);
-    if (pass == 0) {
-      const uint32_t total = __shfl_sync(0xffffffffu, wi, 31);   // tokens that may go
-      gone = static_cast<int32_t>(min(static_cast<uint32_t>(len - p.budget), total));
-      rank = static_cast<uint32_t>(gone);
-    }
+    total = __shfl_sync(0xffffffffu, wi, 31);
+    return incl - mine + __shfl_sync(0xffffffffu, wi - ws, warp);
+  };
+  // the digit of the rank-th key
+  auto find = [&](const uint4& s, uint32_t before) {
     const uint32_t v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -414,6 +422,35 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
       before += v[j];
     }
     __syncthreads();
+  };
+#pragma unroll 1
+  for (;; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 1 ? 21 : 10;
+    const uint32_t digits = pass == 2 ? 1023 : 2047;
+    uint32_t* h = sh.hist[pass & 1];
+    for (int32_t x0 = w0; x0 < w1; x0 += 32) {
+      const uint32_t k = key(x0 + lane);
+      const bool in = k != kProtected && (pass == 0 || k >> above == prefix >> above);
+      tally(h, in, k >> shift & digits);
+    }
+    cluster_sync(C);
+    // every CTA adds all counts, four digits per thread, and finds the same digit
+    uint4 s = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r)
+      if (r < C) {
+        const uint4 v = C == 1 ? *reinterpret_cast<const uint4*>(h + tid * 4) : peer_load4(peer_addr(h + tid * 4, r));
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+      }
+    uint32_t total;
+    const uint32_t before = keys_before(s, total);
+    if (pass == 0) {
+      gone = static_cast<int32_t>(min(static_cast<uint32_t>(len - p.budget), total));   // of those that may go
+      rank = static_cast<uint32_t>(gone);
+      // the sequence's place in the list of moves, long before it is needed
+      if (me == 0 && tid == 31) list_at = atomicAdd(p.alloc, static_cast<unsigned long long>(min(gone, len - gone)));
+    }
+    find(s, before);
     if (gone == 0) {          // every token is protected; as in every CTA of the cluster
       cluster_sync(C);        // the others may still be reading this CTA's counts
       done();
@@ -441,25 +478,39 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
       }
       cluster_sync(C);
       uint2 my = make_uint2(0, 0);
-      uint32_t from = 0;
+      uint32_t m[kMaxCluster], from = 0, place = 0, owner = 0;   // candidates of each CTA: n in all
 #pragma unroll
       for (uint32_t r = 0; r < kMaxCluster; ++r)
-        if (r < C) {
-          const uint32_t m = C == 1 ? sh.n_cand : peer_load(peer_addr(&sh.n_cand, r));
-          const uint32_t at = static_cast<uint32_t>(tid) - from;
-          if (at < m) my = C == 1 ? sh.cand[at] : peer_load2(peer_addr(&sh.cand[at], r));
-          from += m;                               // n in the end
+        m[r] = r >= C ? 0 : C == 1 ? sh.n_cand : peer_load(peer_addr(&sh.n_cand, r));
+#pragma unroll
+      for (uint32_t r = 0; r < kMaxCluster; ++r) {
+        const uint32_t at = static_cast<uint32_t>(tid) - from;
+        if (at < m[r]) {
+          place = at;
+          owner = r;
         }
-      // The rank-th of n <= 512 distinct values, one per thread, bit by bit: the block counts those
-      // that have agreed with it so far and have a zero next.
-      const unsigned long long v = static_cast<unsigned long long>(my.x & ((1u << shift) - 1u)) << 24 | (~my.y & 0xFFFFFFu);
+        from += m[r];
+      }
       bool alive = static_cast<uint32_t>(tid) < n;
-      for (int bit = shift + 23; bit >= 0; --bit) {
-        const bool one = v >> bit & 1ull;
-        const uint32_t zeros = static_cast<uint32_t>(__syncthreads_count(alive && !one));
-        const bool go_one = rank > zeros;
-        if (go_one) rank -= zeros;
-        alive = alive && one == go_one;
+      if (alive) my = C == 1 ? sh.cand[place] : peer_load2(peer_addr(&sh.cand[place], owner));
+      // The rank-th of n <= 512 distinct values, one per thread, by digits of this CTA's own until one is left.
+      // (The others have read this CTA's counts before the barrier above.)
+      const unsigned long long v = static_cast<unsigned long long>(my.x & ((1u << shift) - 1u)) << 24 | (~my.y & 0xFFFFFFu);
+      uint32_t* own = sh.hist[0];
+      for (int top = shift + 24;;) {
+        const int low = max(top - 11, 0);
+        reinterpret_cast<uint4*>(own)[tid] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        const uint32_t digit = static_cast<uint32_t>(v >> low) & ((1u << (top - low)) - 1u);
+        tally(own, alive, digit);
+        __syncthreads();
+        const uint4 mine = reinterpret_cast<uint4*>(own)[tid];
+        uint32_t all;
+        find(mine, keys_before(mine, all));
+        alive = alive && digit == found[0];
+        rank = found[1];
+        top = low;
+        if (found[2] == 1 || low == 0) break;
       }
       if (alive) cut_at = my;
       __syncthreads();
@@ -527,9 +578,10 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   if (tid == 31) {
     sh.n_holes = hi;
     sh.n_backs = bi;
-    if (me == 0) sh.list0 = atomicAdd(p.alloc, static_cast<unsigned long long>(most));
+    sh.list0 = list_at;        // of the first CTA
   }
   cluster_sync(C);
+  const uint2 l2 = C == 1 ? *reinterpret_cast<const uint2*>(&sh.list0) : peer_load2(peer_addr(&sh.list0, 0));
   uint32_t ph = 0, pb = 0;
   if (lane < static_cast<int>(C)) {
     ph = C == 1 ? sh.n_holes : peer_load(peer_addr(&sh.n_holes, lane));
@@ -539,7 +591,6 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   const uint32_t moves = __shfl_sync(0xffffffffu, phi, 31);
   uint32_t h0 = __shfl_sync(0xffffffffu, phi - ph, static_cast<int>(me)) + __shfl_sync(0xffffffffu, hi - hv, warp);
   uint32_t b0 = __shfl_sync(0xffffffffu, pbi - pb, static_cast<int>(me)) + __shfl_sync(0xffffffffu, bi - bv, warp);
-  const uint2 l2 = C == 1 ? *reinterpret_cast<const uint2*>(&sh.list0) : peer_load2(peer_addr(&sh.list0, 0));
   const int64_t list0 = static_cast<int64_t>(l2.y) << 32 | l2.x;
   const bool room = list0 + most <= p.move_cap;
   int2* list = p.moves + list0;
@@ -613,13 +664,12 @@ cudaError_t paged_evict_prepare() {
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
   // CTAs per sequence: a whole cluster while every CTA has an SM to itself, fewer in larger
-  // batches (32 sequences of 4097 tokens: 15.4 us with 4, 20.2 us with 8; 16 of 16896, 512 to move:
-  // 57 us with 4, 46 us with 8), and one where there is little to read and to move (11.3 us, 14.0 us with 8).
-  const int32_t cap = p.c.cap, most = std::min(cap / 2, cap - p.budget);   // moves there can be
+  // batches (32 sequences of 4160 tokens, 64 to move, with an append: 18.4 us with 4, 21.5 us with 8; 64 of
+  // 576, 64 to move: 22.9 us with 2, 37.2 us with 8; 16 of 16896, 512 to move: 51.0 us with 4, 41.3 us with 8).
+  const int32_t cap = p.c.cap;
   const unsigned room = static_cast<unsigned>(std::max(1, sm_count() / p.b.n));
   unsigned C = kMaxCluster;
   while (C > room) C /= 2;
-  if (cap <= 2048 && most <= 64) C = 1;
   const int32_t per = static_cast<int32_t>(C) * kEvictThreads;
   const int key_cap = std::min((cap + per - 1) / per * kEvictThreads, kKeyLimit);
   cudaLaunchConfig_t cfg = {};

@@ -340,6 +340,31 @@ def test_evict_is_exact(n, budget, sink, recent, kind):
     p.ok()
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "protected"])
+@pytest.mark.parametrize("lengths,budget", [([2, 1, 3, 2], 1), ([257, 256, 300, 257], 256), ([4608, 4607, 4608], 4607),
+                                            ([4609, 4608, 4700, 4609], 4608), ([9001, 9000, 9001], 9000)])
+def test_evict_one_token(lengths, budget, kind):
+    """One token too many takes a path of its own, in one CTA or a cluster, beside sequences that lose more or none."""
+    n = len(lengths)
+    p = Pair(2, 1, 64, 16, n, -(-max(lengths) // 16), seed=budget)
+    p.append(list(range(n)), lengths)
+    m = p.rng.lognormal(0, 2, (n, p.cache.capacity)).astype(np.float32)
+    if kind == "ties":
+        m = np.floor(p.rng.random(m.shape) * 3).astype(np.float32)
+    p.cache.token_mass.copy_(torch.from_numpy(m))
+    p.ora.mass[:] = m
+    sink, recent = (budget // 2, budget - budget // 2) if kind == "protected" else (min(4, budget), 0)
+    p.cache.evict(budget, sink, recent)
+    p.ora.evict(range(n), budget, sink, recent)
+    p.check_state(range(n))
+    got = p.cache.token_mass.cpu().numpy()
+    for s in range(n):
+        new = int(p.ora.length[s])
+        assert np.array_equal(got[s, :new], p.ora.mass[s, :new].astype(np.float32))
+        assert np.array_equal(got[s, new:], m[s, new:])
+    p.ok()
+
+
 @pytest.mark.parametrize("odd", [False, True])
 @pytest.mark.parametrize("n0,n1,budget", [(70000, 66001, 60000), (40000, 33007, 32500), (9000, 8999, 8192)])
 def test_evict_long_sequences(n0, n1, budget, odd):
