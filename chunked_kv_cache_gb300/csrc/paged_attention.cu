@@ -38,7 +38,7 @@
 // arithmetic too, since a scheduler has two warps. 8 sessions of 2072 .. 11432 tokens with 40
 // heads of 128: 147 us for 963 MB (6.5 TB/s, 97 % of the copy rate); one of 131071, 8 heads: 85 us for
 // 537 MB (93 %); 32 of 4001 .. 32768, e4m3: 148 us for 935 MB (93 %); 64 of 1 .. 16384: 86 us for
-// 522 MB (89 %); 16 of 1000 .. 8192 with weights: 53 us for 232 MB (64 %).
+// 522 MB (89 %); 16 of 1000 .. 8192 with weights: 52 us for 232 MB (65 %).
 //
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: a weight meets the
 // values as two bf16 numbers, itself rounded and what that leaves (2^-15 of it at most is lost):
