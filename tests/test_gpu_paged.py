@@ -485,6 +485,49 @@ def test_captured_step_serves_later_tokens():
     p.ok()
 
 
+def test_two_graphs_of_one_cache_replayed_in_turn():
+    """Two captured sequences and eager calls share a workspace; one after the other they do not disturb each other."""
+    p = Pair(32, 8, 128, 64, 6, 20, seed=24)
+    seqs = list(range(6))
+    p.append(seqs, [1200, 1100, 0, 64, 1279, 700])
+    q, k = p.randn(6, 32, 128), p.randn(3, 8, 128)
+    p.cache.attention(q, mass_decay=0.0)                      # warm
+    want = p.cache.attention(q)
+    side = torch.cuda.Stream(p.dev)
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graphs[0], stream=side):
+            outs.append(p.cache.attention(q, lse=True))
+        with torch.cuda.graph(graphs[1], stream=side):
+            p.cache.append(k, k, seqs=[2, 3, 5])
+            outs.append(p.cache.attention(q, lse=True, mass_decay=1.0))
+            p.cache.evict(1150, 4, 100)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs[0].replay()
+    assert torch.equal(outs[0][0], want)
+    for step in range(3):
+        graphs[1].replay()
+        mass = p.cache.token_mass.clone()
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0][0], p.cache.attention(q)) and torch.isfinite(mass).all()
+        assert p.cache.seq_len.tolist() == [1150, 1100, step + 1, 65 + step, 1150, 701 + step]
+    p.ok()
+
+
+def test_a_closed_cache_is_refused():
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(4, 2, 64, 16, 2, 4, seed=25)
+    p.append([0, 1], [3, 3])
+    p.cache.close()
+    p.cache.close()
+    q, k = p.randn(2, 4, 64), p.randn(2, 2, 64)
+    for call in (lambda: p.cache.attention(q), lambda: p.cache.append(k, k), lambda: p.cache.reset(), lambda: p.cache.evict(1)):
+        with pytest.raises(N.SrError):
+            call()
+
+
 def test_other_stream_and_reserved_pages():
     import chunked_kv_cache_gb300 as sr
     dev = device()
