@@ -33,7 +33,6 @@ sr_status validate(const sr_paged_config& c) {
   if (c.head_dim != 64 && c.head_dim != 128) return SR_ERR_UNSUPPORTED;
   if (c.page_type != SR_PAGE_BF16 && c.page_type != SR_PAGE_E4M3) return SR_ERR_UNSUPPORTED;
   if (c.n_heads % c.n_kv_heads != 0) return SR_ERR_INVALID_ARG;
-  if (c.n_heads / c.n_kv_heads > SR_MAX_PAGED_GROUP) return SR_ERR_UNSUPPORTED;
   if (c.page_tokens % 16 != 0 || c.page_tokens > 1024) return SR_ERR_UNSUPPORTED;
   if (!std::isfinite(c.softmax_scale)) return SR_ERR_INVALID_ARG;
   if (c.n_heads > 65536 / c.head_dim) return SR_ERR_INVALID_ARG;
@@ -42,8 +41,17 @@ sr_status validate(const sr_paged_config& c) {
   return SR_OK;
 }
 
+// Query heads that attention takes together: the largest share of a key/value head's, at most SR_MAX_PAGED_GROUP.
+int attn_group(const sr_paged_config& c) {
+  const int all = c.n_heads / c.n_kv_heads;
+  int parts = (all + SR_MAX_PAGED_GROUP - 1) / SR_MAX_PAGED_GROUP;
+  while (all % parts) ++parts;
+  return all / parts;
+}
+
 sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   sr::PagedLayout l;
+  const int group = attn_group(c), n_kv = c.n_heads / group;
   size_t at = 0;
   auto take = [&](size_t n) {
     const size_t here = at;
@@ -56,15 +64,15 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   l.move_cap = with_mass ? static_cast<int64_t>(c.n_pages) * c.page_tokens / 2 + sr::kMaxPagedSeqs : 0;
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
-  l.items = take(seqs * c.n_kv_heads * sizeof(int2));
+  l.items = take(seqs * n_kv * sizeof(int2));
   l.unit0 = take(sr::kMaxPagedSeqs * sizeof(int64_t));
-  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(c.n_heads / c.n_kv_heads, c.head_dim) * 4);
+  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(group, c.head_dim) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
   // every token of the pool once, the sequences' lengths rounded up to tiles
   const int64_t tile = sr::paged_tile_tokens(c.head_dim, c.page_type);
   l.score_tiles = with_mass ? sr::paged_score_tiles(static_cast<int64_t>(c.n_pages) * c.page_tokens, static_cast<int>(seqs),
-                                                    c.n_kv_heads, static_cast<int>(tile)) : 0;
-  l.scores = take(static_cast<size_t>(l.score_tiles) * (c.n_heads / c.n_kv_heads) * tile * 4);
+                                                    n_kv, static_cast<int>(tile)) : 0;
+  l.scores = take(static_cast<size_t>(l.score_tiles) * group * tile * 4);
   l.bytes = at;
   return l;
 }
@@ -148,7 +156,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.err_word = b.err_word;
   v.n_heads = cfg->n_heads;
   v.n_kv = cfg->n_kv_heads;
-  v.group = cfg->n_heads / cfg->n_kv_heads;
+  v.group = attn_group(*cfg);
   v.head_dim = cfg->head_dim;
   v.page_tokens = cfg->page_tokens;
   v.n_pages = cfg->n_pages;
@@ -237,6 +245,10 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   if (st != SR_OK) return st;
   p.b.n = n;
   p.c = c->view;
+  p.kv_heads = c->cfg.n_kv_heads;
+  p.c.n_kv = c->cfg.n_heads / p.c.group;
+  const uint32_t parts = static_cast<uint32_t>(p.c.n_kv / p.kv_heads);     // of a key/value head's query heads
+  p.head_magic = ((1u << 22) + parts - 1) / parts;                         // exact for heads and parts up to 1024
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;

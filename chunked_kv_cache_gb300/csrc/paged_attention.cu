@@ -5,7 +5,10 @@
 //   lse_h = ln sum_t e^x_h(t),    mass(t) <- decay * mass(t) + sum_h e^(x_h(t) - lse_h).
 //
 // Bound by the one read of the cache: a token's 2 D values per key/value head meet at
-// most 16 query heads. Every choice below serves that stream.
+// most 16 query heads. Every choice below serves that stream. (More query heads of one key
+// head are taken in equal parts that each read it, side by side, so that most of the reads end
+// in L2: 32 sequences of 4096 tokens and one key head of 128 take 19.7 us with 16 query heads,
+// 27.3 us with 32, 45.2 us with 64, 69.5 us with 128.)
 //
 // Work split. A sequence and key/value head (an item) is cut into tiles of CT
 // tokens; the launch's tiles, item after item, form one line, and every CTA takes an
@@ -437,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   int64_t left_load = left;
   const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
-  const int64_t row_pitch = static_cast<int64_t>(c.n_kv) * G::kRowBytes;
+  const int64_t row_pitch = static_cast<int64_t>(p.kv_heads) * G::kRowBytes;
+  auto kv_head = [&](int h) { return static_cast<int>(static_cast<uint32_t>(h) * p.head_magic >> 22); };
 
   // ---- copy this warp's tokens of one tile into a stage. The block table's entries for the
   // tile after it are fetched on the way, so that no copy waits for them. The lines are marked to
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
             live = 0;
           }
         }
-        int64_t at = row * row_pitch + lane_off + (load.h * S + sub) * G::kRowBytes;
+        int64_t at = row * row_pitch + lane_off + kv_head(load.h * S + sub) * G::kRowBytes;
         if (live >= 16) {
 #pragma unroll
           for (int x = 0; x < 16 / kRowsPer; ++x, at += kRowsPer * row_pitch) {
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     // log2-scaled scores = product * xs, of this lane's heads 8 t + 2 j4 and the next
     float xs[NT][2];
     {
-      const float scale = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[item_h])) : 1.f);
+      const float scale = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv_head(item_h)])) : 1.f);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x = scale;
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     const bool whole = first_tile == 0 && end_tile == tiles;
     float* part = part_at<D>(p, blockIdx.x, first_tile == 0 ? 1 : 0);
     const int free_stage = (stage + kStages - 1) % kStages;
-    const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[c.n_kv + item_h])) : 1.f;
+    const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv_head(item_h)])) : 1.f;
     constexpr int kQuads = D / 4;                 // of a row
 #pragma unroll
     for (int t = 0; t < NT; ++t) {

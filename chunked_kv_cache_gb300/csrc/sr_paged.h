@@ -100,6 +100,10 @@ struct PagedAttnParams {
   int64_t score_tiles;
   int32_t spread;          // neighbouring key/value heads that neighbouring CTAs take side by side; divides n_kv
   int32_t spread_log2;
+  // Key/value heads in memory. Where more query heads than SR_MAX_PAGED_GROUP share one, c.n_kv and c.group are those of
+  // equal subgroups, each an item of its own: item head h reads head h * head_magic >> 22.
+  int32_t kv_heads;
+  uint32_t head_magic;
   // Stretches that end where items end (the rule stands at Geo::kWhole); all in 16ths of a unit, times the stretches
   int32_t each;            // whole items for each CTA, or
   int32_t pieces;          // pieces that an item is cut into (below 2: none)

@@ -464,7 +464,8 @@ typedef struct sr_paged_cache sr_paged_cache;   /* opaque host handle */
 enum { SR_PAGE_BF16 = 0, SR_PAGE_E4M3 = 1 };
 
 typedef struct {
-  int32_t n_heads;         /* query heads; a multiple of n_kv_heads, at most SR_MAX_PAGED_GROUP times it */
+  int32_t n_heads;         /* query heads; a multiple of n_kv_heads. More than SR_MAX_PAGED_GROUP of one key/value head are
+                              taken in equal parts of at most that many, which each read the head */
   int32_t n_kv_heads;      /* key/value heads >= 1; query head h reads head h / (n_heads / n_kv_heads) */
   int32_t head_dim;        /* 64 or 128 */
   int32_t page_tokens;     /* tokens per page: a multiple of 16, at most 1024 */

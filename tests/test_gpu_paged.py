@@ -177,6 +177,26 @@ def test_one_long_sequence_among_many_short_ones(heads, kv, d, e4m3):
     p.ok()
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("heads,kv,d,lengths", [
+    (32, 1, 128, [300, 0, 17, 1000]), (34, 2, 64, [65, 129, 1]), (71, 1, 64, [500, 40]), (128, 4, 128, [2000, 1, 333]),
+    (96, 3, 128, [9000]), (40, 2, 64, [700] * 20), (512, 1, 128, [130, 70]), (1024, 1, 64, [90]),
+])
+def test_more_query_heads_than_one_read_serves(heads, kv, d, lengths, e4m3):
+    n = len(lengths)
+    p = Pair(heads, kv, d, 64, n, -(-max(lengths) // 64) + 1, e4m3, seed=heads + n)
+    seqs = p.rng.permutation(n).tolist()
+    p.append(seqs, [lengths[s] for s in seqs])
+    p.attend(seqs, decay=1.0)
+    p.append(seqs, [1] * n)
+    p.attend(seqs[::-1], decay=0.5)
+    p.cache.evict(max(lengths) // 2, 3, 5)
+    p.ora.evict(range(n), max(lengths) // 2, 3, 5)
+    p.check_state(range(n))
+    p.attend(seqs)
+    p.ok()
+
+
 def test_many_sequences_of_unequal_length():
     n = 256
     p = Pair(8, 2, 64, 16, n, 20, seed=6)

@@ -38,7 +38,7 @@ INV, UNS, ALIGN = N.SR_ERR_INVALID_ARG, N.SR_ERR_UNSUPPORTED, N.SR_ERR_ALIGN
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(n_heads=0), INV), (dict(n_kv_heads=0), INV), (dict(n_heads=7), INV), (dict(n_heads=34), UNS),
+    (dict(n_heads=0), INV), (dict(n_kv_heads=0), INV), (dict(n_heads=7), INV),
     (dict(head_dim=96), UNS), (dict(head_dim=256), UNS), (dict(page_type=2), UNS), (dict(page_type=-1), UNS),
     (dict(page_tokens=0), INV), (dict(page_tokens=8), UNS), (dict(page_tokens=24), UNS),
     (dict(page_tokens=1040), UNS), (dict(n_pages=0), INV), (dict(max_seqs=0), INV), (dict(max_seqs=65537), INV),
@@ -50,6 +50,17 @@ def test_bad_shapes(lib, change, status):
     assert st == status and out is None
     n = ctypes.c_uint64()
     assert lib.sr_paged_workspace_bytes(ctypes.byref(_cfg(**change)), 1, ctypes.byref(n)) == status
+
+
+@pytest.mark.parametrize("heads,kv", [(34, 2), (32, 1), (1024, 1), (71, 1), (512, 16)])
+def test_any_share_of_a_key_head_has_a_workspace(lib, heads, kv):
+    """More query heads than a read serves are split; the weights' scores need the same room however they are."""
+    n, m = ctypes.c_uint64(), ctypes.c_uint64()
+    shape = dict(n_heads=heads, n_kv_heads=kv, head_dim=64, n_pages=1000, max_seqs=1)
+    assert lib.sr_paged_workspace_bytes(ctypes.byref(_cfg(**shape)), 1, ctypes.byref(n)) == N.SR_OK
+    assert lib.sr_paged_workspace_bytes(ctypes.byref(_cfg(**dict(shape, n_kv_heads=heads))), 1, ctypes.byref(m)) == N.SR_OK
+    tokens = 1000 * _cfg(**shape).page_tokens
+    assert n.value >= tokens * heads * 4 and n.value <= 4 * m.value
 
 
 @pytest.mark.parametrize("name,value,status", [
