@@ -145,10 +145,11 @@ def lib() -> ctypes.CDLL:
         L.sr_paged_init.argtypes = [ctypes.POINTER(SrPagedConfig), ctypes.POINTER(SrPagedBuffers), vp,
                                     ctypes.POINTER(vp)]
         L.sr_paged_free.argtypes = [vp]
-        L.sr_paged_reset.argtypes = [vp, pi32, i32, vp]
-        L.sr_paged_append.argtypes = [vp, pi32, pi32, i32, vp, vp, vp]
-        L.sr_paged_attention.argtypes = [vp, pi32, i32, vp, vp, vp, ctypes.c_float, vp]
-        L.sr_paged_evict.argtypes = [vp, pi32, i32, i32, i32, i32, vp]
+        # host arrays of int32 as plain addresses (or ctypes arrays): building one per call costs as much as a launch
+        L.sr_paged_reset.argtypes = [vp, vp, i32, vp]
+        L.sr_paged_append.argtypes = [vp, vp, vp, i32, vp, vp, vp]
+        L.sr_paged_attention.argtypes = [vp, vp, i32, vp, vp, vp, ctypes.c_float, vp]
+        L.sr_paged_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp]
         L.sr_paged_locate.argtypes = [ctypes.POINTER(SrPagedConfig), pi32, i64, ctypes.POINTER(i64)]
         L.sr_device_error_status.argtypes = [i32]
         L.sr_debug_wait_timeout.argtypes = [vp, u64, vp]

@@ -6,7 +6,7 @@ calls of libsr.so. Nothing here computes.
 """
 from __future__ import annotations
 
-import ctypes
+from array import array
 from collections.abc import Sequence
 
 import torch
@@ -99,11 +99,14 @@ class PagedCache:
 
     @staticmethod
     def _ids(seqs: Sequence[int] | None):
+        """The numbers as 32-bit ones, to be kept while their address is used, and that address."""
         if seqs is None:
-            return None
-        if seqs and (min(seqs) < 0 or max(seqs) >= 1 << 31):     # ctypes would cut them to 32 bits
-            raise N.SrError(N.SR_ERR_INVALID_ARG, "sequence or count")
-        return (ctypes.c_int32 * len(seqs))(*seqs)
+            return None, None
+        try:
+            ids = array("i", seqs)
+        except OverflowError:
+            raise N.SrError(N.SR_ERR_INVALID_ARG, "sequence or count") from None
+        return ids, ids.buffer_info()[0]
 
     # The calls below go to the library without N's wrappers: a call is a few microseconds on the host.
     @staticmethod
@@ -151,7 +154,8 @@ class PagedCache:
     def reset(self, seqs: Sequence[int] | None = None) -> None:
         """Empty sequences (None: the first SR_MAX_PAGED_SEQS rows, or all where there are fewer)."""
         n = min(self.max_seqs, N.SR_MAX_PAGED_SEQS) if seqs is None else len(seqs)
-        self._done(self._lib.sr_paged_reset(self.handle, self._ids(seqs), n, self._stream()), "sr_paged_reset")
+        ids, at = self._ids(seqs)
+        self._done(self._lib.sr_paged_reset(self.handle, at, n, self._stream()), "sr_paged_reset")
 
     def append(self, k: torch.Tensor, v: torch.Tensor, seqs: Sequence[int] | None = None,
                counts: Sequence[int] | None = None) -> None:
@@ -166,8 +170,10 @@ class PagedCache:
         takes = n if counts is None else sum(counts)
         if takes != rows:
             raise ValueError(f"k and v have {rows} rows, the sequences take {takes}")
-        self._done(self._lib.sr_paged_append(self.handle, self._ids(seqs), self._ids(counts), n, k.data_ptr(),
-                                             v.data_ptr(), self._stream()), "sr_paged_append")
+        ids, at = self._ids(seqs)
+        each, each_at = self._ids(counts)
+        self._done(self._lib.sr_paged_append(self.handle, at, each_at, n, k.data_ptr(), v.data_ptr(), self._stream()),
+                   "sr_paged_append")
 
     def attention(self, q: torch.Tensor, seqs: Sequence[int] | None = None, out: torch.Tensor | None = None,
                   lse: torch.Tensor | bool | None = None, mass_decay: float | None = None):
@@ -191,7 +197,8 @@ class PagedCache:
             self._check("lse", lse, (n, self.n_heads), torch.float32)
         else:
             lse = None
-        self._done(self._lib.sr_paged_attention(self.handle, self._ids(seqs), n, q.data_ptr(), out.data_ptr(),
+        ids, at = self._ids(seqs)
+        self._done(self._lib.sr_paged_attention(self.handle, at, n, q.data_ptr(), out.data_ptr(),
                                                 None if lse is None else lse.data_ptr(),
                                                 -1.0 if mass_decay is None else mass_decay, self._stream()),
                    "sr_paged_attention")
@@ -205,7 +212,8 @@ class PagedCache:
             raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_evict")
         budget = min(budget, (1 << 31) - 1)                      # no sequence is longer
         n = min(self.max_seqs, N.SR_MAX_PAGED_SEQS) if seqs is None else len(seqs)
-        self._done(self._lib.sr_paged_evict(self.handle, self._ids(seqs), n, budget, n_sink, n_recent, self._stream()),
+        ids, at = self._ids(seqs)
+        self._done(self._lib.sr_paged_evict(self.handle, at, n, budget, n_sink, n_recent, self._stream()),
                    "sr_paged_evict")
 
     # ---------------------------------------------------------------- state
