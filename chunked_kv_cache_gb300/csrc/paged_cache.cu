@@ -153,11 +153,11 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // shared memory. A radix select (11, 11 and 10 bits, the CTAs' counts added through
 // distributed shared memory) narrows the keys down to those that share the digits of
 // the last key to go; as soon as these are few every CTA gathers them, one per thread, and
-// goes on by itself with digits of the key, then of the index, which settles ties (bit by
-// bit with a count of the block each: twice the time). The result is a cut: a token goes if
-// its key lies below the cut's, or equals it at an index at or behind the cut's. Ordered
-// counts turn that into moves (from, to), and all warps move rows, a warp per token. A
-// move reads at or behind the new length and writes below it, so that no move sees another.
+// goes on by itself with digits of the key, then of the index, which settles ties. The
+// result is a cut: a token goes if its key lies below the cut's, or equals it at an index at
+// or behind the cut's. Ordered counts turn that into moves (from, to), and all warps move
+// rows, a warp per token. A move reads at or behind the new length and writes below it, so
+// that no move sees another.
 // Latency bound (barriers, dependent loads, code that runs once) until the moves, which are
 // HBM bound: 512 of 16896 tokens go from each of 16 sequences, 1024 values to a row, in
 // 28 us, where the 70 MB alone would take 10 us. One token of a sequence (the least weight, no
