@@ -182,14 +182,15 @@ __device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
 struct SharedHead {
   int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
-  int32_t longest;                      // units of the longest item
+  int32_t longest;                      // tiles of the longest sequence, and one
   float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
 };
 
 // A place on the line of tiles. Each item takes kItemCost units before its tiles:
-// what changing items costs a CTA, in tiles.
-constexpr int kItemCost = 1;
+// what changing items costs a CTA, in tiles (16 sequences of 300 .. 3000 tokens of 64: 13.9 us with
+// 1, 11.9 us with 2, 12.7 us with 3; 16 of 1000 .. 8192: 44.4 us, 42.8 us, 43.7 us).
+constexpr int kItemCost = 2;
 // Up to kSpread neighbouring heads are read side by side by neighbouring CTAs, so that a
 // token's row, whole in memory, is read at about one time. Rows of 64 bytes per head need
 // it, because DRAM delivers twice that (8 heads, 64 sequences of 8192 tokens, head dim 64,
@@ -369,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
     for (int k = 1; k < kMaxPagedSeqs / 32; ++k) longest = max(longest, len[k]);
     longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) sh.longest = (longest + G::CT - 1) / G::CT + kItemCost;
+    if (lane == 0) sh.longest = (longest + G::CT - 1) / G::CT + 1;
   }
   __syncthreads();
   // sequences without a token: nothing to attend to
@@ -398,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     u0 = start(me * p.each);
     left = start((me + 1) * p.each) - u0;
     if (left == 0) return;
-  } else if (p.pieces > 1 && (sh.longest + 2 * p.pieces) * p.cut_cost <= bound) {
+  } else if (p.pieces > 1 && (sh.longest + 1 + 2 * p.pieces) * p.cut_cost <= bound) {
     // one of `pieces` equal pieces of an item, as far as it has tiles
     const int item = me / p.pieces, i = item / n_kv;
     if (i >= n) return;
@@ -1134,7 +1135,7 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   const int turns = (p.c.group + 3) / 4 * ((parts + kJoinBatch - 1) / kJoinBatch);
   if (turns <= 2 + p.b.n * p.c.n_heads / 2048) p.items = nullptr;
   // no item is cut (see kWhole): nothing to join (1 sequence of 300 tokens, 16 heads: 9.8 us with the launch, 8.5 us)
-  if (p.each == 1 && (p.c.cap + G::CT - 1) / G::CT + kItemCost <= G::kWholeExtra) p.items = nullptr;
+  if (p.each == 1 && (p.c.cap + G::CT - 1) / G::CT + 1 <= G::kWholeExtra) p.items = nullptr;
   cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, NT, MASS>, static_cast<unsigned>(ctas), kThreads,
                                    kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess) return e;
