@@ -39,9 +39,9 @@
 // What bounds it: the stream, at 6.5 - 6.9 TB/s once it runs, and about 7 us per call before
 // and after it (lengths, the first copies, merge, join); with e4m3 pages and head dim 64 the
 // arithmetic too, since a scheduler has two warps. 8 sessions of 2072 .. 11432 tokens with 40
-// heads of 128: 147 us for 963 MB (6.5 TB/s, 97 % of the copy rate); one of 131071, 8 heads: 85 us for
-// 537 MB (93 %); 32 of 4001 .. 32768, e4m3: 148 us for 935 MB (93 %); 64 of 1 .. 16384: 86 us for
-// 522 MB (89 %); 16 of 1000 .. 8192 with weights: 52 us for 232 MB (65 %).
+// heads of 128: 144 us for 963 MB (6.7 TB/s, 99 % of the copy rate); one of 131071, 8 heads: 84 us for
+// 537 MB (95 %); 32 of 4001 .. 32768, e4m3: 144 us for 935 MB (96 %); 64 of 1 .. 16384: 87 us for
+// 522 MB (89 %); 16 of 1000 .. 8192 with weights: 50 us for 232 MB (69 %).
 //
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: a weight meets the
 // values as two bf16 numbers, itself rounded and what that leaves (2^-15 of it at most is lost):
