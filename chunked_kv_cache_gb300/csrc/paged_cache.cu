@@ -356,10 +356,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
       best = __shfl_sync(0xffffffffu, best, 0);
       const int32_t at = static_cast<int32_t>(~static_cast<uint32_t>(best)), last = len - 1;
       if (best != ~0ull) {
+        bool whole = true;                        // nothing to move, or both ends have a page
         if (at != last) {
           const int64_t from = paged_row(table, last, c.page_tokens, c.n_pages);
           const int64_t to = paged_row(table, at, c.page_tokens, c.n_pages);
-          if (from >= 0 && to >= 0) {
+          whole = from >= 0 && to >= 0;
+          if (whole) {
             if (lane == 0) {
               tpos[at] = tpos[last];
               mass[at] = mass[last];
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
             note_error(c, SR_DEVERR_BAD_PAGE);
           }
         }
-        if (lane == 0) c.seq_len[seq] = last;
+        if (whole && lane == 0) c.seq_len[seq] = last;
       }
     }
     if (C > 1) cluster_sync(C);   // this CTA's lightest has been read
@@ -561,22 +563,31 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
       f(t, __ballot_sync(0xffffffffu, go && t < kept), __ballot_sync(0xffffffffu, x < w1 && !go && t >= kept));
     }
   };
+  // A sequence is evicted from whole or not at all: one with an end of a move on no page of the pool stays as it
+  // is. The counts carry that in their top bit, so that all CTAs of the cluster know before anything is written.
+  constexpr uint32_t kNoPage = 1u << 31;
   uint32_t nh = 0, nb = 0;
-  walk([&](int32_t, uint32_t holes, uint32_t backs) {
+  bool off = false;
+  walk([&](int32_t t, uint32_t holes, uint32_t backs) {
     nh += __popc(holes);
     nb += __popc(backs);
+    if ((holes | backs) >> lane & 1u) off |= static_cast<uint32_t>(table[page_of_group(t >> 4, c.magic)]) >= static_cast<uint32_t>(c.n_pages);
   });
+  if (__any_sync(0xffffffffu, off)) nh |= kNoPage;
   __syncthreads();
   if (lane == 0) {
     sums[0][warp] = nh;
     sums[1][warp] = nb;
   }
   __syncthreads();
-  const uint32_t hv = lane < kEvictWarps ? sums[0][lane] : 0, bv = lane < kEvictWarps ? sums[1][lane] : 0;
+  uint32_t hv = lane < kEvictWarps ? sums[0][lane] : 0;
+  const uint32_t bv = lane < kEvictWarps ? sums[1][lane] : 0;
+  const uint32_t off_here = __any_sync(0xffffffffu, hv & kNoPage) ? kNoPage : 0;
+  hv &= ~kNoPage;
   const uint32_t hi = warp_incl_scan(hv, lane), bi = warp_incl_scan(bv, lane);
   const uint32_t most = static_cast<uint32_t>(min(gone, kept));   // moves there can be
   if (tid == 31) {
-    sh.n_holes = hi;
+    sh.n_holes = hi | off_here;
     sh.n_backs = bi;
     sh.list0 = list_at;        // of the first CTA
   }
@@ -587,6 +598,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     ph = C == 1 ? sh.n_holes : peer_load(peer_addr(&sh.n_holes, lane));
     pb = C == 1 ? sh.n_backs : peer_load(peer_addr(&sh.n_backs, lane));
   }
+  const bool paged = !__any_sync(0xffffffffu, ph & kNoPage);
+  ph &= ~kNoPage;
   const uint32_t phi = warp_incl_scan(ph, lane), pbi = warp_incl_scan(pb, lane);
   const uint32_t moves = __shfl_sync(0xffffffffu, phi, 31);
   uint32_t h0 = __shfl_sync(0xffffffffu, phi - ph, static_cast<int>(me)) + __shfl_sync(0xffffffffu, hi - hv, warp);
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
   const int64_t list0 = static_cast<int64_t>(l2.y) << 32 | l2.x;
   const bool room = list0 + most <= p.move_cap;
   int2* list = p.moves + list0;
-  if (room)
+  if (room && paged)
     walk([&](int32_t t, uint32_t holes, uint32_t backs) {
       const uint32_t lt = (1u << lane) - 1u;
       if (holes >> lane & 1u) list[h0 + __popc(holes & lt)].y = t;
@@ -604,8 +617,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     });
   cluster_sync(C);             // the list is whole; nobody reads another CTA's shared memory, or a weight, any more
   done();
-  if (!room) {                 // sequences that share pages: more tokens than the pool has
-    if (tid == 0) note_error(c, SR_DEVERR_WORKSPACE);
+  if (!room || !paged) {       // no room: sequences that share pages, more tokens than the pool has
+    if (tid == 0) note_error(c, paged ? SR_DEVERR_WORKSPACE : SR_DEVERR_BAD_PAGE);
     return;
   }
 
@@ -619,18 +632,13 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
       const int2 m = __ldcg(list + j);
       from = paged_row(table, m.x, c.page_tokens, c.n_pages);
       to = paged_row(table, m.y, c.page_tokens, c.n_pages);
-      if (from < 0 || to < 0) {
-        note_error(c, SR_DEVERR_BAD_PAGE);
-        from = -1;
-      } else {
-        tpos[m.y] = tpos[m.x];
-        mass[m.y] = mass[m.x];
-      }
+      tpos[m.y] = tpos[m.x];
+      mass[m.y] = mass[m.x];
     }
     const int n = static_cast<int>(min((moves - j0 + step - 1) / step, 32u));
     for (int q = 0; q < n; ++q) {
       const int64_t f = __shfl_sync(0xffffffffu, from, q), g = __shfl_sync(0xffffffffu, to, q);
-      if (f < 0) continue;
+      if ((f | g) < 0) continue;      // an entry that the caller changed during the call
       move_rows(c, f, g, vpr, lane);
     }
   }

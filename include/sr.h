@@ -541,7 +541,10 @@ SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int3
  * others, those with the largest token_mass (a tie goes to the lower index; NaN counts as
  * larger than every number). Then the j-th evicted index below the new length takes over
  * the j-th kept token at or behind it: only these tokens move, with their positions and
- * weights, the others stay in place, and what lies behind the new length is left as it was.
+ * weights, the others stay in place, and what lies behind the new length is left as it was. A sequence
+ * is evicted from whole or not at all: if a token that moves, or the index it would take, lies on an entry that is
+ * no page of the pool, the sequence is left as it was, longer than its budget, and err_word receives
+ * SR_DEVERR_BAD_PAGE; the others are not affected.
  * budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget. Needs token_mass
  * (SR_ERR_STATE). Pages of an evicted sequence must not be shared with another one.
  */

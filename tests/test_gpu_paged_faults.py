@@ -1,0 +1,86 @@
+"""The paged cache where a call cannot be carried out, or where the numbers leave nothing to
+weigh: what it then leaves untouched, and what it says. Against the float64 oracle; tolerances
+as derived in test_gpu_paged."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_common import device
+from tests.test_gpu_paged import Pair
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from chunked_kv_cache_gb300 import build
+    build.build()
+    device()
+
+
+# ------------------------------------------------------------------ eviction over a page that is none of the pool's
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("n,length,budget,sink,recent", [
+    (4, 33, 32, 0, 1), (4, 300, 299, 4, 16), (8, 4608, 4607, 4, 256),       # one token, one CTA
+    (4, 5001, 5000, 4, 256),                                                # one token, a cluster
+    (4, 300, 200, 4, 16), (4, 5000, 4000, 16, 500), (8, 9000, 4700, 0, 4),  # a block of them, a cluster
+    (96, 120, 64, 4, 16),                                                   # a block of them, one CTA
+])
+def test_an_eviction_that_cannot_move_its_tokens_changes_nothing(n, length, budget, sink, recent, e4m3):
+    """Sequences in turn: sound; the lightest token on an unmapped page; the last token, which is protected, on
+    one; an unmapped page whose tokens stay in place. The second and third kind are left as they were."""
+    from chunked_kv_cache_gb300 import _native as N
+    p = Pair(2, 1, 64, 16, n, -(-length // 16), e4m3, seed=length + n)
+    seqs = list(range(n))
+    p.append(seqs, [length] * n)
+    m = p.rng.lognormal(0, 2, (n, p.cache.capacity)).astype(np.float32)
+    table = p.cache.block_table.clone()
+    mid = (sink + 16) // 16                         # a page without sinks, below the budget
+    assert 16 * (mid + 1) <= min(budget, length - recent)
+    for s in seqs:
+        bad = [-1, p.cache.n_pages, -(1 << 31), (1 << 31) - 1][s // 4 % 4]
+        if s % 4 == 1:
+            m[s, 16 * mid + 5] = 1e-9
+            p.cache.block_table[s, mid] = bad
+        elif s % 4 == 2:
+            p.cache.block_table[s, (length - 1) // 16] = bad
+        elif s % 4 == 3:
+            m[s, 16 * mid: 16 * mid + 16] = 1e9
+            p.cache.block_table[s, mid] = bad
+    p.cache.token_mass.copy_(torch.from_numpy(m))
+    p.ora.mass[:] = m
+    before = p.cache.token_pos.clone()
+    p.cache.evict(budget, sink, recent)
+    sound = [s for s in seqs if s % 4 in (0, 3)]
+    spoilt = [s for s in seqs if s % 4 in (1, 2)]
+    p.ora.evict(sound, budget, sink, recent)
+    assert int(p.cache.err_word.item()) == N.SR_DEVERR_BAD_PAGE
+    p.check_state(seqs)
+    mass = p.cache.token_mass.cpu().numpy()
+    assert np.array_equal(mass[spoilt], m[spoilt]) and torch.equal(p.cache.token_pos[spoilt], before[spoilt])
+    for s in sound:
+        assert np.array_equal(mass[s, :budget], p.ora.mass[s, :budget].astype(np.float32))
+    # with the pages back, the same call does what it could not do
+    p.cache.block_table.copy_(table)
+    p.cache.err_word.zero_()
+    p.cache.evict(budget, sink, recent)
+    p.ora.evict(seqs, budget, sink, recent)
+    p.check_state(seqs)
+    assert np.array_equal(p.cache.token_mass.cpu().numpy()[:, :budget], p.ora.mass[:, :budget].astype(np.float32))
+    p.ok()
+
+
+@pytest.mark.parametrize("length,budget", [(300, 299), (300, 288), (5009, 5008), (5009, 5000)])
+def test_tokens_at_the_end_go_without_a_move(length, budget):
+    """Nothing moves where the lightest tokens are the last: their page need not be there any more."""
+    p = Pair(2, 1, 64, 16, 2, -(-length // 16), seed=length - budget)
+    p.append([0, 1], [length, length])
+    m = p.rng.lognormal(0, 1, (2, p.cache.capacity)).astype(np.float32)
+    m[:, budget:] = 1e-9
+    p.cache.token_mass.copy_(torch.from_numpy(m))
+    p.ora.mass[:] = m
+    p.cache.block_table[0, (length - 1) // 16] = -1
+    p.cache.evict(budget, 4)
+    p.ora.evict([0, 1], budget, 4)
+    p.check_state([0, 1])
+    p.ok()
