@@ -65,7 +65,7 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   l.moves = take(static_cast<size_t>(l.move_cap) * sizeof(int2));
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
   l.items = take(seqs * n_kv * sizeof(int2));
-  l.unit0 = take(sr::kMaxPagedSeqs * sizeof(int64_t));
+  l.unit0 = take((sr::kMaxPagedSeqs + 1) * sizeof(int64_t));
   l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(group, c.head_dim) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
   // every token of the pool once, the sequences' lengths rounded up to tiles

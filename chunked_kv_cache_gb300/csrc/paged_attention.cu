@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     }
   const int64_t T = sh.cum[n];
   if (MASS && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < n; i += kThreads) p.unit0[i] = sh.cum[i];
+    for (int i = threadIdx.x; i <= n; i += kThreads) p.unit0[i] = sh.cum[i];
   if (T == 0) return;
   int64_t u0, left, share = 0, rest = 0;   // first unit and units of the stretch
   int cut = 0;                             // pieces of each item of the stretch, where all have as many
@@ -1030,8 +1030,8 @@ __global__ void __launch_bounds__(kMassThreads) paged_mass_kernel(const __grid_c
   const int64_t unit0 = p.unit0[i];
   const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
   const int32_t tiles = (len + CT - 1) / CT;
-  if (len > 0 && (unit0 + static_cast<int64_t>(tiles + kItemCost) * (c.n_kv / S)) * S > p.score_tiles) {   // not stored
-    if (threadIdx.x == 0) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
+  if (p.unit0[p.b.n] * S > p.score_tiles) {    // not all are stored: no sequence's weights change
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicCAS(c.err_word, 0, SR_DEVERR_WORKSPACE);
     return;
   }
   const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;

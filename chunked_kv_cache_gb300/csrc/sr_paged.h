@@ -58,7 +58,7 @@ struct PagedLayout {
   size_t moves;            // int2[move_cap]: (from, to) logical indices
   int64_t move_cap;
   size_t items;            // int2[n][n_kv]
-  size_t unit0;            // int64[kMaxPagedSeqs]
+  size_t unit0;            // int64[kMaxPagedSeqs + 1]
   size_t parts;            // [kMaxPagedCtas][2] partial results
   size_t lse2;             // float[kMaxPagedSeqs][n_heads], log2 units
   size_t scores;           // float[score_tiles][group][tile tokens]
@@ -91,7 +91,7 @@ struct PagedAttnParams {
   __nv_bfloat16* o;
   float* lse;
   int2* items;             // [n][n_kv] first part and number of parts, when a launch of its own joins them; else NULL
-  int64_t* unit0;          // [n] first unit of each sequence on the line (see paged_attention.cu)
+  int64_t* unit0;          // [n + 1] first unit of each sequence on the line (see paged_attention.cu), and its end
   int32_t* arrivals;       // [kMaxPagedCtas] parts, or groups of parts, of an item that are done; left at zero
   int32_t* group_arrivals; // [2 * kMaxPagedCtas]
   float* parts;

@@ -529,7 +529,9 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  * 2^-11 (e4m3 pages) for their product with V.
  * mass_decay >= 0 (finite; needs token_mass): also
  *   token_mass[s][t] = mass_decay * token_mass[s][t] + sum over heads of the token's weight.
- * mass_decay < 0: weights are not accumulated. The work is split over the length of the
+ * mass_decay < 0: weights are not accumulated. The workspace has room for the scores of every token of the pool
+ * once; a batch whose sequences share pages and hold more leaves all weights as they were, with SR_DEVERR_WORKSPACE
+ * in err_word (o and lse are written), and can be taken in smaller batches. The work is split over the length of the
  * sequences and joined, whatever their number; results do not depend on timing.
  */
 SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, const void* q, void* o,

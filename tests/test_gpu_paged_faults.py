@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from tests.gpu_common import device
-from tests.test_gpu_paged import Pair
+from tests.test_gpu_paged import U, Pair, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +84,40 @@ def test_tokens_at_the_end_go_without_a_move(length, budget):
     p.ora.evict([0, 1], budget, 4)
     p.check_state([0, 1])
     p.ok()
+
+
+# ------------------------------------------------------------------ weights that there is no room for
+@pytest.mark.parametrize("kv,d,cap", [(1, 64, 1024), (2, 128, 256)])
+def test_weights_of_a_batch_that_does_not_fit_are_left_as_they_were(kv, d, cap):
+    """Sequences that share pages and hold more tokens than the pool: no sequence's weights change, so that the
+    caller can take them in smaller batches. Outputs are written all the same."""
+    import chunked_kv_cache_gb300 as sr
+    from chunked_kv_cache_gb300 import _native as N
+    n, page, heads = 8, 16, 4 * kv
+    p = Pair(heads, kv, d, page, 1, cap // page, seed=d, spare=0)
+    p.append([0], [cap])
+    i32 = dict(dtype=torch.int32, device=p.dev)
+    c = sr.PagedCache(heads, kv, d, page_tokens=page, n_pages=cap // page, max_seqs=n, max_pages=cap // page, device=p.dev,
+                      buffers=dict(k_pages=p.cache.k_pages, v_pages=p.cache.v_pages,
+                                   block_table=torch.from_numpy(np.repeat(p.table, n, 0).astype(np.int32)).to(p.dev),
+                                   seq_len=torch.full((n,), cap, **i32), seq_pos=torch.full((n,), cap, **i32),
+                                   token_pos=torch.arange(cap, **i32).repeat(n, 1)))
+    q = p.randn(n, heads, d)
+    c.token_mass.uniform_(generator=p.g)
+    old = c.token_mass.clone()
+    want, want_lse = c.attention(q, lse=True)
+    o, lse = c.attention(q, lse=True, mass_decay=0.5)
+    assert int(c.err_word.item()) == N.SR_DEVERR_WORKSPACE
+    assert torch.equal(c.token_mass, old)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    c.err_word.zero_()
+    for seqs in ([0, 1], [5, 4], [2, 3], [7, 6]):
+        c.attention(q[seqs], seqs=seqs, mass_decay=0.5)
+    assert c.error_status() == 0
+    got, rows = f64(c.token_mass), f64(old)
+    for s in range(n):
+        _, w, _ = p.ora.weights(0, f64(q[s]))
+        ref = 0.5 * rows[s] + w.sum(0)
+        qa, ka = np.abs(f64(q[s])).reshape(kv, 4, d), np.abs(p.ora.k[0])
+        dx = (d + 8) * U * p.ora.scale * np.einsum("hgd,thd->hgt", qa, ka).max()
+        assert np.all(np.abs(got[s] - ref) <= (2 * dx + cap * U + 2.0 ** -20 + 4 * U) * ref), s
