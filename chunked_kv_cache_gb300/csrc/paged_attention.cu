@@ -230,6 +230,10 @@ __device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {   // a >= 0, 
   return a / b;
 }
 
+// What the weights' launch subtracts from a row's scores: where all of them are -inf, 0 leaves weights of 0, as in the
+// output, and -inf would leave NaN.
+__device__ __forceinline__ float weight_reference(float lse2) { return lse2 == -INFINITY ? 0.f : lse2; }
+
 // ---- joining partial results
 constexpr int kJoin = 48;
 
@@ -311,7 +315,7 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
       if (lane == 0) {
         const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
         if (p.lse) p.lse[out0 + r] = lse2 * kLn2;
-        p.lse2[out0 + r] = lse2;
+        p.lse2[out0 + r] = weight_reference(lse2);
       }
     }
   }
@@ -868,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
           if (quad == 0) {
             const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
             if (p.lse) p.lse[out] = lse2 * kLn2;
-            if (MASS) p.lse2[out] = lse2;
+            if (MASS) p.lse2[out] = weight_reference(lse2);
           }
         } else {
           *reinterpret_cast<float4*>(part + row * D + 4 * quad) = a;
@@ -1000,7 +1004,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   if (threadIdx.x == 0) {
     const float lse2 = l == 0.f ? -INFINITY : all + log2f(l);
     if (p.lse) p.lse[out] = lse2 * kLn2;
-    p.lse2[out] = lse2;
+    p.lse2[out] = weight_reference(lse2);
   }
 }
 

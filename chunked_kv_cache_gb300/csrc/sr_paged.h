@@ -60,7 +60,7 @@ struct PagedLayout {
   size_t items;            // int2[n][n_kv]
   size_t unit0;            // int64[kMaxPagedSeqs + 1]
   size_t parts;            // [kMaxPagedCtas][2] partial results
-  size_t lse2;             // float[kMaxPagedSeqs][n_heads], log2 units
+  size_t lse2;             // float[kMaxPagedSeqs][n_heads], log2 units; 0 for rows whose scores are all -inf
   size_t scores;           // float[score_tiles][group][tile tokens]
   int64_t score_tiles;
   size_t bytes;

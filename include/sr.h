@@ -523,8 +523,9 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  * among them, once appended):
  *   o[i][h] = softmax(scale * q[i][h] . K) V   over the seq_len tokens of seqs[i].
  * q, o: [n][n_heads][head_dim] bf16. lse: optional [n][n_heads] fp32, natural-log sum-exp of
- * the scaled scores. A sequence of length 0 gets o = 0 and lse = -inf. Indices at or past
- * seq_len are never read as values: what the pages hold there does not matter. o may be q.
+ * the scaled scores. A sequence of length 0, and a row whose scores are all -inf, gets o = 0 and
+ * lse = -inf and its tokens draw no weight. Indices at or past seq_len are never read as
+ * values: what the pages hold there does not matter. o may be q.
  * fp32 scores, softmax and sums; the weights are held to 2^-15 of themselves (bf16 pages) or
  * 2^-11 (e4m3 pages) for their product with V.
  * mass_decay >= 0 (finite; needs token_mass): also

@@ -121,3 +121,33 @@ def test_weights_of_a_batch_that_does_not_fit_are_left_as_they_were(kv, d, cap):
         qa, ka = np.abs(f64(q[s])).reshape(kv, 4, d), np.abs(p.ora.k[0])
         dx = (d + 8) * U * p.ora.scale * np.einsum("hgd,thd->hgt", qa, ka).max()
         assert np.all(np.abs(got[s] - ref) <= (2 * dx + cap * U + 2.0 ** -20 + 4 * U) * ref), s
+
+
+# ------------------------------------------------------------------ scores that leave nothing
+@pytest.mark.parametrize("heads,kv,length", [(4, 2, 40), (8, 2, 4000), (2, 2, 20011), (32, 2, 3000), (40, 2, 700)])
+def test_tokens_whose_scores_are_all_minus_infinity_draw_no_weight(heads, kv, length):
+    """Keys of -inf under positive queries: ln of a sum of zeros is -inf, the output 0 and the weight drawn 0, as for
+    an empty sequence; the heads of other keys are not affected. Held whole, joined by the last CTA, by a launch."""
+    d = 64
+    p = Pair(heads, kv, d, 64, 2, -(-length // 64), seed=length)
+    k, v = p.randn(2 * length, kv, d), p.randn(2 * length, kv, d)
+    k[:length, 0] = -float("inf")                                 # sequence 0, key head 0
+    p.cache.append(k, v, counts=[length, length])
+    p.ora.append([0, 1], [length, length], f64(k), f64(v))
+    q = p.randn(2, heads, d).abs() + 0.125
+    p.cache.token_mass.uniform_(generator=p.g)
+    old = f64(p.cache.token_mass)
+    o, lse = p.cache.attention(q, lse=True, mass_decay=0.5)
+    g = heads // kv
+    assert not o[0, :g].any() and torch.all(lse[0, :g] == -np.inf)
+    assert torch.isfinite(o.float()).all() and torch.isfinite(lse[0, g:]).all() and torch.isfinite(lse[1]).all()
+    mass = f64(p.cache.token_mass)
+    p.ora.k[0, :length, 0] = 0.0                                  # the other heads' weights; these are not counted
+    for s in (0, 1):
+        _, w, _ = p.ora.weights(s, f64(q[s]))
+        ref = 0.5 * old[s, :length] + w[g if s == 0 else 0:].sum(0)
+        ka = np.abs(p.ora.k[s, :length])
+        dot = np.einsum("hgd,thd->hgt", np.abs(f64(q[s])).reshape(kv, g, d), ka).max()
+        dx = (d + 8) * U * p.ora.scale * dot
+        assert np.all(np.abs(mass[s, :length] - ref) <= (2 * dx + length * U + 2.0 ** -20 + 4 * U) * ref), s
+    p.ok()
