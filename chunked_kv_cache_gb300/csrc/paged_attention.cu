@@ -85,17 +85,20 @@ struct Geo {
   // step; 8 sessions, bf16: 152 us, 148 us. Rows of 64 bytes have more arithmetic than that gains
   // (64 sequences of 8192: 95 us, 98 us in step).
   static constexpr bool kInStep = kRowBytes > 64;
-  // Stretches end where items end (so many whole items each, or an item in so many pieces), where the largest
-  // is not above kWhole / 16 of an even one or kWholeExtra units more: fewer parts to join, and none twice.
-  // The first bound: DRAM serves the CTAs that are left faster (even stretches, whole items: 32 sequences of
-  // 4096 tokens, 1.19 times an even one, 82.9 us, 78.8 us; 32 of 3500 .. 4096, 1.28, 77.5 us, 76.5 us; 32 of
-  // 3000 .. 4096, 1.37, 73.1 us, 74.1 us), but arithmetic does not get faster (64 of 8192, rows of 64 bytes,
-  // 1.19: 92.3 us, 99.0 us). The second: a join costs as much as a few tiles (16 of 256, 3 more: 11.1 us,
-  // 7.3 us; 16 of 512, 6 more: 12.5 us, 10.8 us; 8 of 512, 8 more: 9.2 us, 10.6 us; rows of 64 bytes, 16 of
-  // 100 .. 1000, 5 more: 8.3 us, 8.8 us). Pieces: 16 of 768 in two 15.5 us, 13.4 us, 8 of 2048 in four
-  // 18.8 us, 17.4 us; where the rule tries them in vain the trial costs 0.1 us.
+  // Stretches end where items end (so many whole items each, or an item in so many pieces), where the largest,
+  // in units of the line, is not above kWhole / 16 of an even one or so many units more: fewer parts to join, and
+  // none twice. The ratio: DRAM serves the CTAs that are left faster (even stretches, whole items: 32 sequences of
+  // 4096 tokens, 1.19 times an even one, 85.3 us, 80.1 us; 32 of 3500 .. 4096, 1.27, 79.9 us, 77.9 us; 32 of
+  // 3000 .. 4096, 1.36, 74.1 us, 75.4 us), but arithmetic does not get faster (64 of 8192, rows of 64 bytes,
+  // 1.19: 93.2 us, 98.8 us). The units: a join costs as much as a few tiles. Where CTAs are left for pieces, these
+  // are the better choice from kWholeExtra on (even, whole, pieces: 16 of 512, 5.8 units more: 11.5, 10.9, 11.0 us;
+  // 16 of 640, 6.9: 12.9, 13.0, 12.2 us; rows of 64 bytes, 8 of 768, 3.9: 9.2, 8.2, 8.5 us; 16 of 1536, 4.6: 12.7,
+  // 12.6, 11.4 us); where there are none, whole items are, up to kAloneExtra (24 of 1280, 8.1: 26.8, 24.9 us; rows of
+  // 64 bytes, 24 of 2560, 4.4: 20.1, 19.0 us; 24 of 4096, 6.6: 25.7, 27.6 us). Where the rule tries pieces in vain the
+  // trial costs 0.1 us.
   static constexpr int kWhole = kInStep ? 21 : 18;
   static constexpr int kWholeExtra = kInStep ? 6 : 4;
+  static constexpr int kAloneExtra = kInStep ? 9 : 6;
   static constexpr int kStageBytes = 8192;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
   // A warp's 8 rows of D sums while the warps merge, in its free stage: rows four floats apart in
@@ -182,7 +185,7 @@ __device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
 struct SharedHead {
   int64_t cum[kMaxPagedSeqs + 1];       // units before each sequence of the batch
   int32_t len[kMaxPagedSeqs];
-  int32_t longest;                      // tiles of the longest sequence, and one
+  int32_t longest;                      // units of the longest item
   float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
 };
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
     for (int k = 1; k < kMaxPagedSeqs / 32; ++k) longest = max(longest, len[k]);
     longest = __reduce_max_sync(0xffffffffu, longest);
-    if (lane == 0) sh.longest = (longest + G::CT - 1) / G::CT + 1;
+    if (lane == 0) sh.longest = (longest + G::CT - 1) / G::CT + kItemCost;
   }
   __syncthreads();
   // sequences without a token: nothing to attend to
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     u0 = start(me * p.each);
     left = start((me + 1) * p.each) - u0;
     if (left == 0) return;
-  } else if (p.pieces > 1 && (sh.longest + 1 + 2 * p.pieces) * p.cut_cost <= bound) {
+  } else if (p.pieces > 1 && (sh.longest + 2 * p.pieces) * p.cut_cost <= bound) {
     // one of `pieces` equal pieces of an item, as far as it has tiles
     const int item = me / p.pieces, i = item / n_kv;
     if (i >= n) return;
@@ -1129,7 +1132,8 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   p.whole_cost = 16ll * p.each * slots;
   p.pieces = slots / items;
   p.cut_cost = p.pieces > 1 ? 16ll * slots / p.pieces : 0;
-  p.whole_extra = 16ll * slots * G::kWholeExtra;
+  const int extra = p.pieces > 1 ? G::kWholeExtra : G::kAloneExtra;
+  p.whole_extra = 16ll * slots * extra;
   p.drop_scores = static_cast<int64_t>(p.b.n) * p.c.cap * p.c.n_heads >= kDropScores;
   // Who joins: the last CTA to arrive (its four warps take rows in turn, sixteen parts at a time, about 1.6 us
   // a turn), or a launch of its own (about 2 us of the GPU and as much of the host, more CTAs than it can use
@@ -1139,7 +1143,7 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   const int turns = (p.c.group + 3) / 4 * ((parts + kJoinBatch - 1) / kJoinBatch);
   if (turns <= 2 + p.b.n * p.c.n_heads / 2048) p.items = nullptr;
   // no item is cut (see kWhole): nothing to join (1 sequence of 300 tokens, 16 heads: 9.8 us with the launch, 8.5 us)
-  if (p.each == 1 && (p.c.cap + G::CT - 1) / G::CT + 1 <= G::kWholeExtra) p.items = nullptr;
+  if (p.each == 1 && (p.c.cap + G::CT - 1) / G::CT + kItemCost <= extra) p.items = nullptr;
   cudaError_t e = launch_dependent(paged_attn_kernel<D, TYPE, NT, MASS>, static_cast<unsigned>(ctas), kThreads,
                                    kSmem<D, TYPE>, st, p);
   if (e != cudaSuccess) return e;

@@ -109,7 +109,7 @@ struct PagedAttnParams {
   int32_t pieces;          // pieces that an item is cut into (below 2: none)
   int64_t whole_cost;      // 16 * each * stretches
   int64_t cut_cost;        // 16 * stretches / pieces
-  int64_t whole_extra;     // 16 * kWholeExtra * stretches
+  int64_t whole_extra;     // 16 * stretches * kWholeExtra, or kAloneExtra
   bool drop_scores;        // the weights' launch drops the scores from L2
   float mass_decay;
   PagedBatch b;
