@@ -102,6 +102,8 @@ class PagedCache:
         """The numbers as 32-bit ones, to be kept while their address is used, and that address."""
         if seqs is None:
             return None, None
+        if isinstance(seqs, (bytes, bytearray)):
+            seqs = list(seqs)                        # an array would take them for its raw memory
         try:
             ids = array("i", seqs)
         except OverflowError:
