@@ -139,8 +139,9 @@ class PagedCache:
             return
         if more > len(self._free):
             raise RuntimeError(f"the pool has {len(self._free)} free pages, {more} are needed")
-        new = [self._free.pop() for _ in range(more)]
+        new = self._free[:-more - 1:-1]
         self.block_table[seq, len(have):need] = torch.tensor(new, dtype=torch.int32, device=self.device)
+        del self._free[-more:]                       # theirs once the table has them
         have.extend(new)
 
     def release(self, seq: int) -> None:
