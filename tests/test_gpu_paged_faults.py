@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle.paged import OraclePagedCache
 from tests.gpu_common import device
-from tests.test_gpu_paged import U, Pair, f64
+from tests.test_gpu_paged import E, U, Pair, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +152,36 @@ def test_tokens_whose_scores_are_all_minus_infinity_draw_no_weight(heads, kv, le
         dx = (d + 8) * U * p.ora.scale * dot
         assert np.all(np.abs(mass[s, :length] - ref) <= (2 * dx + length * U + 2.0 ** -20 + 4 * U) * ref), s
     p.ok()
+
+
+# ------------------------------------------------------------------ far rows, to the stated bounds
+def test_far_rows_meet_the_stated_bounds():
+    """Offsets past 32 bits with outputs, log-sum-exp and weights held to the bounds that near rows are held to."""
+    import chunked_kv_cache_gb300 as sr
+    dev = device()
+    kv, d, page, n_pages = 32, 128, 64, 10240          # 5.4 GB of keys, as much of values
+    k_pages = torch.empty(n_pages, page, kv, d, dtype=torch.bfloat16, device=dev)
+    v_pages = torch.empty_like(k_pages)
+    table = torch.tensor([[n_pages - 1, 1, n_pages - 9], [n_pages - 2, n_pages - 5, 4]], dtype=torch.int32, device=dev)
+    c = sr.PagedCache(kv, kv, d, page_tokens=page, n_pages=n_pages, max_seqs=2, max_pages=3, device=dev,
+                      buffers=dict(k_pages=k_pages, v_pages=v_pages, block_table=table))
+    ora = OraclePagedCache(kv, kv, d, 2, 192)
+    g = torch.Generator(device=dev).manual_seed(31)
+    counts = [180, 120]
+    k, v = (torch.randn(300, kv, d, device=dev, generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(2, kv, d, device=dev, generator=g).to(torch.bfloat16)
+    c.append(k, v, counts=counts)
+    ora.append([0, 1], counts, f64(k), f64(v))
+    o, lse = c.attention(q, lse=True, mass_decay=1.0)
+    ref, ref_lse, wv = ora.attention([0, 1], f64(q), 1.0)
+    o, lse, mass = f64(o), f64(lse), f64(c.token_mass)
+    for s, n in enumerate(counts):
+        dot = np.einsum("hd,thd->ht", np.abs(f64(q[s])), np.abs(ora.k[s, :n])).max(1)
+        dx = (d + 8) * U * ora.scale * dot
+        rel = 2 * dx + n * U + 2.0 ** -20
+        bound = E * np.abs(ref[s]) + (2.0 ** -15 + rel[:, None]) * wv[s] + n * 2.0 ** -31 * np.abs(ora.v[s, :n]).max()
+        assert np.all(np.abs(o[s] - ref[s]) <= bound), s
+        assert np.all(np.abs(lse[s] - ref_lse[s]) <= dx + n * U + 2.0 ** -20 + 4 * U * np.abs(ref_lse[s])), s
+        m = ora.mass[s, :n]
+        assert np.all(np.abs(mass[s, :n] - m) <= (rel.max() + 4 * U) * np.abs(m)), s
+    assert c.error_status() == 0
