@@ -4,11 +4,15 @@
 //   x_h(t) = scale * q_h . k(t),  o_h = sum_t e^(x_h(t) - lse_h) v(t),
 //   lse_h = ln sum_t e^x_h(t),    mass(t) <- decay * mass(t) + sum_h e^(x_h(t) - lse_h).
 //
-// Bound by the one read of the cache: a token's 2 D values per key/value head meet at
-// most 16 query heads. Every choice below serves that stream. (More query heads of one key
-// head are taken in equal parts that each read it, side by side, so that most of the reads end
-// in L2: 32 sequences of 4096 tokens and one key head of 128 take 19.7 us with 16 query heads,
-// 27.3 us with 32, 45.2 us with 64, 69.5 us with 128.)
+// With up to 16 query heads per key/value head it is bound by the one read of the cache, and
+// every choice below serves that stream. More query heads of one key head are taken in equal
+// parts of at most 16, each an item that reads the head for itself; parts lie side by side, so
+// that most of the reads end in L2, as far as 2, 4 or 8 divides the number of items per token.
+// That form is bound by the parts' own copies and products: 32 sequences of 4096 tokens and one
+// key head of 128 (10 us of bytes) take 19.7 us with 16 query heads, 27.2 us with 32, 45.5 us
+// with 64, 69.6 us with 128. Shares without large divisors up to 16 come in many parts and are
+// slow: 18 heads (2 parts of 9) 25.6 us, but 17 (17 of one) and 34 (17 of 2) 110.8 us; 72 (6 of
+// 12) 56.9 us, but 71 (71 of one) 426.6 us, with a head dim of 64 256.2 us.
 //
 // Work split. A sequence and key/value head (an item) is cut into tiles of CT
 // tokens; the launch's tiles, item after item, form one line, and every CTA takes an
@@ -30,7 +34,7 @@
 //
 // The products are transposed: scores = keys (16 rows) x queries (8 columns), sums =
 // values^T (16 dims) x weights (8 columns), so that a group of up to 8 query heads wastes
-// nothing that 16 rows of queries would (e4m3: 97 us with queries as rows, 94 us so). The
+// nothing that 16 rows of queries would (64 sequences of 4096 tokens, e4m3: 94.3 us with queries as rows, 89.5 us so). The
 // weights turn from the one product's result into the other's operand by an 8x8
 // transposition between registers and never leave them. Warp-level products fit here: the
 // rows that a tcgen05 tile would need (128) are not there, and the tensor pipe is idle for
@@ -191,8 +195,9 @@ struct SharedHead {
 };
 
 // A place on the line of tiles. Each item takes kItemCost units before its tiles:
-// what changing items costs a CTA, in tiles (16 sequences of 300 .. 3000 tokens of 64: 13.9 us with
-// 1, 11.9 us with 2, 12.7 us with 3; 16 of 1000 .. 8192: 44.4 us, 42.8 us, 43.7 us).
+// what changing items costs a CTA, in tiles (with 1, 2, 3: 16 sequences of 300 .. 3000 tokens of 64 13.9, 12.2,
+// 12.9 us; 16 of 1000 .. 8192 with 40 heads 43.8, 42.2, 43.0 us; 32 of 100 .. 2000 21.3, 20.7, 22.1 us; slower: 64 of
+// 1 .. 16384 80.3, 80.7, 80.6 us; 64 of 100 .. 600 20.5, 20.7, 20.9 us).
 constexpr int kItemCost = 2;
 // Up to kSpread neighbouring heads are read side by side by neighbouring CTAs, so that a
 // token's row, whole in memory, is read at about one time. Rows of 64 bytes per head need
@@ -1020,7 +1025,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
 // scores meanwhile (8 us for the 17 MB of 32 sequences of 4096 tokens; 1 us if all go to one small
 // place). So in large batches they are stored to leave L2 last and dropped from it once read (DROP):
 // 94.5 us in all without that, 91.2 us with it; 8 of 16384 101.3 us, 98.1 us; 32 of 2048, at
-// kDropScores, 50.5 us, 49.7 us; below, 32 of 512, 19.6 us, 20.4 us.
+// kDropScores, 50.5 us, 49.7 us; below, 32 of 512, 19.6 us, 20.4 us. The rule goes by the capacity, since only the device
+// knows the lengths: short sequences in a large capacity pay that last difference.
 constexpr int64_t kDropScores = 1ll << 21;
 constexpr int kMassTokens = 128;
 constexpr int kMassShare = 8;

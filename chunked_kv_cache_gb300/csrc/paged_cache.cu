@@ -160,14 +160,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 // that no move sees another.
 // Latency bound (barriers, dependent loads, code that runs once) until the moves, which are
 // HBM bound: 512 of 16896 tokens go from each of 16 sequences, 1024 values to a row, in
-// 28 us, where the 70 MB alone would take 10 us. One token of a sequence (the least weight, no
+// 30 us, where the 70 MB alone would take 10 us. One token of a sequence (the least weight, no
 // digits) goes in 4 us of the GPU from 8 sequences of 1025 tokens, 5 us from 32 of 4097.
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-// Up to here the first CTA of a cluster looks for the one lightest token by itself (8 sequences of 1025 tokens:
-// 6.2 us with an append where the clusters did, 5.9 us so; 16 of 8001: 7.3 us, 8.0 us).
+// Up to here the first CTA of a cluster looks for the one lightest token by itself (with an append, by itself and by
+// the cluster: 8 sequences of 1025 tokens 5.9, 7.2 us, of 4097 6.8, 7.3 us, of 8001 7.2, 7.3 us; 16 of 4601 7.4, 7.5 us,
+// of 6001 7.7, 7.4 us; 32 of 4097 7.7, 7.9 us, of 4601 7.9, 7.9 us, of 8001 8.4, 7.9 us).
 constexpr int32_t kAlone = 4608;
 constexpr int kCandidates = 512;      // keys gathered to find the cut among them
 constexpr int kKeyLimit = 45056;      // keys a CTA can hold; longer stretches are read again from global memory

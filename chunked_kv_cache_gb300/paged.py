@@ -29,9 +29,12 @@ class PagedCache:
     buffers: a dict with any of these names, used in place and as found. Sequences
     whose block table the caller does not fill get their pages from reserve().
 
-    Calls run on the current stream of the cache's device, and two of one cache must not
-    run at the same time (they share a workspace). seqs: distinct rows of the
-    block table (host integers); None stands for the first rows, as many as the call has.
+    Calls run on the current stream of the cache's device, which must be the current device, and
+    two of one cache must not run at the same time (they share a workspace). The cache is
+    made on the current stream too: whoever goes on with it on another stream orders that one
+    behind, and keeps the cache until the work there is done (its memory returns to torch's
+    allocator, as a tensor's does). seqs: distinct rows of the block table (host integers), at
+    most SR_MAX_PAGED_SEQS; None stands for the first rows, as many as the call has.
     """
 
     def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, *, page_tokens: int = 64, n_pages: int,
@@ -145,7 +148,8 @@ class PagedCache:
         have.extend(new)
 
     def release(self, seq: int) -> None:
-        """Empty sequence `seq` and give its pages back to the pool."""
+        """Empty sequence `seq` and give its pages back to the pool (the only way back: a sequence
+        that tokens were evicted from keeps its pages, since the host does not know its length)."""
         if self._free is None:
             raise RuntimeError("the caller's block table is the caller's to fill")
         self.reset([seq])
@@ -182,7 +186,8 @@ class PagedCache:
                   lse: torch.Tensor | bool | None = None, mass_decay: float | None = None):
         """Attention of one new token per sequence, q [n][n_heads][head_dim]; returns out, or (out, lse)
         when lse is True or a tensor [n][n_heads] fp32. mass_decay: a number >= 0 also accumulates
-        token_mass = mass_decay * token_mass + the tokens' weights summed over heads."""
+        token_mass = mass_decay * token_mass + the tokens' weights summed over heads (of all sequences or, where
+        they share pages and hold more tokens than the pool, of none: error_status() tells)."""
         n = q.shape[0]
         shape = (n, self.n_heads, self.head_dim)
         self._check("q", q, shape)
@@ -210,7 +215,8 @@ class PagedCache:
     def evict(self, budget: int, n_sink: int = 0, n_recent: int = 0, seqs: Sequence[int] | None = None) -> None:
         """Keep at most `budget` tokens per sequence: positions below n_sink, the last n_recent
         positions, and the tokens with the largest token_mass (None: the first
-        SR_MAX_PAGED_SEQS rows, or all where there are fewer)."""
+        SR_MAX_PAGED_SEQS rows, or all where there are fewer). A sequence whose moves meet an entry that
+        is no page of the pool stays as it is: error_status() tells."""
         if not (0 <= n_sink < 1 << 31 and 0 <= n_recent < 1 << 31 and budget >= 0):
             raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_evict")
         budget = min(budget, (1 << 31) - 1)                      # no sequence is longer

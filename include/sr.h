@@ -448,6 +448,8 @@ SR_API sr_status sr_layer_commit(sr_session* const* sessions, const sr_window* w
  * use the current device, which must be the one sr_paged_init ran on (SR_ERR_STATE).
  * Calls of one cache share its workspace: two that overlap on the GPU (two streams, or
  * two captured graphs replayed at once) race on it, as calls of a session do.
+ * sr_paged_init clears them on its stream: a first call on another stream has to be ordered behind it, and the
+ * buffers have to outlive the calls of every stream.
  * Caches that share pages need a workspace each and may run at the same time as long as
  * none writes what another reads. Sequences may share pages that are only read: the pages
  * that new tokens go to, and every page of a sequence that is evicted from, must be its own.
@@ -465,7 +467,8 @@ enum { SR_PAGE_BF16 = 0, SR_PAGE_E4M3 = 1 };
 
 typedef struct {
   int32_t n_heads;         /* query heads; a multiple of n_kv_heads. More than SR_MAX_PAGED_GROUP of one key/value head are
-                              taken in equal parts of at most that many, which each read the head */
+                              taken in equal parts of at most that many, which each read the head: a share with no large
+                              divisor up to that (17, 34, 71) is several times slower than the next one that has one */
   int32_t n_kv_heads;      /* key/value heads >= 1; query head h reads head h / (n_heads / n_kv_heads) */
   int32_t head_dim;        /* 64 or 128 */
   int32_t page_tokens;     /* tokens per page: a multiple of 16, at most 1024 */
@@ -547,7 +550,8 @@ SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int3
  * weights, the others stay in place, and what lies behind the new length is left as it was. A sequence
  * is evicted from whole or not at all: if a token that moves, or the index it would take, lies on an entry that is
  * no page of the pool, the sequence is left as it was, longer than its budget, and err_word receives
- * SR_DEVERR_BAD_PAGE; the others are not affected.
+ * SR_DEVERR_BAD_PAGE; the others are not affected. The block table is not changed: the pages behind the new
+ * length stay the sequence's.
  * budget >= 1, n_sink, n_recent >= 0, n_sink + n_recent <= budget. Needs token_mass
  * (SR_ERR_STATE). Pages of an evicted sequence must not be shared with another one.
  */
