@@ -18,7 +18,8 @@ from ._native import (SrConfig, SrBuffers, SrError, sr_session_init, sr_session_
                       sr_cache_commit_frames, SrChunkPlan, sr_window_attention, sr_rope3d_qk_at,
                       sr_rope3d_qk_dev, sr_chunk_attention_dev, sr_cache_commit_dev, SR_MAX_BATCH,
                       SrPagedConfig, SrPagedBuffers, sr_paged_workspace_bytes, sr_paged_init, sr_paged_free,
-                      sr_paged_reset, sr_paged_append, sr_paged_attention, sr_paged_evict, sr_paged_locate)
+                      sr_paged_reset, sr_paged_append, sr_paged_attention, sr_paged_evict, sr_paged_locate,
+                      sr_paged_prompt_attention, sr_paged_read)
 from .paged import PagedCache
 
 __all__ = [
@@ -30,7 +31,7 @@ __all__ = [
     "sr_window_attention", "sr_rope3d_qk_at", "sr_rope3d_qk_dev", "sr_chunk_attention_dev",
     "sr_cache_commit_dev", "PagedCache", "SrPagedConfig", "SrPagedBuffers", "sr_paged_workspace_bytes",
     "sr_paged_init", "sr_paged_free", "sr_paged_reset", "sr_paged_append", "sr_paged_attention",
-    "sr_paged_evict", "sr_paged_locate",
+    "sr_paged_evict", "sr_paged_locate", "sr_paged_prompt_attention", "sr_paged_read",
 ]
 
 _BF16 = torch.bfloat16

@@ -29,6 +29,7 @@ SR_MAX_PAGED_SEQS = 256
 SR_MAX_PAGED_GROUP = 16
 SR_PAGE_BF16 = 0
 SR_PAGE_E4M3 = 1
+SR_PAGE_INT4 = 4
 
 # every extern "C" symbol that include/sr.h declares
 EXPORTS = (
@@ -40,7 +41,7 @@ EXPORTS = (
     "sr_chunk_attention_dev", "sr_cache_commit_dev", "sr_window_count", "sr_plan_window",
     "sr_plan_attention", "sr_rope_angle", "sr_layer_rope_gather", "sr_layer_commit",
     "sr_paged_workspace_bytes", "sr_paged_init", "sr_paged_free", "sr_paged_reset", "sr_paged_append",
-    "sr_paged_attention", "sr_paged_evict", "sr_paged_locate",
+    "sr_paged_attention", "sr_paged_evict", "sr_paged_locate", "sr_paged_prompt_attention", "sr_paged_read",
 )
 
 
@@ -149,6 +150,8 @@ def lib() -> ctypes.CDLL:
         L.sr_paged_reset.argtypes = [vp, vp, i32, vp]
         L.sr_paged_append.argtypes = [vp, vp, vp, i32, vp, vp, vp]
         L.sr_paged_attention.argtypes = [vp, vp, i32, vp, vp, vp, ctypes.c_float, vp]
+        L.sr_paged_prompt_attention.argtypes = [vp, vp, vp, i32, vp, vp, vp, i32, vp]
+        L.sr_paged_read.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp]
         L.sr_paged_evict.argtypes = [vp, vp, i32, i32, i32, i32, vp]
         L.sr_paged_locate.argtypes = [ctypes.POINTER(SrPagedConfig), pi32, i64, ctypes.POINTER(i64)]
         L.sr_device_error_status.argtypes = [i32]
@@ -370,6 +373,15 @@ def sr_paged_append(handle: int, seqs, n_tokens, n: int, k: int, v: int, stream:
 def sr_paged_attention(handle: int, seqs, n: int, q: int, o: int, lse: int, mass_decay: float, stream: int) -> None:
     _check(lib().sr_paged_attention(handle, seqs, n, q, o, lse or None, mass_decay, stream or None),
            "sr_paged_attention")
+
+
+def sr_paged_prompt_attention(handle: int, seqs, n_tokens, n: int, q: int, o: int, lse: int, causal: bool, stream: int) -> None:
+    _check(lib().sr_paged_prompt_attention(handle, seqs, n_tokens, n, q, o, lse or None, 1 if causal else 0, stream or None),
+           "sr_paged_prompt_attention")
+
+
+def sr_paged_read(handle: int, seqs, first, n_tokens, n: int, k: int, v: int, stream: int) -> None:
+    _check(lib().sr_paged_read(handle, seqs, first, n_tokens, n, k, v, stream or None), "sr_paged_read")
 
 
 def sr_paged_evict(handle: int, seqs, n: int, budget: int, n_sink: int, n_recent: int, stream: int) -> None:

@@ -31,7 +31,7 @@ sr_status validate(const sr_paged_config& c) {
       c.max_seqs > 65536 || c.max_pages < 1)
     return SR_ERR_INVALID_ARG;
   if (c.head_dim != 64 && c.head_dim != 128) return SR_ERR_UNSUPPORTED;
-  if (c.page_type != SR_PAGE_BF16 && c.page_type != SR_PAGE_E4M3) return SR_ERR_UNSUPPORTED;
+  if (c.page_type != SR_PAGE_BF16 && c.page_type != SR_PAGE_E4M3 && c.page_type != SR_PAGE_INT4) return SR_ERR_UNSUPPORTED;
   if (c.n_heads % c.n_kv_heads != 0) return SR_ERR_INVALID_ARG;
   if (c.page_tokens % 16 != 0 || c.page_tokens > 1024) return SR_ERR_UNSUPPORTED;
   if (!std::isfinite(c.softmax_scale)) return SR_ERR_INVALID_ARG;
@@ -103,6 +103,38 @@ sr_status take_seqs(sr_paged_cache* c, const int32_t* seqs, int32_t n, int32_t* 
   return SR_OK;
 }
 
+// The rows of a call: row0[0..n] from the sequences' counts.
+sr_status take_counts(const int32_t* n_tokens, int32_t n, int32_t* row0) {
+  int64_t rows = 0;
+  for (int i = 0; i < n; ++i) {
+    const int32_t count = n_tokens ? n_tokens[i] : 1;
+    if (count < 0) return SR_ERR_INVALID_ARG;
+    row0[i] = static_cast<int32_t>(rows);
+    rows += count;
+    if (rows > (int64_t(1) << 28)) return SR_ERR_INVALID_ARG;
+  }
+  row0[n] = static_cast<int32_t>(rows);
+  return SR_OK;
+}
+
+// The CTAs that take them: cta0[0..n].
+void share_rows(const int32_t* row0, int32_t n, int32_t rows_per_cta, int32_t* cta0) {
+  int64_t ctas = 0;
+  for (int i = 0; i < n; ++i) {
+    cta0[i] = static_cast<int32_t>(ctas);
+    ctas += (static_cast<int64_t>(row0[i + 1]) - row0[i] + rows_per_cta - 1) / rows_per_cta;
+  }
+  cta0[n] = static_cast<int32_t>(ctas);
+}
+
+// The view's heads as attention takes them: items of at most SR_MAX_PAGED_GROUP query heads.
+void take_heads(const sr_paged_cache* c, sr::PagedView& v, int32_t& kv_heads, uint32_t& head_magic) {
+  kv_heads = c->cfg.n_kv_heads;
+  v.n_kv = c->cfg.n_heads / v.group;
+  const uint32_t parts = static_cast<uint32_t>(v.n_kv / kv_heads);       // of a key/value head's query heads
+  head_magic = ((1u << 22) + parts - 1) / parts;                         // exact for heads and parts up to 1024
+}
+
 template <typename T>
 T* ws_at(const sr_paged_cache* c, size_t offset) {
   return reinterpret_cast<T*>(static_cast<char*>(c->buf.workspace) + offset);
@@ -152,7 +184,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.seq_pos = b.seq_pos;
   v.token_pos = b.token_pos;
   v.token_mass = b.token_mass;
-  v.kv_exp = cfg->page_type == SR_PAGE_E4M3 ? b.kv_exp : nullptr;
+  v.kv_exp = cfg->page_type != SR_PAGE_BF16 ? b.kv_exp : nullptr;
   v.err_word = b.err_word;
   v.n_heads = cfg->n_heads;
   v.n_kv = cfg->n_kv_heads;
@@ -206,25 +238,15 @@ sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const int32_t*
   sr_status st = take_seqs(c, seqs, n, p.id);
   if (st != SR_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16)) return SR_ERR_ALIGN;
-  int64_t rows = 0, ctas = 0;
-  for (int i = 0; i < n; ++i) {
-    const int32_t count = n_tokens ? n_tokens[i] : 1;
-    if (count < 0) return SR_ERR_INVALID_ARG;
-    p.row0[i] = static_cast<int32_t>(rows);
-    rows += count;
-    if (rows > (int64_t(1) << 28)) return SR_ERR_INVALID_ARG;
-  }
-  p.row0[n] = static_cast<int32_t>(rows);
+  st = take_counts(n_tokens, n, p.row0);
+  if (st != SR_OK) return st;
+  const int32_t rows = p.row0[n];
   st = on_device(c);
   if (st != SR_OK) return st;
   if (rows == 0) return SR_OK;
   if (!k || !v) return SR_ERR_INVALID_ARG;
-  p.rows_per_cta = sr::paged_append_rows_per_cta(c->cfg.n_kv_heads, c->cfg.head_dim, rows);
-  for (int i = 0; i < n; ++i) {
-    p.cta0[i] = static_cast<int32_t>(ctas);
-    ctas += (static_cast<int64_t>(p.row0[i + 1]) - p.row0[i] + p.rows_per_cta - 1) / p.rows_per_cta;
-  }
-  p.cta0[n] = static_cast<int32_t>(ctas);
+  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, rows);
+  share_rows(p.row0, n, p.rows_per_cta, p.cta0);
   p.c = c->view;
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.v = static_cast<const __nv_bfloat16*>(v);
@@ -245,10 +267,7 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   if (st != SR_OK) return st;
   p.b.n = n;
   p.c = c->view;
-  p.kv_heads = c->cfg.n_kv_heads;
-  p.c.n_kv = c->cfg.n_heads / p.c.group;
-  const uint32_t parts = static_cast<uint32_t>(p.c.n_kv / p.kv_heads);     // of a key/value head's query heads
-  p.head_magic = ((1u << 22) + parts - 1) / parts;                         // exact for heads and parts up to 1024
+  take_heads(c, p.c, p.kv_heads, p.head_magic);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -262,6 +281,53 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   p.score_tiles = c->layout.score_tiles;
   p.mass_decay = mass_decay;
   return sr::launch_paged_attention(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
+}
+
+sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, const int32_t* n_tokens, int32_t n,
+                                    const void* q, void* o, float* lse, int32_t causal, void* stream) {
+  if (!c) return SR_ERR_INVALID_ARG;
+  sr::PromptParams p;
+  sr_status st = take_seqs(c, seqs, n, p.id);
+  if (st != SR_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4)) return SR_ERR_ALIGN;
+  st = take_counts(n_tokens, n, p.row0);
+  if (st == SR_OK) st = on_device(c);
+  if (st != SR_OK) return st;
+  if (p.row0[n] == 0) return SR_OK;
+  if (!q || !o) return SR_ERR_INVALID_ARG;
+  p.n = n;
+  p.causal = causal != 0;
+  p.c = c->view;
+  take_heads(c, p.c, p.kv_heads, p.head_magic);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  return sr::launch_paged_prompt(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
+}
+
+sr_status sr_paged_read(sr_paged_cache* c, const int32_t* seqs, const int32_t* first, const int32_t* n_tokens, int32_t n,
+                        void* k, void* v, void* stream) {
+  if (!c) return SR_ERR_INVALID_ARG;
+  sr::ReadParams p;
+  sr_status st = take_seqs(c, seqs, n, p.id);
+  if (st != SR_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16)) return SR_ERR_ALIGN;
+  for (int i = 0; i < n; ++i) {
+    p.first[i] = first ? first[i] : -1;
+    if (first && first[i] < 0) return SR_ERR_INVALID_ARG;
+  }
+  st = take_counts(n_tokens, n, p.row0);
+  if (st == SR_OK) st = on_device(c);
+  if (st != SR_OK) return st;
+  if (p.row0[n] == 0) return SR_OK;
+  if (!k || !v) return SR_ERR_INVALID_ARG;
+  p.n = n;
+  p.c = c->view;
+  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, p.row0[n]);
+  share_rows(p.row0, n, p.rows_per_cta, p.cta0);
+  p.k = static_cast<__nv_bfloat16*>(k);
+  p.v = static_cast<__nv_bfloat16*>(v);
+  return sr::launch_paged_read(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
 }
 
 sr_status sr_paged_evict(sr_paged_cache* c, const int32_t* seqs, int32_t n, int32_t budget, int32_t n_sink,

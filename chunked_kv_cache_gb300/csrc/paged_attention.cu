@@ -74,14 +74,16 @@ constexpr int kThreads = kWarps * 32;
 // Two CTAs of three stages per warp fill an SM's shared memory with 128 KB of copies in flight; three
 // CTAs of two stages have 96 KB and were slower (one sequence of 131071 tokens: 87 us, 100 us) or no faster.
 constexpr int kCtasPerSm = 2;
-constexpr int kStages = 3;
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D, int TYPE>
 struct Geo {
+  static constexpr bool kRecords = TYPE == SR_PAGE_INT4;
   static constexpr int kRowBytes = D * (TYPE == SR_PAGE_BF16 ? 2 : 1);   // a token's keys (or values) of one head
   static constexpr int kChunks = kRowBytes / 16;
-  static constexpr int KT = 4096 / kRowBytes;      // tokens per warp and tile: 4 KB of keys, 4 KB of values
+  // tokens per warp and tile: 4 KB of keys, 4 KB of values; of records, 2304 bytes each
+  static constexpr int KT = kRecords ? 4096 / D : 4096 / kRowBytes;
+  static constexpr int kStages = kRecords ? 5 : 3;
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   // Whether the warps take their tiles in step. Nothing in them depends on it, but warps that drift apart
@@ -103,7 +105,8 @@ struct Geo {
   static constexpr int kWhole = kInStep ? 21 : 18;
   static constexpr int kWholeExtra = kInStep ? 6 : 4;
   static constexpr int kAloneExtra = kInStep ? 9 : 6;
-  static constexpr int kStageBytes = 8192;
+  static constexpr int kHalfBytes = kRecords ? KT / 16 * record_bytes(D) : 4096;   // a stage's keys, or its values
+  static constexpr int kStageBytes = 2 * kHalfBytes;
   static constexpr int kStageArea = kWarps * kStages * kStageBytes;
   // A warp's 8 rows of D sums while the warps merge, in its free stage: rows four floats apart in
   // banks beyond a multiple of 32, so that stores and loads spread over all of them.
@@ -172,6 +175,53 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+// ---- 4-bit codes as fp16. A mask puts a code c into the fraction of 16 (16 + c / 32) or of 1 (1 + c / 32); one fused
+// product and sum with its scale s then leaves (c - 8) / 32 * s, exactly: at most 7 significant bits, never below fp16's
+// smallest number. Four pairs of one word in 9 instructions, scale and all.
+__device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+// What a decoding needs of a pair of scales.
+struct ScalePair {
+  uint32_t s, off16, off1;
+};
+__device__ __forceinline__ ScalePair scale_pair(uint32_t s) {
+  return {s, half2_mul(s, 0xCC10CC10u), half2_mul(s, 0xBD00BD00u)};     // -16.25 s, -1.25 s
+}
+// y[i]: the i-th value of the word's low unit and of its high one.
+__device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const ScalePair& s) {
+  const uint32_t z = __byte_perm(w, 0, 0x2301);
+  y[0] = half2_fma((w & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
+  y[1] = half2_fma((w & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
+  y[2] = half2_fma((z & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
+  y[3] = half2_fma((z & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
+}
+constexpr float kDecoded = 32.f;      // a value is so many times what decode_word leaves
+
+__device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+               : "memory");
+}
+constexpr uint64_t kCopyTimeoutNs = 2000000000ull;
+
+// N neighbouring words of shared memory
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], uint32_t addr) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+  else
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
+}
 // two e4m3 values (the low 16 bits) as fp16, exactly
 __device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
   uint32_t y;
@@ -192,6 +242,8 @@ struct SharedHead {
   int32_t longest;                      // units of the longest item
   float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
+  int abort;                            // a copy never came: err_word tells, the outputs are void
+  uint64_t full[kWarps][6];             // 4-bit pages: a stage's copies have landed
 };
 
 // A place on the line of tiles. Each item takes kItemCost units before its tiles:
@@ -332,6 +384,8 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
 template <int D, int TYPE, int NT, bool MASS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using G = Geo<D, TYPE>;
+  constexpr int kStages = G::kStages;
+  static_assert(kStages <= 6, "more stages than barriers");
   extern __shared__ __align__(128) uint8_t smem[];
   SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea);
   grid_dep_launch_dependents();
@@ -347,6 +401,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
       id[k] = p.b.id[lane * (kMaxPagedSeqs / 32) + k];
       asm volatile("" : "+r"(id[k]));
     }
+  }
+  const WaitCtx wc{&sh.abort, c.err_word, kCopyTimeoutNs};
+  if constexpr (G::kRecords) {          // the first barrier below makes them visible
+    if (threadIdx.x == 0) sh.abort = 0;
+    if (lane < kStages) mbar_init(&sh.full[warp][lane], 1);
+    mbar_fence_init();
   }
   grid_dep_wait();
   // S neighbouring CTAs take the same stretch for S neighbouring key/value heads
@@ -468,7 +528,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   [[maybe_unused]] uint64_t keep;      // for the scores
   if constexpr (MASS) keep = p.drop_scores ? l2_policy_evict_last() : l2_policy_evict_normal();
   int32_t page[G::kGroups];
+  // Records: lane g fetches and copies group g's keys, lane kGroups + g its values.
+  const int my_group = lane % G::kGroups, my_half = lane / G::kGroups;
+  [[maybe_unused]] uint32_t phases = 0;           // bit of a stage: the parity its copies complete next
   auto fetch_pages = [&] {
+    if constexpr (G::kRecords) {
+      const int32_t tok = load.tile * G::CT + warp * G::KT + my_group * 16;
+      page[0] = my_half < 2 && tok < load.len
+                    ? c.table[static_cast<int64_t>(p.b.id[load.i]) * c.max_pages + page_of_group(tok >> 4, c.magic)] : -1;
+      return;
+    }
     const int32_t* table = c.table + static_cast<int64_t>(p.b.id[load.i]) * c.max_pages;
 #pragma unroll
     for (int g = 0; g < G::kGroups; ++g) {
@@ -477,9 +546,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     }
   };
   fetch_pages();
+  auto issue_records = [&](int stage) {
+    if (left_load <= 0) return;
+    const int32_t tok = load.tile * G::CT + warp * G::KT + my_group * 16;
+    const bool held = my_half < 2 && tok < load.len, good = held && page[0] >= 0 && page[0] < c.n_pages;
+    const uint32_t ready = __ballot_sync(0xffffffffu, good), all = __ballot_sync(0xffffffffu, held);
+    constexpr uint32_t kMask = (1u << G::kGroups) - 1u;
+    bad = (bad & ~(kMask << (stage * G::kGroups))) | ((all & ~ready & kMask) << (stage * G::kGroups));
+    uint64_t* bar = &sh.full[warp][stage];
+    if (lane == 0) {
+      if (all & ~ready) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
+      mbar_arrive_expect_tx(bar, __popc(ready) * record_bytes(D));
+    }
+    __syncwarp();
+    if (good) {
+      const int32_t slot = tok - page_of_group(tok >> 4, c.magic) * c.page_tokens;
+      const int64_t at = record_at(page[0], slot, kv_head(load.h * S + sub), p.kv_heads, c.page_tokens, D);
+      copy_bulk(stage0 + stage * G::kStageBytes + my_half * G::kHalfBytes + my_group * record_bytes(D),
+                static_cast<const char*>(my_half == 0 ? c.k_pages : c.v_pages) + at, record_bytes(D), bar, policy);
+    }
+    cursor_next<G::CT>(load, sh, n_kv, left_load);
+    if (left_load > 0) fetch_pages();
+  };
   auto issue = [&](int stage) {
+    if constexpr (G::kRecords) {
+      issue_records(stage);
+      return;
+    }
     if (left_load > 0) {
-      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
+      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + G::kHalfBytes;
 #pragma unroll
       for (int g = 0; g < G::kGroups; ++g) {
         const int32_t tok = load.tile * G::CT + warp * G::KT + g * 16;
@@ -540,6 +635,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             qb[t][kk][x] = r < group ? *reinterpret_cast<const uint32_t*>(qp + r * D + kk * 16 + 8 * x + 2 * j4) : 0u;
+        } else if constexpr (TYPE == SR_PAGE_INT4) {
+          // pairs as the decoding of a word of keys leaves them: values i and i + 4 of its eight
+          if (kk % 2 == 0) {
+            const uint4 raw = r < group ? *reinterpret_cast<const uint4*>(qp + r * D + kk * 16 + 8 * j4) : make_uint4(0u, 0u, 0u, 0u);
+            qb[t][kk][0] = __byte_perm(raw.x, raw.z, 0x5410);
+            qb[t][kk][1] = __byte_perm(raw.x, raw.z, 0x7632);
+            qb[t][kk + 1][0] = __byte_perm(raw.y, raw.w, 0x5410);
+            qb[t][kk + 1][1] = __byte_perm(raw.y, raw.w, 0x7632);
+          }
         } else {
           // the order of the dims in which a 16-byte row of keys arrives: four neighbours per lane
           const uint2 raw = r < group ? *reinterpret_cast<const uint2*>(qp + r * D + kk * 16 + 4 * j4) : make_uint2(0u, 0u);
@@ -559,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     // log2-scaled scores = product * xs, of this lane's heads 8 t + 2 j4 and the next
     float xs[NT][2];
     {
-      const float scale = c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv_head(item_h)])) : 1.f);
+      const float scale = c.scale_log2 * (G::kRecords ? kDecoded : 1.f) *
+                          (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv_head(item_h)])) : 1.f);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x = scale;
@@ -609,12 +714,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
       issue((stage + kStages - 1) % kStages);
-      copy_wait<kStages - 1>();
+      if constexpr (G::kRecords) {
+        wait_bounded(&sh.full[warp][stage], phases >> stage & 1u, wc, 0x21);
+        phases ^= 1u << stage;
+      } else {
+        copy_wait<kStages - 1>();
+      }
       if constexpr (G::kInStep)
         __syncthreads();
       else
         __syncwarp();
-      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + 4096;
+      const uint32_t ks = stage0 + stage * G::kStageBytes, vs = ks + G::kHalfBytes;
       const int32_t tok = tile * G::CT + warp * G::KT;
       int32_t live[G::kGroups], any = 0;
 #pragma unroll
@@ -653,6 +763,33 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
                 mma16816<TYPE>(s2[g][t], b[0], b[1], b[2], b[3], qb[t][kk + 1][0], qb[t][kk + 1][1]);
               }
             }
+        } else if constexpr (TYPE == SR_PAGE_INT4) {
+          // a word is eight neighbouring dims of one key: two steps of four. Its scale: of keys r8 and r8 + 8, the
+          // first or the second block of the chunk's two.
+          const uint32_t pick = 0x4040u | (j4 >> 1) * 0x0101u;
+#pragma unroll
+          for (int g = 0; g < G::kGroups; ++g) {
+            const uint32_t rec = ks + g * record_bytes(D);
+            uint32_t sc[2][D / 64];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) load_words(sc[x], rec + 8 * D + (r8 + 8 * x) * (D / 16));
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ch += 2) {
+              uint32_t a[4];
+              ldsm4(a, rec + ch * 256 + lane * 16);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t lo[4], hi[4];
+                decode_word(lo, a[2 * y], scale_pair(__byte_perm(sc[0][ch / 2], 0, pick + y * 0x0202u) << 7));
+                decode_word(hi, a[2 * y + 1], scale_pair(__byte_perm(sc[1][ch / 2], 0, pick + y * 0x0202u) << 7));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  mma16816<TYPE>(s[g][t], lo[0], hi[0], lo[1], hi[1], qb[t][2 * (ch + y)][0], qb[t][2 * (ch + y)][1]);
+                  mma16816<TYPE>(s2[g][t], lo[2], hi[2], lo[3], hi[3], qb[t][2 * (ch + y) + 1][0], qb[t][2 * (ch + y) + 1][1]);
+                }
+              }
+            }
+          }
         } else {
 #pragma unroll
           for (int kk = 0; kk < D / 16; kk += 2)
@@ -776,6 +913,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
                 mma16816<TYPE>(o[t][k + 1], b[0], b[1], b[2], b[3], w_low[g][t][0], w_low[g][t][1]);
               }
             }
+        } else if constexpr (TYPE == SR_PAGE_INT4) {
+          // a transposed 16-bit element is four neighbouring dims of one key, so that a decoded pair is one dim of two
+          // keys: a product's rows 0-7 are the dims 4 r + 0 (or 2) of the chunk, rows 8-15 the next ones. Tokens that are
+          // not there, or whose record is not, get a scale of zero.
+          const uint32_t pick = 0x0400u + (r8 >> 2) * 0x0101u;
+#pragma unroll
+          for (int g = 0; g < G::kGroups; ++g) {
+            const uint32_t rec = vs + g * record_bytes(D);
+            uint32_t sc[2][2 * (D / 64)], keep_scale[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              load_words(sc[x], rec + 8 * D + (2 * j4 + 8 * x) * (D / 16));
+              const int left_here = live[g] - 2 * j4 - 8 * x;
+              keep_scale[x] = left_here >= 2 ? 0x7F807F80u : left_here == 1 ? 0x00007F80u : 0u;
+            }
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ch += 2) {
+              uint32_t a[4];
+              ldsm4t(a, rec + ch * 256 + lane * 16);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t v0[4], v1[4];
+                auto pair_of = [&](int x) {
+                  return scale_pair(__byte_perm(sc[x][ch / 2], sc[x][D / 64 + ch / 2], pick + y * 0x0202u) << 7 & keep_scale[x]);
+                };
+                decode_word(v0, a[2 * y], pair_of(0));
+                decode_word(v1, a[2 * y + 1], pair_of(1));
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                  mma16816<TYPE>(o[t][2 * (ch + y)], v0[0], v0[1], v1[0], v1[1], w[g][t][0], w[g][t][1]);
+                  mma16816<TYPE>(o[t][2 * (ch + y) + 1], v0[2], v0[3], v1[2], v1[3], w[g][t][0], w[g][t][1]);
+                }
+              }
+            }
+          }
         } else {
           // a transposed 16-bit element is two neighbouring dims of one key: rows 0-7 of the
           // product are the even dims, rows 8-15 the odd ones
@@ -819,7 +991,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     const bool whole = first_tile == 0 && end_tile == tiles;
     float* part = part_at<D>(p, blockIdx.x, first_tile == 0 ? 1 : 0);
     const int free_stage = (stage + kStages - 1) % kStages;
-    const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv_head(item_h)])) : 1.f;
+    const float vscale =
+        (G::kRecords ? kDecoded : 1.f) * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv_head(item_h)])) : 1.f);
     constexpr int kQuads = D / 4;                 // of a row
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -843,6 +1016,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
           if constexpr (TYPE == SR_PAGE_BF16) {
             row[r8] = o[t][k][x];
             row[r8 + 8] = o[t][k][x + 2];
+          } else if constexpr (TYPE == SR_PAGE_INT4) {
+            if (k % 2 == 0)
+              *reinterpret_cast<float4*>(row + 4 * r8) = make_float4(o[t][k][x], o[t][k][x + 2], o[t][k + 1][x], o[t][k + 1][x + 2]);
           } else {
             *reinterpret_cast<float2*>(row + 2 * r8) = make_float2(o[t][k][x], o[t][k][x + 2]);
           }
@@ -890,6 +1066,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
           }
         }
       }
+      if constexpr (G::kRecords) fence_proxy_async_smem();
       __syncthreads();   // the stages may be filled again
     }
     if (whole) {
@@ -930,6 +1107,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
         }
       }
     }
+  }
+  if constexpr (G::kRecords) {
+    // a copy that never came: shared memory is not given back before it has, or has had its time once more
+    if (sh.abort)
+      for (int x = 0; x < kStages; ++x) wait_drain(&sh.full[warp][x], (phases >> x & 1u) ^ 1u, kCopyTimeoutNs);
   }
 }
 
@@ -1179,11 +1361,13 @@ cudaError_t prepare(int group) {
 
 size_t paged_part_floats(int group, int head_dim) { return static_cast<size_t>(part_floats(group, head_dim)); }
 int paged_tile_tokens(int head_dim, int page_type) {
+  if (page_type == SR_PAGE_INT4) return head_dim == 128 ? Geo<128, SR_PAGE_INT4>::CT : Geo<64, SR_PAGE_INT4>::CT;
   if (head_dim == 128) return page_type == SR_PAGE_BF16 ? Geo<128, SR_PAGE_BF16>::CT : Geo<128, SR_PAGE_E4M3>::CT;
   return page_type == SR_PAGE_BF16 ? Geo<64, SR_PAGE_BF16>::CT : Geo<64, SR_PAGE_E4M3>::CT;
 }
 
 cudaError_t paged_attn_prepare(int head_dim, int page_type, int group) {
+  if (page_type == SR_PAGE_INT4) return head_dim == 128 ? prepare<128, SR_PAGE_INT4>(group) : prepare<64, SR_PAGE_INT4>(group);
   if (head_dim == 128)
     return page_type == SR_PAGE_BF16 ? prepare<128, SR_PAGE_BF16>(group) : prepare<128, SR_PAGE_E4M3>(group);
   return page_type == SR_PAGE_BF16 ? prepare<64, SR_PAGE_BF16>(group) : prepare<64, SR_PAGE_E4M3>(group);
@@ -1194,6 +1378,8 @@ int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_to
 }
 
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st) {
+  if (p.c.page_type == SR_PAGE_INT4)
+    return p.c.head_dim == 128 ? launch<128, SR_PAGE_INT4>(p, st) : launch<64, SR_PAGE_INT4>(p, st);
   if (p.c.head_dim == 128)
     return p.c.page_type == SR_PAGE_BF16 ? launch<128, SR_PAGE_BF16>(p, st) : launch<128, SR_PAGE_E4M3>(p, st);
   return p.c.page_type == SR_PAGE_BF16 ? launch<64, SR_PAGE_BF16>(p, st) : launch<64, SR_PAGE_E4M3>(p, st);

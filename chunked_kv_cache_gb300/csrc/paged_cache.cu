@@ -1,6 +1,7 @@
 // paged_cache.cu -- the paged token cache's state: appending tokens to pages and
 // evicting them by accumulated attention weight.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -48,6 +49,101 @@ __device__ __forceinline__ uint2 to_e4m3(const uint4& x, float inv_scale) {
   return make_uint2(out[0] | (uint32_t(out[1]) << 16), out[2] | (uint32_t(out[3]) << 16));
 }
 
+__device__ __forceinline__ uint4 from_e4m3(const uint2& x, float scale) {
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = (i < 2 ? x.x : x.y) >> (16 * (i & 1)) & 0xFFFFu;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(pair), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    out[i] = pack_bf16x2(f.x * scale, f.y * scale);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// ---- 4-bit pages. A scale's byte b is the fp16 number with the bits b << 7; as fp32, b << 20 has its bits at an
+// exponent that is 2^112 off, subnormal numbers among them, so that one product moves it to its place or back.
+constexpr uint32_t kScaleTop = 215;      // 3840: times the 16.25 of attention's decoding still an fp16 number
+constexpr uint32_t kScaleNan = 255;
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return b == kScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 20) * 0x1p112f;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// The scale's byte of 16 values of which `top` is the largest |x|. Everything is decided as in exact arithmetic: x
+// has 8 significant bits and a border (7 times a number of 5 bits) at most 8, so that a quotient is on a border or off by
+// more than 2^-9 of itself; the factor is a little above 1/7, so that one on a border goes up.
+__device__ __forceinline__ uint32_t scale_byte(float top) {
+  if (top != top) return kScaleNan;
+  const uint32_t b = (__float_as_uint(top * 0x1.24924Ap-3f * 0x1p-112f) + (1u << 19)) >> 20;
+  return min(b, kScaleTop);
+}
+// What a value is multiplied by before it is rounded: 1 / s, and 2^-19 of that more, so that halves go away from zero
+// (4 bits of s and the 4 of a half are 8 as well; a quotient that is no half is 2^-9 or more off one, the reciprocal 2^-22).
+__device__ __forceinline__ float scale_factor(uint32_t b) {
+  if (b == 0 || b == kScaleNan) return 0.f;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale_value(b)));
+  return r * (1.f + 0x1p-19f);
+}
+// eight values of bf16, times 2^-e
+__device__ __forceinline__ void load_values(float (&f)[8], const uint4& x, float inv_exp) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(in[i] << 16) * inv_exp;
+    f[2 * i + 1] = __uint_as_float(in[i] & 0xFFFF0000u) * inv_exp;
+  }
+}
+__device__ __forceinline__ float top_of(const float (&f)[8]) {
+  float t = fabsf(f[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t = max_nan(t, fabsf(f[i]));
+  return t;
+}
+// Codes of eight values: two units of four, each turned left by one bit. The sum with 1.5 * 2^23 + 8 leaves the rounded
+// quotient plus 8 in the lowest bits.
+__device__ __forceinline__ uint32_t codes_of(const float (&f)[8], float factor) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = fminf(fmaxf(f[i] * factor, -8.f), 7.f) + 12582920.f;
+    w |= (__float_as_uint(q) & 15u) << (4 * i);
+  }
+  return (w << 1 & 0xFFFEFFFEu) | (w >> 15 & 0x00010001u);
+}
+// the eight values of such codes, as bf16
+__device__ __forceinline__ uint4 values_of(uint32_t w, float scale) {
+  w = (w >> 1 & 0x7FFF7FFFu) | (w << 15 & 0x80008000u);
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = static_cast<float>(static_cast<int>(w >> (8 * i) & 15u) - 8) * scale;
+    const float b = static_cast<float>(static_cast<int>(w >> (8 * i + 4) & 15u) - 8) * scale;
+    out[i] = pack_bf16x2(a, b);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// How a warp's lanes share rows of records: four lanes a chunk of 32 values of a token (64 bytes of bf16, 16 of codes),
+// eight chunks in all: of 8 neighbouring tokens, whose codes lie together, or, where there are fewer, of neighbouring
+// chunks of 4, 2 or 1. f(row, chunk of the row, the lane's place in it) for every chunk of `rows` rows; the lanes of
+// a chunk always call it together, a warp's in step, with a row of -1 where there is none.
+template <typename F>
+__device__ __forceinline__ void each_chunk(int rows, int chunks, int warp, int warps, int lane, F&& f) {
+  const int tokens_log2 = rows >= 8 ? 3 : rows >= 4 ? 2 : rows >= 2 ? 1 : 0;
+  const int across = 8 >> tokens_log2;                       // chunks of a row that a warp takes at once
+  const int steps = (chunks + across - 1) / across, blocks = (rows + (1 << tokens_log2) - 1) >> tokens_log2;
+  const int tok = (lane >> 2) & ((1 << tokens_log2) - 1), ch = lane >> 2 >> tokens_log2;
+  for (int u = warp; u < blocks * steps; u += warps) {
+    const int block = u / steps, c = (u - block * steps) * across + ch, r = (block << tokens_log2) + tok;
+    f(r < rows && c < chunks ? r : -1, c, lane & 3);
+  }
+}
+
 template <int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendParams p) {
   grid_dep_wait();
@@ -85,6 +181,38 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     const int32_t r0 = (static_cast<int32_t>(blockIdx.x) - p.cta0[i]) * p.rows_per_cta;
     const int32_t rows = min(p.rows_per_cta, count - r0);
     const int vpr = c.n_kv * c.head_dim / 8;    // vectors per row
+    if constexpr (TYPE == SR_PAGE_INT4) {
+      const int cph_log2 = c.head_dim == 128 ? 2 : 1;           // chunks of a head
+      const uint4* src[2] = {reinterpret_cast<const uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr,
+                             reinterpret_cast<const uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr};
+      each_chunk(rows, c.n_kv << cph_log2, threadIdx.x / 32, kAppendThreads / 32, threadIdx.x % 32, [&](int r, int ch, int j) {
+        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (r >= 0) {
+#pragma unroll
+          for (int y = 0; y < 2; ++y) x[y] = __ldcs(src[y] + static_cast<int64_t>(r) * vpr + ch * 4 + j);
+        }
+        const int head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
+        const int32_t t = len + r0 + max(r, 0), pg = page_of_group(t >> 4, c.magic);
+        const int32_t slot = t - pg * c.page_tokens;
+        const int64_t rec = r >= 0 ? record_at(table[pg], slot, head, c.n_kv, c.page_tokens, c.head_dim) : 0;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          float f[8];
+          const float inv = c.kv_exp && r >= 0 ? exp2f(-static_cast<float>(c.kv_exp[y * c.n_kv + head])) : 1.f;
+          load_values(f, x[y], inv);
+          const float mine = top_of(f);
+          const uint32_t b = scale_byte(max_nan(mine, __shfl_xor_sync(0xffffffffu, mine, 1)));   // of two lanes' 16
+          const uint32_t b2 = __shfl_xor_sync(0xffffffffu, b, 2);
+          if (r >= 0) {
+            uint8_t* at = static_cast<uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + rec;
+            reinterpret_cast<uint32_t*>(at + part * 256 + (slot & 15) * 16)[j] = codes_of(f, scale_factor(b));
+            if (j == 0)
+              *reinterpret_cast<uint16_t*>(at + 8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2) =
+                  static_cast<uint16_t>(b | b2 << 8);
+          }
+        }
+      });
+    } else {
     const uint4* ksrc = reinterpret_cast<const uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
     const uint4* vsrc = reinterpret_cast<const uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
     const int head_shift = c.head_dim == 128 ? 4 : 3;
@@ -125,6 +253,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
         }
       }
     }
+    }
     const int64_t t0 = static_cast<int64_t>(seq) * c.cap + len + r0;
     for (int r = threadIdx.x; r < rows; r += kAppendThreads) {
       c.token_pos[t0 + r] = pos + r0 + r;
@@ -143,6 +272,84 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     if (last && !bad) {
       c.seq_len[seq] = len + count;
       c.seq_pos[seq] = pos + count;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read back
+// The way back of append: rows of the sequences' tokens as bf16, zeros where a sequence holds no such token.
+template <int TYPE>
+__global__ void __launch_bounds__(kAppendThreads) paged_read_kernel(const __grid_constant__ ReadParams p) {
+  grid_dep_wait();
+  grid_dep_launch_dependents();
+  const PagedView& c = p.c;
+  int lo = 0, hi = p.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (p.cta0[mid] <= static_cast<int>(blockIdx.x)) lo = mid; else hi = mid - 1;
+  }
+  const int i = lo;
+  const int32_t seq = p.id[i], count = p.row0[i + 1] - p.row0[i];
+  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
+  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
+  const int32_t r0 = (static_cast<int32_t>(blockIdx.x) - p.cta0[i]) * p.rows_per_cta;
+  const int32_t rows = min(p.rows_per_cta, count - r0);
+  const int64_t t0 = (p.first[i] >= 0 ? static_cast<int64_t>(p.first[i]) : static_cast<int64_t>(len) - count) + r0;   // index of row 0
+  const int vpr = c.n_kv * c.head_dim / 8;    // vectors per row
+  uint4* dst[2] = {reinterpret_cast<uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr,
+                   reinterpret_cast<uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr};
+  // the page of row r, or -1 where there is nothing to read
+  auto page_at = [&](int r, int32_t& slot) {
+    const int64_t t = t0 + r;
+    if (t < 0 || t >= len) return -1;
+    const int32_t pg = page_of_group(static_cast<int32_t>(t) >> 4, c.magic);
+    slot = static_cast<int32_t>(t) - pg * c.page_tokens;
+    const int32_t page = table[pg];
+    if (page >= 0 && page < c.n_pages) return page;
+    note_error(c, SR_DEVERR_BAD_PAGE);
+    return -1;
+  };
+  if constexpr (TYPE == SR_PAGE_INT4) {
+    const int cph_log2 = c.head_dim == 128 ? 2 : 1;
+    each_chunk(rows, c.n_kv << cph_log2, threadIdx.x / 32, kAppendThreads / 32, threadIdx.x % 32, [&](int r, int ch, int j) {
+      if (r < 0) return;
+      int32_t slot = 0;
+      const int32_t page = page_at(r, slot);
+      const int head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
+      const int64_t rec = page >= 0 ? record_at(page, slot, head, c.n_kv, c.page_tokens, c.head_dim) : 0;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint4 out = make_uint4(0, 0, 0, 0);
+        if (page >= 0) {
+          const uint8_t* at = static_cast<const uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + rec;
+          const uint32_t w = reinterpret_cast<const uint32_t*>(at + part * 256 + (slot & 15) * 16)[j];
+          const uint32_t b = at[8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2 + (j >> 1)];
+          out = values_of(w, scale_value(b) * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[y * c.n_kv + head])) : 1.f));
+        }
+        __stcs(dst[y] + static_cast<int64_t>(r) * vpr + ch * 4 + j, out);
+      }
+    });
+  } else {
+    const int head_shift = c.head_dim == 128 ? 4 : 3;
+    for (int x = threadIdx.x; x < rows * vpr; x += kAppendThreads) {
+      const int r = x / vpr, col = x - r * vpr;
+      int32_t slot = 0;
+      const int32_t page = page_at(r, slot);
+      const int64_t at = (static_cast<int64_t>(page) * c.page_tokens + slot) * vpr + col;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint4 out = make_uint4(0, 0, 0, 0);
+        const void* pages = y == 0 ? c.k_pages : c.v_pages;
+        if (page >= 0) {
+          if constexpr (TYPE == SR_PAGE_BF16) {
+            out = __ldcs(static_cast<const uint4*>(pages) + at);
+          } else {
+            const float scale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[y * c.n_kv + (col >> head_shift)])) : 1.f;
+            out = from_e4m3(__ldcs(static_cast<const uint2*>(pages) + at), scale);
+          }
+        }
+        __stcs(dst[y] + x, out);
+      }
     }
   }
 }
@@ -262,6 +469,33 @@ __device__ __forceinline__ void move_rows(const PagedView& c, int64_t from, int6
   }
 }
 
+// The same of records: 16 bytes of codes per chunk of 32 values, a head's scales in words.
+__device__ __forceinline__ void move_records(const PagedView& c, int64_t from, int64_t to, int lane) {
+  const int32_t fp = static_cast<int32_t>(from / c.page_tokens), fs = static_cast<int32_t>(from - static_cast<int64_t>(fp) * c.page_tokens);
+  const int32_t tp = static_cast<int32_t>(to / c.page_tokens), ts = static_cast<int32_t>(to - static_cast<int64_t>(tp) * c.page_tokens);
+  const int64_t f0 = record_at(fp, fs, 0, c.n_kv, c.page_tokens, c.head_dim), t0 = record_at(tp, ts, 0, c.n_kv, c.page_tokens, c.head_dim);
+  const int head_bytes = (c.page_tokens >> 4) * record_bytes(c.head_dim);
+  const int cph_log2 = c.head_dim == 128 ? 2 : 1, wph_log2 = cph_log2 - 1;     // chunks and words of scales per head
+  const int row = c.head_dim >> 4;                                            // bytes of a token's scales
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    uint8_t* pages = static_cast<uint8_t*>(y == 0 ? c.k_pages : c.v_pages);
+#pragma unroll 4
+    for (int x = lane; x < c.n_kv << cph_log2; x += 32) {
+      const int64_t off = static_cast<int64_t>(x >> cph_log2) * head_bytes + (x & ((1 << cph_log2) - 1)) * 256;
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(pages + f0 + off + (fs & 15) * 16));
+      *reinterpret_cast<uint4*>(pages + t0 + off + (ts & 15) * 16) = a;
+    }
+#pragma unroll 4
+    for (int x = lane; x < c.n_kv << wph_log2; x += 32) {
+      const int64_t off = static_cast<int64_t>(x >> wph_log2) * head_bytes + 8 * c.head_dim + (x & ((1 << wph_log2) - 1)) * 4;
+      const uint32_t a = __ldcs(reinterpret_cast<const uint32_t*>(pages + f0 + off + (fs & 15) * row));
+      *reinterpret_cast<uint32_t*>(pages + t0 + off + (ts & 15) * row) = a;
+    }
+  }
+}
+
+template <bool RECORDS>
 __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __grid_constant__ EvictParams p, int key_cap) {
   extern __shared__ uint32_t keys[];              // [key_cap]
   __shared__ __align__(16) EvictShared sh;
@@ -367,7 +601,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
               tpos[at] = tpos[last];
               mass[at] = mass[last];
             }
-            move_rows(c, from, to, vpr, lane);
+            if constexpr (RECORDS) move_records(c, from, to, lane); else move_rows(c, from, to, vpr, lane);
           } else if (lane == 0) {
             note_error(c, SR_DEVERR_BAD_PAGE);
           }
@@ -640,7 +874,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
     for (int q = 0; q < n; ++q) {
       const int64_t f = __shfl_sync(0xffffffffu, from, q), g = __shfl_sync(0xffffffffu, to, q);
       if ((f | g) < 0) continue;      // an entry that the caller changed during the call
-      move_rows(c, f, g, vpr, lane);
+      if constexpr (RECORDS) move_records(c, f, g, lane); else move_rows(c, f, g, vpr, lane);
     }
   }
 }
@@ -650,8 +884,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
 // One wave of the four CTAs that an SM holds, but at least a vector of each tensor per thread; two
 // waves where a thread would have more than 16 (42,700 rows of 1024 values: 61.3 us in one, 58.9 us in
 // two; 4,000 rows: 7.5 us, 9.1 us).
-int paged_append_rows_per_cta(int n_kv, int head_dim, int64_t rows) {
-  const int64_t vectors = static_cast<int64_t>(n_kv) * head_dim / 8;     // of a row
+int paged_append_rows_per_cta(const PagedView& c, int64_t rows) {
+  const int64_t vectors = static_cast<int64_t>(c.n_kv) * c.head_dim / 8;     // of a row
   const int64_t wave = 4ll * sm_count();
   const int64_t ctas = rows * vectors > 16 * wave * kAppendThreads ? 2 * wave : wave;
   return static_cast<int>(std::max((kAppendThreads + vectors - 1) / vectors, (rows + ctas - 1) / ctas));
@@ -664,11 +898,22 @@ cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStre
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(p.cta0[p.n]);
   if (p.c.page_type == SR_PAGE_BF16) return launch_dependent(paged_append_kernel<SR_PAGE_BF16>, grid, kAppendThreads, 0, st, p);
+  if (p.c.page_type == SR_PAGE_INT4) return launch_dependent(paged_append_kernel<SR_PAGE_INT4>, grid, kAppendThreads, 0, st, p);
   return launch_dependent(paged_append_kernel<SR_PAGE_E4M3>, grid, kAppendThreads, 0, st, p);
 }
 
+cudaError_t launch_paged_read(const ReadParams& p, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(p.cta0[p.n]);
+  if (p.c.page_type == SR_PAGE_BF16) return launch_dependent(paged_read_kernel<SR_PAGE_BF16>, grid, kAppendThreads, 0, st, p);
+  if (p.c.page_type == SR_PAGE_INT4) return launch_dependent(paged_read_kernel<SR_PAGE_INT4>, grid, kAppendThreads, 0, st, p);
+  return launch_dependent(paged_read_kernel<SR_PAGE_E4M3>, grid, kAppendThreads, 0, st, p);
+}
+
 cudaError_t paged_evict_prepare() {
-  return cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
+  const cudaError_t e =
+      cudaFuncSetAttribute(paged_evict_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(paged_evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyLimit * 4);
 }
 
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
@@ -695,7 +940,8 @@ cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p, key_cap);
+  return p.c.page_type == SR_PAGE_INT4 ? cudaLaunchKernelEx(&cfg, paged_evict_kernel<true>, p, key_cap)
+                                       : cudaLaunchKernelEx(&cfg, paged_evict_kernel<false>, p, key_cap);
 }
 
 }  // namespace sr

@@ -33,6 +33,14 @@ __device__ __forceinline__ int32_t page_of_group(int32_t g, uint32_t magic) {
   return magic == 0 ? g : static_cast<int32_t>(__umulhi(static_cast<uint32_t>(g), magic));
 }
 
+// 4-bit pages: a record holds the codes and scales of 16 tokens of one key/value head.
+__host__ __device__ constexpr int record_bytes(int head_dim) { return 9 * head_dim; }
+// Byte offset of the record of head `h` that holds slot `slot` of page `page`.
+__device__ __forceinline__ int64_t record_at(int32_t page, int32_t slot, int32_t h, int32_t n_kv, int32_t page_tokens,
+                                             int32_t head_dim) {
+  return ((static_cast<int64_t>(page) * n_kv + h) * (page_tokens >> 4) + (slot >> 4)) * record_bytes(head_dim);
+}
+
 struct PagedView {
   void* k_pages;
   void* v_pages;
@@ -115,6 +123,31 @@ struct PagedAttnParams {
   PagedBatch b;
 };
 
+struct ReadParams {
+  PagedView c;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int32_t n;
+  int32_t rows_per_cta;
+  int32_t id[kMaxPagedSeqs];
+  int32_t first[kMaxPagedSeqs];    // first index of each sequence; negative: its last rows
+  int32_t row0[kMaxPagedSeqs + 1];
+  int32_t cta0[kMaxPagedSeqs + 1];
+};
+
+struct PromptParams {
+  PagedView c;             // n_kv, group: items of at most SR_MAX_PAGED_GROUP query heads, as in PagedAttnParams
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;
+  int32_t kv_heads;
+  uint32_t head_magic;
+  int32_t n;
+  int32_t causal;
+  int32_t id[kMaxPagedSeqs];
+  int32_t row0[kMaxPagedSeqs + 1]; // first row of each sequence
+};
+
 struct EvictParams {
   PagedView c;
   int32_t budget, n_sink, n_recent;
@@ -126,6 +159,8 @@ struct EvictParams {
 
 cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_paged_read(const ReadParams& p, cudaStream_t st);
+cudaError_t launch_paged_prompt(const PromptParams& p, cudaStream_t st);
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
@@ -133,6 +168,6 @@ cudaError_t paged_evict_prepare();
 cudaError_t paged_attn_prepare(int head_dim, int page_type, int group);
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int group, int head_dim);                   // floats of one partial result
-int paged_append_rows_per_cta(int n_kv, int head_dim, int64_t rows);
+int paged_append_rows_per_cta(const PagedView& c, int64_t rows);
 
 }  // namespace sr

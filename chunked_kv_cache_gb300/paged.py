@@ -14,14 +14,16 @@ import torch
 from . import _native as N
 
 _BF16 = torch.bfloat16
-_PAGE_TYPES = {torch.bfloat16: N.SR_PAGE_BF16, torch.float8_e4m3fn: N.SR_PAGE_E4M3}
+_PAGE_TYPES = {torch.bfloat16: N.SR_PAGE_BF16, torch.float8_e4m3fn: N.SR_PAGE_E4M3, "int4": N.SR_PAGE_INT4}
 
 
 class PagedCache:
     """Keys and values of up to max_seqs sequences in pages of page_tokens tokens.
 
     Tensors, all on one device: k_pages, v_pages [n_pages][page_tokens][n_kv_heads][head_dim]
-    (bf16, or e4m3 with value = e4m3 * 2^kv_exp[0 or 1][head]); block_table
+    (bf16, or e4m3 with value = e4m3 * 2^kv_exp[0 or 1][head]), or, with page_dtype="int4" (codes of 4 bits and
+    a scale for each 16 values, also times 2^kv_exp; the layout stands at sr_paged_cache in include/sr.h),
+    [n_pages][page_tokens * n_kv_heads * 9 * head_dim // 16] uint8; block_table
     [max_seqs][max_pages] int32; seq_len, seq_pos [max_seqs] int32; token_pos
     [max_seqs][max_pages * page_tokens] int32; token_mass, the same shape in fp32 (mass=True);
     kv_exp [2][n_kv_heads] int32.
@@ -38,7 +40,7 @@ class PagedCache:
     """
 
     def __init__(self, n_heads: int, n_kv_heads: int, head_dim: int, *, page_tokens: int = 64, n_pages: int,
-                 max_seqs: int, max_pages: int, page_dtype: torch.dtype = _BF16, softmax_scale: float = 0.0,
+                 max_seqs: int, max_pages: int, page_dtype: torch.dtype | str = _BF16, softmax_scale: float = 0.0,
                  mass: bool = True, buffers: dict | None = None, device="cuda"):
         self.handle = None
         if page_dtype not in _PAGE_TYPES:
@@ -68,12 +70,14 @@ class PagedCache:
                                  f"got {t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
             return t
 
-        pages = (n_pages, page_tokens, n_kv_heads, head_dim)
+        pages, stored = (n_pages, page_tokens, n_kv_heads, head_dim), page_dtype
+        if page_dtype == "int4":
+            pages, stored = (n_pages, page_tokens * n_kv_heads * 9 * head_dim // 16), torch.uint8
         per_token = (max_seqs, self.capacity)
         i32 = torch.int32
         own_table = "block_table" not in given
-        self.k_pages = take("k_pages", pages, page_dtype, None)
-        self.v_pages = take("v_pages", pages, page_dtype, None)
+        self.k_pages = take("k_pages", pages, stored, None)
+        self.v_pages = take("v_pages", pages, stored, None)
         self.block_table = take("block_table", (max_seqs, max_pages), i32, -1)
         self.seq_len = take("seq_len", (max_seqs,), i32, 0)
         self.seq_pos = take("seq_pos", (max_seqs,), i32, 0)
@@ -126,6 +130,17 @@ class PagedCache:
             raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {self.device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
 
+    @staticmethod
+    def _seqs_of(what: str, rows: int, seqs, counts) -> int:
+        """The sequences of a call whose tensors have `rows` rows."""
+        n = len(seqs) if seqs is not None else len(counts) if counts is not None else rows
+        if counts is not None and len(counts) != n:
+            raise ValueError(f"{len(counts)} counts for {n} sequences")
+        takes = n if counts is None else sum(counts)
+        if takes != rows:
+            raise ValueError(f"{what} {rows} rows, the sequences take {takes}")
+        return n
+
     # ---------------------------------------------------------------- pages
     def reserve(self, seq: int, n_tokens: int) -> None:
         """Give sequence `seq` the pages it needs to hold n_tokens tokens (those it has stay)."""
@@ -171,12 +186,7 @@ class PagedCache:
         shape = (rows, self.n_kv_heads, self.head_dim)
         self._check("k", k, shape)
         self._check("v", v, shape)
-        n = len(seqs) if seqs is not None else len(counts) if counts is not None else rows
-        if counts is not None and len(counts) != n:
-            raise ValueError(f"{len(counts)} counts for {n} sequences")
-        takes = n if counts is None else sum(counts)
-        if takes != rows:
-            raise ValueError(f"k and v have {rows} rows, the sequences take {takes}")
+        n = self._seqs_of("k and v have", rows, seqs, counts)
         ids, at = self._ids(seqs)
         each, each_at = self._ids(counts)
         self._done(self._lib.sr_paged_append(self.handle, at, each_at, n, k.data_ptr(), v.data_ptr(), self._stream()),
@@ -211,6 +221,59 @@ class PagedCache:
                                                 -1.0 if mass_decay is None else mass_decay, self._stream()),
                    "sr_paged_attention")
         return out if lse is None else (out, lse)
+
+    def prompt_attention(self, q: torch.Tensor, counts: Sequence[int] | None = None, seqs: Sequence[int] | None = None,
+                         out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = None, causal: bool = True):
+        """Attention of the last counts[i] tokens of sequence seqs[i] (None: one each), appended before: q
+        [rows][n_heads][head_dim], the sequences' rows back to back. causal: a row sees the tokens up to its own, else all
+        that its sequence holds. Returns out, or (out, lse) when lse is True or a tensor [rows][n_heads] fp32."""
+        rows = q.shape[0]
+        shape = (rows, self.n_heads, self.head_dim)
+        self._check("q", q, shape)
+        n = self._seqs_of("q has", rows, seqs, counts)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._check("out", out, shape)
+        if lse is True:
+            lse = torch.empty((rows, self.n_heads), dtype=torch.float32, device=self.device)
+        elif isinstance(lse, torch.Tensor):
+            self._check("lse", lse, (rows, self.n_heads), torch.float32)
+        else:
+            lse = None
+        ids, at = self._ids(seqs)
+        each, each_at = self._ids(counts)
+        self._done(self._lib.sr_paged_prompt_attention(self.handle, at, each_at, n, q.data_ptr(), out.data_ptr(),
+                                                       None if lse is None else lse.data_ptr(), 1 if causal else 0,
+                                                       self._stream()), "sr_paged_prompt_attention")
+        return out if lse is None else (out, lse)
+
+    def read(self, counts: Sequence[int] | None = None, seqs: Sequence[int] | None = None,
+             first: Sequence[int] | None = None, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+        """Tokens back in bf16: counts[i] of sequence seqs[i] (None: one each), from index first[i] on, or (None) its
+        last ones. Returns k, v [rows][n_kv_heads][head_dim] (the given tensors, or new ones), the sequences' rows back to
+        back; rows that a sequence does not hold are zero."""
+        n = len(counts) if counts is not None else len(seqs) if seqs is not None else len(first) if first is not None \
+            else min(self.max_seqs, N.SR_MAX_PAGED_SEQS)
+        for name, given in (("seqs", seqs), ("first", first)):
+            if given is not None and len(given) != n:
+                raise ValueError(f"{len(given)} {name} for {n} sequences")
+        if counts is not None and any(x < 0 for x in counts):
+            raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_read")
+        shape = (n if counts is None else sum(counts), self.n_kv_heads, self.head_dim)
+        both = []
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                t = torch.empty(shape, dtype=_BF16, device=self.device)
+            else:
+                self._check(name, t, shape)
+            both.append(t)
+        ids, at = self._ids(seqs)
+        start, start_at = self._ids(first)
+        each, each_at = self._ids(counts)
+        self._done(self._lib.sr_paged_read(self.handle, at, start_at, each_at, n, both[0].data_ptr(), both[1].data_ptr(),
+                                           self._stream()), "sr_paged_read")
+        return both[0], both[1]
 
     def evict(self, budget: int, n_sink: int = 0, n_recent: int = 0, seqs: Sequence[int] | None = None) -> None:
         """Keep at most `budget` tokens per sequence: positions below n_sink, the last n_recent

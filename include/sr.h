@@ -440,6 +440,19 @@ SR_API sr_status sr_layer_commit(sr_session* const* sessions, const sr_window* w
  * value = e4m3 * 2^e. A power of two makes the scaling exact, so that the one rounding
  * of a stored value is the conversion (to nearest even, saturating at +-448 * 2^e).
  *
+ * Or pages hold 4 bits: 16 neighbouring values of a head share a scale s, and value = (c - 8) * s * 2^e with a
+ * code c, 0 .. 15 (4.5 bits a value in all). A scale is a byte b: the fp16 number with the bits b << 7, five bits of
+ * exponent and three of fraction. With x the 16 values times 2^-e: s is max |x| / 7 to four significant bits (below
+ * 2^-14 to a multiple of 2^-17; halves go up), at most 3840 (b = 215); c - 8 is x / s to an integer (halves go away from
+ * zero), within -8 .. 7, so that infinities saturate; s = 0 stands for 16 zeros. 16 values with a NaN among them get
+ * b = 255, a NaN, and are all NaN when read. Such a page is [n_kv_heads][page_tokens / 16] records of 9 * head_dim
+ * bytes, each of 16 tokens of one head, so that what attention reads next lies together whole:
+ *   codes   [head_dim / 32][16 tokens][16 bytes]: two bytes are four values, the 16-bit little-endian number
+ *           c0 | c1 << 4 | c2 << 8 | c3 << 12 turned left by one bit (a mask then puts each code into an fp16 fraction);
+ *   scales  [16 tokens][head_dim / 16].
+ * k_pages and v_pages are [n_pages][page_tokens * n_kv_heads * 9 * head_dim / 16] bytes, and sr_paged_locate's row r is
+ * slot r % page_tokens of page r / page_tokens.
+ *
  * The state that changes per token (lengths, positions, weights) lives on the device,
  * and no call reads it on the host: a captured sequence of these calls serves every
  * later token. What cannot be known on the host is checked on the device: a token
@@ -463,7 +476,7 @@ typedef struct sr_paged_cache sr_paged_cache;   /* opaque host handle */
 #define SR_MAX_PAGED_SEQS 256
 #define SR_MAX_PAGED_GROUP 16
 
-enum { SR_PAGE_BF16 = 0, SR_PAGE_E4M3 = 1 };
+enum { SR_PAGE_BF16 = 0, SR_PAGE_E4M3 = 1, SR_PAGE_INT4 = 4 };
 
 typedef struct {
   int32_t n_heads;         /* query heads; a multiple of n_kv_heads. More than SR_MAX_PAGED_GROUP of one key/value head are
@@ -475,13 +488,13 @@ typedef struct {
   int32_t n_pages;         /* pages of the pool >= 1 */
   int32_t max_seqs;        /* rows of the block table, 1 .. 65536 */
   int32_t max_pages;       /* pages a sequence may have >= 1; max_pages * page_tokens <= 2^24 */
-  int32_t page_type;       /* SR_PAGE_BF16 or SR_PAGE_E4M3 */
+  int32_t page_type;       /* SR_PAGE_BF16, SR_PAGE_E4M3 or SR_PAGE_INT4 */
   float softmax_scale;     /* <= 0 selects 1/sqrt(head_dim) */
 } sr_paged_config;
 
 /* Caller-owned device buffers. cap = max_pages * page_tokens. */
 typedef struct {
-  void* k_pages;            /* [n_pages * page_tokens][n_kv_heads][head_dim], 16-byte aligned */
+  void* k_pages;            /* [n_pages * page_tokens][n_kv_heads][head_dim], or records (4 bits); 16-byte aligned */
   void* v_pages;
   int32_t* block_table;     /* [max_seqs][max_pages]: pages of each sequence (negative: none); the caller's to change */
   int32_t* seq_len;         /* [max_seqs] tokens held */
@@ -489,7 +502,7 @@ typedef struct {
   int32_t* token_pos;       /* [max_seqs][cap] position of each token */
   float* token_mass;        /* [max_seqs][cap] accumulated attention weight, or NULL (no weights, no eviction) */
   const int32_t* kv_exp;    /* [2][n_kv_heads] exponents e of the keys' and the values' scales, each -64..64;
-                               e4m3 pages only, NULL: all zero */
+                               e4m3 and 4-bit pages only, NULL: all zero */
   int32_t* err_word;        /* [1] device error word (see SR_DEVERR_*) */
   void* workspace;          /* sr_paged_workspace_bytes() long, 256-byte aligned */
 } sr_paged_buffers;
@@ -530,7 +543,7 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  * lse = -inf and its tokens draw no weight. Indices at or past seq_len are never read as
  * values: what the pages hold there does not matter. o may be q.
  * fp32 scores, softmax and sums; the weights are held to 2^-15 of themselves (bf16 pages) or
- * 2^-11 (e4m3 pages) for their product with V.
+ * 2^-11 (e4m3 and 4-bit pages) for their product with V.
  * mass_decay >= 0 (finite; needs token_mass): also
  *   token_mass[s][t] = mass_decay * token_mass[s][t] + sum over heads of the token's weight.
  * mass_decay < 0: weights are not accumulated. The workspace has room for the scores of every token of the pool
@@ -540,6 +553,31 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  */
 SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, const void* q, void* o,
                                     float* lse, float mass_decay, void* stream);
+
+/*
+ * Attention of several new tokens per sequence: a prompt, drafted tokens to verify, a chunk of frames. The
+ * sequence's last n_tokens[i] tokens (appended before) are the queries, its seq_len tokens the keys:
+ *   o[r][h] = softmax(scale * q[r][h] . K) V   over the tokens that query row r sees.
+ * q, o: [rows][n_heads][head_dim] bf16, the sequences' rows back to back in the order of seqs; lse: optional
+ * [rows][n_heads] fp32, natural-log sum-exp of the scaled scores. causal != 0: row j of m sees indices
+ * 0 .. seq_len - m + j, itself the last of them (the new tokens lie in order: no eviction came after their append);
+ * causal == 0: all seq_len tokens. A row that sees no token (a sequence shorter than m has m - seq_len of them in
+ * front), or whose scores are all -inf, gets o = 0 and lse = -inf. n_tokens: HOST array of n counts >= 0, NULL for
+ * one each. o may be q. fp32 scores, softmax and sums; for their product with V weights are rounded to bf16
+ * (bf16 pages: 2^-8 of themselves) or fp16 (2^-11). token_mass is neither read nor written. Pages that are none
+ * of the pool are left out as above. The work is split over the lengths and joined; results do not depend on timing.
+ */
+SR_API sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, const int32_t* n_tokens, int32_t n,
+                                           const void* q, void* o, float* lse, int32_t causal, void* stream);
+
+/*
+ * Read tokens back: k, v [rows][n_kv_heads][head_dim] bf16, n_tokens[i] (HOST array of counts >= 0, NULL for one each) of
+ * sequence seqs[i] back to back, from index first[i] >= 0 on (HOST array), or, with first NULL, the last ones. bf16 holds every
+ * value of every page type exactly. A row whose index the sequence does not hold (negative, or seq_len and more) is
+ * zero; so is one on an entry that is no page of the pool, with SR_DEVERR_BAD_PAGE in err_word. The cache is not changed.
+ */
+SR_API sr_status sr_paged_read(sr_paged_cache* c, const int32_t* seqs, const int32_t* first, const int32_t* n_tokens,
+                               int32_t n, void* k, void* v, void* stream);
 
 /*
  * Evict down to `budget` tokens per sequence. A sequence with more keeps its sinks

@@ -22,13 +22,32 @@ def round_e4m3(x: np.ndarray) -> np.ndarray:
     return np.where(np.isnan(x), np.nan, np.copysign(y, x))
 
 
+def round_int4(x: np.ndarray) -> np.ndarray:
+    """What 4-bit pages hold for values x [..., 16 n]: blocks of 16 as integers -8 .. 7 times a scale of four
+    significant bits (a multiple of 2^-17), max |x| / 7 rounded with halves up, at most 3840; quotients round with halves
+    away from zero. A block with a NaN is NaN."""
+    x = np.asarray(x, np.float64)
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
+    nan = np.isnan(b).any(-1, keepdims=True)
+    b = np.where(nan, 0.0, b)
+    want = np.minimum(np.abs(b).max(-1, keepdims=True) / 7.0, 3840.0)
+    _, e = np.frexp(np.maximum(want, 2.0 ** -14))
+    step = np.ldexp(1.0, e - 4)
+    scale = np.floor(want / step + 0.5) * step
+    with np.errstate(invalid="ignore"):
+        t = np.where(scale > 0, b / np.where(scale > 0, scale, 1.0), 0.0)
+    c = np.clip(np.copysign(np.floor(np.abs(t) + 0.5), t), -8, 7)
+    return np.where(nan, np.nan, c * scale).reshape(x.shape)
+
+
 class OraclePagedCache:
     """k, v: [max_seqs][cap][n_kv][d]; pos, mass: [max_seqs][cap]; length, next_pos: [max_seqs]."""
 
-    def __init__(self, n_heads, n_kv, d, max_seqs, cap, e4m3=False, kv_exp=None, scale=None):
+    def __init__(self, n_heads, n_kv, d, max_seqs, cap, e4m3=False, kv_exp=None, scale=None,
+                 int4=False):
         self.n_heads, self.n_kv, self.d, self.cap = n_heads, n_kv, d, cap
         self.scale = 1.0 / np.sqrt(d) if scale is None else float(scale)
-        self.e4m3 = e4m3
+        self.e4m3, self.int4 = e4m3, int4
         self.exp = np.zeros((2, n_kv)) if kv_exp is None else np.asarray(kv_exp, np.float64)
         self.k = np.zeros((max_seqs, cap, n_kv, d))
         self.v = np.zeros((max_seqs, cap, n_kv, d))
@@ -44,10 +63,10 @@ class OraclePagedCache:
     def stored(self, x, which):
         """What the cache holds for rows x [n][n_kv][d] of the keys (which 0) or the values (1)."""
         x = np.asarray(x, np.float64)
-        if not self.e4m3:
+        if not self.e4m3 and not self.int4:
             return x
         s = (2.0 ** self.exp[which])[:, None]
-        return round_e4m3(x / s) * s
+        return (round_int4 if self.int4 else round_e4m3)(x / s) * s
 
     def append(self, seqs, counts, k, v):
         r = 0
@@ -96,6 +115,34 @@ class OraclePagedCache:
                 seen = slice(0, n) if vis is None else np.nonzero(vis)[0]
                 self.mass[s, seen] = mass_decay * self.mass[s, seen] + w.sum(0)[seen if vis is not None else slice(None)]
         return np.stack(out), np.stack(lses), np.stack(bounds)
+
+    def prompt_attention(self, seqs, counts, q, causal=True, visible=None):
+        """As attention, for the last counts[i] tokens of each sequence; q [rows][n_heads][d]. visible: masks of the
+        tokens, one per sequence."""
+        out, lses, bounds = [np.zeros((0, self.n_heads, self.d))], [np.zeros((0, self.n_heads))], [np.zeros((0, self.n_heads, self.d))]
+        r = 0
+        for i, (s, m) in enumerate(zip(seqs, counts)):
+            n = int(self.length[s])
+            for j in range(m):
+                mask = np.arange(n) < n - m + j + 1 if causal else np.ones(n, bool)
+                if visible is not None:
+                    mask &= visible[i]
+                for dst, x in zip((out, lses, bounds), self.attention([s], q[r + j: r + j + 1], visible=[mask])):
+                    dst.append(x)
+            r += m
+        return np.concatenate(out), np.concatenate(lses), np.concatenate(bounds)
+
+    def read(self, seqs, counts, first=None):
+        both = [np.zeros((sum(counts), self.n_kv, self.d)) for _ in range(2)]
+        r = 0
+        for i, (s, m) in enumerate(zip(seqs, counts)):
+            n = int(self.length[s])
+            t0 = n - m if first is None else first[i]
+            for j in range(m):
+                if 0 <= t0 + j < n:
+                    both[0][r + j], both[1][r + j] = self.k[s, t0 + j], self.v[s, t0 + j]
+            r += m
+        return both
 
     def evict(self, seqs, budget, n_sink=0, n_recent=0):
         for s in seqs:
