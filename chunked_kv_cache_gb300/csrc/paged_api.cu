@@ -3,6 +3,7 @@
 // call validates only what the host knows; nothing here waits for the device.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -66,7 +67,7 @@ sr::PagedLayout paged_layout(const sr_paged_config& c, bool with_mass) {
   const size_t seqs = static_cast<size_t>(c.max_seqs < sr::kMaxPagedSeqs ? c.max_seqs : sr::kMaxPagedSeqs);
   l.items = take(seqs * n_kv * sizeof(int2));
   l.unit0 = take((sr::kMaxPagedSeqs + 1) * sizeof(int64_t));
-  l.parts = take(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(group, c.head_dim) * 4);
+  l.parts = take(std::max(sr::kMaxPagedCtas * 2 * sr::paged_part_floats(group, c.head_dim), sr::paged_prompt_floats(c.head_dim)) * 4);
   l.lse2 = take(seqs * c.n_heads * 4);
   // every token of the pool once, the sequences' lengths rounded up to tiles
   const int64_t tile = sr::paged_tile_tokens(c.head_dim, c.page_type);
@@ -201,6 +202,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type, v.group);
+  if (e == cudaSuccess) e = sr::paged_prompt_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::paged_evict_prepare();
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);
@@ -297,6 +299,8 @@ sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, cons
   if (!q || !o) return SR_ERR_INVALID_ARG;
   p.n = n;
   p.causal = causal != 0;
+  p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
+  p.parts = ws_at<float>(c, c->layout.parts);
   p.c = c->view;
   take_heads(c, p.c, p.kv_heads, p.head_magic);
   p.q = static_cast<const __nv_bfloat16*>(q);

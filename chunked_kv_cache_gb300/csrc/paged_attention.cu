@@ -64,6 +64,7 @@
 #include "sr_device.cuh"
 #include "sr_kernels.h"
 #include "sr_paged.h"
+#include "sr_paged_device.cuh"
 
 namespace sr {
 
@@ -175,36 +176,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// ---- 4-bit codes as fp16. A mask puts a code c into the fraction of 16 (16 + c / 32) or of 1 (1 + c / 32); one fused
-// product and sum with its scale s then leaves (c - 8) / 32 * s, exactly: at most 7 significant bits, never below fp16's
-// smallest number. Four pairs of one word in 9 instructions, scale and all.
-__device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t y;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
-  return y;
-}
-__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-// What a decoding needs of a pair of scales.
-struct ScalePair {
-  uint32_t s, off16, off1;
-};
-__device__ __forceinline__ ScalePair scale_pair(uint32_t s) {
-  return {s, half2_mul(s, 0xCC10CC10u), half2_mul(s, 0xBD00BD00u)};     // -16.25 s, -1.25 s
-}
-// y[i]: the i-th value of the word's low unit and of its high one.
-__device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const ScalePair& s) {
-  const uint32_t z = __byte_perm(w, 0, 0x2301);
-  y[0] = half2_fma((w & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
-  y[1] = half2_fma((w & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
-  y[2] = half2_fma((z & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
-  y[3] = half2_fma((z & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
-}
-constexpr float kDecoded = 32.f;      // a value is so many times what decode_word leaves
-
 __device__ __forceinline__ void copy_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
@@ -222,13 +193,6 @@ __device__ __forceinline__ void load_words(uint32_t (&r)[N], uint32_t addr) {
   else
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r[0]) : "r"(addr) : "memory");
 }
-// two e4m3 values (the low 16 bits) as fp16, exactly
-__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
-  uint32_t y;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
-  return y;
-}
-
 // Releases what this thread has seen written, and acquires what earlier such additions released.
 __device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t x) {
   int32_t old;

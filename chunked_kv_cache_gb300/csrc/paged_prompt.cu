@@ -1,105 +1,1254 @@
-// paged_prompt.cu -- attention of several new tokens per sequence over the paged token cache.
+// paged_prompt.cu -- attention of several new tokens per sequence over the paged token cache, on the tcgen05
+// tensor cores:  o[r][h] = softmax(scale * q[r][h] . K) V  over the tokens that row r sees.
 //
-// The plainest form: a warp per query row and head walks the tokens that the row sees, its lanes share the head's
-// dims, softmax statistics run along.
+// A block is up to 256 query rows of one sequence and one key/value head: the rows of tile t are t * tpt .. of the
+// block's new tokens, each with the heads that share the key head (tpt = 128 / group tokens fill a tile). Two tiles
+// share every tile of 128 keys. A block whose rows fill one tile only gives the keys' even tiles to softmax group 0 and
+// the odd ones to group 1, which merge at the end. A step is two score tiles in both forms, and all blocks' steps
+// form one line that the CTAs, one per SM, share in equal stretches; whoever has a block whole writes its
+// output, of a block cut between CTAs each writes a partial result, and the last of them to arrive joins them in the
+// order of the line. The lengths never reach the host and results do not depend on timing.
+//
+// Keys and values come out of the pages by loads of four warps, which put them where the tensor cores read them
+// (128-byte swizzle): bf16 by asynchronous copies, e4m3 and 4 bits decoded to fp16, exactly, from registers that were
+// filled a tile ahead. Queries are bf16, or for fp16 products each row times a power of two (as in paged_attention.cu).
+//
+// Warp roles: 0-3 and 4-7 softmax groups (thread i owns row i of its tile), 8 issues the MMAs, 9-11 load queries,
+// 12-15 load keys and values. TMEM: S0 [0,128) S1 [128,256) scores, O0 [256,256+d) O1 [384,384+d) sums; the
+// weights go over the first half of their scores and from there to the second product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "sr_device.cuh"
 #include "sr_kernels.h"
 #include "sr_paged.h"
+#include "sr_paged_device.cuh"
 
 namespace sr {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 512;
+constexpr int BM = 128, BN = 128;
+constexpr int kMmaWarp = 8, kQWarp0 = 9, kLoadWarp0 = 12;
+constexpr int kQWarps = 3, kLoadWarps = 4;
+constexpr int kLaunchRegs = 128;
+constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 48, kRegsLoad = 96;
+static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsLoad) <= kThreads * kLaunchRegs,
+              "register split exceeds what the block is launched with");
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+constexpr int kItemCost = 1;           // steps that changing blocks costs
+// Flags of a block are kept for kFlagSlots blocks: a loading warp that begins the eighth block behind one has had a stage
+// back (of 8 at most, two tiles a block) that the third block behind it used, whose weights both softmax groups
+// made after they had read the first one's flags.
+constexpr int kFlagSlots = 8, kFlagTiles = 3;
 
-// D / 32 neighbouring values of a token, in 32 bits and without 2^e
 template <int D, int TYPE>
-__device__ __forceinline__ void load_token(float (&x)[D / 32], const void* pages, const PagedView& c, int32_t page, int32_t slot,
-                                           int head, int kv_heads, int lane) {
-  constexpr int N = D / 32;
+struct Cfg {
+  static constexpr bool kHalf = TYPE != SR_PAGE_BF16;       // products of fp16, else of bf16
+  static constexpr int kAtoms = D / 64;
+  static constexpr int kAtomBytes = BM * 128;
+  static constexpr int kTileBytes = kAtoms * kAtomBytes;
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kSmemQ = 2 * kTileBytes;
+  static constexpr int kSmemKV = kStages * kTileBytes;
+  static constexpr int kSmemBytes = kSmemQ + kSmemKV + 2048 + 1024;
+  static_assert(kSmemBytes <= 232448, "more than 227 KB of shared memory per block");
+  static constexpr uint32_t kIdescS = kHalf ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
+  static constexpr uint32_t kIdescPV = kHalf ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
+  // the reference of the exponentials lies kLift below an earlier maximum and is raised when a score passes it by kSlack
+  static constexpr float kLift = kHalf ? 6.f : 0.f, kSlack = 8.f;
+  static constexpr float kDecodedBy = TYPE == SR_PAGE_INT4 ? kDecoded : 1.f;
+};
+
+// One block of query rows, and the part of its steps that this CTA takes.
+struct Block {
+  int i, h, b;           // sequence of the call, item head, block of the sequence
+  int32_t base;          // tokens before the new ones; negative where the sequence is shorter than its rows
+  int32_t tok0, ntok;    // its new tokens
+  int32_t lim_min, lim;  // tokens that its first and last row see
+  int32_t tiles, steps;  // key tiles, steps in all
+  bool split;            // one query tile: the groups share the key tiles
+  int32_t s0, s1;        // steps of this CTA
+  __device__ __forceinline__ int count(int t) const {
+    return !split ? s1 - s0 : t == 0 ? s1 - s0 : max(min(s1, tiles / 2) - s0, 0);
+  }
+  __device__ __forceinline__ int tile(int t, int j) const { return split ? 2 * (s0 + j) + t : s0 + j; }
+};
+
+struct Start {
+  int64_t left;          // units of this CTA's stretch from its first step on
+  int64_t share, rest;   // units of every CTA, and how many have one more
+  int32_t i, h, b, s0;
+  int64_t u;             // unit of the first block's first step (not this CTA's)
+};
+
+struct Bars {
+  uint64_t q_full, q_empty, q_seen;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
+  uint64_t x_full, x_empty, part_done, part_last, drain;
+  uint64_t flags_full[kFlagSlots];
+  uint32_t tmem_base;
+  int abort;
+  int last;
+  Start start;
+  // of a block: new tokens with values that are no finite numbers, by loading warp and key tile from the first that some
+  // row does not see whole
+  uint32_t flags[kFlagSlots][kLoadWarps][kFlagTiles];
+  int8_t qexp[2][BM];
+  float xm[BM], xl[BM];
+};
+static_assert(sizeof(Bars) <= 2048, "barrier area too small");
+
+struct Setup {                   // overlays the stages before they are used
+  int64_t cum[kMaxPagedSeqs + 1];
+  unsigned long long per_head[kMaxPagedSeqs];
+};
+
+__device__ __forceinline__ void set_block(const PromptParams& p, Block& k, int32_t len) {
+  const int32_t count = p.row0[k.i + 1] - p.row0[k.i];
+  k.base = len - count;
+  k.tok0 = k.b * 2 * p.tpt;
+  k.ntok = min(2 * p.tpt, count - k.tok0);
+  k.lim = max(p.causal ? k.base + k.tok0 + k.ntok : len, 0);
+  k.lim_min = max(p.causal ? k.base + k.tok0 + 1 : len, 0);
+  k.split = k.ntok <= p.tpt;
+  k.tiles = (k.lim + BN - 1) / BN;
+  k.steps = k.split ? (k.tiles + 1) / 2 : k.tiles;
+}
+__device__ __forceinline__ int32_t seq_length(const PromptParams& p, int i) {
+  return min(max(__ldg(p.c.seq_len + p.id[i]), 0), p.c.cap);
+}
+__device__ __forceinline__ int blocks_of(const PromptParams& p, int i) {
+  return (p.row0[i + 1] - p.row0[i] + 2 * p.tpt - 1) / (2 * p.tpt);
+}
+__device__ __forceinline__ int seq_of_block(const PromptParams& p, int x) {   // x among the blocks of all sequences
+  int lo = 0, hi = p.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (p.blk0[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int64_t units_of(const Block& k) { return k.steps > 0 ? k.steps + kItemCost : 0; }
+
+// This CTA's blocks, one after the other; every role walks them by itself.
+struct Walker {
+  const PromptParams& p;
+  Block k;
+  int64_t left, u;               // units left, unit of the block's first step
+  int32_t len;
+  int nb;
+  bool first;
+  __device__ __forceinline__ Walker(const PromptParams& p_, const Start& s) : p(p_) {
+    k.i = s.i;
+    k.h = s.h;
+    k.b = s.b;
+    left = s.left;
+    u = s.u;
+    first = true;
+    if (left > 0) {
+      len = seq_length(p, k.i);
+      nb = blocks_of(p, k.i);
+      set_block(p, k, len);
+      k.s0 = s.s0;
+    }
+  }
+  __device__ __forceinline__ bool next() {
+    if (!first) {
+      if (left <= 0) return false;
+      u += k.steps;
+      do {                       // the line holds a unit here, so that some block has steps
+        if (++k.b == nb) {
+          k.b = 0;
+          if (++k.h == p.c.n_kv) {
+            k.h = 0;
+            do {
+              ++k.i;
+              nb = blocks_of(p, k.i);
+            } while (nb == 0);
+            len = seq_length(p, k.i);
+          }
+        }
+        set_block(p, k, len);
+      } while (k.steps == 0);
+      k.s0 = 0;
+      u += kItemCost;
+      left -= kItemCost;
+    }
+    if (left <= 0) return false;
+    first = false;
+    k.s1 = static_cast<int32_t>(min(static_cast<int64_t>(k.steps), k.s0 + left));
+    left -= k.s1 - k.s0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ int owner_of(int64_t u, int64_t share, int64_t rest) {
+  const int64_t longer = rest * (share + 1);
+  return static_cast<int>(u < longer ? u / (share + 1) : rest + (u - longer) / share);
+}
+
+// -------------------------------------------------------------- loading keys and values
+// One tile of 128 tokens' keys or values for the loading warps.
+struct TileRef {
+  int32_t tok0;        // first token
+  int32_t lim;         // tokens of the sequence from here on are zeros
+  int32_t watch;       // tokens from here on are seen by some rows only: values that are no finite numbers leave the tile
+  int32_t seq, head;   // row of the block table, key/value head
+  int32_t meta;        // bit 0: values; bit 1: a block's first tile; bit 2: its last; bits 8..: flag word
+  __device__ __forceinline__ bool values() const { return meta & 1; }
+};
+
+// The tiles of this CTA in the order in which the MMAs take them: before every step's keys the values of the step before.
+template <int UNUSED = 0>
+struct TileWalk {
+  Walker w;
+  int j, t, part;      // step of the block (0 .. n), softmax group, 0 values 1 keys
+  int n;
+  bool open, fresh;
+  __device__ __forceinline__ TileWalk(const PromptParams& p, const Start& s) : w(p, s) {
+    open = w.next();
+    begin();
+  }
+  __device__ __forceinline__ void begin() {
+    j = t = part = 0;
+    n = open ? w.k.s1 - w.k.s0 : 0;
+    fresh = true;
+  }
+  __device__ __forceinline__ bool next(TileRef& r, const PromptParams& p) {
+    while (open) {
+      while (j <= n) {
+        const int jj = part == 0 ? j - 1 : j, tt = t, pp = part;
+        const bool there = jj >= 0 && jj < w.k.count(tt);
+        // on to the next place
+        if (++part == 2) {
+          part = 0;
+          if (w.k.split && t == 0) {
+            t = 1;
+          } else {
+            t = 0;
+            ++j;
+          }
+        }
+        if (!there) continue;
+        const int tile = w.k.tile(tt, jj);
+        const int flag = max(tile - w.k.lim_min / BN, 0);
+        const bool last = pp == 0 && jj == n - 1 && (!w.k.split || tt == 1 || w.k.count(1) < n);
+        r.tok0 = tile * BN;
+        r.lim = w.k.lim;
+        r.watch = p.causal ? w.k.lim_min : INT32_MAX;
+        r.seq = p.id[w.k.i];
+        r.head = static_cast<int>(static_cast<uint32_t>(w.k.h) * p.head_magic >> 22);
+        r.meta = (pp == 0 ? 1 : 0) | (fresh ? 2 : 0) | (last ? 4 : 0) | flag << 8;
+        fresh = false;
+        return true;
+      }
+      open = w.next();
+      begin();
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void store16(uint32_t dst, const uint4& x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t src) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(src) : "memory");
+  return x;
+}
+// 16-byte piece `piece` (of 8 elements) of row r of a tile
+template <int D>
+__device__ __forceinline__ uint32_t piece_at(int r, int piece) {
+  return static_cast<uint32_t>((piece >> 3) * (BM * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+}
+// zero the elements that are no finite numbers; true if there were any
+template <bool HALF>
+__device__ __forceinline__ bool finite_only(uint32_t& x) {
+  constexpr uint32_t kExp = HALF ? 0x7C00u : 0x7F80u;
+  const bool lo = (x & kExp) == kExp, hi = (x & kExp << 16) == kExp << 16;
+  if (lo) x &= 0xFFFF0000u;
+  if (hi) x &= 0x0000FFFFu;
+  return lo || hi;
+}
+template <bool HALF>
+__device__ __forceinline__ bool finite_only(uint4& x) {
+  bool any = finite_only<HALF>(x.x);
+  any |= finite_only<HALF>(x.y);
+  any |= finite_only<HALF>(x.z);
+  any |= finite_only<HALF>(x.w);
+  return any;
+}
+
+// A loading warp's share of a tile, 32 tokens: two groups of 16, which never cross a page.
+struct Pages {
+  int32_t page[2], slot[2];    // page -1: zeros
+};
+__device__ __forceinline__ void fetch_pages(Pages& g, const TileRef& r, const PagedView& c, int w, int lane) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int32_t tok = r.tok0 + w * 32 + x * 16;
+    g.page[x] = -1;
+    if (tok < r.lim) {
+      const int32_t pg = page_of_group(tok >> 4, c.magic);
+      g.slot[x] = tok - pg * c.page_tokens;
+      g.page[x] = __ldg(c.table + static_cast<int64_t>(r.seq) * c.max_pages + pg);
+    }
+  }
+}
+// after the entries have arrived: those that are no page of the pool are reported and read as zeros
+__device__ __forceinline__ void check_pages(Pages& g, const TileRef& r, const PagedView& c, int w, int lane) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+    if (r.tok0 + w * 32 + x * 16 < r.lim && (g.page[x] < 0 || g.page[x] >= c.n_pages)) {
+      if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
+      g.page[x] = -1;
+    }
+}
+
+template <int D, int TYPE>
+struct Raw {
+  static constexpr int kVec = TYPE == SR_PAGE_E4M3 ? D / 16 : TYPE == SR_PAGE_INT4 ? D / 32 : 1;
+  uint4 x[kVec];
+  uint32_t s[TYPE == SR_PAGE_INT4 ? kVec : 1];
+};
+
+// e4m3: lane l of 8 (or 4) takes 16 bytes of a token's row; 4 bits: lanes 0-15 a chunk of the group's 16 tokens, lanes
+// 16-31 the next one. Tokens at or past the limit are zeros (their scales are, for 4 bits).
+template <int D, int TYPE>
+__device__ __forceinline__ void load_raw(Raw<D, TYPE>& v, const TileRef& r, const Pages& g, const PagedView& c, int kv_heads, int w,
+                                         int lane) {
+  const uint8_t* pages = static_cast<const uint8_t*>(r.values() ? c.v_pages : c.k_pages);
   if constexpr (TYPE == SR_PAGE_INT4) {
-    const uint8_t* rec = static_cast<const uint8_t*>(pages) + record_at(page, slot, head, kv_heads, c.page_tokens, D);
-    const int dim = lane * N;
-    const uint32_t u = *reinterpret_cast<const uint16_t*>(rec + (dim / 32) * 256 + (slot & 15) * 16 + (dim % 32) / 4 * 2);
-    const uint32_t codes = (u >> 1 | u << 15) & 0xFFFFu;
-    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(rec[8 * D + (slot & 15) * (D / 16) + dim / 16] << 7)));
+    constexpr int kPer = D / 64;              // loads per group
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = (static_cast<int>(codes >> (4 * (dim % 4 + i)) & 15u) - 8) * s;
-  } else {
-    const int64_t at = ((static_cast<int64_t>(page) * c.page_tokens + slot) * kv_heads + head) * D + lane * N;
+    for (int x = 0; x < 2; ++x) {
+      const uint8_t* rec = pages + record_at(g.page[x] < 0 ? 0 : g.page[x], g.page[x] < 0 ? 0 : g.slot[x], r.head, kv_heads, c.page_tokens, D);
+      const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + (lane & 15) < r.lim;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (TYPE == SR_PAGE_BF16)
-        x[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(pages)[at + i]);
-      else
-        x[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at + i], __NV_E4M3)));
+      for (int y = 0; y < kPer; ++y) {
+        const int ch = 2 * y + lane / 16;
+        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(rec + ch * 256 + (lane & 15) * 16)) : make_uint4(0, 0, 0, 0);
+        v.s[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (lane & 15) * (D / 16) + 2 * ch)) : 0;
+      }
+    }
+  } else if constexpr (TYPE == SR_PAGE_E4M3) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = 16 / kRows;   // lanes of a row, rows per load, loads per group
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t row0 = g.page[x] < 0 ? 0 : static_cast<int64_t>(g.page[x]) * c.page_tokens + g.slot[x];
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        const int slot = y * kRows + lane / kLanes;
+        const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + slot < r.lim;
+        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(pages + ((row0 + slot) * kv_heads + r.head) * D) + lane % kLanes)
+                                  : make_uint4(0, 0, 0, 0);
+      }
     }
   }
 }
 
+// Decodes and stores; returns a bit per token of the warp's 32 whose values were no finite numbers (and are zeros now).
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads) paged_prompt_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int N = D / 32;
-  grid_dep_wait();
-  grid_dep_launch_dependents();
-  const PagedView& c = p.c;
-  const int lane = threadIdx.x % 32;
-  const int64_t task = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
-  const int32_t row = static_cast<int32_t>(task / c.n_heads), h = static_cast<int32_t>(task % c.n_heads);
-  if (row >= p.row0[p.n]) return;
-  int i = 0;
-  while (p.row0[i + 1] <= row) ++i;
-  const int32_t count = p.row0[i + 1] - p.row0[i], seq = p.id[i];
-  const int32_t len = min(max(c.seq_len[seq], 0), c.cap);
-  const int32_t sees = p.causal ? max(len - count + (row - p.row0[i]) + 1, 0) : len;
-  const int head = h / (c.n_heads / p.kv_heads);
-  const int32_t* table = c.table + static_cast<int64_t>(seq) * c.max_pages;
-  const int64_t at = (static_cast<int64_t>(row) * c.n_heads + h) * D + lane * N;
-  float q[N], o[N], top = -INFINITY, sum = 0.f;
+__device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const TileRef& r, uint32_t tile, int w, int lane) {
+  uint32_t odd = 0;
+  const bool watch = r.values() && r.tok0 + w * 32 + 32 > r.watch;
+  auto put = [&](int row, int piece, uint4 y) {          // row of the warp's 32
+    if (watch && r.tok0 + w * 32 + row >= r.watch && finite_only<true>(y)) odd |= 1u << row;
+    store16(tile + piece_at<D>(w * 32 + row, piece), y);
+  };
+  if constexpr (TYPE == SR_PAGE_INT4) {
+    constexpr int kPer = D / 64;
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    q[k] = __bfloat162float(p.q[at + k]);
-    o[k] = 0.f;
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        const int ch = 2 * y + lane / 16;
+        const uint32_t b = v.s[x * kPer + y];
+        const uint4 z = v.x[x * kPer + y];
+        const uint32_t word[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const ScalePair s = scale_pair(__byte_perm(b, 0, q < 2 ? 0x4040 : 0x4141) << 7);
+          uint32_t e[4];
+          decode_word(e, word[q], s);
+          put(x * 16 + (lane & 15), ch * 4 + q, make_uint4(e[0], e[1], e[2], e[3]));
+        }
+      }
+  } else if constexpr (TYPE == SR_PAGE_E4M3) {
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = 16 / kRows;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int y = 0; y < kPer; ++y) {
+        const uint4 z = v.x[x * kPer + y];
+        const uint4 a = make_uint4(half2_of_e4m3(z.x), half2_of_e4m3(z.x >> 16), half2_of_e4m3(z.y), half2_of_e4m3(z.y >> 16));
+        const uint4 b = make_uint4(half2_of_e4m3(z.z), half2_of_e4m3(z.z >> 16), half2_of_e4m3(z.w), half2_of_e4m3(z.w >> 16));
+        const int row = x * 16 + y * kRows + lane / kLanes, l = lane % kLanes;
+        // lanes of the two atoms begin with different pieces: none meets another's banks
+        const bool swap = l >= 4;
+        put(row, 2 * l + (swap ? 1 : 0), swap ? b : a);
+        put(row, 2 * l + (swap ? 0 : 1), swap ? a : b);
+      }
   }
-  const float scale = fmaxf(c.scale_log2 * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[head])) : 1.f), 0x1p-126f);
-  const float vscale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + head])) : 1.f;
-  for (int32_t t = 0; t < sees; ++t) {
-    const int32_t pg = page_of_group(t >> 4, c.magic), page = table[pg], slot = t - pg * c.page_tokens;
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
-      continue;
+  return odd;
+}
+
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+// bf16: 16 (or 8) lanes copy a token's row; past the limit zeros
+template <int D>
+__device__ __forceinline__ void copy_tile(const TileRef& r, const Pages& g, const PagedView& c, int kv_heads, uint32_t tile, int w,
+                                          int lane) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  const __nv_bfloat16* pages = static_cast<const __nv_bfloat16*>(r.values() ? c.v_pages : c.k_pages);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int64_t row0 = g.page[x] < 0 ? 0 : static_cast<int64_t>(g.page[x]) * c.page_tokens + g.slot[x];
+#pragma unroll
+    for (int y = 0; y < 16 / kRows; ++y) {
+      const int slot = y * kRows + lane / kLanes;
+      const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + slot < r.lim;
+      const __nv_bfloat16* src = pages + ((row0 + (there ? slot : 0)) * kv_heads + r.head) * D + lane % kLanes * 8;
+      copy16_or_zero(tile + piece_at<D>(w * 32 + x * 16 + slot, lane % kLanes), src, there);
     }
-    float k[N], v[N], x = 0.f;
-    load_token<D, TYPE>(k, c.k_pages, c, page, slot, head, p.kv_heads, lane);
-    load_token<D, TYPE>(v, c.v_pages, c, page, slot, head, p.kv_heads, lane);
-#pragma unroll
-    for (int y = 0; y < N; ++y) x = fmaf(q[y], k[y], x);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    x *= scale;
-    const float m = fmaxf(top, x);
-    const float f = top == -INFINITY ? 0.f : ex2_approx(top - m), w = m == -INFINITY ? (x == x ? 0.f : x) : ex2_approx(x - m);
-    top = m;
-    sum = fmaf(sum, f, w);
-#pragma unroll
-    for (int y = 0; y < N; ++y) o[y] = fmaf(w, v[y], o[y] * f);
   }
-  const float inv = sum == 0.f ? 0.f : vscale / sum;
+}
+// The same lanes look at what they copied, where some rows do not see all of it.
+template <int D>
+__device__ __forceinline__ uint32_t clean_tile(const TileRef& r, uint32_t tile, int w, int lane) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  uint32_t odd = 0;
+#pragma unroll 1
+  for (int row = lane / kLanes; row < 32; row += kRows)
+    if (r.tok0 + w * 32 + row >= r.watch) {
+      const uint32_t at = tile + piece_at<D>(w * 32 + row, lane % kLanes);
+      uint4 y = load16(at);
+      if (finite_only<false>(y)) {
+        odd |= 1u << row;
+        store16(at, y);
+      }
+    }
+  return odd;
+}
+
+// -------------------------------------------------------------- values that are no finite numbers, seen by some rows only
+// Value `dim` of token t (16-bit floats of the pages' type, fp16 for those of fewer bits), as the tiles would hold it.
+template <int D, int TYPE>
+__device__ __forceinline__ float page_value(const PromptParams& p, const void* pages, int32_t seq, int32_t t, int head, int dim) {
+  const PagedView& c = p.c;
+  const int32_t pg = page_of_group(t >> 4, c.magic), slot = t - pg * c.page_tokens;
+  const int32_t page = __ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg);
+  if (page < 0 || page >= c.n_pages) return 0.f;
+  if constexpr (TYPE == SR_PAGE_INT4) {
+    const uint8_t* rec = static_cast<const uint8_t*>(pages) + record_at(page, slot, head, p.kv_heads, c.page_tokens, D);
+    const uint32_t u = *reinterpret_cast<const uint16_t*>(rec + (dim / 32) * 256 + (slot & 15) * 16 + (dim % 32) / 4 * 2);
+    const int code = static_cast<int>(((u >> 1 | u << 15) & 0xFFFFu) >> (4 * (dim % 4)) & 15u);
+    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(rec[8 * D + (slot & 15) * (D / 16) + dim / 16] << 7)));
+    return static_cast<float>(code - 8) * s / kDecoded;
+  } else {
+    const int64_t at = ((static_cast<int64_t>(page) * c.page_tokens + slot) * p.kv_heads + head) * D + dim;
+    if constexpr (TYPE == SR_PAGE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(pages)[at]);
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at], __NV_E4M3)));
+  }
+}
+// Adds the weight of token t times its values that are no finite numbers to 32 sums of a row from dim0 on. Runs only where
+// such values lie among a block's new tokens; the weight is computed again, from the query row and the key.
+template <int D, int TYPE>
+__device__ __noinline__ void add_odd(const PromptParams& p, float* o, int dim0, int32_t seq, int32_t t, int head, const __nv_bfloat16* q,
+                                     float scale, float m) {
+  float x = 0.f;
+  for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), page_value<D, TYPE>(p, p.c.k_pages, seq, t, head, d), x);
+  const float w = ex2_approx(x * scale - (m == -INFINITY ? 0.f : m));
+  for (int k = 0; k < 32; ++k) {
+    const float v = page_value<D, TYPE>(p, p.c.v_pages, seq, t, head, dim0 + k);
+    if (!(fabsf(v) < INFINITY)) o[k] = fmaf(w, v, o[k]);
+  }
+}
+
+// -------------------------------------------------------------- partial results
+template <int D>
+__host__ __device__ constexpr int64_t slot_floats() { return 2 * BM * (D + 2); }
+template <int D>
+__device__ __forceinline__ float* slot_at(const PromptParams& p, int cta, int slot) {
+  return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * slot_floats<D>();
+}
+
+// Joins a block's n parts, that of CTA c0 (slot 1) and of those behind it (slot 0): a warp per row, its lanes the dims.
+template <int D>
+__device__ __noinline__ void join_block(const PromptParams& p, const Block& k, int c0, int n, int warp, int lane) {
+  constexpr int N = D / 32;
+  __threadfence();
+  const int group = p.c.group, rows = k.ntok * group;
+  for (int r = warp; r < rows; r += 8) {
+    const int tok = r / group, hh = r - tok * group;
+    const int at = (tok / p.tpt) * BM + (tok % p.tpt) * group + hh;          // row of the two tiles
+    float top = -INFINITY;
+    for (int x = lane; x < n; x += 32) top = fmaxf(top, __ldcg(slot_at<D>(p, c0 + x, x == 0 ? 1 : 0) + 2 * BM * D + 2 * at));
 #pragma unroll
-  for (int y = 0; y < N; ++y) p.o[at + y] = __float2bfloat16(sum == 0.f ? 0.f : o[y] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[static_cast<int64_t>(row) * c.n_heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    float sum = 0.f, a[N];
+#pragma unroll
+    for (int y = 0; y < N; ++y) a[y] = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < n; ++x) {
+      const float* src = slot_at<D>(p, c0 + x, x == 0 ? 1 : 0);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + 2 * BM * D) + at);
+      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
+      sum = fmaf(w, ml.y, sum);
+      if constexpr (N == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + at * D) + lane);
+        a[0] = fmaf(w, v.x, a[0]); a[1] = fmaf(w, v.y, a[1]); a[2] = fmaf(w, v.z, a[2]); a[3] = fmaf(w, v.w, a[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + at * D) + lane);
+        a[0] = fmaf(w, v.x, a[0]); a[1] = fmaf(w, v.y, a[1]);
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + tok) * p.c.n_heads + k.h * group + hh;
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * N);
+    o[0] = sum == 0.f ? 0u : pack_bf16x2(a[0] * inv, a[1] * inv);
+    if constexpr (N == 4) o[1] = sum == 0.f ? 0u : pack_bf16x2(a[2] * inv, a[3] * inv);
+    if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+// place of dim i (of 8) among the columns of a tile: 4-bit words decode to the pairs (0,4) (1,5) (2,6) (3,7)
+template <int TYPE>
+__device__ __forceinline__ constexpr int column_of(int i) {
+  return TYPE == SR_PAGE_INT4 ? (i & ~7) + ((i & 3) * 2 + ((i >> 2) & 1)) : i;
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_constant__ PromptParams p) {
+  using C = Cfg<D, TYPE>;
+  grid_dep_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + C::kSmemQ;
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::kSmemQ + C::kSmemKV);
+  Setup* setup = reinterpret_cast<Setup*>(sKV);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const PagedView& c = p.c;
+  WaitCtx wc{&bars->abort, c.err_word, kTimeoutNs};
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, kQWarps);
+    mbar_init(&bars->q_empty, 1);
+    mbar_init(&bars->q_seen, 8);
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(&bars->kv_full[s], kLoadWarps);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_half[t], BM);
+      mbar_init(&bars->p_full[t], BM);
+      mbar_init(&bars->o_done[t], 1);
+    }
+    mbar_init(&bars->x_full, BM);
+    mbar_init(&bars->x_empty, BM);
+    mbar_init(&bars->part_done, 2 * BM);
+    mbar_init(&bars->part_last, 1);
+    mbar_init(&bars->drain, 1);
+    for (int s = 0; s < kFlagSlots; ++s) mbar_init(&bars->flags_full[s], kLoadWarps);
+    bars->abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < p.n; i += kThreads) setup->per_head[i] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  grid_dep_wait();
+  const uint32_t tmem = bars->tmem_base;
+
+  // ---- the line of steps: units of each sequence's blocks for one head, then of the sequences one after the other
+  {
+    for (int x = threadIdx.x; x < p.blocks; x += kThreads) {
+      const int lo = seq_of_block(p, x);
+      Block k;
+      k.i = lo;
+      k.b = x - p.blk0[lo];
+      set_block(p, k, seq_length(p, lo));
+      if (k.steps > 0) atomicAdd(&setup->per_head[lo], static_cast<unsigned long long>(units_of(k)));
+    }
+    // blocks of rows that see nothing
+    for (int x = blockIdx.x; x < p.blocks; x += gridDim.x) {
+      Block k;
+      k.i = seq_of_block(p, x);
+      k.b = x - p.blk0[k.i];
+      set_block(p, k, seq_length(p, k.i));
+      if (k.steps > 0) continue;
+      const int64_t row = static_cast<int64_t>(p.row0[k.i]) + k.tok0;
+      uint4* o = reinterpret_cast<uint4*>(p.o + row * c.n_heads * D);
+      for (int y = threadIdx.x; y < k.ntok * c.n_heads * (D / 8); y += kThreads) o[y] = make_uint4(0, 0, 0, 0);
+      for (int y = threadIdx.x; y < k.ntok * c.n_heads; y += kThreads)
+        if (p.lse) p.lse[row * c.n_heads + y] = -INFINITY;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      constexpr int kPer = kMaxPagedSeqs / 32;
+      int64_t mine = 0;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int i = lane * kPer + k;
+        mine += i < p.n ? static_cast<int64_t>(setup->per_head[i]) * c.n_kv : 0;
+      }
+      int64_t incl = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += y;
+      }
+      int64_t at = incl - mine;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int i = lane * kPer + k;
+        if (i <= p.n) setup->cum[i] = at;
+        at += i < p.n ? static_cast<int64_t>(setup->per_head[i]) * c.n_kv : 0;
+      }
+      if (lane == 31 && p.n == kMaxPagedSeqs) setup->cum[p.n] = at;
+      __syncwarp();
+      const int64_t T = setup->cum[p.n];
+      Start s;
+      s.left = 0;
+      s.share = s.rest = s.u = 0;
+      s.i = s.h = s.b = s.s0 = 0;
+      const int64_t ctas = min(static_cast<int64_t>(gridDim.x), T);
+      if (static_cast<int64_t>(blockIdx.x) < ctas) {
+        s.share = T / ctas;
+        s.rest = T - s.share * ctas;
+        const int64_t u0 = blockIdx.x * s.share + min(static_cast<int64_t>(blockIdx.x), s.rest);
+        s.left = s.share + (static_cast<int64_t>(blockIdx.x) < s.rest ? 1 : 0);
+        int lo = 0, hi = p.n - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) / 2;
+          if (setup->cum[mid] <= u0) lo = mid; else hi = mid - 1;
+        }
+        const int64_t per_head = static_cast<int64_t>(setup->per_head[lo]);
+        int64_t within = u0 - setup->cum[lo];
+        s.i = lo;
+        s.h = static_cast<int>(within / per_head);
+        within -= s.h * per_head;
+        const int32_t len = seq_length(p, lo);
+        const int nb = blocks_of(p, lo);
+        for (int b0 = 0; b0 < nb; b0 += 32) {          // the block that holds unit `within` of this head's
+          Block k;
+          k.i = lo;
+          k.b = b0 + lane;
+          int64_t units = 0;
+          if (k.b < nb) {
+            set_block(p, k, len);
+            units = units_of(k);
+          }
+          int64_t run = units;
+#pragma unroll
+          for (int x = 1; x < 32; x <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, run, x);
+            if (lane >= x) run += y;
+          }
+          const uint32_t past = __ballot_sync(0xffffffffu, run > within);
+          if (past) {
+            const int l = __ffs(past) - 1;
+            s.b = b0 + l;
+            within -= __shfl_sync(0xffffffffu, run - units, l);
+            break;
+          }
+          within -= __shfl_sync(0xffffffffu, run, 31);
+        }
+        // `within` the block: its cost comes before its steps
+        const int64_t before = max(kItemCost - within, static_cast<int64_t>(0));
+        s.left -= before;
+        s.s0 = static_cast<int32_t>(max(within - kItemCost, static_cast<int64_t>(0)));
+        s.u = u0 + before - s.s0;
+      }
+      if (lane == 0) bars->start = s;
+    }
+    __syncthreads();
+  }
+
+  if (warp >= kLoadWarp0) {
+    regs_dec<kRegsLoad>();
+    // ------------------------------------------------------------ keys and values
+    const int w = warp - kLoadWarp0;
+    const uint32_t skv = smem_u32(sKV);
+    bool ok = true;
+    int stage = 0;
+    uint32_t round = 0;                 // times that the ring has gone around
+    int slot = -1;                      // of the block's flags
+    auto acquire = [&]() {
+      if (ok && round > 0) ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_empty[stage], (round - 1) & 1u, wc, 1));
+    };
+    auto note = [&](const TileRef& r, uint32_t odd) {      // where a block begins, what it holds, where it ends
+      if (r.meta & 2) {
+        slot = (slot + 1) % kFlagSlots;
+        if (lane < kFlagTiles) bars->flags[slot][w][lane] = 0;
+        __syncwarp();
+      }
+      if (r.values() && r.tok0 + BN > r.watch) {
+        odd = __reduce_or_sync(0xffffffffu, odd);
+        if (odd && lane == 0) bars->flags[slot][w][min(r.meta >> 8, kFlagTiles - 1)] = odd;
+      }
+      if (r.meta & 4) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->flags_full[slot]);
+      }
+    };
+    auto publish = [&](int s) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+    };
+    auto advance = [&]() {
+      if (++stage == C::kStages) {
+        stage = 0;
+        ++round;
+      }
+    };
+    TileWalk<> walk(p, bars->start);
+    if constexpr (TYPE == SR_PAGE_BF16) {
+      // copies of kAhead tiles in flight
+      constexpr int kAhead = 2;
+      TileRef r[kAhead + 1];
+      bool live[kAhead + 1];
+      int at[kAhead + 1];
+#pragma unroll
+      for (int k = 0; k <= kAhead; ++k) live[k] = false;
+      TileRef nr;
+      Pages ng;
+      bool more = walk.next(nr, p);
+      if (more) fetch_pages(ng, nr, c, w, lane);
+      while (ok) {
+        bool any = false;
+#pragma unroll
+        for (int k = 0; k <= kAhead; ++k) {
+          const int old = (k + 1) % (kAhead + 1);
+          live[k] = more;
+          if (more) {
+            r[k] = nr;
+            Pages g = ng;
+            check_pages(g, nr, c, w, lane);
+            acquire();
+            if (!ok) break;
+            at[k] = stage;
+            copy_tile<D>(r[k], g, c, p.kv_heads, skv + stage * C::kTileBytes, w, lane);
+            advance();
+            more = walk.next(nr, p);
+            if (more) fetch_pages(ng, nr, c, w, lane);
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+          if (live[old]) {
+            uint32_t odd = 0;
+            if (r[old].values() && r[old].tok0 + w * 32 + 32 > r[old].watch) odd = clean_tile<D>(r[old], skv + at[old] * C::kTileBytes, w, lane);
+            note(r[old], odd);
+            publish(at[old]);
+            live[old] = false;
+          }
+          any |= live[k];
+        }
+        if (!any && !more) {
+          bool left = false;
+#pragma unroll
+          for (int k = 0; k <= kAhead; ++k) left |= live[k];
+          if (!left) break;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+      // registers: the next tile's bytes, the page entries of the one after it
+      Raw<D, TYPE> raw[2];
+      TileRef r[2], nr;
+      Pages ng;
+      bool have[2] = {false, false};
+      bool more = walk.next(nr, p);
+      if (more) fetch_pages(ng, nr, c, w, lane);
+      auto fill = [&](Raw<D, TYPE>& v, TileRef& t, bool& h) {
+        h = more;
+        if (!more) return;
+        t = nr;
+        Pages g = ng;
+        check_pages(g, t, c, w, lane);
+        load_raw<D, TYPE>(v, t, g, c, p.kv_heads, w, lane);
+        more = walk.next(nr, p);
+        if (more) fetch_pages(ng, nr, c, w, lane);
+      };
+      fill(raw[0], r[0], have[0]);
+      while (ok && (have[0] || have[1])) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          fill(raw[k ^ 1], r[k ^ 1], have[k ^ 1]);
+          if (!have[k]) continue;
+          acquire();
+          if (!ok) break;
+          note(r[k], store_raw<D, TYPE>(raw[k], r[k], skv + stage * C::kTileBytes, w, lane));
+          publish(stage);
+          advance();
+          have[k] = false;
+        }
+      }
+    }
+  } else if (warp >= kMmaWarp) {
+    regs_dec<kRegsOther>();
+    Walker walk(p, bars->start);
+    bool ok = true;
+    uint32_t items = 0;
+    if (warp >= kQWarp0) {
+      // ---------------------------------------------------------- queries
+      constexpr int kLanes = D / 8, kRows = 32 / kLanes;      // lanes of a row, rows per load
+      const int w = warp - kQWarp0;
+      const uint32_t sq = smem_u32(sQ);
+      const int group = c.group;
+      while (walk.next()) {
+        const Block& k = walk.k;
+        if (items > 0) {
+          // the MMAs are done with the last block's, and its scales are read
+          ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_empty, (items - 1) & 1u, wc, 2) &&
+                                           wait_bounded(&bars->q_seen, (items - 1) & 1u, wc, 2));
+          if (!ok) break;
+        }
+        const int tiles = k.split ? 1 : 2;
+        const int64_t row00 = static_cast<int64_t>(p.row0[k.i]) + k.tok0;
+        constexpr int kBatch = 4;
+        for (int x0 = w * kRows * kBatch; x0 < tiles * BM; x0 += kQWarps * kRows * kBatch) {
+          uint4 v[kBatch];
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) {
+            const int x = x0 + y * kRows + lane / kLanes, tr = x % BM;
+            const int tok = static_cast<int>(static_cast<uint32_t>(tr) * p.group_magic >> 16);
+            const int token = x / BM * p.tpt + tok, hh = tr - tok * group;
+            const bool there = x < tiles * BM && tok < p.tpt && token < k.ntok;
+            v[y] = there ? *reinterpret_cast<const uint4*>(p.q + ((row00 + token) * c.n_heads + k.h * group + hh) * D + lane % kLanes * 8)
+                         : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int y = 0; y < kBatch; ++y) {
+            const int x = x0 + y * kRows + lane / kLanes, tr = x % BM, t = x / BM;
+            if constexpr (C::kHalf) {
+              // fp16, scaled by a power of two to a largest element in [1, 2)
+              auto pair = [](uint32_t z) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&z)); };
+              const float2 f[4] = {pair(v[y].x), pair(v[y].y), pair(v[y].z), pair(v[y].w)};
+              float top = 0.f;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) top = fmaxf(top, fmaxf(fabsf(f[z].x), fabsf(f[z].y)));
+#pragma unroll
+              for (int s = 1; s < kLanes; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+              const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
+              const float down = ldexpf(1.f, -e);
+              uint32_t h[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const __half2 hz = __floats2half2_rn(f[z].x * down, f[z].y * down);
+                h[z] = *reinterpret_cast<const uint32_t*>(&hz);
+              }
+              if constexpr (TYPE == SR_PAGE_INT4)
+                v[y] = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632), __byte_perm(h[1], h[3], 0x5410),
+                                  __byte_perm(h[1], h[3], 0x7632));
+              else
+                v[y] = make_uint4(h[0], h[1], h[2], h[3]);
+              if (x < tiles * BM && lane % kLanes == 0) bars->qexp[t][tr] = static_cast<int8_t>(e);
+            }
+            if (x < tiles * BM) store16(sq + t * C::kTileBytes + piece_at<D>(tr, lane % kLanes), v[y]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+        ++items;
+      }
+    } else {
+      // ---------------------------------------------------------- MMA issuer (the warp in step, one lane issues)
+      const uint32_t leader = elect_one();
+      const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
+      bool issued = false;
+      int stage = 0;
+      uint32_t phase = 0, pb[2] = {0, 0};       // ring position; P tiles of each group waited on
+      auto take = [&]() -> int {                // the next tile of the ring
+        const int s = stage;
+        if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_full[s], phase, wc, 3));
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return s;
+      };
+      auto qk = [&](int t, bool split, int s) {
+        const uint32_t qt = sq + (split ? 0 : t) * C::kTileBytes, kt = skv + s * C::kTileBytes;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * C::kAtomBytes + (kk % 4) * 32;
+          mma_ss_w(tmem + t * BN, sdesc_sw128(qt + off, 16, 1024), sdesc_sw128(kt + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u, leader);
+        }
+        tc_commit_w(&bars->s_full[t], leader);
+        issued = true;
+      };
+      auto pv = [&](int t, int s, bool acc) {
+        const uint32_t vt = skv + s * C::kTileBytes;
+        const uint32_t par = pb[t] & 1u;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (ok) ok = __all_sync(0xffffffffu, wait_bounded(half == 0 ? &bars->p_half[t] : &bars->p_full[t], par, wc, 4));
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            mma_ts_w(tmem + 256 + t * 128, tmem + t * BN + kk * 8, sdesc_sw128(vt + kk * 16 * 128, C::kAtomBytes, 1024), C::kIdescPV,
+                     (acc || kk > 0) ? 1u : 0u, leader);
+        }
+        ++pb[t];
+      };
+      while (walk.next()) {
+        const Block& k = walk.k;
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 2));
+        if (!ok) break;
+        const int n = k.s1 - k.s0;
+        if (!k.split) {
+          for (int j = 0; j <= n && ok; ++j) {
+            const int v = j > 0 ? take() : 0, kt = j < n ? take() : 0;
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j > 0) {
+                pv(t, v, j > 1);
+                if (!ok) break;
+                if (j == n) tc_commit_w(&bars->o_done[t], leader);
+              }
+              if (j < n) qk(t, false, kt);
+            }
+            if (!ok) break;
+            if (j > 0) tc_commit_w(&bars->kv_empty[v], leader);
+            if (j < n) tc_commit_w(&bars->kv_empty[kt], leader);
+            if (j == n - 1) tc_commit_w(&bars->q_empty, leader);
+          }
+        } else {
+          const int n1 = k.count(1);
+          for (int j = 0; j <= n && ok; ++j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int cnt = t == 0 ? n : n1;
+              if (j > 0 && j <= cnt) {
+                const int v = take();
+                if (!ok) break;
+                tc_fence_after();
+                pv(t, v, j > 1);
+                if (!ok) break;
+                if (j == cnt) tc_commit_w(&bars->o_done[t], leader);
+                tc_commit_w(&bars->kv_empty[v], leader);
+              }
+              if (j < cnt) {
+                const int kt = take();
+                if (!ok) break;
+                tc_fence_after();
+                qk(t, true, kt);
+                tc_commit_w(&bars->kv_empty[kt], leader);
+              }
+            }
+            if (ok && j == n - 1) tc_commit_w(&bars->q_empty, leader);
+          }
+        }
+        ++items;
+        if (!ok) break;
+      }
+      if ((!ok || bars->abort) && issued) {
+        // no tensor-core work may still be running when TMEM is released
+        tc_commit_w(&bars->drain, leader);
+        wait_drain(&bars->drain, 0, kTimeoutNs);
+      }
+    }
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax groups
+    const int t = warp / 4, row = threadIdx.x % BM;
+    const uint32_t lane_base = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + t * BN, t_o = tmem + lane_base + 256 + t * 128;
+    const int group = c.group;
+    const int tr = static_cast<int>(static_cast<uint32_t>(row) * p.group_magic >> 16), hh = row - tr * group;
+    bool ok = true;
+    uint32_t items = 0, sb = 0, od[2] = {0, 0}, nx = 0, cuts = 0;
+    Walker walk(p, bars->start);
+    while (ok && walk.next()) {
+      const Block& k = walk.k;
+      ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 5));
+      if (!ok) break;
+      const int kv = static_cast<int>(static_cast<uint32_t>(k.h) * p.head_magic >> 22);
+      float sl2 = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
+      if constexpr (C::kHalf) sl2 *= ldexpf(1.f, bars->qexp[k.split ? 0 : t][row]);
+      sl2 = fmaxf(sl2, 0x1p-126f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->q_seen);
+      const int token = (k.split ? 0 : t * p.tpt) + tr;          // of the block's
+      const bool live = tr < p.tpt && token < k.ntok;
+      const int32_t lim = !live ? k.lim : p.causal ? max(k.base + k.tok0 + token + 1, 0) : k.lim;
+      const int32_t* table = c.table + static_cast<int64_t>(p.id[k.i]) * c.max_pages;
+      const int cnt = k.count(t);
+      // the pages of a key tile's groups, by lanes 0-7: those that are none of the pool are not seen
+      auto fetch = [&](int j) {
+        const int32_t tok = k.tile(t, j) * BN + (lane & 7) * 16;
+        return j < cnt && tok < k.lim ? __ldg(table + page_of_group(tok >> 4, c.magic)) : 0;
+      };
+      int32_t page = fetch(0);
+      float m = -INFINITY, l = 0.f;
+      const float2 sl2x2 = make_float2(sl2, sl2);
+      for (int j = 0; j < cnt; ++j) {
+        const int valid = lim - k.tile(t, j) * BN;
+        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && page < c.n_pages);
+        page = fetch(j + 1);
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->s_full[t], (sb + static_cast<uint32_t>(j)) & 1u, wc, 5));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t rr[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32(t_s + x * 32, rr[x]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_fix(rr[x]);
+        float* s = reinterpret_cast<float*>(&rr[0][0]);
+        if (__any_sync(0xffffffffu, valid < BN)) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+            if (i >= valid) s[i] = -INFINITY;
+        }
+        if (there != 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+            if (!(there >> (i / 16) & 1u)) s[i] = -INFINITY;
+        }
+        float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
+#pragma unroll
+        for (int i = 8; i < BN; i += 8) {
+          a0 = fmax3(a0, s[i], s[i + 1]);
+          a1 = fmax3(a1, s[i + 2], s[i + 3]);
+          a2 = fmax3(a2, s[i + 4], s[i + 5]);
+          a3 = fmax3(a3, s[i + 6], s[i + 7]);
+        }
+        const float top = fmax3(a0, a1, fmaxf(a2, a3)) * sl2 - C::kLift;
+        float f = 1.f;                    // factor that takes O and l to the new reference
+        const bool rescale = __any_sync(0xffffffffu, top > m + C::kSlack);
+        if (rescale) {
+          const float m1 = fmaxf(m, top);
+          f = m == -INFINITY ? 0.f : ex2_approx(m - m1);
+          m = m1;
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const float2 negm = make_float2(neg, neg);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const int i = x * 32 + 2 * q;
+            const float2 y = __ffma2_rn(make_float2(s[i], s[i + 1]), sl2x2, negm);
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            acc[q % 4] = __fadd2_rn(acc[q % 4], e);
+            if constexpr (C::kHalf) {
+              const __half2 h = __floats2half2_rn(e.x, e.y);
+              pk[q] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+              pk[q] = pack_bf16x2(e.x, e.y);
+            }
+          }
+          tmem_st16(t_s + x * 16, pk);
+          if (x == 1) {
+            if (rescale && j > 0) {
+              // O was last written by the last step's product, which the commit behind S covers
+#pragma unroll
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[32];
+                tmem_ld32(t_o + q * 32, o);
+                tmem_wait_ld();
+                tmem_fix(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st32(t_o + q * 32, o);
+              }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_half[t]);
+          }
+        }
+        const float2 s01 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+        l = l * f + (s01.x + s01.y);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[t]);
+      }
+      if (!ok) break;
+      sb += static_cast<uint32_t>(cnt);
+
+      // ---- the block's end
+      const bool whole = k.s0 == 0 && k.s1 == k.steps;
+      const uint32_t w0 = od[0], w1 = od[1];
+      const bool merge = k.split && k.count(1) > 0;
+      od[0] += 1;
+      od[1] += !k.split || merge ? 1u : 0u;
+      const int slot = items % kFlagSlots;
+      ok = __all_sync(0xffffffffu, wait_bounded(&bars->flags_full[slot], (items / kFlagSlots) & 1u, wc, 7));
+      if (!ok) break;
+      ++items;
+      if (k.split && t == 1) {
+        // hand (m, l) to group 0 and wait until it has read them and O_1
+        bars->xm[row] = cnt > 0 ? m : -INFINITY;
+        bars->xl[row] = cnt > 0 ? l : 0.f;
+        mbar_arrive(&bars->x_full);
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->x_empty, nx & 1u, wc, 9));
+        ++nx;
+        if (!ok) break;
+      } else {
+        if (k.split) ok = wait_bounded(&bars->x_full, nx & 1u, wc, 9);
+        ok = ok && wait_bounded(&bars->o_done[t], (t == 0 ? w0 : w1) & 1u, wc, 6);
+        if (merge) ok = ok && wait_bounded(&bars->o_done[1], w1 & 1u, wc, 6);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float f0 = 1.f, f1 = 0.f;
+        if (merge) {
+          const float m1 = bars->xm[row], l1 = bars->xl[row];
+          const float mm = fmaxf(m, m1);
+          f0 = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m - mm);
+          f1 = m1 == -INFINITY ? (l1 == 0.f ? 0.f : 1.f) : ex2_approx(m1 - mm);
+          l = l * f0 + l1 * f1;
+          m = mm;
+        }
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int x = 0; x < kLoadWarps * kFlagTiles; ++x) odd |= bars->flags[slot][x / kFlagTiles][x % kFlagTiles];
+        const float vscale = C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv])) : 1.f);
+        const float to = whole ? (l == 0.f ? 0.f : vscale / l) : vscale;
+        const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + token) * c.n_heads + k.h * group + hh;
+        // a whole block with odd values goes through the slot too (free: only the last block can be cut behind it), since
+        // add_odd reads the query row, whose place the output may take
+        float* part = slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0);
+        const int prow = (k.split ? 0 : t) * BM + row;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          tmem_ld32(t_o + x * 32, o);
+          tmem_wait_ld();
+          tmem_fix(o);
+          float* of = reinterpret_cast<float*>(o);
+          if (merge) {
+            uint32_t o1[32];
+            tmem_ld32(tmem + lane_base + 256 + 128 + x * 32, o1);
+            tmem_wait_ld();
+            tmem_fix(o1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              of[i] = (f0 == 0.f ? 0.f : of[i] * f0) + (f1 == 0.f ? 0.f : __uint_as_float(o1[i]) * f1);
+          }
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = of[column_of<TYPE>(i)];
+          if (odd && live) {
+#pragma unroll 1
+            for (int z = 0; z < kLoadWarps * kFlagTiles; ++z) {
+              uint32_t bits = bars->flags[slot][z / kFlagTiles][z % kFlagTiles];
+              const int32_t tok = (k.lim_min / BN + z % kFlagTiles) * BN + z / kFlagTiles * 32;
+              while (bits) {
+                const int32_t at = tok + __ffs(bits) - 1;
+                bits &= bits - 1;
+                if (at < lim) {
+                  float sc = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
+                  add_odd<D, TYPE>(p, y, x * 32, p.id[k.i], at, kv, p.q + out * D, sc, m);
+                }
+              }
+            }
+          }
+          if (live) {
+            if (whole && !odd) {
+              uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x * 32);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 z;
+                z.x = pack_bf16x2(y[8 * i] * to, y[8 * i + 1] * to);
+                z.y = pack_bf16x2(y[8 * i + 2] * to, y[8 * i + 3] * to);
+                z.z = pack_bf16x2(y[8 * i + 4] * to, y[8 * i + 5] * to);
+                z.w = pack_bf16x2(y[8 * i + 6] * to, y[8 * i + 7] * to);
+                dst[i] = z;
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + prow * D + x * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i] * to, y[4 * i + 1] * to, y[4 * i + 2] * to, y[4 * i + 3] * to);
+            }
+          }
+        }
+        if (whole && odd && live)
+#pragma unroll 1
+          for (int i = 0; i < D; i += 2)
+            *reinterpret_cast<uint32_t*>(p.o + out * D + i) = pack_bf16x2(part[prow * D + i], part[prow * D + i + 1]);
+        if (live) {
+          if (!whole)
+            *reinterpret_cast<float2*>(part + 2 * BM * D + 2 * prow) = make_float2(m, l);
+          else if (p.lse)
+            p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+        if (k.split) {
+          tc_fence_before();
+          mbar_arrive(&bars->x_empty);
+          ++nx;
+        }
+      }
+      if (!whole) {
+        // the last of the block's CTAs to arrive joins their parts
+        const Start& s = bars->start;
+        const int c0 = owner_of(walk.u, s.share, s.rest), c1 = owner_of(walk.u + k.steps - 1, s.share, s.rest);
+        __threadfence();
+        mbar_arrive(&bars->part_done);
+        if (threadIdx.x == 0) {
+          int last = 0;
+          if (wait_bounded(&bars->part_done, cuts & 1u, wc, 10)) {
+            __threadfence();
+            last = atomicAdd(p.arrivals + c0, 1) == c1 - c0;
+            if (last) p.arrivals[c0] = 0;
+          }
+          bars->last = last;
+          mbar_arrive(&bars->part_last);
+        }
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->part_last, cuts & 1u, wc, 10));
+        ++cuts;
+        if (ok && bars->last) join_block<D>(p, k, c0, c1 - c0 + 1, warp, lane);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int TYPE>
+cudaError_t prepare() {
+  cudaFuncAttributes a;
+  cudaError_t e = cudaFuncGetAttributes(&a, paged_prompt_kernel<D, TYPE>);
+  if (e != cudaSuccess) return e;
+  // the softmax groups' registers are granted only if the launch has as many as the split assumes
+  if (a.numRegs != kLaunchRegs || a.maxThreadsPerBlock < kThreads) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(paged_prompt_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, TYPE>::kSmemBytes);
 }
 
 template <int D, int TYPE>
 cudaError_t launch(const PromptParams& p, cudaStream_t st) {
-  const int64_t tasks = static_cast<int64_t>(p.row0[p.n]) * p.c.n_heads;
-  return launch_dependent(paged_prompt_kernel<D, TYPE>, static_cast<unsigned>((tasks + kThreads / 32 - 1) / (kThreads / 32)),
-                          kThreads, 0, st, p);
+  return launch_dependent(paged_prompt_kernel<D, TYPE>, static_cast<unsigned>(std::min(sm_count(), kMaxPromptCtas)), kThreads,
+                          Cfg<D, TYPE>::kSmemBytes, st, p);
 }
 
 template <int D>
@@ -111,7 +1260,25 @@ cudaError_t launch(const PromptParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_paged_prompt(const PromptParams& p, cudaStream_t st) {
+size_t paged_prompt_floats(int head_dim) {
+  return static_cast<size_t>(2 * kMaxPromptCtas) * (head_dim == 128 ? slot_floats<128>() : slot_floats<64>());
+}
+
+cudaError_t paged_prompt_prepare(int head_dim, int page_type) {
+  if (page_type == SR_PAGE_BF16) return head_dim == 128 ? prepare<128, SR_PAGE_BF16>() : prepare<64, SR_PAGE_BF16>();
+  if (page_type == SR_PAGE_INT4) return head_dim == 128 ? prepare<128, SR_PAGE_INT4>() : prepare<64, SR_PAGE_INT4>();
+  return head_dim == 128 ? prepare<128, SR_PAGE_E4M3>() : prepare<64, SR_PAGE_E4M3>();
+}
+
+cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st) {
+  p.tpt = BM / p.c.group;
+  p.group_magic = (65536u + static_cast<uint32_t>(p.c.group) - 1u) / static_cast<uint32_t>(p.c.group);   // exact below 128
+  int64_t blocks = 0;
+  for (int i = 0; i < p.n; ++i) {
+    p.blk0[i] = static_cast<int32_t>(blocks);
+    blocks += (p.row0[i + 1] - p.row0[i] + 2 * p.tpt - 1) / (2 * p.tpt);
+  }
+  p.blocks = static_cast<int32_t>(blocks);
   return p.c.head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
 }
 

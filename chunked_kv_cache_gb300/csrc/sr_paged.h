@@ -11,6 +11,7 @@
 namespace sr {
 
 constexpr int kMaxPagedSeqs = SR_MAX_PAGED_SEQS;
+constexpr int kMaxPromptCtas = 160;  // most CTAs a launch over several new tokens per sequence may have
 constexpr int kMaxPagedCtas = 512;   // most CTAs an attention launch may have (partial result slots)
 
 // The pool row of logical index `idx` of a sequence whose block table row is
@@ -142,10 +143,17 @@ struct PromptParams {
   float* lse;
   int32_t kv_heads;
   uint32_t head_magic;
+  int32_t* arrivals;       // [kMaxPromptCtas] parts of a block that are done; left at zero
+  float* parts;            // [kMaxPromptCtas][2] partial results
   int32_t n;
   int32_t causal;
   int32_t id[kMaxPagedSeqs];
   int32_t row0[kMaxPagedSeqs + 1]; // first row of each sequence
+  // set by the launcher
+  int32_t tpt;             // tokens of a tile of 128 query rows
+  uint32_t group_magic;    // r / group = r * group_magic >> 16 for r < 128
+  int32_t blocks;          // of query rows, over all sequences
+  int32_t blk0[kMaxPagedSeqs];     // first block of each sequence
 };
 
 struct EvictParams {
@@ -160,7 +168,9 @@ struct EvictParams {
 cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_read(const ReadParams& p, cudaStream_t st);
-cudaError_t launch_paged_prompt(const PromptParams& p, cudaStream_t st);
+cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st);
+cudaError_t paged_prompt_prepare(int head_dim, int page_type);
+size_t paged_prompt_floats(int head_dim);                            // floats of all partial results of a prompt's launch
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile

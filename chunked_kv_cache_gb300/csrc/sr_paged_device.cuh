@@ -1,0 +1,48 @@
+// sr_paged_device.cuh -- decoding of the paged cache's pages of fewer than 16 bits, shared by the kernels that read
+// them. Internal to libsr.so.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace sr {
+
+// two e4m3 values (the low 16 bits) as fp16, exactly
+__device__ __forceinline__ uint32_t half2_of_e4m3(uint32_t x) {
+  uint32_t y;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y) : "h"(static_cast<uint16_t>(x)));
+  return y;
+}
+
+// ---- 4-bit codes as fp16. A mask puts a code c into the fraction of 16 (16 + c / 32) or of 1 (1 + c / 32); one fused
+// product and sum with its scale s then leaves (c - 8) / 32 * s, exactly: at most 7 significant bits, never below fp16's
+// smallest number. Four pairs of one word in 9 instructions, scale and all.
+__device__ __forceinline__ uint32_t half2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+// What a decoding needs of a pair of scales.
+struct ScalePair {
+  uint32_t s, off16, off1;
+};
+__device__ __forceinline__ ScalePair scale_pair(uint32_t s) {
+  return {s, half2_mul(s, 0xCC10CC10u), half2_mul(s, 0xBD00BD00u)};     // -16.25 s, -1.25 s
+}
+// y[i]: the i-th value of the word's low unit and of its high one.
+__device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const ScalePair& s) {
+  const uint32_t z = __byte_perm(w, 0, 0x2301);
+  y[0] = half2_fma((w & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
+  y[1] = half2_fma((w & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
+  y[2] = half2_fma((z & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
+  y[3] = half2_fma((z & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
+}
+constexpr float kDecoded = 32.f;      // a value is so many times what decode_word leaves
+
+}  // namespace sr
