@@ -18,6 +18,7 @@ struct sr_paged_cache {
   sr_paged_buffers buf;
   sr::PagedView view;
   sr::PagedLayout layout;
+  CUtensorMap kmap, vmap;   // bf16 pages
   int device;
   int32_t* mark;         // [max_seqs] the last call that named a row (finds repeated rows)
   int32_t stamp;
@@ -204,6 +205,12 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type, v.group);
   if (e == cudaSuccess) e = sr::paged_prompt_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::paged_evict_prepare();
+  if (e == cudaSuccess && cfg->page_type == SR_PAGE_BF16) {
+    const int64_t rows = static_cast<int64_t>(cfg->n_pages) * cfg->page_tokens, row = static_cast<int64_t>(cfg->n_kv_heads) * cfg->head_dim;
+    const int box = sr::paged_box_rows(cfg->page_tokens);
+    if (!sr::encode_rows(&c->kmap, b.k_pages, rows, row, box) || !sr::encode_rows(&c->vmap, b.v_pages, rows, row, box))
+      e = cudaErrorUnknown;
+  }
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);
   if (e != cudaSuccess) {
@@ -301,6 +308,8 @@ sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, cons
   p.causal = causal != 0;
   p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
   p.parts = ws_at<float>(c, c->layout.parts);
+  p.kmap = c->kmap;
+  p.vmap = c->vmap;
   p.c = c->view;
   take_heads(c, p.c, p.kv_heads, p.head_magic);
   p.q = static_cast<const __nv_bfloat16*>(q);

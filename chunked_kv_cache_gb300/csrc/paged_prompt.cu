@@ -33,12 +33,10 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int BM = 128, BN = 128;
-constexpr int kMmaWarp = 8, kQWarp0 = 9, kLoadWarp0 = 12;
-constexpr int kQWarps = 3, kLoadWarps = 4;
+constexpr int kMmaWarp = 8, kPlanWarp = 9, kQWarp0 = 10, kLoadWarp0 = 12;
+constexpr int kQWarps = 2, kLoadWarps = 4;
 constexpr int kLaunchRegs = 128;
-constexpr uint32_t kRegsSoftmax = 184, kRegsOther = 48, kRegsLoad = 96;
-static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsLoad) <= kThreads * kLaunchRegs,
-              "register split exceeds what the block is launched with");
+constexpr uint32_t kRegsSoftmax = 176;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kItemCost = 1;           // steps that changing blocks costs
@@ -47,16 +45,21 @@ constexpr int kItemCost = 1;           // steps that changing blocks costs
 // made after they had read the first one's flags.
 constexpr int kFlagSlots = 8, kFlagTiles = 3;
 
+constexpr int kBarBytes = 3072;
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool kHalf = TYPE != SR_PAGE_BF16;       // products of fp16, else of bf16
+  // 8-bit pages come through more registers
+  static constexpr uint32_t kRegsOther = TYPE == SR_PAGE_E4M3 ? 48 : 56, kRegsLoad = 160 - kRegsOther;
+  static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsLoad) <= kThreads * kLaunchRegs,
+                "register split exceeds what the block is launched with");
   static constexpr int kAtoms = D / 64;
   static constexpr int kAtomBytes = BM * 128;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
   static constexpr int kSmemQ = 2 * kTileBytes;
   static constexpr int kSmemKV = kStages * kTileBytes;
-  static constexpr int kSmemBytes = kSmemQ + kSmemKV + 2048 + 1024;
+  static constexpr int kSmemBytes = kSmemQ + kSmemKV + kBarBytes;
   static_assert(kSmemBytes <= 232448, "more than 227 KB of shared memory per block");
   static constexpr uint32_t kIdescS = kHalf ? idesc_f16_f32(BM, BN, 0) : idesc_bf16_f32(BM, BN, 0);
   static constexpr uint32_t kIdescPV = kHalf ? idesc_f16_f32(BM, D, 1) : idesc_bf16_f32(BM, D, 1);
@@ -87,12 +90,30 @@ struct Start {
   int64_t u;             // unit of the first block's first step (not this CTA's)
 };
 
+// A tile of 128 tokens' keys or values, for the loading warps.
+struct Tile {
+  int64_t off[8];      // where each group of 16 tokens begins for this head (bf16: its pool row); -1: zeros
+  int32_t lim;         // tokens from here on (within the tile) are zeros
+  int32_t watch;       // tokens from here on are seen by some rows only: values that are no finite numbers leave the tile
+  int32_t head;        // key/value head
+  int32_t meta;        // bit 0: values; bit 1: a block's first tile; bit 2: its last; bits 8..: flag word. -1: no more tiles
+};
+constexpr int kTileSlots = 8;
+
+struct Record {        // a block, as the softmax groups read it
+  Block k;
+  int64_t u;
+};
+
 struct Bars {
   uint64_t q_full, q_empty, q_seen;
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t x_full, x_empty, part_done, part_last, drain;
   uint64_t flags_full[kFlagSlots];
+  uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
+  Tile tile[kTileSlots];
+  Record rec[2];
   uint32_t tmem_base;
   int abort;
   int last;
@@ -103,7 +124,7 @@ struct Bars {
   int8_t qexp[2][BM];
   float xm[BM], xl[BM];
 };
-static_assert(sizeof(Bars) <= 2048, "barrier area too small");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier area too small");
 
 struct Setup {                   // overlays the stages before they are used
   int64_t cum[kMaxPagedSeqs + 1];
@@ -195,18 +216,12 @@ __device__ __forceinline__ int owner_of(int64_t u, int64_t share, int64_t rest) 
 }
 
 // -------------------------------------------------------------- loading keys and values
-// One tile of 128 tokens' keys or values for the loading warps.
 struct TileRef {
-  int32_t tok0;        // first token
-  int32_t lim;         // tokens of the sequence from here on are zeros
-  int32_t watch;       // tokens from here on are seen by some rows only: values that are no finite numbers leave the tile
-  int32_t seq, head;   // row of the block table, key/value head
-  int32_t meta;        // bit 0: values; bit 1: a block's first tile; bit 2: its last; bits 8..: flag word
-  __device__ __forceinline__ bool values() const { return meta & 1; }
+  int32_t tok0, lim, watch;      // first token; as in Tile, of the sequence
+  int32_t seq, head, meta;       // row of the block table
 };
 
 // The tiles of this CTA in the order in which the MMAs take them: before every step's keys the values of the step before.
-template <int UNUSED = 0>
 struct TileWalk {
   Walker w;
   int j, t, part;      // step of the block (0 .. n), softmax group, 0 values 1 keys
@@ -287,31 +302,13 @@ __device__ __forceinline__ bool finite_only(uint4& x) {
   return any;
 }
 
-// A loading warp's share of a tile, 32 tokens: two groups of 16, which never cross a page.
-struct Pages {
-  int32_t page[2], slot[2];    // page -1: zeros
+// A loading warp's share of a tile: 32 tokens, two groups of 16.
+struct Share {
+  int64_t off[2];
+  int32_t lim, watch, head, meta;         // lim, watch: of the warp's 32
+  __device__ __forceinline__ bool values() const { return meta & 1; }
+  __device__ __forceinline__ bool watched() const { return values() && watch < 32; }
 };
-__device__ __forceinline__ void fetch_pages(Pages& g, const TileRef& r, const PagedView& c, int w, int lane) {
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int32_t tok = r.tok0 + w * 32 + x * 16;
-    g.page[x] = -1;
-    if (tok < r.lim) {
-      const int32_t pg = page_of_group(tok >> 4, c.magic);
-      g.slot[x] = tok - pg * c.page_tokens;
-      g.page[x] = __ldg(c.table + static_cast<int64_t>(r.seq) * c.max_pages + pg);
-    }
-  }
-}
-// after the entries have arrived: those that are no page of the pool are reported and read as zeros
-__device__ __forceinline__ void check_pages(Pages& g, const TileRef& r, const PagedView& c, int w, int lane) {
-#pragma unroll
-  for (int x = 0; x < 2; ++x)
-    if (r.tok0 + w * 32 + x * 16 < r.lim && (g.page[x] < 0 || g.page[x] >= c.n_pages)) {
-      if (lane == 0) atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
-      g.page[x] = -1;
-    }
-}
 
 template <int D, int TYPE>
 struct Raw {
@@ -323,15 +320,14 @@ struct Raw {
 // e4m3: lane l of 8 (or 4) takes 16 bytes of a token's row; 4 bits: lanes 0-15 a chunk of the group's 16 tokens, lanes
 // 16-31 the next one. Tokens at or past the limit are zeros (their scales are, for 4 bits).
 template <int D, int TYPE>
-__device__ __forceinline__ void load_raw(Raw<D, TYPE>& v, const TileRef& r, const Pages& g, const PagedView& c, int kv_heads, int w,
-                                         int lane) {
+__device__ __forceinline__ void load_raw(Raw<D, TYPE>& v, const Share& r, const PagedView& c, int kv_heads, int lane) {
   const uint8_t* pages = static_cast<const uint8_t*>(r.values() ? c.v_pages : c.k_pages);
   if constexpr (TYPE == SR_PAGE_INT4) {
     constexpr int kPer = D / 64;              // loads per group
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* rec = pages + record_at(g.page[x] < 0 ? 0 : g.page[x], g.page[x] < 0 ? 0 : g.slot[x], r.head, kv_heads, c.page_tokens, D);
-      const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + (lane & 15) < r.lim;
+      const uint8_t* rec = pages + max(r.off[x], static_cast<int64_t>(0));
+      const bool there = r.off[x] >= 0 && x * 16 + (lane & 15) < r.lim;
 #pragma unroll
       for (int y = 0; y < kPer; ++y) {
         const int ch = 2 * y + lane / 16;
@@ -341,27 +337,26 @@ __device__ __forceinline__ void load_raw(Raw<D, TYPE>& v, const TileRef& r, cons
     }
   } else if constexpr (TYPE == SR_PAGE_E4M3) {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = 16 / kRows;   // lanes of a row, rows per load, loads per group
+    const int64_t pitch = static_cast<int64_t>(kv_heads) * D;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int64_t row0 = g.page[x] < 0 ? 0 : static_cast<int64_t>(g.page[x]) * c.page_tokens + g.slot[x];
+      const uint8_t* row = pages + max(r.off[x], static_cast<int64_t>(0)) + lane / kLanes * pitch + lane % kLanes * 16;
 #pragma unroll
       for (int y = 0; y < kPer; ++y) {
-        const int slot = y * kRows + lane / kLanes;
-        const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + slot < r.lim;
-        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(pages + ((row0 + slot) * kv_heads + r.head) * D) + lane % kLanes)
-                                  : make_uint4(0, 0, 0, 0);
+        const bool there = r.off[x] >= 0 && x * 16 + y * kRows + lane / kLanes < r.lim;
+        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(row + y * kRows * pitch)) : make_uint4(0, 0, 0, 0);
       }
     }
   }
 }
 
 // Decodes and stores; returns a bit per token of the warp's 32 whose values were no finite numbers (and are zeros now).
-template <int D, int TYPE>
-__device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const TileRef& r, uint32_t tile, int w, int lane) {
+template <int D, int TYPE, bool WATCH>
+__device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const Share& r, uint32_t tile, int w, int lane) {
   uint32_t odd = 0;
-  const bool watch = r.values() && r.tok0 + w * 32 + 32 > r.watch;
   auto put = [&](int row, int piece, uint4 y) {          // row of the warp's 32
-    if (watch && r.tok0 + w * 32 + row >= r.watch && finite_only<true>(y)) odd |= 1u << row;
+    if constexpr (WATCH)
+      if (row >= r.watch && finite_only<true>(y)) odd |= 1u << row;
     store16(tile + piece_at<D>(w * 32 + row, piece), y);
   };
   if constexpr (TYPE == SR_PAGE_INT4) {
@@ -374,11 +369,11 @@ __device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const TileR
         const uint32_t b = v.s[x * kPer + y];
         const uint4 z = v.x[x * kPer + y];
         const uint32_t word[4] = {z.x, z.y, z.z, z.w};
+        const ScalePair s0 = scale_pair(__byte_perm(b, 0, 0x4040) << 7), s1 = scale_pair(__byte_perm(b, 0, 0x4141) << 7);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const ScalePair s = scale_pair(__byte_perm(b, 0, q < 2 ? 0x4040 : 0x4141) << 7);
           uint32_t e[4];
-          decode_word(e, word[q], s);
+          decode_word(e, word[q], q < 2 ? s0 : s1);
           put(x * 16 + (lane & 15), ch * 4 + q, make_uint4(e[0], e[1], e[2], e[3]));
         }
       }
@@ -404,32 +399,32 @@ __device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const TileR
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-// bf16: 16 (or 8) lanes copy a token's row; past the limit zeros
+// bf16, where a share is not whole: 16 (or 8) lanes copy a token's row, zeros past the limit
 template <int D>
-__device__ __forceinline__ void copy_tile(const TileRef& r, const Pages& g, const PagedView& c, int kv_heads, uint32_t tile, int w,
-                                          int lane) {
+__device__ __forceinline__ void copy_share(const Share& r, const PagedView& c, int kv_heads, uint32_t tile, int w, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   const __nv_bfloat16* pages = static_cast<const __nv_bfloat16*>(r.values() ? c.v_pages : c.k_pages);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const int64_t row0 = g.page[x] < 0 ? 0 : static_cast<int64_t>(g.page[x]) * c.page_tokens + g.slot[x];
-#pragma unroll
+    const int64_t row0 = max(r.off[x], static_cast<int64_t>(0));
+#pragma unroll 4
     for (int y = 0; y < 16 / kRows; ++y) {
       const int slot = y * kRows + lane / kLanes;
-      const bool there = g.page[x] >= 0 && r.tok0 + w * 32 + x * 16 + slot < r.lim;
+      const bool there = r.off[x] >= 0 && x * 16 + slot < r.lim;
       const __nv_bfloat16* src = pages + ((row0 + (there ? slot : 0)) * kv_heads + r.head) * D + lane % kLanes * 8;
       copy16_or_zero(tile + piece_at<D>(w * 32 + x * 16 + slot, lane % kLanes), src, there);
     }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 // The same lanes look at what they copied, where some rows do not see all of it.
 template <int D>
-__device__ __forceinline__ uint32_t clean_tile(const TileRef& r, uint32_t tile, int w, int lane) {
+__device__ __forceinline__ uint32_t clean_share(const Share& r, uint32_t tile, int w, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   uint32_t odd = 0;
 #pragma unroll 1
   for (int row = lane / kLanes; row < 32; row += kRows)
-    if (r.tok0 + w * 32 + row >= r.watch) {
+    if (row >= r.watch) {
       const uint32_t at = tile + piece_at<D>(w * 32 + row, lane % kLanes);
       uint4 y = load16(at);
       if (finite_only<false>(y)) {
@@ -460,17 +455,17 @@ __device__ __forceinline__ float page_value(const PromptParams& p, const void* p
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at], __NV_E4M3)));
   }
 }
-// Adds the weight of token t times its values that are no finite numbers to 32 sums of a row from dim0 on. Runs only where
-// such values lie among a block's new tokens; the weight is computed again, from the query row and the key.
+// Adds to a row of sums (in memory, each times `to`) the weight of token t times its values that are no finite numbers.
+// Runs only where such values lie among a block's new tokens; the weight is computed again, from the query row and the key.
 template <int D, int TYPE>
-__device__ __noinline__ void add_odd(const PromptParams& p, float* o, int dim0, int32_t seq, int32_t t, int head, const __nv_bfloat16* q,
-                                     float scale, float m) {
+__device__ __noinline__ void add_odd(const PromptParams& p, float* o, int32_t seq, int32_t t, int head, const __nv_bfloat16* q,
+                                     float scale, float m, float to) {
   float x = 0.f;
   for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), page_value<D, TYPE>(p, p.c.k_pages, seq, t, head, d), x);
-  const float w = ex2_approx(x * scale - (m == -INFINITY ? 0.f : m));
-  for (int k = 0; k < 32; ++k) {
-    const float v = page_value<D, TYPE>(p, p.c.v_pages, seq, t, head, dim0 + k);
-    if (!(fabsf(v) < INFINITY)) o[k] = fmaf(w, v, o[k]);
+  const float w = ex2_approx(x * scale - (m == -INFINITY ? 0.f : m)) * to;
+  for (int d = 0; d < D; ++d) {
+    const float v = page_value<D, TYPE>(p, p.c.v_pages, seq, t, head, d);
+    if (!(fabsf(v) < INFINITY)) o[d] = fmaf(w, v, o[d]);
   }
 }
 
@@ -483,41 +478,70 @@ __device__ __forceinline__ float* slot_at(const PromptParams& p, int cta, int sl
 }
 
 // Joins a block's n parts, that of CTA c0 (slot 1) and of those behind it (slot 0): a warp per row, its lanes the dims.
-template <int D>
+// What it costs is the latency of the loads, so kJoinBatch of them are on their way: of as many rows, part by
+// part, or, where a warp has few rows, of one row's parts.
+constexpr int kJoinBatch = 8;
+template <int D, bool ROWS>
 __device__ __noinline__ void join_block(const PromptParams& p, const Block& k, int c0, int n, int warp, int lane) {
-  constexpr int N = D / 32;
+  constexpr int N = D / 32, B = kJoinBatch, R = ROWS ? B : 1;
   __threadfence();
   const int group = p.c.group, rows = k.ntok * group;
-  for (int r = warp; r < rows; r += 8) {
-    const int tok = r / group, hh = r - tok * group;
-    const int at = (tok / p.tpt) * BM + (tok % p.tpt) * group + hh;          // row of the two tiles
-    float top = -INFINITY;
-    for (int x = lane; x < n; x += 32) top = fmaxf(top, __ldcg(slot_at<D>(p, c0 + x, x == 0 ? 1 : 0) + 2 * BM * D + 2 * at));
+  for (int r0 = warp * R; r0 < rows; r0 += 8 * R) {
+    int at[R];                                  // rows of the two tiles
+    float top[R], sum[R], a[R][N];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    float sum = 0.f, a[N];
+    for (int y = 0; y < R; ++y) {
+      const int r = min(r0 + y, rows - 1), tok = r / group;
+      at[y] = tok >= p.tpt ? BM + (tok - p.tpt) * group + r % group : r;
+      top[y] = -INFINITY;
+      sum[y] = 0.f;
 #pragma unroll
-    for (int y = 0; y < N; ++y) a[y] = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < n; ++x) {
-      const float* src = slot_at<D>(p, c0 + x, x == 0 ? 1 : 0);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + 2 * BM * D) + at);
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
-      sum = fmaf(w, ml.y, sum);
-      if constexpr (N == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + at * D) + lane);
-        a[0] = fmaf(w, v.x, a[0]); a[1] = fmaf(w, v.y, a[1]); a[2] = fmaf(w, v.z, a[2]); a[3] = fmaf(w, v.w, a[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(src + at * D) + lane);
-        a[0] = fmaf(w, v.x, a[0]); a[1] = fmaf(w, v.y, a[1]);
+      for (int z = 0; z < N; ++z) a[y][z] = 0.f;
+    }
+#pragma unroll 1
+    for (int x0 = 0; x0 < n; x0 += ROWS ? 1 : B) {
+      float2 ml[B];
+      float v[B][N];
+#pragma unroll
+      for (int y = 0; y < B; ++y) {
+        const int x = ROWS ? x0 : min(x0 + y, n - 1);
+        const float* src = slot_at<D>(p, c0 + x, x == 0 ? 1 : 0);
+        const int row = at[ROWS ? y : 0];
+        ml[y] = __ldcg(reinterpret_cast<const float2*>(src + 2 * BM * D) + row);
+        if constexpr (N == 4) {
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(src + row * D) + lane);
+          v[y][0] = z.x; v[y][1] = z.y; v[y][2] = z.z; v[y][3] = z.w;
+        } else {
+          const float2 z = __ldcg(reinterpret_cast<const float2*>(src + row * D) + lane);
+          v[y][0] = z.x; v[y][1] = z.y;
+        }
+      }
+#pragma unroll
+      for (int y = 0; y < B; ++y) {
+        const int q = ROWS ? y : 0;
+        if (!ROWS && x0 + y >= n) break;
+        // a maximum of -inf stands for no score, or for NaN alone
+        const float t = fmaxf(top[q], ml[y].x);
+        const float f = top[q] == -INFINITY ? (sum[q] == 0.f ? 0.f : 1.f) : ex2_approx(top[q] - t);
+        const float w = ml[y].x == -INFINITY ? (ml[y].y == 0.f ? 0.f : 1.f) : ex2_approx(ml[y].x - t);
+        top[q] = t;
+        sum[q] = fmaf(w, ml[y].y, sum[q] * f);
+#pragma unroll
+        for (int z = 0; z < N; ++z) a[q][z] = fmaf(w, v[y][z], a[q][z] * f);
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + tok) * p.c.n_heads + k.h * group + hh;
-    uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * N);
-    o[0] = sum == 0.f ? 0u : pack_bf16x2(a[0] * inv, a[1] * inv);
-    if constexpr (N == 4) o[1] = sum == 0.f ? 0u : pack_bf16x2(a[2] * inv, a[3] * inv);
-    if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+#pragma unroll
+    for (int y = 0; y < R; ++y) {
+      const int r = r0 + y;
+      if (r >= rows) break;
+      const int tok = r / group, hh = r - tok * group;
+      const float inv = sum[y] == 0.f ? 0.f : 1.f / sum[y];
+      const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + tok) * p.c.n_heads + k.h * group + hh;
+      uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * N);
+      o[0] = pack_bf16x2(a[y][0] * inv, a[y][1] * inv);
+      if constexpr (N == 4) o[1] = pack_bf16x2(a[y][2] * inv, a[y][3] * inv);
+      if (lane == 0 && p.lse) p.lse[out] = sum[y] == 0.f ? -INFINITY : (top[y] + log2f(sum[y])) * kLn2;
+    }
   }
 }
 
@@ -531,8 +555,8 @@ template <int D, int TYPE>
 __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_constant__ PromptParams p) {
   using C = Cfg<D, TYPE>;
   grid_dep_launch_dependents();
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;                  // the kernel has no other shared memory: it begins on a multiple of 1024
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + C::kSmemQ;
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kSmemQ + C::kSmemKV);
@@ -561,6 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     mbar_init(&bars->part_last, 1);
     mbar_init(&bars->drain, 1);
     for (int s = 0; s < kFlagSlots; ++s) mbar_init(&bars->flags_full[s], kLoadWarps);
+    for (int s = 0; s < kTileSlots; ++s) {
+      mbar_init(&bars->tile_full[s], 1);
+      mbar_init(&bars->tile_empty[s], kLoadWarps);
+    }
     bars->abort = 0;
     mbar_fence_init();
   }
@@ -677,28 +705,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       }
       if (lane == 0) bars->start = s;
     }
+    fence_proxy_async_smem();        // the stages, which held the set-up, may be filled by tensor copies
     __syncthreads();
   }
 
   if (warp >= kLoadWarp0) {
-    regs_dec<kRegsLoad>();
+    regs_dec<C::kRegsLoad>();
     // ------------------------------------------------------------ keys and values
     const int w = warp - kLoadWarp0;
     const uint32_t skv = smem_u32(sKV);
     bool ok = true;
-    int stage = 0;
-    uint32_t round = 0;                 // times that the ring has gone around
+    int stage = 0, tslot = 0;
+    uint32_t round = 0, tround = 0;     // times that the stages' and the tiles' rings have gone around
     int slot = -1;                      // of the block's flags
+    auto take = [&](Share& r) -> bool { // the next tile's share
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_full[tslot], tround & 1u, wc, 11));
+      if (!ok) return false;
+      const Tile& d = bars->tile[tslot];
+      r.off[0] = d.off[2 * w];
+      r.off[1] = d.off[2 * w + 1];
+      r.lim = d.lim - w * 32;
+      r.watch = d.watch - w * 32;
+      r.head = d.head;
+      r.meta = d.meta;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->tile_empty[tslot]);
+      if (++tslot == kTileSlots) {
+        tslot = 0;
+        ++tround;
+      }
+      return r.meta >= 0;
+    };
     auto acquire = [&]() {
       if (ok && round > 0) ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_empty[stage], (round - 1) & 1u, wc, 1));
     };
-    auto note = [&](const TileRef& r, uint32_t odd) {      // where a block begins, what it holds, where it ends
+    auto note = [&](const Share& r, uint32_t odd) {      // where a block begins, what it holds, where it ends
       if (r.meta & 2) {
         slot = (slot + 1) % kFlagSlots;
         if (lane < kFlagTiles) bars->flags[slot][w][lane] = 0;
         __syncwarp();
       }
-      if (r.values() && r.tok0 + BN > r.watch) {
+      if (r.watched()) {
         odd = __reduce_or_sync(0xffffffffu, odd);
         if (odd && lane == 0) bars->flags[slot][w][min(r.meta >> 8, kFlagTiles - 1)] = odd;
       }
@@ -707,10 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         if (lane == 0) mbar_arrive(&bars->flags_full[slot]);
       }
     };
-    auto publish = [&](int s) {
+    auto publish = [&]() {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->kv_full[s]);
+      if (lane == 0) mbar_arrive(&bars->kv_full[stage]);
     };
     auto advance = [&]() {
       if (++stage == C::kStages) {
@@ -718,95 +765,130 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         ++round;
       }
     };
-    TileWalk<> walk(p, bars->start);
     if constexpr (TYPE == SR_PAGE_BF16) {
-      // copies of kAhead tiles in flight
-      constexpr int kAhead = 2;
-      TileRef r[kAhead + 1];
-      bool live[kAhead + 1];
-      int at[kAhead + 1];
+      const uint64_t policy = l2_policy_evict_last();
+      const bool wide = c.page_tokens % 32 == 0;       // boxes of 32 rows, else of 16
+      Share r;
+      while (take(r)) {
+        acquire();
+        if (!ok) break;
+        const uint32_t tile = skv + stage * C::kTileBytes;
+        if (r.off[0] >= 0 && r.off[1] >= 0 && r.lim >= 32 && !r.watched()) {
+          note(r, 0);
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->kv_full[stage], 32 * D * 2);
+            const CUtensorMap* map = r.values() ? &p.vmap : &p.kmap;
 #pragma unroll
-      for (int k = 0; k <= kAhead; ++k) live[k] = false;
-      TileRef nr;
-      Pages ng;
-      bool more = walk.next(nr, p);
-      if (more) fetch_pages(ng, nr, c, w, lane);
-      while (ok) {
-        bool any = false;
+            for (int a = 0; a < C::kAtoms; ++a) {
+              uint8_t* dst = sKV + stage * C::kTileBytes + a * C::kAtomBytes + w * 32 * 128;
+              tma_load_2d(dst, map, &bars->kv_full[stage], r.head * D + a * 64, static_cast<int>(r.off[0]), policy);
+              if (!wide) tma_load_2d(dst + 16 * 128, map, &bars->kv_full[stage], r.head * D + a * 64, static_cast<int>(r.off[1]), policy);
+            }
+          }
+          __syncwarp();
+        } else {
+          copy_share<D>(r, c, p.kv_heads, tile, w, lane);
+          note(r, r.watched() ? clean_share<D>(r, tile, w, lane) : 0);
+          publish();
+        }
+        advance();
+      }
+      // copies that nobody waited for (after an error) land before shared memory is given back
+      if (!ok || bars->abort)
+        for (int x = 0; x < C::kStages; ++x)
+          if (x < stage || round > 0) wait_drain(&bars->kv_full[x], (x < stage ? round : round - 1) & 1u, kTimeoutNs);
+    } else {
+      // the bytes of kAhead tiles are on their way in registers
+      constexpr int kAhead = 1;
+      Raw<D, TYPE> raw[kAhead + 1];
+      Share r[kAhead + 1];
+      bool have[kAhead + 1];
+      bool more = true;
+      auto fill = [&](int k) {
+        have[k] = more && (more = take(r[k]));
+        if (have[k]) load_raw<D, TYPE>(raw[k], r[k], c, p.kv_heads, lane);
+      };
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) fill(k);
+      bool busy = true;
+      while (ok && busy) {
+        busy = false;
 #pragma unroll
         for (int k = 0; k <= kAhead; ++k) {
-          const int old = (k + 1) % (kAhead + 1);
-          live[k] = more;
-          if (more) {
-            r[k] = nr;
-            Pages g = ng;
-            check_pages(g, nr, c, w, lane);
-            acquire();
-            if (!ok) break;
-            at[k] = stage;
-            copy_tile<D>(r[k], g, c, p.kv_heads, skv + stage * C::kTileBytes, w, lane);
-            advance();
-            more = walk.next(nr, p);
-            if (more) fetch_pages(ng, nr, c, w, lane);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-          if (live[old]) {
-            uint32_t odd = 0;
-            if (r[old].values() && r[old].tok0 + w * 32 + 32 > r[old].watch) odd = clean_tile<D>(r[old], skv + at[old] * C::kTileBytes, w, lane);
-            note(r[old], odd);
-            publish(at[old]);
-            live[old] = false;
-          }
-          any |= live[k];
-        }
-        if (!any && !more) {
-          bool left = false;
-#pragma unroll
-          for (int k = 0; k <= kAhead; ++k) left |= live[k];
-          if (!left) break;
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {
-      // registers: the next tile's bytes, the page entries of the one after it
-      Raw<D, TYPE> raw[2];
-      TileRef r[2], nr;
-      Pages ng;
-      bool have[2] = {false, false};
-      bool more = walk.next(nr, p);
-      if (more) fetch_pages(ng, nr, c, w, lane);
-      auto fill = [&](Raw<D, TYPE>& v, TileRef& t, bool& h) {
-        h = more;
-        if (!more) return;
-        t = nr;
-        Pages g = ng;
-        check_pages(g, t, c, w, lane);
-        load_raw<D, TYPE>(v, t, g, c, p.kv_heads, w, lane);
-        more = walk.next(nr, p);
-        if (more) fetch_pages(ng, nr, c, w, lane);
-      };
-      fill(raw[0], r[0], have[0]);
-      while (ok && (have[0] || have[1])) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          fill(raw[k ^ 1], r[k ^ 1], have[k ^ 1]);
+          fill((k + kAhead) % (kAhead + 1));
           if (!have[k]) continue;
           acquire();
           if (!ok) break;
-          note(r[k], store_raw<D, TYPE>(raw[k], r[k], skv + stage * C::kTileBytes, w, lane));
-          publish(stage);
+          const uint32_t tile = skv + stage * C::kTileBytes;
+          note(r[k], r[k].watched() ? store_raw<D, TYPE, true>(raw[k], r[k], tile, w, lane)
+                                    : store_raw<D, TYPE, false>(raw[k], r[k], tile, w, lane));
+          publish();
           advance();
-          have[k] = false;
+          busy = true;
         }
       }
     }
   } else if (warp >= kMmaWarp) {
-    regs_dec<kRegsOther>();
-    Walker walk(p, bars->start);
+    regs_dec<C::kRegsOther>();
     bool ok = true;
     uint32_t items = 0;
-    if (warp >= kQWarp0) {
+    if (warp == kPlanWarp) {
+      // ---------------------------------------------------------- the order of the tiles, and where their tokens lie
+      TileWalk walk(p, bars->start);
+      TileRef r, nr;
+      int32_t page = 0, npage = 0;
+      const int g = lane & 7;
+      auto entry = [&](const TileRef& t) {
+        const int32_t tok = t.tok0 + g * 16;
+        return tok < t.lim ? __ldg(c.table + static_cast<int64_t>(t.seq) * c.max_pages + page_of_group(tok >> 4, c.magic)) : 0;
+      };
+      bool more = walk.next(nr, p);
+      if (more) npage = entry(nr);
+      for (int n = 0; ok; ++n) {
+        const int slot = n % kTileSlots;
+        if (n >= kTileSlots) ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_empty[slot], (n / kTileSlots - 1) & 1u, wc, 12));
+        if (!ok) break;
+        Tile& d = bars->tile[slot];
+        if (!more) {
+          if (lane == 0) {
+            d.meta = -1;
+            mbar_arrive(&bars->tile_full[slot]);
+          }
+          break;
+        }
+        r = nr;
+        page = npage;
+        more = walk.next(nr, p);
+        if (more) npage = entry(nr);
+        const int32_t tok = r.tok0 + g * 16;
+        if (lane < 8) {
+          int64_t off = -1;
+          if (tok < r.lim) {
+            if (page >= 0 && page < c.n_pages) {
+              const int32_t slot_in = tok - page_of_group(tok >> 4, c.magic) * c.page_tokens;
+              if constexpr (TYPE == SR_PAGE_INT4) {
+                off = record_at(page, slot_in, r.head, p.kv_heads, c.page_tokens, D);
+              } else {
+                off = static_cast<int64_t>(page) * c.page_tokens + slot_in;
+                if constexpr (TYPE == SR_PAGE_E4M3) off = (off * p.kv_heads + r.head) * D;
+              }
+            } else {
+              atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
+            }
+          }
+          d.off[g] = off;
+          if (lane == 0) {
+            d.lim = min(r.lim - r.tok0, BN);
+            d.watch = r.watch == INT32_MAX ? BN : min(max(r.watch - r.tok0, 0), BN);
+            d.head = r.head;
+            d.meta = r.meta;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->tile_full[slot]);
+      }
+    } else if (warp >= kQWarp0) {
+      Walker walk(p, bars->start);
       // ---------------------------------------------------------- queries
       constexpr int kLanes = D / 8, kRows = 32 / kLanes;      // lanes of a row, rows per load
       const int w = warp - kQWarp0;
@@ -820,48 +902,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                                            wait_bounded(&bars->q_seen, (items - 1) & 1u, wc, 2));
           if (!ok) break;
         }
+        if (w == 0 && lane == 0) bars->rec[items & 1] = Record{k, walk.u};
         const int tiles = k.split ? 1 : 2;
         const int64_t row00 = static_cast<int64_t>(p.row0[k.i]) + k.tok0;
-        constexpr int kBatch = 4;
-        for (int x0 = w * kRows * kBatch; x0 < tiles * BM; x0 += kQWarps * kRows * kBatch) {
-          uint4 v[kBatch];
-#pragma unroll
-          for (int y = 0; y < kBatch; ++y) {
-            const int x = x0 + y * kRows + lane / kLanes, tr = x % BM;
-            const int tok = static_cast<int>(static_cast<uint32_t>(tr) * p.group_magic >> 16);
-            const int token = x / BM * p.tpt + tok, hh = tr - tok * group;
-            const bool there = x < tiles * BM && tok < p.tpt && token < k.ntok;
-            v[y] = there ? *reinterpret_cast<const uint4*>(p.q + ((row00 + token) * c.n_heads + k.h * group + hh) * D + lane % kLanes * 8)
-                         : make_uint4(0, 0, 0, 0);
+        // this warp's half of each tile's rows: all copies in flight together, then, for fp16, a row per lane
+        for (int t = 0; t < tiles; ++t) {
+          const uint32_t tile = sq + t * C::kTileBytes;
+          const __nv_bfloat16* src = p.q + (row00 * c.n_heads + k.h * group) * D + lane % kLanes * 8;
+#pragma unroll 4
+          for (int x = w * (BM / kQWarps) + lane / kLanes; x < (w + 1) * (BM / kQWarps); x += kRows) {
+            const int tok = static_cast<int>(static_cast<uint32_t>(x) * p.group_magic >> 16);
+            const int token = t * p.tpt + tok, hh = x - tok * group;
+            const bool there = tok < p.tpt && token < k.ntok;
+            copy16_or_zero(tile + piece_at<D>(x, lane % kLanes), src + (there ? (static_cast<int64_t>(token) * c.n_heads + hh) * D : 0), there);
           }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (C::kHalf) {
+          // fp16, scaled by a power of two to a largest element in [1, 2)
+          __syncwarp();
+          for (int x = lane; x < tiles * (BM / kQWarps); x += 32) {
+            const int t = x / (BM / kQWarps), tr = w * (BM / kQWarps) + x % (BM / kQWarps);
+            const uint32_t tile = sq + t * C::kTileBytes;
+            uint32_t top = 0;                         // of |x|, as bf16 bits: their order, NaN last
 #pragma unroll
-          for (int y = 0; y < kBatch; ++y) {
-            const int x = x0 + y * kRows + lane / kLanes, tr = x % BM, t = x / BM;
-            if constexpr (C::kHalf) {
-              // fp16, scaled by a power of two to a largest element in [1, 2)
-              auto pair = [](uint32_t z) { return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&z)); };
-              const float2 f[4] = {pair(v[y].x), pair(v[y].y), pair(v[y].z), pair(v[y].w)};
-              float top = 0.f;
-#pragma unroll
-              for (int z = 0; z < 4; ++z) top = fmaxf(top, fmaxf(fabsf(f[z].x), fabsf(f[z].y)));
-#pragma unroll
-              for (int s = 1; s < kLanes; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-              const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -120) : 0;
-              const float down = ldexpf(1.f, -e);
-              uint32_t h[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const __half2 hz = __floats2half2_rn(f[z].x * down, f[z].y * down);
-                h[z] = *reinterpret_cast<const uint32_t*>(&hz);
-              }
-              if constexpr (TYPE == SR_PAGE_INT4)
-                v[y] = make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632), __byte_perm(h[1], h[3], 0x5410),
-                                  __byte_perm(h[1], h[3], 0x7632));
-              else
-                v[y] = make_uint4(h[0], h[1], h[2], h[3]);
-              if (x < tiles * BM && lane % kLanes == 0) bars->qexp[t][tr] = static_cast<int8_t>(e);
+            for (int y = 0; y < D / 8; ++y) {
+              const uint4 v = load16(tile + piece_at<D>(tr, y));
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
             }
-            if (x < tiles * BM) store16(sq + t * C::kTileBytes + piece_at<D>(tr, lane % kLanes), v[y]);
+            const float most = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+            const int e = most > 0.f && most < INFINITY ? max(ilogbf(most), -120) : 0;
+            const float down = ldexpf(1.f, -e);
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y) {
+              const uint32_t at = tile + piece_at<D>(tr, y);
+              const uint4 v = load16(at);
+              auto half = [&](uint32_t z) {
+                const __half2 h = __floats2half2_rn(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
+                return *reinterpret_cast<const uint32_t*>(&h);
+              };
+              const uint32_t h[4] = {half(v.x), half(v.y), half(v.z), half(v.w)};
+              if constexpr (TYPE == SR_PAGE_INT4)
+                store16(at, make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
+                                       __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632)));
+              else
+                store16(at, make_uint4(h[0], h[1], h[2], h[3]));
+            }
+            bars->qexp[t][tr] = static_cast<int8_t>(e);
           }
         }
         fence_proxy_async_smem();
@@ -869,8 +956,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         if (lane == 0) mbar_arrive(&bars->q_full);
         ++items;
       }
+      // the end: a record of no block, once the last one but one has been read
+      if (ok && items > 0) ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_seen, (items - 1) & 1u, wc, 2));
+      if (ok && w == 0 && lane == 0) bars->rec[items & 1].k.i = -1;
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bars->q_full);
     } else {
       // ---------------------------------------------------------- MMA issuer (the warp in step, one lane issues)
+      Walker walk(p, bars->start);
       const uint32_t leader = elect_one();
       const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
       bool issued = false;
@@ -912,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       };
       while (walk.next()) {
         const Block& k = walk.k;
-        ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 2));
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 3));
         if (!ok) break;
         const int n = k.s1 - k.s0;
         if (!k.split) {
@@ -979,11 +1072,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     const int tr = static_cast<int>(static_cast<uint32_t>(row) * p.group_magic >> 16), hh = row - tr * group;
     bool ok = true;
     uint32_t items = 0, sb = 0, od[2] = {0, 0}, nx = 0, cuts = 0;
-    Walker walk(p, bars->start);
-    while (ok && walk.next()) {
-      const Block& k = walk.k;
+    while (ok) {
       ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 5));
       if (!ok) break;
+      const Block& k = bars->rec[items & 1].k;       // there until every warp has begun the next block
+      if (k.i < 0) break;
       const int kv = static_cast<int>(static_cast<uint32_t>(k.h) * p.head_magic >> 22);
       float sl2 = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
       if constexpr (C::kHalf) sl2 *= ldexpf(1.f, bars->qexp[k.split ? 0 : t][row]);
@@ -994,19 +1087,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       const bool live = tr < p.tpt && token < k.ntok;
       const int32_t lim = !live ? k.lim : p.causal ? max(k.base + k.tok0 + token + 1, 0) : k.lim;
       const int32_t* table = c.table + static_cast<int64_t>(p.id[k.i]) * c.max_pages;
-      const int cnt = k.count(t);
+      const int cnt = k.count(t), step = k.split ? 2 * BN : BN;
+      int32_t ks = k.tile(t, 0) * BN;                 // first token of the key tile
+      const int32_t seen = k.lim;
       // the pages of a key tile's groups, by lanes 0-7: those that are none of the pool are not seen
-      auto fetch = [&](int j) {
-        const int32_t tok = k.tile(t, j) * BN + (lane & 7) * 16;
-        return j < cnt && tok < k.lim ? __ldg(table + page_of_group(tok >> 4, c.magic)) : 0;
+      auto fetch = [&](int32_t tok, bool more) {
+        tok += (lane & 7) * 16;
+        return more && tok < seen ? __ldg(table + page_of_group(tok >> 4, c.magic)) : 0;
       };
-      int32_t page = fetch(0);
+      int32_t page = fetch(ks, cnt > 0);
       float m = -INFINITY, l = 0.f;
       const float2 sl2x2 = make_float2(sl2, sl2);
       for (int j = 0; j < cnt; ++j) {
-        const int valid = lim - k.tile(t, j) * BN;
+        const int valid = lim - ks;
         const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && page < c.n_pages);
-        page = fetch(j + 1);
+        ks += step;
+        page = fetch(ks, j + 1 < cnt);
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->s_full[t], (sb + static_cast<uint32_t>(j)) & 1u, wc, 5));
         if (!ok) break;
         tc_fence_after();
@@ -1066,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           if (x == 1) {
             if (rescale && j > 0) {
               // O was last written by the last step's product, which the commit behind S covers
-#pragma unroll
+#pragma unroll 1
               for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tmem_ld32(t_o + q * 32, o);
@@ -1100,7 +1196,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       const int slot = items % kFlagSlots;
       ok = __all_sync(0xffffffffu, wait_bounded(&bars->flags_full[slot], (items / kFlagSlots) & 1u, wc, 7));
       if (!ok) break;
-      ++items;
       if (k.split && t == 1) {
         // hand (m, l) to group 0 and wait until it has read them and O_1
         bars->xm[row] = cnt > 0 ? m : -INFINITY;
@@ -1133,8 +1228,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + token) * c.n_heads + k.h * group + hh;
         // a whole block with odd values goes through the slot too (free: only the last block can be cut behind it), since
         // add_odd reads the query row, whose place the output may take
-        float* part = slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0);
         const int prow = (k.split ? 0 : t) * BM + row;
+        float* part = slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0) + prow * D;
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
           uint32_t o[32];
@@ -1151,50 +1246,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             for (int i = 0; i < 32; ++i)
               of[i] = (f0 == 0.f ? 0.f : of[i] * f0) + (f1 == 0.f ? 0.f : __uint_as_float(o1[i]) * f1);
           }
-          float y[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = of[column_of<TYPE>(i)];
-          if (odd && live) {
-#pragma unroll 1
-            for (int z = 0; z < kLoadWarps * kFlagTiles; ++z) {
-              uint32_t bits = bars->flags[slot][z / kFlagTiles][z % kFlagTiles];
-              const int32_t tok = (k.lim_min / BN + z % kFlagTiles) * BN + z / kFlagTiles * 32;
-              while (bits) {
-                const int32_t at = tok + __ffs(bits) - 1;
-                bits &= bits - 1;
-                if (at < lim) {
-                  float sc = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
-                  add_odd<D, TYPE>(p, y, x * 32, p.id[k.i], at, kv, p.q + out * D, sc, m);
-                }
-              }
-            }
-          }
+          auto y = [&](int i) { return of[column_of<TYPE>(i)] * to; };
           if (live) {
             if (whole && !odd) {
               uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x * 32);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 z;
-                z.x = pack_bf16x2(y[8 * i] * to, y[8 * i + 1] * to);
-                z.y = pack_bf16x2(y[8 * i + 2] * to, y[8 * i + 3] * to);
-                z.z = pack_bf16x2(y[8 * i + 4] * to, y[8 * i + 5] * to);
-                z.w = pack_bf16x2(y[8 * i + 6] * to, y[8 * i + 7] * to);
-                dst[i] = z;
-              }
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(y(8 * i), y(8 * i + 1)), pack_bf16x2(y(8 * i + 2), y(8 * i + 3)),
+                                    pack_bf16x2(y(8 * i + 4), y(8 * i + 5)), pack_bf16x2(y(8 * i + 6), y(8 * i + 7)));
             } else {
-              float4* dst = reinterpret_cast<float4*>(part + prow * D + x * 32);
+              float4* dst = reinterpret_cast<float4*>(part + x * 32);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i] * to, y[4 * i + 1] * to, y[4 * i + 2] * to, y[4 * i + 3] * to);
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y(4 * i), y(4 * i + 1), y(4 * i + 2), y(4 * i + 3));
             }
           }
         }
-        if (whole && odd && live)
+        if (odd && live) {
+          const float raw_scale = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
 #pragma unroll 1
-          for (int i = 0; i < D; i += 2)
-            *reinterpret_cast<uint32_t*>(p.o + out * D + i) = pack_bf16x2(part[prow * D + i], part[prow * D + i + 1]);
+          for (int z = 0; z < kLoadWarps * kFlagTiles; ++z) {
+            uint32_t bits = bars->flags[slot][z / kFlagTiles][z % kFlagTiles];
+            const int32_t tok = (k.lim_min / BN + z % kFlagTiles) * BN + z / kFlagTiles * 32;
+#pragma unroll 1
+            for (; bits; bits &= bits - 1) {
+              const int32_t at = tok + __ffs(bits) - 1;
+              if (at < lim) add_odd<D, TYPE>(p, part, p.id[k.i], at, kv, p.q + out * D, raw_scale, m, to);
+            }
+          }
+          if (whole)
+#pragma unroll 1
+            for (int i = 0; i < D; i += 2)
+              *reinterpret_cast<uint32_t*>(p.o + out * D + i) = pack_bf16x2(part[i], part[i + 1]);
+        }
         if (live) {
           if (!whole)
-            *reinterpret_cast<float2*>(part + 2 * BM * D + 2 * prow) = make_float2(m, l);
+            *reinterpret_cast<float2*>(slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0) + 2 * BM * D + 2 * prow) = make_float2(m, l);
           else if (p.lse)
             p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
@@ -1207,7 +1293,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       if (!whole) {
         // the last of the block's CTAs to arrive joins their parts
         const Start& s = bars->start;
-        const int c0 = owner_of(walk.u, s.share, s.rest), c1 = owner_of(walk.u + k.steps - 1, s.share, s.rest);
+        const int64_t u = bars->rec[items & 1].u;
+        const int c0 = owner_of(u, s.share, s.rest), c1 = owner_of(u + k.steps - 1, s.share, s.rest);
         __threadfence();
         mbar_arrive(&bars->part_done);
         if (threadIdx.x == 0) {
@@ -1222,8 +1309,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         }
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->part_last, cuts & 1u, wc, 10));
         ++cuts;
-        if (ok && bars->last) join_block<D>(p, k, c0, c1 - c0 + 1, warp, lane);
+        if (ok && bars->last) {
+          if (k.ntok * group > 32)
+            join_block<D, true>(p, k, c0, c1 - c0 + 1, warp, lane);
+          else
+            join_block<D, false>(p, k, c0, c1 - c0 + 1, warp, lane);
+        }
       }
+      ++items;
     }
   }
 

@@ -97,30 +97,36 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// 2D map over a token-major bf16 tensor [rows][row_elems], box {64, 128},
+}  // namespace
+
+namespace sr {
+// 2D map over a token-major bf16 tensor [rows][row_elems], box {64, box_rows},
 // 128-byte swizzle, zero fill outside [0, rows).
-bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t row_elems) {
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t row_elems, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_elems), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_elems * 2)};
-  cuuint32_t box[2] = {kBoxCols, kBoxRows};
+  cuuint32_t box[2] = {kBoxCols, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+}  // namespace sr
+
+namespace {
 
 // encode_rows through the session's map cache (s may be NULL: no cache).
 bool encode_cached(sr_session* s, CUtensorMap* map, const void* base, int64_t rows, int64_t row_elems) {
-  if (s == nullptr) return encode_rows(map, base, rows, row_elems);
+  if (s == nullptr) return sr::encode_rows(map, base, rows, row_elems, kBoxRows);
   for (const auto& e : s->maps)
     if (e.base == base && e.rows == rows && base != nullptr) {
       *map = e.map;
       return true;
     }
-  if (!encode_rows(map, base, rows, row_elems)) return false;
+  if (!sr::encode_rows(map, base, rows, row_elems, kBoxRows)) return false;
   auto& e = s->maps[s->map_next];
   s->map_next = (s->map_next + 1) % 16;
   e.base = base;

@@ -44,6 +44,9 @@ inline cudaError_t launch_plain(void (*kernel)(KArgs...), unsigned grid, unsigne
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// 2D tensor map over [rows][row_elems] bf16, box {64, box_rows}, 128-byte swizzle, zeros outside (sr_api.cu).
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t row_elems, int box_rows);
+
 // ------------------------------------------------------------ attention
 // One session's view for one launch: up to four key/value segments -- the sink
 // bank of the step, the visible ring frames as one or two contiguous row

@@ -2,6 +2,7 @@
 // by its host API (paged_api.cu) and kernels. Internal to libsr.so.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -82,6 +83,8 @@ struct PagedBatch {
   int32_t id[kMaxPagedSeqs];
 };
 
+constexpr int paged_box_rows(int page_tokens) { return page_tokens % 32 == 0 ? 32 : 16; }
+
 struct AppendParams {
   PagedView c;
   const __nv_bfloat16* k;
@@ -136,7 +139,8 @@ struct ReadParams {
   int32_t cta0[kMaxPagedSeqs + 1];
 };
 
-struct PromptParams {
+struct alignas(64) PromptParams {
+  CUtensorMap kmap, vmap;  // bf16 pages: [n_pages * page_tokens][n_kv_heads * head_dim], boxes of 64 values of paged_box_rows() tokens
   PagedView c;             // n_kv, group: items of at most SR_MAX_PAGED_GROUP query heads, as in PagedAttnParams
   const __nv_bfloat16* q;
   __nv_bfloat16* o;
