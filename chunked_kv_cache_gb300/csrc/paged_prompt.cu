@@ -40,23 +40,24 @@ constexpr uint32_t kRegsSoftmax = 176;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kItemCost = 1;           // steps that changing blocks costs
-// Flags of a block are kept for kFlagSlots blocks: a loading warp that begins the eighth block behind one has had a stage
-// back (of 8 at most, two tiles a block) that the third block behind it used, whose weights both softmax groups
-// made after they had read the first one's flags.
+// A block's flags are kept for kFlagSlots blocks: who writes those of the eighth block behind one has had a stage back (of
+// 8 at most, two tiles a block) that the second block behind it used, whose weights softmax group 0 made after both
+// groups had read the first one's flags.
 constexpr int kFlagSlots = 8, kFlagTiles = 3;
-
 constexpr int kBarBytes = 3072;
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool kHalf = TYPE != SR_PAGE_BF16;       // products of fp16, else of bf16
-  // 8-bit pages come through more registers
-  static constexpr uint32_t kRegsOther = TYPE == SR_PAGE_E4M3 ? 48 : 56, kRegsLoad = 160 - kRegsOther;
+  static constexpr uint32_t kRegsOther = 72, kRegsLoad = 160 - kRegsOther;
   static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsLoad) <= kThreads * kLaunchRegs,
                 "register split exceeds what the block is launched with");
   static constexpr int kAtoms = D / 64;
   static constexpr int kAtomBytes = BM * 128;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
   static constexpr int kStages = D == 128 ? 5 : 8;
+  // loading warps that share a tile; the others are at the next tiles meanwhile
+  static constexpr int kPerTile = TYPE == SR_PAGE_BF16 ? 1 : 2;
+  static constexpr int kTeams = kLoadWarps / kPerTile, kSubs = 4 / kPerTile;     // a warp's shares of a tile, 32 tokens each
   static constexpr int kSmemQ = 2 * kTileBytes;
   static constexpr int kSmemKV = kStages * kTileBytes;
   static constexpr int kSmemBytes = kSmemQ + kSmemKV + kBarBytes;
@@ -96,7 +97,7 @@ struct Tile {
   int32_t lim;         // tokens from here on (within the tile) are zeros
   int32_t watch;       // tokens from here on are seen by some rows only: values that are no finite numbers leave the tile
   int32_t head;        // key/value head
-  int32_t meta;        // bit 0: values; bit 1: a block's first tile; bit 2: its last; bits 8..: flag word. -1: no more tiles
+  int32_t meta;        // bit 0: values; bits 1-3: slot of the block's flags; bits 8..: flag word. -1: no more tiles
 };
 constexpr int kTileSlots = 8;
 
@@ -110,17 +111,17 @@ struct Bars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t x_full, x_empty, part_done, part_last, drain;
-  uint64_t flags_full[kFlagSlots];
   uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
   Tile tile[kTileSlots];
   Record rec[2];
   uint32_t tmem_base;
+  int bad;               // an entry that is no page of the pool has been met
   int abort;
   int last;
   Start start;
-  // of a block: new tokens with values that are no finite numbers, by loading warp and key tile from the first that some
-  // row does not see whole
-  uint32_t flags[kFlagSlots][kLoadWarps][kFlagTiles];
+  // of a block: new tokens with values that are no finite numbers, by 32 tokens of a key tile, the tiles counted from the
+  // first that some row does not see whole
+  uint32_t flags[kFlagSlots][4][kFlagTiles];
   int8_t qexp[2][BM];
   float xm[BM], xl[BM];
 };
@@ -162,7 +163,8 @@ __device__ __forceinline__ int64_t units_of(const Block& k) { return k.steps > 0
 struct Walker {
   const PromptParams& p;
   Block k;
-  int64_t left, u;               // units left, unit of the block's first step
+  int32_t left;                  // units left (launch_paged_prompt takes no call whose stretches hold 2^31)
+  int64_t u;                     // unit of the block's first step
   int32_t len;
   int nb;
   bool first;
@@ -170,7 +172,7 @@ struct Walker {
     k.i = s.i;
     k.h = s.h;
     k.b = s.b;
-    left = s.left;
+    left = static_cast<int32_t>(s.left);
     u = s.u;
     first = true;
     if (left > 0) {
@@ -204,7 +206,7 @@ struct Walker {
     }
     if (left <= 0) return false;
     first = false;
-    k.s1 = static_cast<int32_t>(min(static_cast<int64_t>(k.steps), k.s0 + left));
+    k.s1 = min(k.steps, k.s0 + left);
     left -= k.s1 - k.s0;
     return true;
   }
@@ -226,15 +228,17 @@ struct TileWalk {
   Walker w;
   int j, t, part;      // step of the block (0 .. n), softmax group, 0 values 1 keys
   int n;
-  bool open, fresh;
+  bool open;
+  int block;           // blocks so far
   __device__ __forceinline__ TileWalk(const PromptParams& p, const Start& s) : w(p, s) {
+    block = -1;
     open = w.next();
     begin();
   }
   __device__ __forceinline__ void begin() {
     j = t = part = 0;
     n = open ? w.k.s1 - w.k.s0 : 0;
-    fresh = true;
+    ++block;
   }
   __device__ __forceinline__ bool next(TileRef& r, const PromptParams& p) {
     while (open) {
@@ -254,14 +258,12 @@ struct TileWalk {
         if (!there) continue;
         const int tile = w.k.tile(tt, jj);
         const int flag = max(tile - w.k.lim_min / BN, 0);
-        const bool last = pp == 0 && jj == n - 1 && (!w.k.split || tt == 1 || w.k.count(1) < n);
         r.tok0 = tile * BN;
         r.lim = w.k.lim;
         r.watch = p.causal ? w.k.lim_min : INT32_MAX;
         r.seq = p.id[w.k.i];
         r.head = static_cast<int>(static_cast<uint32_t>(w.k.h) * p.head_magic >> 22);
-        r.meta = (pp == 0 ? 1 : 0) | (fresh ? 2 : 0) | (last ? 4 : 0) | flag << 8;
-        fresh = false;
+        r.meta = (pp == 0 ? 1 : 0) | (block % kFlagSlots) << 1 | flag << 8;
         return true;
       }
       open = w.next();
@@ -302,98 +304,75 @@ __device__ __forceinline__ bool finite_only(uint4& x) {
   return any;
 }
 
-// A loading warp's share of a tile: 32 tokens, two groups of 16.
+// A share of a tile: 32 tokens, two groups of 16.
 struct Share {
   int64_t off[2];
-  int32_t lim, watch, head, meta;         // lim, watch: of the warp's 32
+  int32_t lim, watch, head, meta;         // lim, watch: of these 32
   __device__ __forceinline__ bool values() const { return meta & 1; }
   __device__ __forceinline__ bool watched() const { return values() && watch < 32; }
+  __device__ __forceinline__ bool whole() const { return (off[0] | off[1]) >= 0 && lim >= 32; }
 };
 
+// 16-byte pieces of a share that a lane holds. e4m3: four lanes take 64 bytes of a token's row, eight tokens at once;
+// 4 bits: lanes 0-15 a chunk of a group's 16 tokens, lanes 16-31 the next one.
 template <int D, int TYPE>
 struct Raw {
   static constexpr int kVec = TYPE == SR_PAGE_E4M3 ? D / 16 : TYPE == SR_PAGE_INT4 ? D / 32 : 1;
   uint4 x[kVec];
   uint32_t s[TYPE == SR_PAGE_INT4 ? kVec : 1];
 };
-
-// e4m3: lane l of 8 (or 4) takes 16 bytes of a token's row; 4 bits: lanes 0-15 a chunk of the group's 16 tokens, lanes
-// 16-31 the next one. Tokens at or past the limit are zeros (their scales are, for 4 bits).
+// Where a lane's pieces lie. Tokens that are not there are zeros (their scales are, for 4 bits).
 template <int D, int TYPE>
-__device__ __forceinline__ void load_raw(Raw<D, TYPE>& v, const Share& r, const PagedView& c, int kv_heads, int lane) {
-  const uint8_t* pages = static_cast<const uint8_t*>(r.values() ? c.v_pages : c.k_pages);
-  if constexpr (TYPE == SR_PAGE_INT4) {
-    constexpr int kPer = D / 64;              // loads per group
+struct Source {
+  const uint8_t* at[2];        // this lane's place in each group
+  int32_t live[2];             // tokens of the group that are there
+  __device__ __forceinline__ void set(const Share& r, const PagedView& c, int kv_heads, int lane) {
+    const uint8_t* pages = static_cast<const uint8_t*>(r.values() ? c.v_pages : c.k_pages);
+    const int64_t mine = TYPE == SR_PAGE_INT4 ? lane * 16 : static_cast<int64_t>(lane / 4) * kv_heads * D + lane % 4 * 16;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const uint8_t* rec = pages + max(r.off[x], static_cast<int64_t>(0));
-      const bool there = r.off[x] >= 0 && x * 16 + (lane & 15) < r.lim;
-#pragma unroll
-      for (int y = 0; y < kPer; ++y) {
-        const int ch = 2 * y + lane / 16;
-        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(rec + ch * 256 + (lane & 15) * 16)) : make_uint4(0, 0, 0, 0);
-        v.s[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (lane & 15) * (D / 16) + 2 * ch)) : 0;
-      }
-    }
-  } else if constexpr (TYPE == SR_PAGE_E4M3) {
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = 16 / kRows;   // lanes of a row, rows per load, loads per group
-    const int64_t pitch = static_cast<int64_t>(kv_heads) * D;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint8_t* row = pages + max(r.off[x], static_cast<int64_t>(0)) + lane / kLanes * pitch + lane % kLanes * 16;
-#pragma unroll
-      for (int y = 0; y < kPer; ++y) {
-        const bool there = r.off[x] >= 0 && x * 16 + y * kRows + lane / kLanes < r.lim;
-        v.x[x * kPer + y] = there ? __ldg(reinterpret_cast<const uint4*>(row + y * kRows * pitch)) : make_uint4(0, 0, 0, 0);
-      }
+      at[x] = pages + r.off[x] + mine;
+      live[x] = r.off[x] < 0 ? 0 : r.lim - x * 16;
     }
   }
-}
-
-// Decodes and stores; returns a bit per token of the warp's 32 whose values were no finite numbers (and are zeros now).
-template <int D, int TYPE, bool WATCH>
-__device__ __forceinline__ uint32_t store_raw(const Raw<D, TYPE>& v, const Share& r, uint32_t tile, int w, int lane) {
-  uint32_t odd = 0;
-  auto put = [&](int row, int piece, uint4 y) {          // row of the warp's 32
-    if constexpr (WATCH)
-      if (row >= r.watch && finite_only<true>(y)) odd |= 1u << row;
-    store16(tile + piece_at<D>(w * 32 + row, piece), y);
-  };
+  __device__ __forceinline__ void load(Raw<D, TYPE>& v, int i, int kv_heads, int lane) const {
+    constexpr int kPer = Raw<D, TYPE>::kVec / 2;
+    const int x = i / kPer, y = i % kPer;
+    if constexpr (TYPE == SR_PAGE_INT4) {
+      const bool there = (lane & 15) < live[x];
+      v.x[i] = there ? __ldg(reinterpret_cast<const uint4*>(at[x] + y * 512)) : make_uint4(0, 0, 0, 0);
+      v.s[i] = there ? __ldg(reinterpret_cast<const uint16_t*>(at[x] + 8 * D - lane * 16 + (lane & 15) * (D / 16) + 2 * (lane / 16) + 4 * y)) : 0;
+    } else if constexpr (TYPE == SR_PAGE_E4M3) {
+      constexpr int kAcross = D / 64;         // pieces of a token
+      const bool there = y / kAcross * 8 + lane / 4 < live[x];
+      v.x[i] = there ? __ldg(reinterpret_cast<const uint4*>(at[x] + y / kAcross * 8 * static_cast<int64_t>(kv_heads) * D + y % kAcross * 64))
+                     : make_uint4(0, 0, 0, 0);
+    }
+  }
+};
+// Decodes piece i into rows chunk * 32 .. of a tile.
+template <int D, int TYPE>
+__device__ __forceinline__ void store_raw(const Raw<D, TYPE>& v, int i, uint32_t tile, int chunk, int lane) {
+  constexpr int kPer = Raw<D, TYPE>::kVec / 2;
+  const int x = i / kPer, y = i % kPer;
+  const uint4 z = v.x[i];
   if constexpr (TYPE == SR_PAGE_INT4) {
-    constexpr int kPer = D / 64;
+    const uint32_t b = v.s[i], word[4] = {z.x, z.y, z.z, z.w};
+    const ScalePair s0 = scale_pair(__byte_perm(b, 0, 0x4040) << 7), s1 = scale_pair(__byte_perm(b, 0, 0x4141) << 7);
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < kPer; ++y) {
-        const int ch = 2 * y + lane / 16;
-        const uint32_t b = v.s[x * kPer + y];
-        const uint4 z = v.x[x * kPer + y];
-        const uint32_t word[4] = {z.x, z.y, z.z, z.w};
-        const ScalePair s0 = scale_pair(__byte_perm(b, 0, 0x4040) << 7), s1 = scale_pair(__byte_perm(b, 0, 0x4141) << 7);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t e[4];
-          decode_word(e, word[q], q < 2 ? s0 : s1);
-          put(x * 16 + (lane & 15), ch * 4 + q, make_uint4(e[0], e[1], e[2], e[3]));
-        }
-      }
+    for (int q = 0; q < 4; ++q) {
+      uint32_t e[4];
+      decode_word(e, word[q], q < 2 ? s0 : s1);
+      store16(tile + piece_at<D>(chunk * 32 + x * 16 + (lane & 15), (2 * y + lane / 16) * 4 + q), make_uint4(e[0], e[1], e[2], e[3]));
+    }
   } else if constexpr (TYPE == SR_PAGE_E4M3) {
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes, kPer = 16 / kRows;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int y = 0; y < kPer; ++y) {
-        const uint4 z = v.x[x * kPer + y];
-        const uint4 a = make_uint4(half2_of_e4m3(z.x), half2_of_e4m3(z.x >> 16), half2_of_e4m3(z.y), half2_of_e4m3(z.y >> 16));
-        const uint4 b = make_uint4(half2_of_e4m3(z.z), half2_of_e4m3(z.z >> 16), half2_of_e4m3(z.w), half2_of_e4m3(z.w >> 16));
-        const int row = x * 16 + y * kRows + lane / kLanes, l = lane % kLanes;
-        // lanes of the two atoms begin with different pieces: none meets another's banks
-        const bool swap = l >= 4;
-        put(row, 2 * l + (swap ? 1 : 0), swap ? b : a);
-        put(row, 2 * l + (swap ? 0 : 1), swap ? a : b);
-      }
+    constexpr int kAcross = D / 64;
+    const int row = chunk * 32 + x * 16 + y / kAcross * 8 + lane / 4, piece = y % kAcross * 8 + lane % 4 * 2;
+    store16(tile + piece_at<D>(row, piece),
+            make_uint4(half2_of_e4m3(z.x), half2_of_e4m3(z.x >> 16), half2_of_e4m3(z.y), half2_of_e4m3(z.y >> 16)));
+    store16(tile + piece_at<D>(row, piece + 1),
+            make_uint4(half2_of_e4m3(z.z), half2_of_e4m3(z.z >> 16), half2_of_e4m3(z.w), half2_of_e4m3(z.w >> 16)));
   }
-  return odd;
 }
 
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
@@ -407,7 +386,7 @@ __device__ __forceinline__ void copy_share(const Share& r, const PagedView& c, i
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int64_t row0 = max(r.off[x], static_cast<int64_t>(0));
-#pragma unroll 4
+#pragma unroll 2
     for (int y = 0; y < 16 / kRows; ++y) {
       const int slot = y * kRows + lane / kLanes;
       const bool there = r.off[x] >= 0 && x * 16 + slot < r.lim;
@@ -417,17 +396,18 @@ __device__ __forceinline__ void copy_share(const Share& r, const PagedView& c, i
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
-// The same lanes look at what they copied, where some rows do not see all of it.
-template <int D>
-__device__ __forceinline__ uint32_t clean_share(const Share& r, uint32_t tile, int w, int lane) {
+// What some rows do not see has to be finite; returns a bit per token of the 32 whose values were not (and are zeros now).
+template <int D, bool HALF>
+__device__ __forceinline__ uint32_t clean_share(const Share& r, uint32_t tile, int chunk, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   uint32_t odd = 0;
+  __syncwarp();
 #pragma unroll 1
   for (int row = lane / kLanes; row < 32; row += kRows)
     if (row >= r.watch) {
-      const uint32_t at = tile + piece_at<D>(w * 32 + row, lane % kLanes);
+      const uint32_t at = tile + piece_at<D>(chunk * 32 + row, lane % kLanes);
       uint4 y = load16(at);
-      if (finite_only<false>(y)) {
+      if (finite_only<HALF>(y)) {
         odd |= 1u << row;
         store16(at, y);
       }
@@ -570,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->q_seen, 8);
     for (int s = 0; s < 8; ++s) {
-      mbar_init(&bars->kv_full[s], kLoadWarps);
+      mbar_init(&bars->kv_full[s], C::kPerTile);
       mbar_init(&bars->kv_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -584,12 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     mbar_init(&bars->part_done, 2 * BM);
     mbar_init(&bars->part_last, 1);
     mbar_init(&bars->drain, 1);
-    for (int s = 0; s < kFlagSlots; ++s) mbar_init(&bars->flags_full[s], kLoadWarps);
     for (int s = 0; s < kTileSlots; ++s) {
       mbar_init(&bars->tile_full[s], 1);
-      mbar_init(&bars->tile_empty[s], kLoadWarps);
+      mbar_init(&bars->tile_empty[s], C::kPerTile);
     }
     bars->abort = 0;
+    bars->bad = 0;
     mbar_fence_init();
   }
   if (warp == 0) {
@@ -712,119 +692,138 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
   if (warp >= kLoadWarp0) {
     regs_dec<C::kRegsLoad>();
     // ------------------------------------------------------------ keys and values
-    const int w = warp - kLoadWarp0;
+    const int team = (warp - kLoadWarp0) / C::kPerTile, member = (warp - kLoadWarp0) % C::kPerTile;
     const uint32_t skv = smem_u32(sKV);
     bool ok = true;
-    int stage = 0, tslot = 0;
-    uint32_t round = 0, tround = 0;     // times that the stages' and the tiles' rings have gone around
-    int slot = -1;                      // of the block's flags
-    auto take = [&](Share& r) -> bool { // the next tile's share
-      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_full[tslot], tround & 1u, wc, 11));
-      if (!ok) return false;
-      const Tile& d = bars->tile[tslot];
-      r.off[0] = d.off[2 * w];
-      r.off[1] = d.off[2 * w + 1];
-      r.lim = d.lim - w * 32;
-      r.watch = d.watch - w * 32;
+    int n = team;                        // the tile that this team loads next
+    auto acquire = [&](int tile) {       // its stage
+      if (ok && tile >= C::kStages)
+        ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_empty[tile % C::kStages], (tile / C::kStages - 1) & 1u, wc, 1));
+    };
+    auto ready = [&](int tile) -> const Tile& {
+      if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_full[tile % kTileSlots], (tile / kTileSlots) & 1u, wc, 11));
+      return bars->tile[tile % kTileSlots];
+    };
+    auto release = [&](int tile) {       // its description has been read
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->tile_empty[tile % kTileSlots]);
+    };
+    auto share = [&](Share& r, const Tile& d, int chunk) {
+      r.off[0] = d.off[2 * chunk];
+      r.off[1] = d.off[2 * chunk + 1];
+      r.lim = d.lim - chunk * 32;
+      r.watch = d.watch - chunk * 32;
       r.head = d.head;
       r.meta = d.meta;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->tile_empty[tslot]);
-      if (++tslot == kTileSlots) {
-        tslot = 0;
-        ++tround;
-      }
-      return r.meta >= 0;
     };
-    auto acquire = [&]() {
-      if (ok && round > 0) ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_empty[stage], (round - 1) & 1u, wc, 1));
+    auto note = [&](const Share& r, int chunk, uint32_t odd) {
+      if (!r.values() || r.watch >= 32 + (3 - chunk) * 32) return;        // of tiles that some rows do not see whole
+      odd = __reduce_or_sync(0xffffffffu, odd);
+      if (lane == 0) bars->flags[r.meta >> 1 & 7][chunk][min(r.meta >> 8, kFlagTiles - 1)] = odd;
     };
-    auto note = [&](const Share& r, uint32_t odd) {      // where a block begins, what it holds, where it ends
-      if (r.meta & 2) {
-        slot = (slot + 1) % kFlagSlots;
-        if (lane < kFlagTiles) bars->flags[slot][w][lane] = 0;
-        __syncwarp();
-      }
-      if (r.watched()) {
-        odd = __reduce_or_sync(0xffffffffu, odd);
-        if (odd && lane == 0) bars->flags[slot][w][min(r.meta >> 8, kFlagTiles - 1)] = odd;
-      }
-      if (r.meta & 4) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->flags_full[slot]);
-      }
-    };
-    auto publish = [&]() {
+    auto publish = [&](int tile) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->kv_full[stage]);
+      if (lane == 0) mbar_arrive(&bars->kv_full[tile % C::kStages]);
     };
-    auto advance = [&]() {
-      if (++stage == C::kStages) {
-        stage = 0;
-        ++round;
-      }
-    };
+    // (few instructions in each role's loop: they share the instruction cache with the softmax groups, and a kernel whose
+    // loops were unrolled further took up to a quarter longer)
     if constexpr (TYPE == SR_PAGE_BF16) {
       const uint64_t policy = l2_policy_evict_last();
       const bool wide = c.page_tokens % 32 == 0;       // boxes of 32 rows, else of 16
-      Share r;
-      while (take(r)) {
-        acquire();
+      for (;; n += C::kTeams) {
+        const Tile& d = ready(n);
+        if (!ok || d.meta < 0) break;
+        acquire(n);
         if (!ok) break;
-        const uint32_t tile = skv + stage * C::kTileBytes;
-        if (r.off[0] >= 0 && r.off[1] >= 0 && r.lim >= 32 && !r.watched()) {
-          note(r, 0);
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&bars->kv_full[stage], 32 * D * 2);
+        uint64_t* full = &bars->kv_full[n % C::kStages];
+        uint8_t* tile = sKV + n % C::kStages * C::kTileBytes;
+        uint32_t bytes = 0;
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          Share r;
+          share(r, d, x);
+          const bool copy = r.whole() && !r.watched();
+          uint32_t odd = 0;
+          if (copy) {
+            bytes += 32 * D * 2;
+          } else {
+            copy_share<D>(r, c, p.kv_heads, smem_u32(tile), x, lane);
+            if (r.watched()) odd = clean_share<D, false>(r, smem_u32(tile), x, lane);
+            fence_proxy_async_smem();
+          }
+          note(r, x, odd);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(full, bytes);
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            Share r;
+            share(r, d, x);
+            if (!r.whole() || r.watched()) continue;
             const CUtensorMap* map = r.values() ? &p.vmap : &p.kmap;
 #pragma unroll
             for (int a = 0; a < C::kAtoms; ++a) {
-              uint8_t* dst = sKV + stage * C::kTileBytes + a * C::kAtomBytes + w * 32 * 128;
-              tma_load_2d(dst, map, &bars->kv_full[stage], r.head * D + a * 64, static_cast<int>(r.off[0]), policy);
-              if (!wide) tma_load_2d(dst + 16 * 128, map, &bars->kv_full[stage], r.head * D + a * 64, static_cast<int>(r.off[1]), policy);
+              uint8_t* dst = tile + a * C::kAtomBytes + x * 32 * 128;
+              tma_load_2d(dst, map, full, r.head * D + a * 64, static_cast<int>(r.off[0]), policy);
+              if (!wide) tma_load_2d(dst + 16 * 128, map, full, r.head * D + a * 64, static_cast<int>(r.off[1]), policy);
             }
           }
-          __syncwarp();
-        } else {
-          copy_share<D>(r, c, p.kv_heads, tile, w, lane);
-          note(r, r.watched() ? clean_share<D>(r, tile, w, lane) : 0);
-          publish();
         }
-        advance();
+        release(n);
       }
       // copies that nobody waited for (after an error) land before shared memory is given back
       if (!ok || bars->abort)
-        for (int x = 0; x < C::kStages; ++x)
-          if (x < stage || round > 0) wait_drain(&bars->kv_full[x], (x < stage ? round : round - 1) & 1u, kTimeoutNs);
+        for (int k = 1; k <= C::kStages; ++k)
+          if (n - k >= 0 && (n - k) % C::kTeams == team)
+            wait_drain(&bars->kv_full[(n - k) % C::kStages], ((n - k) / C::kStages) & 1u, kTimeoutNs);
     } else {
-      // the bytes of kAhead tiles are on their way in registers
-      constexpr int kAhead = 1;
-      Raw<D, TYPE> raw[kAhead + 1];
-      Share r[kAhead + 1];
-      bool have[kAhead + 1];
+      // a share's bytes are on their way in registers: as soon as one of them is stored the next share's follows it
+      Raw<D, TYPE> raw;
+      Source<D, TYPE> from;
+      Share r;
+      int sub = 0, at = n;                 // of tile n, the next to be taken; the tile of the share in hand
       bool more = true;
-      auto fill = [&](int k) {
-        have[k] = more && (more = take(r[k]));
-        if (have[k]) load_raw<D, TYPE>(raw[k], r[k], c, p.kv_heads, lane);
+      auto next = [&]() {
+        r.off[0] = r.off[1] = -1;
+        r.lim = 0;
+        r.meta = 0;
+        if (more) {
+          const Tile& d = ready(n);
+          more = ok && d.meta >= 0;
+          if (more) share(r, d, member * C::kSubs + sub);
+        }
+        if (more && ++sub == C::kSubs) {
+          release(n);
+          sub = 0;
+          n += C::kTeams;
+        }
+        from.set(r, c, p.kv_heads, lane);
       };
+      int done = 0;                        // shares of the tile in hand that are stored
+      next();
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) fill(k);
-      bool busy = true;
-      while (ok && busy) {
-        busy = false;
+      for (int i = 0; i < Raw<D, TYPE>::kVec; ++i) from.load(raw, i, p.kv_heads, lane);
+      bool have = more;
+      while (have) {
+        const Share mine = r;
+        const int chunk = member * C::kSubs + done;
+        next();
+        have = more;
+        if (done == 0) acquire(at);
+        if (!ok) break;
+        const uint32_t tile = skv + at % C::kStages * C::kTileBytes;
 #pragma unroll
-        for (int k = 0; k <= kAhead; ++k) {
-          fill((k + kAhead) % (kAhead + 1));
-          if (!have[k]) continue;
-          acquire();
-          if (!ok) break;
-          const uint32_t tile = skv + stage * C::kTileBytes;
-          note(r[k], r[k].watched() ? store_raw<D, TYPE, true>(raw[k], r[k], tile, w, lane)
-                                    : store_raw<D, TYPE, false>(raw[k], r[k], tile, w, lane));
-          publish();
-          advance();
-          busy = true;
+        for (int i = 0; i < Raw<D, TYPE>::kVec; ++i) {
+          store_raw<D, TYPE>(raw, i, tile, chunk, lane);
+          from.load(raw, i, p.kv_heads, lane);
+        }
+        note(mine, chunk, mine.watched() ? clean_share<D, true>(mine, tile, chunk, lane) : 0);
+        if (++done == C::kSubs) {
+          publish(at);
+          done = 0;
+          at += C::kTeams;
         }
       }
     }
@@ -834,34 +833,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     uint32_t items = 0;
     if (warp == kPlanWarp) {
       // ---------------------------------------------------------- the order of the tiles, and where their tokens lie
+      // four tiles at a time, lane 8 q + g with group g of tile q; the entries of the next four are on their way
       TileWalk walk(p, bars->start);
       TileRef r, nr;
       int32_t page = 0, npage = 0;
-      const int g = lane & 7;
-      auto entry = [&](const TileRef& t) {
-        const int32_t tok = t.tok0 + g * 16;
-        return tok < t.lim ? __ldg(c.table + static_cast<int64_t>(t.seq) * c.max_pages + page_of_group(tok >> 4, c.magic)) : 0;
-      };
-      bool more = walk.next(nr, p);
-      if (more) npage = entry(nr);
-      for (int n = 0; ok; ++n) {
-        const int slot = n % kTileSlots;
-        if (n >= kTileSlots) ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_empty[slot], (n / kTileSlots - 1) & 1u, wc, 12));
-        if (!ok) break;
-        Tile& d = bars->tile[slot];
-        if (!more) {
-          if (lane == 0) {
-            d.meta = -1;
-            mbar_arrive(&bars->tile_full[slot]);
-          }
-          break;
+      const int g = lane & 7, mine = lane / 8;
+      int count = 0, ncount = 0;                   // tiles of the four that there are
+      auto next = [&]() {
+        ncount = 0;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          TileRef t;
+          if (!walk.next(t, p)) break;
+          if (mine == q) nr = t;
+          ++ncount;
         }
+        const int32_t tok = nr.tok0 + g * 16;
+        if (mine < ncount)
+          npage = tok < nr.lim ? __ldg(c.table + static_cast<int64_t>(nr.seq) * c.max_pages + page_of_group(tok >> 4, c.magic)) : 0;
+      };
+      for (int n = -4; ok; n += 4) {
         r = nr;
         page = npage;
-        more = walk.next(nr, p);
-        if (more) npage = entry(nr);
-        const int32_t tok = r.tok0 + g * 16;
-        if (lane < 8) {
+        count = ncount;
+        if (count == 4 || n < 0) next(); else ncount = 0;
+        if (n < 0) continue;
+        // behind the last tile an end for each team
+#pragma unroll 1
+        for (int q = 0; ok && q < 4; ++q)
+          if (n + q >= kTileSlots)
+            ok = __all_sync(0xffffffffu, wait_bounded(&bars->tile_empty[(n + q) % kTileSlots], ((n + q) / kTileSlots - 1) & 1u, wc, 12));
+        if (!ok) break;
+        Tile& d = bars->tile[(n + mine) % kTileSlots];
+        if (mine < count) {
+          const int32_t tok = r.tok0 + g * 16;
           int64_t off = -1;
           if (tok < r.lim) {
             if (page >= 0 && page < c.n_pages) {
@@ -874,18 +879,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
               }
             } else {
               atomicCAS(c.err_word, 0, SR_DEVERR_BAD_PAGE);
+              bars->bad = 1;
             }
           }
           d.off[g] = off;
-          if (lane == 0) {
+          if (g == 0) {
             d.lim = min(r.lim - r.tok0, BN);
             d.watch = r.watch == INT32_MAX ? BN : min(max(r.watch - r.tok0, 0), BN);
             d.head = r.head;
             d.meta = r.meta;
           }
+        } else if (g == 0) {
+          d.meta = -1;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->tile_full[slot]);
+        if (g == 0) mbar_arrive(&bars->tile_full[(n + mine) % kTileSlots]);
+        if (count < 4) {
+          // as many ends again, for the teams whose turn came before the last tile
+          if (count == 0) break;
+          r.lim = 0;
+          nr = r;
+          ncount = 0;
+        }
       }
     } else if (warp >= kQWarp0) {
       Walker walk(p, bars->start);
@@ -968,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
       bool issued = false;
       int stage = 0;
-      uint32_t phase = 0, pb[2] = {0, 0};       // ring position; P tiles of each group waited on
+      uint32_t phase = 0, pb = 0;               // ring position; bit t: parity of group t's next P
       auto take = [&]() -> int {                // the next tile of the ring
         const int s = stage;
         if (ok) ok = __all_sync(0xffffffffu, wait_bounded(&bars->kv_full[s], phase, wc, 3));
@@ -990,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       };
       auto pv = [&](int t, int s, bool acc) {
         const uint32_t vt = skv + s * C::kTileBytes;
-        const uint32_t par = pb[t] & 1u;
+        const uint32_t par = pb >> t & 1u;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (ok) ok = __all_sync(0xffffffffu, wait_bounded(half == 0 ? &bars->p_half[t] : &bars->p_full[t], par, wc, 4));
@@ -1001,57 +1016,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             mma_ts_w(tmem + 256 + t * 128, tmem + t * BN + kk * 8, sdesc_sw128(vt + kk * 16 * 128, C::kAtomBytes, 1024), C::kIdescPV,
                      (acc || kk > 0) ? 1u : 0u, leader);
         }
-        ++pb[t];
+        pb ^= 1u << t;
       };
       while (walk.next()) {
         const Block& k = walk.k;
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 3));
         if (!ok) break;
         const int n = k.s1 - k.s0;
-        if (!k.split) {
-          for (int j = 0; j <= n && ok; ++j) {
-            const int v = j > 0 ? take() : 0, kt = j < n ? take() : 0;
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (j > 0) {
-                pv(t, v, j > 1);
-                if (!ok) break;
-                if (j == n) tc_commit_w(&bars->o_done[t], leader);
-              }
-              if (j < n) qk(t, false, kt);
+        const int n1 = k.count(1);
+        const bool split = k.split;
+        int v = 0, kt = 0;
+#pragma unroll 1
+        for (int j = 0; j <= n && ok; ++j) {
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int cnt = t == 0 ? n : n1;
+            if (j > 0 && j <= cnt) {
+              if (split || t == 0) v = take();
+              if (!ok) break;
+              tc_fence_after();
+              pv(t, v, j > 1);
+              if (!ok) break;
+              if (j == cnt) tc_commit_w(&bars->o_done[t], leader);
+              if (split || t == 1) tc_commit_w(&bars->kv_empty[v], leader);
             }
-            if (!ok) break;
-            if (j > 0) tc_commit_w(&bars->kv_empty[v], leader);
-            if (j < n) tc_commit_w(&bars->kv_empty[kt], leader);
-            if (j == n - 1) tc_commit_w(&bars->q_empty, leader);
-          }
-        } else {
-          const int n1 = k.count(1);
-          for (int j = 0; j <= n && ok; ++j) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int cnt = t == 0 ? n : n1;
-              if (j > 0 && j <= cnt) {
-                const int v = take();
-                if (!ok) break;
-                tc_fence_after();
-                pv(t, v, j > 1);
-                if (!ok) break;
-                if (j == cnt) tc_commit_w(&bars->o_done[t], leader);
-                tc_commit_w(&bars->kv_empty[v], leader);
-              }
-              if (j < cnt) {
-                const int kt = take();
-                if (!ok) break;
-                tc_fence_after();
-                qk(t, true, kt);
-                tc_commit_w(&bars->kv_empty[kt], leader);
-              }
+            if (j < cnt) {
+              if (split || t == 0) kt = take();
+              if (!ok) break;
+              tc_fence_after();
+              qk(t, split, kt);
+              if (split || t == 1) tc_commit_w(&bars->kv_empty[kt], leader);
             }
-            if (ok && j == n - 1) tc_commit_w(&bars->q_empty, leader);
           }
+          if (ok && j == n - 1) tc_commit_w(&bars->q_empty, leader);
         }
         ++items;
         if (!ok) break;
@@ -1090,22 +1087,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       const int cnt = k.count(t), step = k.split ? 2 * BN : BN;
       int32_t ks = k.tile(t, 0) * BN;                 // first token of the key tile
       const int32_t seen = k.lim;
-      // the pages of a key tile's groups, by lanes 0-7: those that are none of the pool are not seen
-      auto fetch = [&](int32_t tok, bool more) {
-        tok += (lane & 7) * 16;
-        return more && tok < seen ? __ldg(table + page_of_group(tok >> 4, c.magic)) : 0;
-      };
-      int32_t page = fetch(ks, cnt > 0);
       float m = -INFINITY, l = 0.f;
       const float2 sl2x2 = make_float2(sl2, sl2);
       for (int j = 0; j < cnt; ++j) {
         const int valid = lim - ks;
-        const uint32_t there = __ballot_sync(0xffffffffu, page >= 0 && page < c.n_pages);
         ks += step;
-        page = fetch(ks, j + 1 < cnt);
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->s_full[t], (sb + static_cast<uint32_t>(j)) & 1u, wc, 5));
         if (!ok) break;
         tc_fence_after();
+        const bool bad = *reinterpret_cast<volatile int*>(&bars->bad);
+        if (bad || __any_sync(0xffffffffu, valid < BN)) {
+          // keys that the row does not see, or that have no page (once the planning warp has met an entry that is none of
+          // the pool, in whatever tile): in tensor memory, 32 at a time, which keeps the common path short
+          uint32_t there = 0xFFu;
+          if (bad) {
+            const int32_t tok = ks - step + (lane & 7) * 16;
+            const int32_t page = tok < seen ? __ldg(table + page_of_group(tok >> 4, c.magic)) : 0;
+            there = __ballot_sync(0xffffffffu, page >= 0 && page < c.n_pages);
+          }
+#pragma unroll 1
+          for (int x = 0; x < 4; ++x) {
+            uint32_t z[32];
+            tmem_ld32(t_s + x * 32, z);
+            tmem_wait_ld();
+            tmem_fix(z);
+            const int left = valid - x * 32;
+            uint32_t keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+            keep &= (there >> (2 * x) & 1u ? 0x0000FFFFu : 0u) | (there >> (2 * x) & 2u ? 0xFFFF0000u : 0u);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(keep >> i & 1u)) z[i] = 0xFF800000u;
+            tmem_st32(t_s + x * 32, z);
+          }
+          tmem_wait_st();
+        }
         uint32_t rr[4][32];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld32(t_s + x * 32, rr[x]);
@@ -1113,16 +1128,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_fix(rr[x]);
         float* s = reinterpret_cast<float*>(&rr[0][0]);
-        if (__any_sync(0xffffffffu, valid < BN)) {
-#pragma unroll
-          for (int i = 0; i < BN; ++i)
-            if (i >= valid) s[i] = -INFINITY;
-        }
-        if (there != 0xffffffffu) {
-#pragma unroll
-          for (int i = 0; i < BN; ++i)
-            if (!(there >> (i / 16) & 1u)) s[i] = -INFINITY;
-        }
         float a0 = fmaxf(s[0], s[1]), a1 = fmaxf(s[2], s[3]), a2 = fmaxf(s[4], s[5]), a3 = fmaxf(s[6], s[7]);
 #pragma unroll
         for (int i = 8; i < BN; i += 8) {
@@ -1194,8 +1199,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       od[0] += 1;
       od[1] += !k.split || merge ? 1u : 0u;
       const int slot = items % kFlagSlots;
-      ok = __all_sync(0xffffffffu, wait_bounded(&bars->flags_full[slot], (items / kFlagSlots) & 1u, wc, 7));
-      if (!ok) break;
       if (k.split && t == 1) {
         // hand (m, l) to group 0 and wait until it has read them and O_1
         bars->xm[row] = cnt > 0 ? m : -INFINITY;
@@ -1220,9 +1223,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           l = l * f0 + l1 * f1;
           m = mm;
         }
+        // (the values' loading came before the products that o_done stands for)
+        const int f_lo = k.split ? 2 * k.s0 : k.s0, f_hi = k.split ? min(2 * k.s1, k.tiles) : k.s1, f_0 = k.lim_min / BN;
         uint32_t odd = 0;
+        if (p.causal)
 #pragma unroll 1
-        for (int x = 0; x < kLoadWarps * kFlagTiles; ++x) odd |= bars->flags[slot][x / kFlagTiles][x % kFlagTiles];
+          for (int x = max(f_lo, f_0); x < f_hi; ++x)
+            for (int y = 0; y < 4; ++y) odd |= bars->flags[slot][y][min(x - f_0, kFlagTiles - 1)];
         const float vscale = C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv])) : 1.f);
         const float to = whole ? (l == 0.f ? 0.f : vscale / l) : vscale;
         const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + token) * c.n_heads + k.h * group + hh;
@@ -1264,12 +1271,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         if (odd && live) {
           const float raw_scale = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
 #pragma unroll 1
-          for (int z = 0; z < kLoadWarps * kFlagTiles; ++z) {
-            uint32_t bits = bars->flags[slot][z / kFlagTiles][z % kFlagTiles];
-            const int32_t tok = (k.lim_min / BN + z % kFlagTiles) * BN + z / kFlagTiles * 32;
+          for (int z = 4 * max(f_lo, f_0); z < 4 * f_hi; ++z) {
+            uint32_t bits = bars->flags[slot][z % 4][min(z / 4 - f_0, kFlagTiles - 1)];
 #pragma unroll 1
             for (; bits; bits &= bits - 1) {
-              const int32_t at = tok + __ffs(bits) - 1;
+              const int32_t at = z * 32 + __ffs(bits) - 1;
               if (at < lim) add_odd<D, TYPE>(p, part, p.id[k.i], at, kv, p.q + out * D, raw_scale, m, to);
             }
           }
@@ -1372,6 +1378,8 @@ cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st) {
     blocks += (p.row0[i + 1] - p.row0[i] + 2 * p.tpt - 1) / (2 * p.tpt);
   }
   p.blocks = static_cast<int32_t>(blocks);
+  const int ctas = std::min(sm_count(), kMaxPromptCtas);
+  if (blocks * p.c.n_kv > (int64_t(1) << 31) / (p.c.cap / BN + 2) * ctas) return cudaErrorInvalidValue;   // an hour or more
   return p.c.head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
 }
 
