@@ -51,6 +51,7 @@ struct Cfg {
   static constexpr uint32_t kRegsOther = 72, kRegsLoad = 160 - kRegsOther;
   static_assert(2 * 128 * kRegsSoftmax + 128 * (kRegsOther + kRegsLoad) <= kThreads * kLaunchRegs,
                 "register split exceeds what the block is launched with");
+  static constexpr int kUnrollT = kHalf ? 1 : 2;            // (where the loading warps' loops are longer, this one is shorter)
   static constexpr int kAtoms = D / 64;
   static constexpr int kAtomBytes = BM * 128;
   static constexpr int kTileBytes = kAtoms * kAtomBytes;
@@ -103,11 +104,12 @@ constexpr int kTileSlots = 8;
 
 struct Record {        // a block, as the softmax groups read it
   Block k;
-  int64_t u;
+  int32_t c0, parts;   // the first of the CTAs that share it, and how many do
+  bool last;           // the others had written their parts before this CTA began
 };
 
 struct Bars {
-  uint64_t q_full, q_empty, q_seen;
+  uint64_t q_raw, q_full, q_empty, q_seen;   // q_raw: fp16 products, the rows as they came
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t x_full, x_empty, part_done, part_last, drain;
@@ -118,11 +120,12 @@ struct Bars {
   int bad;               // an entry that is no page of the pool has been met
   int abort;
   int last;
+  int joined;            // split blocks: group 0 has joined the parts
   Start start;
   // of a block: new tokens with values that are no finite numbers, by 32 tokens of a key tile, the tiles counted from the
   // first that some row does not see whole
   uint32_t flags[kFlagSlots][4][kFlagTiles];
-  int8_t qexp[2][BM];
+  int8_t qexp[BM];               // split blocks, fp16 products: the rows' exponents for group 1
   float xm[BM], xl[BM];
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier area too small");
@@ -130,6 +133,8 @@ static_assert(sizeof(Bars) <= kBarBytes, "barrier area too small");
 struct Setup {                   // overlays the stages before they are used
   int64_t cum[kMaxPagedSeqs + 1];
   unsigned long long per_head[kMaxPagedSeqs];
+  int32_t len[kMaxPagedSeqs];
+  int none;                      // some block's rows see nothing
 };
 
 __device__ __forceinline__ void set_block(const PromptParams& p, Block& k, int32_t len) {
@@ -212,9 +217,13 @@ struct Walker {
   }
 };
 
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {   // a >= 0, b > 0; mostly short numbers
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 __device__ __forceinline__ int owner_of(int64_t u, int64_t share, int64_t rest) {
   const int64_t longer = rest * (share + 1);
-  return static_cast<int>(u < longer ? u / (share + 1) : rest + (u - longer) / share);
+  return static_cast<int>(u < longer ? div_pos(u, share + 1) : rest + div_pos(u - longer, share));
 }
 
 // -------------------------------------------------------------- loading keys and values
@@ -457,7 +466,21 @@ __device__ __forceinline__ float* slot_at(const PromptParams& p, int cta, int sl
   return p.parts + (static_cast<int64_t>(cta) * 2 + slot) * slot_floats<D>();
 }
 
-// Joins a block's n parts, that of CTA c0 (slot 1) and of those behind it (slot 0): a warp per row, its lanes the dims.
+// A block's parts are joined in the order of the line: a = sum of w_x v_x, l = sum of w_x l_x with w_x = 2^(m_x - top) and
+// top the largest m_x. A maximum of -inf stands for no score, or for NaN alone.
+__device__ __forceinline__ float part_weight(float2 ml, float top) {
+  return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - top);
+}
+template <int D>
+__device__ __forceinline__ const float* part_at(const PromptParams& p, int c0, int x) {
+  return slot_at<D>(p, c0 + x, x == 0 ? 1 : 0);
+}
+template <int D>
+__device__ __forceinline__ float2 part_ml(const PromptParams& p, int c0, int x, int row) {
+  return __ldcg(reinterpret_cast<const float2*>(part_at<D>(p, c0, x) + 2 * BM * D) + row);
+}
+
+// Joins the n parts of a block, that of CTA c0 (slot 1) and of those behind it (slot 0): a warp per row, its lanes the dims.
 // What it costs is the latency of the loads, so kJoinBatch of them are on their way: of as many rows, part by
 // part, or, where a warp has few rows, of one row's parts.
 constexpr int kJoinBatch = 8;
@@ -471,12 +494,26 @@ __device__ __noinline__ void join_block(const PromptParams& p, const Block& k, i
     float top[R], sum[R], a[R][N];
 #pragma unroll
     for (int y = 0; y < R; ++y) {
-      const int r = min(r0 + y, rows - 1), tok = r / group;
-      at[y] = tok >= p.tpt ? BM + (tok - p.tpt) * group + r % group : r;
+      const int r = min(r0 + y, rows - 1), tok = static_cast<int>(static_cast<uint32_t>(r) * p.group_magic >> 16);
+      at[y] = tok >= p.tpt ? BM + r - p.tpt * group : r;
       top[y] = -INFINITY;
       sum[y] = 0.f;
 #pragma unroll
       for (int z = 0; z < N; ++z) a[y][z] = 0.f;
+    }
+    if constexpr (ROWS) {
+#pragma unroll 1
+      for (int x = 0; x < n; ++x) {
+        float m[R];
+#pragma unroll
+        for (int y = 0; y < R; ++y) m[y] = part_ml<D>(p, c0, x, at[y]).x;
+#pragma unroll
+        for (int y = 0; y < R; ++y) top[y] = fmaxf(top[y], m[y]);
+      }
+    } else {
+      for (int x = lane; x < n; x += 32) top[0] = fmaxf(top[0], part_ml<D>(p, c0, x, at[0]).x);
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], s));
     }
 #pragma unroll 1
     for (int x0 = 0; x0 < n; x0 += ROWS ? 1 : B) {
@@ -484,15 +521,14 @@ __device__ __noinline__ void join_block(const PromptParams& p, const Block& k, i
       float v[B][N];
 #pragma unroll
       for (int y = 0; y < B; ++y) {
-        const int x = ROWS ? x0 : min(x0 + y, n - 1);
-        const float* src = slot_at<D>(p, c0 + x, x == 0 ? 1 : 0);
-        const int row = at[ROWS ? y : 0];
-        ml[y] = __ldcg(reinterpret_cast<const float2*>(src + 2 * BM * D) + row);
+        const int x = ROWS ? x0 : min(x0 + y, n - 1), row = at[ROWS ? y : 0];
+        ml[y] = part_ml<D>(p, c0, x, row);
+        const float* src = part_at<D>(p, c0, x) + row * D;
         if constexpr (N == 4) {
-          const float4 z = __ldcg(reinterpret_cast<const float4*>(src + row * D) + lane);
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(src) + lane);
           v[y][0] = z.x; v[y][1] = z.y; v[y][2] = z.z; v[y][3] = z.w;
         } else {
-          const float2 z = __ldcg(reinterpret_cast<const float2*>(src + row * D) + lane);
+          const float2 z = __ldcg(reinterpret_cast<const float2*>(src) + lane);
           v[y][0] = z.x; v[y][1] = z.y;
         }
       }
@@ -500,21 +536,17 @@ __device__ __noinline__ void join_block(const PromptParams& p, const Block& k, i
       for (int y = 0; y < B; ++y) {
         const int q = ROWS ? y : 0;
         if (!ROWS && x0 + y >= n) break;
-        // a maximum of -inf stands for no score, or for NaN alone
-        const float t = fmaxf(top[q], ml[y].x);
-        const float f = top[q] == -INFINITY ? (sum[q] == 0.f ? 0.f : 1.f) : ex2_approx(top[q] - t);
-        const float w = ml[y].x == -INFINITY ? (ml[y].y == 0.f ? 0.f : 1.f) : ex2_approx(ml[y].x - t);
-        top[q] = t;
-        sum[q] = fmaf(w, ml[y].y, sum[q] * f);
+        const float w = part_weight(ml[y], top[q]);
+        sum[q] = fmaf(w, ml[y].y, sum[q]);
 #pragma unroll
-        for (int z = 0; z < N; ++z) a[q][z] = fmaf(w, v[y][z], a[q][z] * f);
+        for (int z = 0; z < N; ++z) a[q][z] = fmaf(w, v[y][z], a[q][z]);
       }
     }
 #pragma unroll
     for (int y = 0; y < R; ++y) {
       const int r = r0 + y;
       if (r >= rows) break;
-      const int tok = r / group, hh = r - tok * group;
+      const int tok = static_cast<int>(static_cast<uint32_t>(r) * p.group_magic >> 16), hh = r - tok * group;
       const float inv = sum[y] == 0.f ? 0.f : 1.f / sum[y];
       const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + tok) * p.c.n_heads + k.h * group + hh;
       uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * N);
@@ -546,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
   WaitCtx wc{&bars->abort, c.err_word, kTimeoutNs};
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, kQWarps);
+    mbar_init(&bars->q_raw, kQWarps);
+    mbar_init(&bars->q_full, C::kHalf ? 8 : kQWarps);
     mbar_init(&bars->q_empty, 1);
     mbar_init(&bars->q_seen, 8);
     for (int s = 0; s < 8; ++s) {
@@ -555,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_half[t], BM);
-      mbar_init(&bars->p_full[t], BM);
+      mbar_init(&bars->p_half[t], 4);
+      mbar_init(&bars->p_full[t], 4);
       mbar_init(&bars->o_done[t], 1);
     }
     mbar_init(&bars->x_full, BM);
@@ -576,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     tmem_alloc(&bars->tmem_base, 512);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < p.n; i += kThreads) setup->per_head[i] = 0;
+  if (threadIdx.x < p.n) setup->per_head[threadIdx.x] = 0;
+  if (threadIdx.x == 0) setup->none = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -585,20 +619,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
 
   // ---- the line of steps: units of each sequence's blocks for one head, then of the sequences one after the other
   {
+    if (threadIdx.x < p.n) setup->len[threadIdx.x] = seq_length(p, threadIdx.x);
+    __syncthreads();
     for (int x = threadIdx.x; x < p.blocks; x += kThreads) {
-      const int lo = seq_of_block(p, x);
+      const int lo = p.n == 1 ? 0 : seq_of_block(p, x);
       Block k;
       k.i = lo;
       k.b = x - p.blk0[lo];
-      set_block(p, k, seq_length(p, lo));
-      if (k.steps > 0) atomicAdd(&setup->per_head[lo], static_cast<unsigned long long>(units_of(k)));
+      set_block(p, k, setup->len[lo]);
+      if (k.steps > 0)
+        atomicAdd(&setup->per_head[lo], static_cast<unsigned long long>(units_of(k)));
+      else
+        setup->none = 1;
     }
-    // blocks of rows that see nothing
-    for (int x = blockIdx.x; x < p.blocks; x += gridDim.x) {
+    __syncthreads();
+    for (int x = setup->none ? blockIdx.x : p.blocks; x < p.blocks; x += gridDim.x) {
       Block k;
       k.i = seq_of_block(p, x);
       k.b = x - p.blk0[k.i];
-      set_block(p, k, seq_length(p, k.i));
+      set_block(p, k, setup->len[k.i]);
       if (k.steps > 0) continue;
       const int64_t row = static_cast<int64_t>(p.row0[k.i]) + k.tok0;
       uint4* o = reinterpret_cast<uint4*>(p.o + row * c.n_heads * D);
@@ -606,7 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       for (int y = threadIdx.x; y < k.ntok * c.n_heads; y += kThreads)
         if (p.lse) p.lse[row * c.n_heads + y] = -INFINITY;
     }
-    __syncthreads();
     if (warp == 0) {
       constexpr int kPer = kMaxPagedSeqs / 32;
       int64_t mine = 0;
@@ -637,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
       s.i = s.h = s.b = s.s0 = 0;
       const int64_t ctas = min(static_cast<int64_t>(gridDim.x), T);
       if (static_cast<int64_t>(blockIdx.x) < ctas) {
-        s.share = T / ctas;
+        s.share = div_pos(T, ctas);
         s.rest = T - s.share * ctas;
         const int64_t u0 = blockIdx.x * s.share + min(static_cast<int64_t>(blockIdx.x), s.rest);
         s.left = s.share + (static_cast<int64_t>(blockIdx.x) < s.rest ? 1 : 0);
@@ -649,9 +687,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         const int64_t per_head = static_cast<int64_t>(setup->per_head[lo]);
         int64_t within = u0 - setup->cum[lo];
         s.i = lo;
-        s.h = static_cast<int>(within / per_head);
+        s.h = static_cast<int>(div_pos(within, per_head));
         within -= s.h * per_head;
-        const int32_t len = seq_length(p, lo);
+        const int32_t len = setup->len[lo];
         const int nb = blocks_of(p, lo);
         for (int b0 = 0; b0 < nb; b0 += 32) {          // the block that holds unit `within` of this head's
           Block k;
@@ -917,10 +955,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
                                            wait_bounded(&bars->q_seen, (items - 1) & 1u, wc, 2));
           if (!ok) break;
         }
-        if (w == 0 && lane == 0) bars->rec[items & 1] = Record{k, walk.u};
+        if (w == 0 && lane == 0) {
+          const Start& s = bars->start;
+          Record r{k, 0, 1, false};
+          if (k.s0 > 0 || k.s1 < k.steps) {
+            r.c0 = owner_of(walk.u, s.share, s.rest);
+            r.parts = owner_of(walk.u + k.steps - 1, s.share, s.rest) - r.c0 + 1;
+            int32_t done;
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(done) : "l"(p.arrivals + r.c0) : "memory");
+            r.last = done == r.parts - 1;
+          }
+          bars->rec[items & 1] = r;
+        }
         const int tiles = k.split ? 1 : 2;
         const int64_t row00 = static_cast<int64_t>(p.row0[k.i]) + k.tok0;
-        // this warp's half of each tile's rows: all copies in flight together, then, for fp16, a row per lane
+        // this warp's half of each tile's rows, all copies in flight together
         for (int t = 0; t < tiles; ++t) {
           const uint32_t tile = sq + t * C::kTileBytes;
           const __nv_bfloat16* src = p.q + (row00 * c.n_heads + k.h * group) * D + lane % kLanes * 8;
@@ -933,54 +982,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (C::kHalf) {
-          // fp16, scaled by a power of two to a largest element in [1, 2)
-          __syncwarp();
-          for (int x = lane; x < tiles * (BM / kQWarps); x += 32) {
-            const int t = x / (BM / kQWarps), tr = w * (BM / kQWarps) + x % (BM / kQWarps);
-            const uint32_t tile = sq + t * C::kTileBytes;
-            uint32_t top = 0;                         // of |x|, as bf16 bits: their order, NaN last
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-              const uint4 v = load16(tile + piece_at<D>(tr, y));
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-            }
-            const float most = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
-            const int e = most > 0.f && most < INFINITY ? max(ilogbf(most), -120) : 0;
-            const float down = ldexpf(1.f, -e);
-#pragma unroll
-            for (int y = 0; y < D / 8; ++y) {
-              const uint32_t at = tile + piece_at<D>(tr, y);
-              const uint4 v = load16(at);
-              auto half = [&](uint32_t z) {
-                const __half2 h = __floats2half2_rn(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
-                return *reinterpret_cast<const uint32_t*>(&h);
-              };
-              const uint32_t h[4] = {half(v.x), half(v.y), half(v.z), half(v.w)};
-              if constexpr (TYPE == SR_PAGE_INT4)
-                store16(at, make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
-                                       __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632)));
-              else
-                store16(at, make_uint4(h[0], h[1], h[2], h[3]));
-            }
-            bars->qexp[t][tr] = static_cast<int8_t>(e);
-          }
-        }
-        fence_proxy_async_smem();
+        if constexpr (!C::kHalf) fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->q_full);
+        if (lane == 0) mbar_arrive(C::kHalf ? &bars->q_raw : &bars->q_full);
         ++items;
       }
       // the end: a record of no block, once the last one but one has been read
       if (ok && items > 0) ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_seen, (items - 1) & 1u, wc, 2));
       if (ok && w == 0 && lane == 0) bars->rec[items & 1].k.i = -1;
       __syncwarp();
-      if (ok && lane == 0) mbar_arrive(&bars->q_full);
+      if (ok && lane == 0) mbar_arrive(C::kHalf ? &bars->q_raw : &bars->q_full);
     } else {
       // ---------------------------------------------------------- MMA issuer (the warp in step, one lane issues)
       Walker walk(p, bars->start);
       const uint32_t leader = elect_one();
-      const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV);
+      const uint32_t sq = smem_u32(sQ), skv = smem_u32(sKV), tm = __shfl_sync(0xffffffffu, tmem, 0);
       bool issued = false;
       int stage = 0;
       uint32_t phase = 0, pb = 0;               // ring position; bit t: parity of group t's next P
@@ -998,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk / 4) * C::kAtomBytes + (kk % 4) * 32;
-          mma_ss_w(tmem + t * BN, sdesc_sw128(qt + off, 16, 1024), sdesc_sw128(kt + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u, leader);
+          mma_ss_w(tm + t * BN, sdesc_sw128(qt + off, 16, 1024), sdesc_sw128(kt + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u, leader);
         }
         tc_commit_w(&bars->s_full[t], leader);
         issued = true;
@@ -1013,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           tc_fence_after();
 #pragma unroll
           for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-            mma_ts_w(tmem + 256 + t * 128, tmem + t * BN + kk * 8, sdesc_sw128(vt + kk * 16 * 128, C::kAtomBytes, 1024), C::kIdescPV,
+            mma_ts_w(tm + 256 + t * 128, tm + t * BN + kk * 8, sdesc_sw128(vt + kk * 16 * 128, C::kAtomBytes, 1024), C::kIdescPV,
                      (acc || kk > 0) ? 1u : 0u, leader);
         }
         pb ^= 1u << t;
@@ -1022,13 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         const Block& k = walk.k;
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 3));
         if (!ok) break;
-        const int n = k.s1 - k.s0;
-        const int n1 = k.count(1);
-        const bool split = k.split;
+        // the same in all lanes, and known to be
+        const int n = __shfl_sync(0xffffffffu, k.s1 - k.s0, 0), n1 = __shfl_sync(0xffffffffu, k.count(1), 0);
+        const bool split = __shfl_sync(0xffffffffu, k.split ? 1 : 0, 0) != 0;
         int v = 0, kt = 0;
 #pragma unroll 1
         for (int j = 0; j <= n && ok; ++j) {
-#pragma unroll 1
+#pragma unroll C::kUnrollT
           for (int t = 0; t < 2; ++t) {
             const int cnt = t == 0 ? n : n1;
             if (j > 0 && j <= cnt) {
@@ -1070,13 +1086,54 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     bool ok = true;
     uint32_t items = 0, sb = 0, od[2] = {0, 0}, nx = 0, cuts = 0;
     while (ok) {
-      ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 5));
+      ok = __all_sync(0xffffffffu, wait_bounded(C::kHalf ? &bars->q_raw : &bars->q_full, items & 1u, wc, 5));
       if (!ok) break;
-      const Block& k = bars->rec[items & 1].k;       // there until every warp has begun the next block
+      const Record& rec = bars->rec[items & 1];      // there until every warp has begun the next block
+      const Block& k = rec.k;
       if (k.i < 0) break;
       const int kv = static_cast<int>(static_cast<uint32_t>(k.h) * p.head_magic >> 22);
       float sl2 = c.scale_log2 * C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[kv])) : 1.f);
-      if constexpr (C::kHalf) sl2 *= ldexpf(1.f, bars->qexp[k.split ? 0 : t][row]);
+      if constexpr (C::kHalf) {
+        // the query row becomes fp16 in place, scaled by a power of two to a largest element in [1, 2)
+        int e = 0;
+        if (t == 0 || !k.split) {
+          const uint32_t tile = smem_u32(sQ) + t * C::kTileBytes;
+          uint32_t top = 0;                         // of |x|, as bf16 bits: their order, NaN last
+#pragma unroll 4
+          for (int y = 0; y < D / 8; ++y) {
+            const uint4 v = load16(tile + piece_at<D>(row, y));
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+          }
+          const float most = __uint_as_float(max(top & 0xFFFFu, top >> 16) << 16);
+          e = most > 0.f && most < INFINITY ? max(ilogbf(most), -120) : 0;
+          const float down = ldexpf(1.f, -e);
+#pragma unroll 4
+          for (int y = 0; y < D / 8; ++y) {
+            const uint32_t at = tile + piece_at<D>(row, y);
+            const uint4 v = load16(at);
+            auto half = [&](uint32_t z) {
+              const __half2 h = __floats2half2_rn(__uint_as_float(z << 16) * down, __uint_as_float(z & 0xFFFF0000u) * down);
+              return *reinterpret_cast<const uint32_t*>(&h);
+            };
+            const uint32_t h[4] = {half(v.x), half(v.y), half(v.z), half(v.w)};
+            if constexpr (TYPE == SR_PAGE_INT4)
+              store16(at, make_uint4(__byte_perm(h[0], h[2], 0x5410), __byte_perm(h[0], h[2], 0x7632),
+                                     __byte_perm(h[1], h[3], 0x5410), __byte_perm(h[1], h[3], 0x7632)));
+            else
+              store16(at, make_uint4(h[0], h[1], h[2], h[3]));
+          }
+          if (k.split) bars->qexp[row] = static_cast<int8_t>(e);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full);
+        if (k.split && t == 1) {
+          ok = __all_sync(0xffffffffu, wait_bounded(&bars->q_full, items & 1u, wc, 5));
+          if (!ok) break;
+          e = bars->qexp[row];
+        }
+        sl2 *= ldexpf(1.f, e);
+      }
       sl2 = fmaxf(sl2, 0x1p-126f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->q_seen);
@@ -1180,20 +1237,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bars->p_half[t]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->p_half[t]);
           }
         }
         const float2 s01 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         l = l * f + (s01.x + s01.y);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bars->p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->p_full[t]);
       }
       if (!ok) break;
       sb += static_cast<uint32_t>(cnt);
 
       // ---- the block's end
       const bool whole = k.s0 == 0 && k.s1 == k.steps;
+      bool joined = false;
       const uint32_t w0 = od[0], w1 = od[1];
       const bool merge = k.split && k.count(1) > 0;
       od[0] += 1;
@@ -1207,6 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         ok = __all_sync(0xffffffffu, wait_bounded(&bars->x_empty, nx & 1u, wc, 9));
         ++nx;
         if (!ok) break;
+        joined = bars->joined;
       } else {
         if (k.split) ok = wait_bounded(&bars->x_full, nx & 1u, wc, 9);
         ok = ok && wait_bounded(&bars->o_done[t], (t == 0 ? w0 : w1) & 1u, wc, 6);
@@ -1231,11 +1292,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           for (int x = max(f_lo, f_0); x < f_hi; ++x)
             for (int y = 0; y < 4; ++y) odd |= bars->flags[slot][y][min(x - f_0, kFlagTiles - 1)];
         const float vscale = C::kDecodedBy * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[p.kv_heads + kv])) : 1.f);
+        // a block whose other parts are there is joined on the way, as join_block would
+        const int c0 = rec.c0, parts = rec.parts, me = static_cast<int>(blockIdx.x) - c0;
+        const bool join = !whole && rec.last && !odd;
+        joined = join;
         const float to = whole ? (l == 0.f ? 0.f : vscale / l) : vscale;
+        const int prow = (k.split ? 0 : t) * BM + row;
+        float top = m, sum = 0.f, inv = 0.f;
+        if (join) {
+          for (int x = 0; x < parts; ++x)
+            if (x != me) top = fmaxf(top, part_ml<D>(p, c0, x, prow).x);
+          for (int x = 0; x < parts; ++x) {
+            const float2 ml = x == me ? make_float2(m, l) : part_ml<D>(p, c0, x, prow);
+            sum = fmaf(part_weight(ml, top), ml.y, sum);
+          }
+          inv = sum == 0.f ? 0.f : 1.f / sum;
+        }
         const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + token) * c.n_heads + k.h * group + hh;
         // a whole block with odd values goes through the slot too (free: only the last block can be cut behind it), since
         // add_odd reads the query row, whose place the output may take
-        const int prow = (k.split ? 0 : t) * BM + row;
         float* part = slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0) + prow * D;
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
@@ -1253,18 +1328,48 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             for (int i = 0; i < 32; ++i)
               of[i] = (f0 == 0.f ? 0.f : of[i] * f0) + (f1 == 0.f ? 0.f : __uint_as_float(o1[i]) * f1);
           }
-          auto y = [&](int i) { return of[column_of<TYPE>(i)] * to; };
+          float y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = of[column_of<TYPE>(i)] * to;
+          if (join && live) {
+            float a[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = 0.f;
+#pragma unroll 1
+            for (int z = 0; z < parts; ++z) {
+              const float2 ml = z == me ? make_float2(m, l) : part_ml<D>(p, c0, z, prow);
+              const float w = part_weight(ml, top);
+              if (z == me) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) a[i] = fmaf(w, y[i], a[i]);
+              } else {
+                const float4* src = reinterpret_cast<const float4*>(part_at<D>(p, c0, z) + prow * D + x * 32);
+                float4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  a[4 * i] = fmaf(w, v[i].x, a[4 * i]);
+                  a[4 * i + 1] = fmaf(w, v[i].y, a[4 * i + 1]);
+                  a[4 * i + 2] = fmaf(w, v[i].z, a[4 * i + 2]);
+                  a[4 * i + 3] = fmaf(w, v[i].w, a[4 * i + 3]);
+                }
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = a[i] * inv;
+          }
           if (live) {
-            if (whole && !odd) {
+            if ((whole && !odd) || join) {
               uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x * 32);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16x2(y(8 * i), y(8 * i + 1)), pack_bf16x2(y(8 * i + 2), y(8 * i + 3)),
-                                    pack_bf16x2(y(8 * i + 4), y(8 * i + 5)), pack_bf16x2(y(8 * i + 6), y(8 * i + 7)));
+                dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
+                                    pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
             } else {
               float4* dst = reinterpret_cast<float4*>(part + x * 32);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y(4 * i), y(4 * i + 1), y(4 * i + 2), y(4 * i + 3));
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
             }
           }
         }
@@ -1285,30 +1390,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
               *reinterpret_cast<uint32_t*>(p.o + out * D + i) = pack_bf16x2(part[i], part[i + 1]);
         }
         if (live) {
-          if (!whole)
+          if (join) {
+            if (p.lse) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          } else if (!whole)
             *reinterpret_cast<float2*>(slot_at<D>(p, blockIdx.x, k.s0 == 0 ? 1 : 0) + 2 * BM * D + 2 * prow) = make_float2(m, l);
           else if (p.lse)
             p.lse[out] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
+        if (join && threadIdx.x == 0) p.arrivals[c0] = 0;
         if (k.split) {
+          if (threadIdx.x == 0) bars->joined = join;
           tc_fence_before();
           mbar_arrive(&bars->x_empty);
           ++nx;
         }
       }
-      if (!whole) {
-        // the last of the block's CTAs to arrive joins their parts
-        const Start& s = bars->start;
-        const int64_t u = bars->rec[items & 1].u;
-        const int c0 = owner_of(u, s.share, s.rest), c1 = owner_of(u + k.steps - 1, s.share, s.rest);
+      if (!whole && !joined) {
+        // the last of the block's CTAs to arrive joins their parts, if it has not done so above
         __threadfence();
         mbar_arrive(&bars->part_done);
         if (threadIdx.x == 0) {
           int last = 0;
           if (wait_bounded(&bars->part_done, cuts & 1u, wc, 10)) {
             __threadfence();
-            last = atomicAdd(p.arrivals + c0, 1) == c1 - c0;
-            if (last) p.arrivals[c0] = 0;
+            last = atomicAdd(p.arrivals + rec.c0, 1) == rec.parts - 1;
+            if (last) p.arrivals[rec.c0] = 0;
           }
           bars->last = last;
           mbar_arrive(&bars->part_last);
@@ -1317,9 +1423,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         ++cuts;
         if (ok && bars->last) {
           if (k.ntok * group > 32)
-            join_block<D, true>(p, k, c0, c1 - c0 + 1, warp, lane);
+            join_block<D, true>(p, k, rec.c0, rec.parts, warp, lane);
           else
-            join_block<D, false>(p, k, c0, c1 - c0 + 1, warp, lane);
+            join_block<D, false>(p, k, rec.c0, rec.parts, warp, lane);
         }
       }
       ++items;
