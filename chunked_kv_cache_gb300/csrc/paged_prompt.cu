@@ -459,6 +459,18 @@ __device__ __noinline__ void add_odd(const PromptParams& p, float* o, int32_t se
 }
 
 // -------------------------------------------------------------- partial results
+// 32 bytes, aligned to as many: whole sectors, where a lane has a row to itself
+__device__ __forceinline__ void store32(void* dst, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]),
+               "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+__device__ __forceinline__ void load32(float* x, const float* src) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+               : "l"(src)
+               : "memory");
+}
 template <int D>
 __host__ __device__ constexpr int64_t slot_floats() { return 2 * BM * (D + 2); }
 template <int D>
@@ -1343,17 +1355,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
 #pragma unroll
                 for (int i = 0; i < 32; ++i) a[i] = fmaf(w, y[i], a[i]);
               } else {
-                const float4* src = reinterpret_cast<const float4*>(part_at<D>(p, c0, z) + prow * D + x * 32);
-                float4 v[8];
+                const float* src = part_at<D>(p, c0, z) + prow * D + x * 32;
+                float v[32];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i);
+                for (int i = 0; i < 4; ++i) load32(v + 8 * i, src + 8 * i);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  a[4 * i] = fmaf(w, v[i].x, a[4 * i]);
-                  a[4 * i + 1] = fmaf(w, v[i].y, a[4 * i + 1]);
-                  a[4 * i + 2] = fmaf(w, v[i].z, a[4 * i + 2]);
-                  a[4 * i + 3] = fmaf(w, v[i].w, a[4 * i + 3]);
-                }
+                for (int i = 0; i < 32; ++i) a[i] = fmaf(w, v[i], a[i]);
               }
             }
 #pragma unroll
@@ -1361,15 +1368,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           }
           if (live) {
             if ((whole && !odd) || join) {
-              uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x * 32);
+              uint32_t z[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]), pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                    pack_bf16x2(y[8 * i + 4], y[8 * i + 5]), pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+              for (int i = 0; i < 16; ++i) z[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+              __nv_bfloat16* dst = p.o + out * D + x * 32;
+              if (p.o_aligned) {
+                store32(dst, z);
+                store32(dst + 16, z + 8);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
+              }
             } else {
-              float4* dst = reinterpret_cast<float4*>(part + x * 32);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              for (int i = 0; i < 4; ++i) store32(part + x * 32 + 8 * i, reinterpret_cast<const uint32_t*>(y) + 8 * i);
             }
           }
         }
@@ -1484,6 +1496,7 @@ cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st) {
     blocks += (p.row0[i + 1] - p.row0[i] + 2 * p.tpt - 1) / (2 * p.tpt);
   }
   p.blocks = static_cast<int32_t>(blocks);
+  p.o_aligned = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   const int ctas = std::min(sm_count(), kMaxPromptCtas);
   if (blocks * p.c.n_kv > (int64_t(1) << 31) / (p.c.cap / BN + 2) * ctas) return cudaErrorInvalidValue;   // an hour or more
   return p.c.head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);

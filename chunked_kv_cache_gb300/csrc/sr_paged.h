@@ -157,6 +157,7 @@ struct alignas(64) PromptParams {
   int32_t tpt;             // tokens of a tile of 128 query rows
   uint32_t group_magic;    // r / group = r * group_magic >> 16 for r < 128
   int32_t blocks;          // of query rows, over all sequences
+  bool o_aligned;          // o begins on a multiple of 32 bytes
   int32_t blk0[kMaxPagedSeqs];     // first block of each sequence
 };
 
