@@ -74,17 +74,18 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 // Two CTAs of three stages per warp fill an SM's shared memory with 128 KB of copies in flight; three
 // CTAs of two stages have 96 KB and were slower (one sequence of 131071 tokens: 87 us, 100 us) or no faster.
-constexpr int kCtasPerSm = 2;
 constexpr float kLn2 = 0.69314718055994531f;
 
+constexpr int kRecTokens = 8192, kRecStages = 2;
 template <int D, int TYPE>
 struct Geo {
   static constexpr bool kRecords = TYPE == SR_PAGE_INT4;
   static constexpr int kRowBytes = D * (TYPE == SR_PAGE_BF16 ? 2 : 1);   // a token's keys (or values) of one head
   static constexpr int kChunks = kRowBytes / 16;
   // tokens per warp and tile: 4 KB of keys, 4 KB of values; of records, 2304 bytes each
-  static constexpr int KT = kRecords ? 4096 / D : 4096 / kRowBytes;
-  static constexpr int kStages = kRecords ? 5 : 3;
+  static constexpr int KT = kRecords ? kRecTokens / D : 4096 / kRowBytes;
+  static constexpr int kCtasPerSm = 2;
+  static constexpr int kStages = kRecords ? kRecStages : 3;
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   // Whether the warps take their tiles in step. Nothing in them depends on it, but warps that drift apart
@@ -207,7 +208,7 @@ struct SharedHead {
   float ml[kWarps][8][2];               // each warp's maximum and sum of eight heads, while warps merge
   int last;                             // this CTA is the last of its item's to arrive
   int abort;                            // a copy never came: err_word tells, the outputs are void
-  uint64_t full[kWarps][6];             // 4-bit pages: a stage's copies have landed
+  uint64_t full[kWarps][8];             // 4-bit pages: a stage's copies have landed
 };
 
 // A place on the line of tiles. Each item takes kItemCost units before its tiles:
@@ -237,7 +238,7 @@ __device__ __forceinline__ void cursor_seq(Cursor& c, const SharedHead& s) {
   c.tiles = (c.len + CT - 1) / CT;
 }
 template <int CT>
-__device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int n_kv, int64_t& left) {
+__device__ __forceinline__ void cursor_next(Cursor& c, const SharedHead& s, int n_kv, int32_t& left) {
   // left: units of this CTA's stretch from the cursor's tile on
   --left;
   if (++c.tile < c.tiles) return;
@@ -346,10 +347,10 @@ __device__ __noinline__ void join_parts(const PagedAttnParams& p, int first, int
 }
 
 template <int D, int TYPE, int NT, bool MASS>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtasPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using G = Geo<D, TYPE>;
   constexpr int kStages = G::kStages;
-  static_assert(kStages <= 6, "more stages than barriers");
+  static_assert(kStages <= 8, "more stages than barriers");
   extern __shared__ __align__(128) uint8_t smem[];
   SharedHead& sh = *reinterpret_cast<SharedHead*>(smem + G::kStageArea);
   grid_dep_launch_dependents();
@@ -423,18 +424,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   if (MASS && blockIdx.x == 0)
     for (int i = threadIdx.x; i <= n; i += kThreads) p.unit0[i] = sh.cum[i];
   if (T == 0) return;
-  int64_t u0, left, share = 0, rest = 0;   // first unit and units of the stretch
+  int64_t u0, left64, share = 0, rest = 0;   // first unit and units of the stretch
   int cut = 0;                             // pieces of each item of the stretch, where all have as many
   const int64_t bound = max(T * G::kWhole, T * 16 + p.whole_extra);
   if (sh.longest * p.whole_cost <= bound) {
-    // whole items; left == 0: none but empty ones
+    // whole items; left64 == 0: none but empty ones
     auto start = [&](int item) {
       const int i = item / n_kv;
       return i < n ? sh.cum[i] + (item - i * n_kv) * seq_units<G::CT>(sh.len[i], 1) : T;
     };
     u0 = start(me * p.each);
-    left = start((me + 1) * p.each) - u0;
-    if (left == 0) return;
+    left64 = start((me + 1) * p.each) - u0;
+    if (left64 == 0) return;
   } else if (p.pieces > 1 && (sh.longest + 2 * p.pieces) * p.cut_cost <= bound) {
     // one of `pieces` equal pieces of an item, as far as it has tiles
     const int item = me / p.pieces, i = item / n_kv;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     if (x >= cut) return;
     const int32_t t0 = x * tiles / cut;
     u0 = sh.cum[i] + (item - i * n_kv) * static_cast<int64_t>(tiles + kItemCost) + kItemCost + t0;
-    left = (x + 1) * tiles / cut - t0;
+    left64 = (x + 1) * tiles / cut - t0;
   } else {
     // CTAs that work: each gets one unit at least, so that all between an item's first and last have a part of it
     const int64_t ctas = min(static_cast<int64_t>(gridDim.x >> p.spread_log2), T);
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     share = div_pos(T, ctas);
     rest = T - share * ctas;
     u0 = me * share + min(static_cast<int64_t>(me), rest);
-    left = share + (me < rest ? 1 : 0);
+    left64 = share + (me < rest ? 1 : 0);
   }
   Cursor comp;
   {
@@ -470,11 +471,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     comp.h = static_cast<int>(div_pos(within, units));
     const int32_t unit = static_cast<int32_t>(within - static_cast<int64_t>(comp.h) * units);
     comp.tile = max(unit - kItemCost, 0);
-    left -= max(kItemCost - unit, 0);
+    left64 -= max(kItemCost - unit, 0);
   }
+  // of at most 2^36 units (256 sequences of 2^24 tokens, 1024 heads) a CTA's stretch has fewer than 2^31
+  int32_t left = static_cast<int32_t>(left64);
   if (left <= 0) return;    // nothing but the units before an item
   Cursor load = comp;
-  int64_t left_load = left;
+  int32_t left_load = left;
   const uint32_t stage0 = smem_u32(smem) + warp * kStages * G::kStageBytes;
   uint32_t bad = 0;       // bit stage * kGroups + group: the group's page is none of the pool's
   const int64_t row_pitch = static_cast<int64_t>(p.kv_heads) * G::kRowBytes;
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   int32_t page[G::kGroups];
   // Records: lane g fetches and copies group g's keys, lane kGroups + g its values.
   const int my_group = lane % G::kGroups, my_half = lane / G::kGroups;
+  [[maybe_unused]] const int32_t page_records = p.kv_heads * (c.page_tokens >> 4);
   [[maybe_unused]] uint32_t phases = 0;           // bit of a stage: the parity its copies complete next
   auto fetch_pages = [&] {
     if constexpr (G::kRecords) {
@@ -524,8 +528,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
     }
     __syncwarp();
     if (good) {
-      const int32_t slot = tok - page_of_group(tok >> 4, c.magic) * c.page_tokens;
-      const int64_t at = record_at(page[0], slot, kv_head(load.h * S + sub), p.kv_heads, c.page_tokens, D);
+      // records before this one: of the pages before, of the heads before, of the page
+      const int32_t in_page = (tok >> 4) - page_of_group(tok >> 4, c.magic) * (c.page_tokens >> 4);
+      const int64_t at = (static_cast<int64_t>(page[0]) * page_records + kv_head(load.h * S + sub) * (c.page_tokens >> 4) + in_page) *
+                         record_bytes(D);
       copy_bulk(stage0 + stage * G::kStageBytes + my_half * G::kHalfBytes + my_group * record_bytes(D),
                 static_cast<const char*>(my_half == 0 ? c.k_pages : c.v_pages) + at, record_bytes(D), bar, policy);
     }
@@ -582,6 +588,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) issue(s);
 
+  // 4 bits: products with 128 instead of shifts, since the pipe that shifts also masks and permutes, and is the one that
+  // bounds this kernel
+  [[maybe_unused]] uint32_t shift7;
+  asm volatile("mov.u32 %0, 128;" : "=r"(shift7));
+  [[maybe_unused]] const DecodeMasks masks = decode_masks();
   // ---- the items of this stretch, one after the other
   int stage = 0;
   const int j4 = lane % 4, r8 = lane / 4;
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
   while (left > 0) {
     const int item_i = comp.i, comp_h = comp.h, item_h = comp_h * S + sub;
     const int32_t first_tile = comp.tile, tiles = comp.tiles;
-    const int32_t end_tile = static_cast<int32_t>(min(static_cast<int64_t>(tiles), first_tile + left));
+    const int32_t end_tile = min(tiles, first_tile + left);
     const int32_t len = comp.len;
     const int64_t item_u = sh.cum[item_i] + static_cast<int64_t>(comp.h) * (tiles + kItemCost) + kItemCost;   // its first tile
     // log2-scaled scores = product * xs, of this lane's heads 8 t + 2 j4 and the next
@@ -744,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 uint32_t lo[4], hi[4];
-                decode_word(lo, a[2 * y], scale_pair(__byte_perm(sc[0][ch / 2], 0, pick + y * 0x0202u) << 7));
-                decode_word(hi, a[2 * y + 1], scale_pair(__byte_perm(sc[1][ch / 2], 0, pick + y * 0x0202u) << 7));
+                decode_word(lo, a[2 * y], scale_pair(__byte_perm(sc[0][ch / 2], 0, pick + y * 0x0202u) * shift7), masks);
+                decode_word(hi, a[2 * y + 1], scale_pair(__byte_perm(sc[1][ch / 2], 0, pick + y * 0x0202u) * shift7), masks);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                   mma16816<TYPE>(s[g][t], lo[0], hi[0], lo[1], hi[1], qb[t][2 * (ch + y)][0], qb[t][2 * (ch + y)][1]);
@@ -881,16 +892,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
           // a transposed 16-bit element is four neighbouring dims of one key, so that a decoded pair is one dim of two
           // keys: a product's rows 0-7 are the dims 4 r + 0 (or 2) of the chunk, rows 8-15 the next ones. Tokens that are
           // not there, or whose record is not, get a scale of zero.
-          const uint32_t pick = 0x0400u + (r8 >> 2) * 0x0101u;
+          const uint32_t pick = 0x4240u + (r8 >> 2) * 0x0101u;     // of a word's four scales the two of this lane's blocks
 #pragma unroll
           for (int g = 0; g < G::kGroups; ++g) {
             const uint32_t rec = vs + g * record_bytes(D);
-            uint32_t sc[2][2 * (D / 64)], keep_scale[2];
+            uint32_t sc[2][2 * (D / 64)];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               load_words(sc[x], rec + 8 * D + (2 * j4 + 8 * x) * (D / 16));
-              const int left_here = live[g] - 2 * j4 - 8 * x;
-              keep_scale[x] = left_here >= 2 ? 0x7F807F80u : left_here == 1 ? 0x00007F80u : 0u;
+              if (live[g] != 16) {
+#pragma unroll
+                for (int y = 0; y < 2 * (D / 64); ++y)
+                  if (live[g] <= 2 * j4 + 8 * x + y / (D / 64)) sc[x][y] = 0;
+              }
+#pragma unroll
+              for (int y = 0; y < 2 * (D / 64); ++y) sc[x][y] = __byte_perm(sc[x][y], 0, pick) * shift7;
             }
 #pragma unroll
             for (int ch = 0; ch < D / 32; ch += 2) {
@@ -900,10 +916,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attn_kernel(const 
               for (int y = 0; y < 2; ++y) {
                 uint32_t v0[4], v1[4];
                 auto pair_of = [&](int x) {
-                  return scale_pair(__byte_perm(sc[x][ch / 2], sc[x][D / 64 + ch / 2], pick + y * 0x0202u) << 7 & keep_scale[x]);
+                  return scale_pair(__byte_perm(sc[x][ch / 2], sc[x][D / 64 + ch / 2], y == 0 ? 0x5410 : 0x7632));
                 };
-                decode_word(v0, a[2 * y], pair_of(0));
-                decode_word(v1, a[2 * y + 1], pair_of(1));
+                decode_word(v0, a[2 * y], pair_of(0), masks);
+                decode_word(v1, a[2 * y + 1], pair_of(1), masks);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                   mma16816<TYPE>(o[t][2 * (ch + y)], v0[0], v0[1], v1[0], v1[1], w[g][t][0], w[g][t][1]);
@@ -1263,7 +1279,7 @@ constexpr int kSmem = Geo<D, TYPE>::kStageArea + static_cast<int>(sizeof(SharedH
 
 template <int D, int TYPE, int NT>
 cudaError_t prepare() {
-  static_assert(kCtasPerSm * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "the CTAs of an SM do not fit");
+  static_assert(Geo<D, TYPE>::kCtasPerSm * (kSmem<D, TYPE> + 1024) <= 228 * 1024, "the CTAs of an SM do not fit");
   const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE, NT, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, TYPE>);
   if (e != cudaSuccess) return e;
@@ -1278,7 +1294,7 @@ cudaError_t launch(const PagedAttnParams& p0, cudaStream_t st) {
   p.spread = kSpread;
   p.spread_log2 = kSpreadLog2;
   while (p.c.n_kv % p.spread) p.spread /= 2, --p.spread_log2;
-  const int ctas = std::min(kCtasPerSm * sm_count(), kMaxPagedCtas) / p.spread * p.spread;
+  const int ctas = std::min(G::kCtasPerSm * sm_count(), kMaxPagedCtas) / p.spread * p.spread;
   const int slots = ctas >> p.spread_log2, items = p.b.n * (p.c.n_kv >> p.spread_log2);
   p.each = (items + slots - 1) / slots;
   p.whole_cost = 16ll * p.each * slots;

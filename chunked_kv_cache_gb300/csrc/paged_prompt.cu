@@ -361,7 +361,7 @@ struct Source {
 };
 // Decodes piece i into rows chunk * 32 .. of a tile.
 template <int D, int TYPE>
-__device__ __forceinline__ void store_raw(const Raw<D, TYPE>& v, int i, uint32_t tile, int chunk, int lane) {
+__device__ __forceinline__ void store_raw(const Raw<D, TYPE>& v, int i, uint32_t tile, int chunk, int lane, const DecodeMasks& masks) {
   constexpr int kPer = Raw<D, TYPE>::kVec / 2;
   const int x = i / kPer, y = i % kPer;
   const uint4 z = v.x[i];
@@ -371,7 +371,7 @@ __device__ __forceinline__ void store_raw(const Raw<D, TYPE>& v, int i, uint32_t
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t e[4];
-      decode_word(e, word[q], q < 2 ? s0 : s1);
+      decode_word(e, word[q], q < 2 ? s0 : s1, masks);
       store16(tile + piece_at<D>(chunk * 32 + x * 16 + (lane & 15), (2 * y + lane / 16) * 4 + q), make_uint4(e[0], e[1], e[2], e[3]));
     }
   } else if constexpr (TYPE == SR_PAGE_E4M3) {
@@ -633,16 +633,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
   {
     if (threadIdx.x < p.n) setup->len[threadIdx.x] = seq_length(p, threadIdx.x);
     __syncthreads();
-    for (int x = threadIdx.x; x < p.blocks; x += kThreads) {
-      const int lo = p.n == 1 ? 0 : seq_of_block(p, x);
+    for (int x0 = warp * 32; x0 < p.blocks; x0 += kThreads) {
+      const int x = min(x0 + lane, p.blocks - 1), lo = p.n == 1 ? 0 : seq_of_block(p, x);
       Block k;
       k.i = lo;
       k.b = x - p.blk0[lo];
       set_block(p, k, setup->len[lo]);
-      if (k.steps > 0)
-        atomicAdd(&setup->per_head[lo], static_cast<unsigned long long>(units_of(k)));
-      else
-        setup->none = 1;
+      // one addition for a warp's blocks of a sequence: on shared memory 64 bits are added one after the other
+      const uint32_t same = __match_any_sync(0xffffffffu, lo);
+      const uint32_t units = __reduce_add_sync(same, x0 + lane < p.blocks ? static_cast<uint32_t>(units_of(k)) : 0u);
+      if (lane == __ffs(same) - 1) atomicAdd(&setup->per_head[lo], static_cast<unsigned long long>(units));
+      if (k.steps == 0) setup->none = 1;
     }
     __syncthreads();
     for (int x = setup->none ? blockIdx.x : p.blocks; x < p.blocks; x += gridDim.x) {
@@ -830,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             wait_drain(&bars->kv_full[(n - k) % C::kStages], ((n - k) / C::kStages) & 1u, kTimeoutNs);
     } else {
       // a share's bytes are on their way in registers: as soon as one of them is stored the next share's follows it
+      const DecodeMasks masks = decode_masks();
       Raw<D, TYPE> raw;
       Source<D, TYPE> from;
       Share r;
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         const uint32_t tile = skv + at % C::kStages * C::kTileBytes;
 #pragma unroll
         for (int i = 0; i < Raw<D, TYPE>::kVec; ++i) {
-          store_raw<D, TYPE>(raw, i, tile, chunk, lane);
+          store_raw<D, TYPE>(raw, i, tile, chunk, lane, masks);
           from.load(raw, i, p.kv_heads, lane);
         }
         note(mine, chunk, mine.watched() ? clean_share<D, true>(mine, tile, chunk, lane) : 0);

@@ -28,6 +28,21 @@ __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
+// (x & mask) | bits in one instruction: both constants from registers, since it has room for one of its own
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+struct DecodeMasks {
+  uint32_t lo, hi, in16, in1;
+};
+__device__ __forceinline__ DecodeMasks decode_masks() {
+  DecodeMasks m;
+  asm volatile("mov.u32 %0, 0x001E001E; mov.u32 %1, 0x01E001E0; mov.u32 %2, 0x4C004C00; mov.u32 %3, 0x3C003C00;"
+               : "=r"(m.lo), "=r"(m.hi), "=r"(m.in16), "=r"(m.in1));
+  return m;
+}
 // What a decoding needs of a pair of scales.
 struct ScalePair {
   uint32_t s, off16, off1;
@@ -36,12 +51,12 @@ __device__ __forceinline__ ScalePair scale_pair(uint32_t s) {
   return {s, half2_mul(s, 0xCC10CC10u), half2_mul(s, 0xBD00BD00u)};     // -16.25 s, -1.25 s
 }
 // y[i]: the i-th value of the word's low unit and of its high one.
-__device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const ScalePair& s) {
+__device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const ScalePair& s, const DecodeMasks& m) {
   const uint32_t z = __byte_perm(w, 0, 0x2301);
-  y[0] = half2_fma((w & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
-  y[1] = half2_fma((w & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
-  y[2] = half2_fma((z & 0x001E001Eu) | 0x4C004C00u, s.s, s.off16);
-  y[3] = half2_fma((z & 0x01E001E0u) | 0x3C003C00u, s.s, s.off1);
+  y[0] = half2_fma(and_or(w, m.lo, m.in16), s.s, s.off16);
+  y[1] = half2_fma(and_or(w, m.hi, m.in1), s.s, s.off1);
+  y[2] = half2_fma(and_or(z, m.lo, m.in16), s.s, s.off16);
+  y[3] = half2_fma(and_or(z, m.hi, m.in1), s.s, s.off1);
 }
 constexpr float kDecoded = 32.f;      // a value is so many times what decode_word leaves
 
