@@ -76,16 +76,17 @@ constexpr int kThreads = kWarps * 32;
 // CTAs of two stages have 96 KB and were slower (one sequence of 131071 tokens: 87 us, 100 us) or no faster.
 constexpr float kLn2 = 0.69314718055994531f;
 
-constexpr int kRecTokens = 8192, kRecStages = 2;
 template <int D, int TYPE>
 struct Geo {
   static constexpr bool kRecords = TYPE == SR_PAGE_INT4;
   static constexpr int kRowBytes = D * (TYPE == SR_PAGE_BF16 ? 2 : 1);   // a token's keys (or values) of one head
   static constexpr int kChunks = kRowBytes / 16;
-  // tokens per warp and tile: 4 KB of keys, 4 KB of values; of records, 2304 bytes each
-  static constexpr int KT = kRecords ? kRecTokens / D : 4096 / kRowBytes;
-  static constexpr int kCtasPerSm = 2;
-  static constexpr int kStages = kRecords ? kRecStages : 3;
+  // tokens per warp and tile: 4 KB of keys, 4 KB of values; 64 tokens of records
+  static constexpr int KT = kRecords ? 64 : 4096 / kRowBytes;
+  // Records are bound by their decoding: more warps (rows of 64 values), fewer stages (two CTAs, 64 tokens, of 128 values: 3
+  // stages 127.4 us for 32 sequences of 4001 .. 32768 tokens, 2 stages 125.6 us; 32 tokens, 5 stages 148.3 us).
+  static constexpr int kCtasPerSm = kRecords && D == 64 ? 3 : 2;
+  static constexpr int kStages = kRecords && D == 128 ? 2 : 3;
   static constexpr int CT = kWarps * KT;           // tokens per tile
   static constexpr int kGroups = KT / 16;          // 16-token groups: a group never crosses a page
   // Whether the warps take their tiles in step. Nothing in them depends on it, but warps that drift apart

@@ -5,6 +5,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "sr_device.cuh"
 #include "sr_kernels.h"
@@ -68,11 +69,6 @@ constexpr uint32_t kScaleNan = 255;
 __device__ __forceinline__ float scale_value(uint32_t b) {
   return b == kScaleNan ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 20) * 0x1p112f;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 // The scale's byte of 16 values of which `top` is the largest |x|. Everything is decided as in exact arithmetic: x
 // has 8 significant bits and a border (7 times a number of 5 bits) at most 8, so that a quotient is on a border or off by
 // more than 2^-9 of itself; the factor is a little above 1/7, so that one on a border goes up.
@@ -89,60 +85,61 @@ __device__ __forceinline__ float scale_factor(uint32_t b) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale_value(b)));
   return r * (1.f + 0x1p-19f);
 }
-// eight values of bf16, times 2^-e
-__device__ __forceinline__ void load_values(float (&f)[8], const uint4& x, float inv_exp) {
+__device__ __forceinline__ float two_to(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }   // |e| <= 126
+// The largest |x| of eight values of bf16, as bf16 bits: their order is the numbers', NaN last.
+__device__ __forceinline__ uint32_t top_of(const uint4& x) {
+  const uint32_t t = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(t & 0xFFFFu, t >> 16);
+}
+// Codes of eight values of bf16, factor 2^-e / s: two units of four, each turned left by one bit. The sum with
+// 1.5 * 2^23 + 8 leaves the rounded quotient plus 8 behind the bits of 1.5 * 2^23, which the products leave in the word too
+// and one subtraction takes out. CLAMP: a quotient may lie outside of -8 .. 7.
+template <bool CLAMP>
+__device__ __forceinline__ uint32_t codes_of(const uint4& x, float factor) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(in[i] << 16) * inv_exp;
-    f[2 * i + 1] = __uint_as_float(in[i] & 0xFFFF0000u) * inv_exp;
-  }
-}
-__device__ __forceinline__ float top_of(const float (&f)[8]) {
-  float t = fabsf(f[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) t = max_nan(t, fabsf(f[i]));
-  return t;
-}
-// Codes of eight values: two units of four, each turned left by one bit. The sum with 1.5 * 2^23 + 8 leaves the rounded
-// quotient plus 8 in the lowest bits.
-__device__ __forceinline__ uint32_t codes_of(const float (&f)[8], float factor) {
-  uint32_t w = 0;
+  constexpr float kMagic = 12582920.f;
+  uint32_t w = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(f[i] * factor, -8.f), 7.f) + 12582920.f;
-    w |= (__float_as_uint(q) & 15u) << (4 * i);
+    const float f = __uint_as_float(i % 2 ? in[i / 2] & 0xFFFF0000u : in[i / 2] << 16);
+    const float q = CLAMP ? fminf(fmaxf(f * factor, -8.f), 7.f) + kMagic : fmaf(f, factor, kMagic);
+    w += __float_as_uint(q) * (1u << (4 * i));
   }
   return (w << 1 & 0xFFFEFFFEu) | (w >> 15 & 0x00010001u);
 }
-// the eight values of such codes, as bf16
+// The eight values of such codes, as bf16, exactly: a mask puts a code c into the fraction of 1 (1 + c / 64), and a fused
+// product and sum with 64 s 2^e leaves (c - 8) s 2^e, of at most 7 significant bits.
 __device__ __forceinline__ uint4 values_of(uint32_t w, float scale) {
-  w = (w >> 1 & 0x7FFF7FFFu) | (w << 15 & 0x80008000u);
-  uint32_t out[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = static_cast<float>(static_cast<int>(w >> (8 * i) & 15u) - 8) * scale;
-    const float b = static_cast<float>(static_cast<int>(w >> (8 * i + 4) & 15u) - 8) * scale;
-    out[i] = pack_bf16x2(a, b);
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+  const uint32_t s = pack_bf16x2(scale * 64.f, scale * 64.f), off = pack_bf16x2(scale * -72.f, scale * -72.f);
+  const uint32_t z = __byte_perm(w, 0, 0x2301);
+  auto pair = [&](uint32_t x) {         // of the low unit and the high one
+    uint32_t y;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"((x & 0x001E001Eu) | 0x3F803F80u), "r"(s), "r"(off));
+    return y;
+  };
+  const uint32_t a = pair(w), b = pair(w >> 4), c = pair(z), d = pair(z >> 4);
+  return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(c, d, 0x7632));
 }
 
 // How a warp's lanes share rows of records: four lanes a chunk of 32 values of a token (64 bytes of bf16, 16 of codes),
-// eight chunks in all: of 8 neighbouring tokens, whose codes lie together, or, where there are fewer, of neighbouring
-// chunks of 4, 2 or 1. f(row, chunk of the row, the lane's place in it) for every chunk of `rows` rows; the lanes of
-// a chunk always call it together, a warp's in step, with a row of -1 where there is none.
-template <typename F>
-__device__ __forceinline__ void each_chunk(int rows, int chunks, int warp, int warps, int lane, F&& f) {
-  const int tokens_log2 = rows >= 8 ? 3 : rows >= 4 ? 2 : rows >= 2 ? 1 : 0;
-  const int across = 8 >> tokens_log2;                       // chunks of a row that a warp takes at once
-  const int steps = (chunks + across - 1) / across, blocks = (rows + (1 << tokens_log2) - 1) >> tokens_log2;
-  const int tok = (lane >> 2) & ((1 << tokens_log2) - 1), ch = lane >> 2 >> tokens_log2;
-  for (int u = warp; u < blocks * steps; u += warps) {
-    const int block = u / steps, c = (u - block * steps) * across + ch, r = (block << tokens_log2) + tok;
-    f(r < rows && c < chunks ? r : -1, c, lane & 3);
+// eight chunks at once: of 8 neighbouring tokens, whose codes lie together, or, where there are fewer, of neighbouring
+// chunks of 4, 2 or 1. A warp takes kChunkBatch such steps of its tokens together, all their loads in flight.
+constexpr int kChunkBatch = 4;
+struct ChunkWalk {
+  int tokens_log2, steps, items;       // a row's steps, in batches; batches of all rows
+  __device__ __forceinline__ ChunkWalk(int rows, int chunks) {
+    tokens_log2 = rows >= 8 ? 3 : rows >= 4 ? 2 : rows >= 2 ? 1 : 0;
+    const int across = 8 >> tokens_log2;
+    steps = ((chunks + across - 1) / across + kChunkBatch - 1) / kChunkBatch;
+    items = ((rows + (1 << tokens_log2) - 1) >> tokens_log2) * steps;
   }
-}
+  // of batch `item`: this lane's row and its chunk in the first step; a step is 8 >> tokens_log2 chunks
+  __device__ __forceinline__ void at(int item, int lane, int& row, int& chunk) const {
+    const int block = item / steps, eighth = lane >> 2;
+    row = (block << tokens_log2) + (eighth & ((1 << tokens_log2) - 1));
+    chunk = (item - block * steps) * kChunkBatch * (8 >> tokens_log2) + (eighth >> tokens_log2);
+  }
+};
 
 template <int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendParams p) {
@@ -182,36 +179,50 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
     const int32_t rows = min(p.rows_per_cta, count - r0);
     const int vpr = c.n_kv * c.head_dim / 8;    // vectors per row
     if constexpr (TYPE == SR_PAGE_INT4) {
-      const int cph_log2 = c.head_dim == 128 ? 2 : 1;           // chunks of a head
+      const int cph_log2 = c.head_dim == 128 ? 2 : 1, chunks = c.n_kv << cph_log2;    // chunks of a head, of a row
+      const int lane = threadIdx.x % 32, j = lane & 3, head_bytes = (c.page_tokens >> 4) * record_bytes(c.head_dim);
       const uint4* src[2] = {reinterpret_cast<const uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr,
                              reinterpret_cast<const uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr};
-      each_chunk(rows, c.n_kv << cph_log2, threadIdx.x / 32, kAppendThreads / 32, threadIdx.x % 32, [&](int r, int ch, int j) {
-        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (r >= 0) {
+      const ChunkWalk walk(rows, chunks);
+      const int step = 8 >> walk.tokens_log2;
+      for (int item = threadIdx.x / 32; item < walk.items; item += kAppendThreads / 32) {
+        int r, ch0;
+        walk.at(item, lane, r, ch0);
+        uint4 x[kChunkBatch][2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) x[y] = __ldcs(src[y] + static_cast<int64_t>(r) * vpr + ch * 4 + j);
-        }
-        const int head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
-        const int32_t t = len + r0 + max(r, 0), pg = page_of_group(t >> 4, c.magic);
+        for (int u = 0; u < kChunkBatch; ++u)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            x[u][y] = r < rows && ch0 + u * step < chunks ? __ldcs(src[y] + static_cast<int64_t>(r) * vpr + (ch0 + u * step) * 4 + j)
+                                                          : make_uint4(0, 0, 0, 0);
+        const int32_t t = len + r0 + min(r, rows - 1), pg = page_of_group(t >> 4, c.magic);
         const int32_t slot = t - pg * c.page_tokens;
-        const int64_t rec = r >= 0 ? record_at(table[pg], slot, head, c.n_kv, c.page_tokens, c.head_dim) : 0;
+        const int64_t rec = record_at(table[pg], slot, 0, c.n_kv, c.page_tokens, c.head_dim);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float f[8];
-          const float inv = c.kv_exp && r >= 0 ? exp2f(-static_cast<float>(c.kv_exp[y * c.n_kv + head])) : 1.f;
-          load_values(f, x[y], inv);
-          const float mine = top_of(f);
-          const uint32_t b = scale_byte(max_nan(mine, __shfl_xor_sync(0xffffffffu, mine, 1)));   // of two lanes' 16
-          const uint32_t b2 = __shfl_xor_sync(0xffffffffu, b, 2);
-          if (r >= 0) {
-            uint8_t* at = static_cast<uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + rec;
-            reinterpret_cast<uint32_t*>(at + part * 256 + (slot & 15) * 16)[j] = codes_of(f, scale_factor(b));
-            if (j == 0)
-              *reinterpret_cast<uint16_t*>(at + 8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2) =
-                  static_cast<uint16_t>(b | b2 << 8);
+        for (int u = 0; u < kChunkBatch; ++u) {
+          const int ch = ch0 + u * step, head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
+          const bool there = r < rows && ch < chunks;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float inv = c.kv_exp && there ? two_to(-c.kv_exp[y * c.n_kv + head]) : 1.f;
+            const uint32_t mine = top_of(x[u][y]);
+            const uint32_t top = max(mine, __shfl_xor_sync(0xffffffffu, mine, 1));            // of two lanes' 16
+            const uint32_t b = scale_byte(__uint_as_float(top << 16) * inv);
+            const uint32_t b2 = __shfl_xor_sync(0xffffffffu, b, 2);
+            // Between 2^-14 and the largest scale a quotient is at most 7 * 17 / 16, which rounds to 7.
+            const bool clamp = __any_sync(0xffffffffu, b <= 8 || b >= kScaleTop);
+            const float factor = scale_factor(b) * inv;
+            const uint32_t codes = clamp ? codes_of<true>(x[u][y], factor) : codes_of<false>(x[u][y], factor);
+            if (there) {
+              uint8_t* at = static_cast<uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + rec + static_cast<int64_t>(head) * head_bytes;
+              reinterpret_cast<uint32_t*>(at + part * 256 + (slot & 15) * 16)[j] = codes;
+              if (j == 0)
+                *reinterpret_cast<uint16_t*>(at + 8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2) =
+                    static_cast<uint16_t>(b | b2 << 8);
+            }
           }
         }
-      });
+      }
     } else {
     const uint4* ksrc = reinterpret_cast<const uint4*>(p.k) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
     const uint4* vsrc = reinterpret_cast<const uint4*>(p.v) + static_cast<int64_t>(p.row0[i] + r0) * vpr;
@@ -310,45 +321,76 @@ __global__ void __launch_bounds__(kAppendThreads) paged_read_kernel(const __grid
     return -1;
   };
   if constexpr (TYPE == SR_PAGE_INT4) {
-    const int cph_log2 = c.head_dim == 128 ? 2 : 1;
-    each_chunk(rows, c.n_kv << cph_log2, threadIdx.x / 32, kAppendThreads / 32, threadIdx.x % 32, [&](int r, int ch, int j) {
-      if (r < 0) return;
+    const int cph_log2 = c.head_dim == 128 ? 2 : 1, chunks = c.n_kv << cph_log2;
+    const int lane = threadIdx.x % 32, j = lane & 3, head_bytes = (c.page_tokens >> 4) * record_bytes(c.head_dim);
+    const ChunkWalk walk(rows, chunks);
+    const int step = 8 >> walk.tokens_log2;
+    for (int item = threadIdx.x / 32; item < walk.items; item += kAppendThreads / 32) {
+      int r, ch0;
+      walk.at(item, lane, r, ch0);
+      if (r >= rows) continue;
       int32_t slot = 0;
       const int32_t page = page_at(r, slot);
-      const int head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
-      const int64_t rec = page >= 0 ? record_at(page, slot, head, c.n_kv, c.page_tokens, c.head_dim) : 0;
+      const int64_t rec = page >= 0 ? record_at(page, slot, 0, c.n_kv, c.page_tokens, c.head_dim) : 0;
+      uint32_t w[kChunkBatch][2], b[kChunkBatch][2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint4 out = make_uint4(0, 0, 0, 0);
-        if (page >= 0) {
-          const uint8_t* at = static_cast<const uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + rec;
-          const uint32_t w = reinterpret_cast<const uint32_t*>(at + part * 256 + (slot & 15) * 16)[j];
-          const uint32_t b = at[8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2 + (j >> 1)];
-          out = values_of(w, scale_value(b) * (c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[y * c.n_kv + head])) : 1.f));
+      for (int u = 0; u < kChunkBatch; ++u) {
+        const int ch = ch0 + u * step, head = ch >> cph_log2, part = ch & ((1 << cph_log2) - 1);
+        const int64_t off = rec + static_cast<int64_t>(head) * head_bytes;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const uint8_t* at = static_cast<const uint8_t*>(y == 0 ? c.k_pages : c.v_pages) + off;
+          const bool there = page >= 0 && ch < chunks;
+          w[u][y] = there ? __ldcs(reinterpret_cast<const uint32_t*>(at + part * 256 + (slot & 15) * 16) + j) : 0;
+          b[u][y] = there ? __ldg(at + 8 * c.head_dim + (slot & 15) * (c.head_dim >> 4) + part * 2 + (j >> 1)) : 0;
         }
-        __stcs(dst[y] + static_cast<int64_t>(r) * vpr + ch * 4 + j, out);
       }
-    });
+#pragma unroll
+      for (int u = 0; u < kChunkBatch; ++u) {
+        const int ch = ch0 + u * step, head = ch >> cph_log2;
+        if (ch >= chunks) break;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float scale = scale_value(b[u][y]) * (c.kv_exp ? two_to(c.kv_exp[y * c.n_kv + head]) : 1.f);
+          __stcs(dst[y] + static_cast<int64_t>(r) * vpr + ch * 4 + j, page >= 0 ? values_of(w[u][y], scale) : make_uint4(0, 0, 0, 0));
+        }
+      }
+    }
   } else {
     const int head_shift = c.head_dim == 128 ? 4 : 3;
-    for (int x = threadIdx.x; x < rows * vpr; x += kAppendThreads) {
-      const int r = x / vpr, col = x - r * vpr;
-      int32_t slot = 0;
-      const int32_t page = page_at(r, slot);
-      const int64_t at = (static_cast<int64_t>(page) * c.page_tokens + slot) * vpr + col;
+    using Vec = std::conditional_t<TYPE == SR_PAGE_BF16, uint4, uint2>;
+    for (int x0 = threadIdx.x; x0 < rows * vpr; x0 += kAppendUnroll * kAppendThreads) {
+      Vec in[kAppendUnroll][2];
+      bool held[kAppendUnroll];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint4 out = make_uint4(0, 0, 0, 0);
-        const void* pages = y == 0 ? c.k_pages : c.v_pages;
-        if (page >= 0) {
-          if constexpr (TYPE == SR_PAGE_BF16) {
-            out = __ldcs(static_cast<const uint4*>(pages) + at);
-          } else {
-            const float scale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[y * c.n_kv + (col >> head_shift)])) : 1.f;
-            out = from_e4m3(__ldcs(static_cast<const uint2*>(pages) + at), scale);
-          }
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int x = x0 + u * kAppendThreads, r = x / vpr, col = x - r * vpr;
+        int32_t slot = 0;
+        const int32_t page = x < rows * vpr ? page_at(r, slot) : -1;
+        held[u] = page >= 0;
+        const int64_t at = (static_cast<int64_t>(page) * c.page_tokens + slot) * vpr + col;
+        if (held[u]) {
+          in[u][0] = __ldcs(static_cast<const Vec*>(c.k_pages) + at);
+          in[u][1] = __ldcs(static_cast<const Vec*>(c.v_pages) + at);
         }
-        __stcs(dst[y] + x, out);
+      }
+#pragma unroll
+      for (int u = 0; u < kAppendUnroll; ++u) {
+        const int x = x0 + u * kAppendThreads;
+        if (x >= rows * vpr) break;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint4 out = make_uint4(0, 0, 0, 0);
+          if (held[u]) {
+            if constexpr (TYPE == SR_PAGE_BF16) {
+              out = in[u][y];
+            } else {
+              const float scale = c.kv_exp ? exp2f(static_cast<float>(c.kv_exp[y * c.n_kv + (x % vpr >> head_shift)])) : 1.f;
+              out = from_e4m3(in[u][y], scale);
+            }
+          }
+          __stcs(dst[y] + x, out);
+        }
       }
     }
   }
@@ -888,7 +930,9 @@ int paged_append_rows_per_cta(const PagedView& c, int64_t rows) {
   const int64_t vectors = static_cast<int64_t>(c.n_kv) * c.head_dim / 8;     // of a row
   const int64_t wave = 4ll * sm_count();
   const int64_t ctas = rows * vectors > 16 * wave * kAppendThreads ? 2 * wave : wave;
-  return static_cast<int>(std::max((kAppendThreads + vectors - 1) / vectors, (rows + ctas - 1) / ctas));
+  const int64_t per = std::max((kAppendThreads + vectors - 1) / vectors, (rows + ctas - 1) / ctas);
+  // records: whole steps of 8 tokens, where a CTA has as many
+  return static_cast<int>(c.page_type == SR_PAGE_INT4 && per > 8 ? (per + 7) / 8 * 8 : per);
 }
 
 cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st) {

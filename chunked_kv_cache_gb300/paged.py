@@ -258,22 +258,21 @@ class PagedCache:
         for name, given in (("seqs", seqs), ("first", first)):
             if given is not None and len(given) != n:
                 raise ValueError(f"{len(given)} {name} for {n} sequences")
-        if counts is not None and any(x < 0 for x in counts):
+        if counts is not None and n > 0 and min(counts) < 0:
             raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_read")
         shape = (n if counts is None else sum(counts), self.n_kv_heads, self.head_dim)
-        both = []
-        for name, t in (("k", k), ("v", v)):
-            if t is None:
-                t = torch.empty(shape, dtype=_BF16, device=self.device)
-            else:
-                self._check(name, t, shape)
-            both.append(t)
+        if k is None and v is None:
+            k, v = torch.empty((2, *shape), dtype=_BF16, device=self.device).unbind()
+        else:
+            k, v = (torch.empty(shape, dtype=_BF16, device=self.device) if t is None else t for t in (k, v))
+            self._check("k", k, shape)
+            self._check("v", v, shape)
         ids, at = self._ids(seqs)
         start, start_at = self._ids(first)
         each, each_at = self._ids(counts)
-        self._done(self._lib.sr_paged_read(self.handle, at, start_at, each_at, n, both[0].data_ptr(), both[1].data_ptr(),
+        self._done(self._lib.sr_paged_read(self.handle, at, start_at, each_at, n, k.data_ptr(), v.data_ptr(),
                                            self._stream()), "sr_paged_read")
-        return both[0], both[1]
+        return k, v
 
     def evict(self, budget: int, n_sink: int = 0, n_recent: int = 0, seqs: Sequence[int] | None = None) -> None:
         """Keep at most `budget` tokens per sequence: positions below n_sink, the last n_recent
