@@ -23,7 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsr.so")
 SOURCES = ["attention.cu", "rope_commit.cu", "rope_phase.cu", "sr_api.cu", "sr_noalloc.cu",
-           "paged_api.cu", "paged_attention.cu", "paged_cache.cu", "paged_prompt.cu"]
+           "paged_api.cu", "paged_attention.cu", "paged_attention_bf16.cu", "paged_attention_e4m3.cu",
+           "paged_attention_int4.cu", "paged_cache.cu", "paged_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -105,6 +105,11 @@ sr_status take_seqs(sr_paged_cache* c, const int32_t* seqs, int32_t n, int32_t* 
   return SR_OK;
 }
 
+template <typename T>
+T* ws_at(const sr_paged_cache* c, size_t offset) {
+  return reinterpret_cast<T*>(static_cast<char*>(c->buf.workspace) + offset);
+}
+
 // The rows of a call: row0[0..n] from the sequences' counts.
 sr_status take_counts(const int32_t* n_tokens, int32_t n, int32_t* row0) {
   int64_t rows = 0;
@@ -129,17 +134,32 @@ void share_rows(const int32_t* row0, int32_t n, int32_t rows_per_cta, int32_t* c
   cta0[n] = static_cast<int32_t>(ctas);
 }
 
+void take_heads(const sr_paged_cache* c, sr::PagedView& v, int32_t& kv_heads, uint32_t& head_magic);
+// What all attention calls of a few columns per sequence hand to their launch.
+void attn_params(const sr_paged_cache* c, sr::PagedAttnParams& p, int32_t n, const void* q, void* o, float* lse) {
+  p.b.n = n;
+  p.c = c->view;
+  take_heads(c, p.c, p.kv_heads, p.head_magic);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.items = ws_at<int2>(c, c->layout.items);
+  p.unit0 = ws_at<int64_t>(c, c->layout.unit0);
+  p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
+  p.group_arrivals = p.arrivals + sr::kMaxPagedCtas;
+  p.parts = ws_at<float>(c, c->layout.parts);
+  p.lse2 = ws_at<float>(c, c->layout.lse2);
+  p.scores = ws_at<float>(c, c->layout.scores);
+  p.score_tiles = c->layout.score_tiles;
+  p.part_rows = p.c.group;
+}
+
 // The view's heads as attention takes them: items of at most SR_MAX_PAGED_GROUP query heads.
 void take_heads(const sr_paged_cache* c, sr::PagedView& v, int32_t& kv_heads, uint32_t& head_magic) {
   kv_heads = c->cfg.n_kv_heads;
   v.n_kv = c->cfg.n_heads / v.group;
   const uint32_t parts = static_cast<uint32_t>(v.n_kv / kv_heads);       // of a key/value head's query heads
   head_magic = ((1u << 22) + parts - 1) / parts;                         // exact for heads and parts up to 1024
-}
-
-template <typename T>
-T* ws_at(const sr_paged_cache* c, size_t offset) {
-  return reinterpret_cast<T*>(static_cast<char*>(c->buf.workspace) + offset);
 }
 
 }  // namespace
@@ -274,20 +294,7 @@ sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, 
   if (mass_decay >= 0.f && !c->buf.token_mass) return SR_ERR_STATE;
   st = on_device(c);
   if (st != SR_OK) return st;
-  p.b.n = n;
-  p.c = c->view;
-  take_heads(c, p.c, p.kv_heads, p.head_magic);
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.o = static_cast<__nv_bfloat16*>(o);
-  p.lse = lse;
-  p.items = ws_at<int2>(c, c->layout.items);
-  p.unit0 = ws_at<int64_t>(c, c->layout.unit0);
-  p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
-  p.group_arrivals = p.arrivals + sr::kMaxPagedCtas;
-  p.parts = ws_at<float>(c, c->layout.parts);
-  p.lse2 = ws_at<float>(c, c->layout.lse2);
-  p.scores = ws_at<float>(c, c->layout.scores);
-  p.score_tiles = c->layout.score_tiles;
+  attn_params(c, p, n, q, o, lse);
   p.mass_decay = mass_decay;
   return sr::launch_paged_attention(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
 }
@@ -304,6 +311,21 @@ sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, cons
   if (st != SR_OK) return st;
   if (p.row0[n] == 0) return SR_OK;
   if (!q || !o) return SR_ERR_INVALID_ARG;
+  // A few new tokens each, whose heads are columns of one product: the kernel for single tokens, which is bound by the one
+  // read of the cache, where the other fills 128 rows of a tile whatever there is.
+  int32_t most = 0;
+  for (int i = 0; i < n; ++i) most = std::max(most, p.row0[i + 1] - p.row0[i]);
+  if (static_cast<int64_t>(most) * c->view.group <= SR_MAX_PAGED_GROUP) {
+    sr::PagedRowsParams r;
+    attn_params(c, r, n, q, o, lse);
+    std::memcpy(r.b.id, p.id, sizeof(int32_t) * static_cast<size_t>(n));
+    std::memcpy(r.row0, p.row0, sizeof(int32_t) * (static_cast<size_t>(n) + 1));
+    r.part_rows = most * c->view.group;
+    r.causal = causal != 0;
+    r.group_magic = (65536u + static_cast<uint32_t>(r.c.group) - 1u) / static_cast<uint32_t>(r.c.group);
+    r.mass_decay = -1.f;
+    return sr::launch_paged_rows(r, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
+  }
   p.n = n;
   p.causal = causal != 0;
   p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;

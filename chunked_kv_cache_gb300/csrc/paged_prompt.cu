@@ -425,35 +425,16 @@ __device__ __forceinline__ uint32_t clean_share(const Share& r, uint32_t tile, i
 }
 
 // -------------------------------------------------------------- values that are no finite numbers, seen by some rows only
-// Value `dim` of token t (16-bit floats of the pages' type, fp16 for those of fewer bits), as the tiles would hold it.
-template <int D, int TYPE>
-__device__ __forceinline__ float page_value(const PromptParams& p, const void* pages, int32_t seq, int32_t t, int head, int dim) {
-  const PagedView& c = p.c;
-  const int32_t pg = page_of_group(t >> 4, c.magic), slot = t - pg * c.page_tokens;
-  const int32_t page = __ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg);
-  if (page < 0 || page >= c.n_pages) return 0.f;
-  if constexpr (TYPE == SR_PAGE_INT4) {
-    const uint8_t* rec = static_cast<const uint8_t*>(pages) + record_at(page, slot, head, p.kv_heads, c.page_tokens, D);
-    const uint32_t u = *reinterpret_cast<const uint16_t*>(rec + (dim / 32) * 256 + (slot & 15) * 16 + (dim % 32) / 4 * 2);
-    const int code = static_cast<int>(((u >> 1 | u << 15) & 0xFFFFu) >> (4 * (dim % 4)) & 15u);
-    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(rec[8 * D + (slot & 15) * (D / 16) + dim / 16] << 7)));
-    return static_cast<float>(code - 8) * s / kDecoded;
-  } else {
-    const int64_t at = ((static_cast<int64_t>(page) * c.page_tokens + slot) * p.kv_heads + head) * D + dim;
-    if constexpr (TYPE == SR_PAGE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(pages)[at]);
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at], __NV_E4M3)));
-  }
-}
 // Adds to a row of sums (in memory, each times `to`) the weight of token t times its values that are no finite numbers.
 // Runs only where such values lie among a block's new tokens; the weight is computed again, from the query row and the key.
 template <int D, int TYPE>
 __device__ __noinline__ void add_odd(const PromptParams& p, float* o, int32_t seq, int32_t t, int head, const __nv_bfloat16* q,
                                      float scale, float m, float to) {
   float x = 0.f;
-  for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), page_value<D, TYPE>(p, p.c.k_pages, seq, t, head, d), x);
+  for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(q[d]), page_value<D, TYPE>(p.c, p.kv_heads, p.c.k_pages, seq, t, head, d), x);
   const float w = ex2_approx(x * scale - (m == -INFINITY ? 0.f : m)) * to;
   for (int d = 0; d < D; ++d) {
-    const float v = page_value<D, TYPE>(p, p.c.v_pages, seq, t, head, d);
+    const float v = page_value<D, TYPE>(p.c, p.kv_heads, p.c.v_pages, seq, t, head, d);
     if (!(fabsf(v) < INFINITY)) o[d] = fmaf(w, v, o[d]);
   }
 }

@@ -12,6 +12,7 @@
 namespace sr {
 
 constexpr int kMaxPagedSeqs = SR_MAX_PAGED_SEQS;
+constexpr int kPagedItemCost = 2;    // units of the line of tiles before an item's tiles (paged_attention.cuh)
 constexpr int kMaxPromptCtas = 160;  // most CTAs a launch over several new tokens per sequence may have
 constexpr int kMaxPagedCtas = 512;   // most CTAs an attention launch may have (partial result slots)
 
@@ -107,6 +108,7 @@ struct PagedAttnParams {
   int32_t* arrivals;       // [kMaxPagedCtas] parts, or groups of parts, of an item that are done; left at zero
   int32_t* group_arrivals; // [2 * kMaxPagedCtas]
   float* parts;
+  int32_t part_rows;       // rows that a partial result has room for
   float* lse2;
   float* scores;
   int64_t score_tiles;
@@ -125,6 +127,13 @@ struct PagedAttnParams {
   bool drop_scores;        // the weights' launch drops the scores from L2
   float mass_decay;
   PagedBatch b;
+};
+
+// Attention of a few new tokens per sequence, whose heads fit the columns of one product.
+struct PagedRowsParams : PagedAttnParams {
+  int32_t causal;
+  uint32_t group_magic;            // r / group = r * group_magic >> 16 for r < 128
+  int32_t row0[kMaxPagedSeqs + 1]; // first row of each sequence
 };
 
 struct ReadParams {
@@ -172,6 +181,7 @@ struct EvictParams {
 
 cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st);
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t st);
 cudaError_t launch_paged_read(const ReadParams& p, cudaStream_t st);
 cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st);
 cudaError_t paged_prompt_prepare(int head_dim, int page_type);

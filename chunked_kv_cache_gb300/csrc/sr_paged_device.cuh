@@ -2,9 +2,13 @@
 // them. Internal to libsr.so.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include <cstdint>
+
+#include "sr_paged.h"
 
 namespace sr {
 
@@ -59,5 +63,25 @@ __device__ __forceinline__ void decode_word(uint32_t (&y)[4], uint32_t w, const 
   y[3] = half2_fma(and_or(z, m.hi, m.in1), s.s, s.off1);
 }
 constexpr float kDecoded = 32.f;      // a value is so many times what decode_word leaves
+
+
+// Value `dim` of token t (16-bit floats of the pages' type, fp16 for those of fewer bits), as the tiles would hold it.
+template <int D, int TYPE>
+__device__ __forceinline__ float page_value(const PagedView& c, int32_t kv_heads, const void* pages, int32_t seq, int32_t t, int head, int dim) {
+  const int32_t pg = page_of_group(t >> 4, c.magic), slot = t - pg * c.page_tokens;
+  const int32_t page = __ldg(c.table + static_cast<int64_t>(seq) * c.max_pages + pg);
+  if (page < 0 || page >= c.n_pages) return 0.f;
+  if constexpr (TYPE == SR_PAGE_INT4) {
+    const uint8_t* rec = static_cast<const uint8_t*>(pages) + record_at(page, slot, head, kv_heads, c.page_tokens, D);
+    const uint32_t u = *reinterpret_cast<const uint16_t*>(rec + (dim / 32) * 256 + (slot & 15) * 16 + (dim % 32) / 4 * 2);
+    const int code = static_cast<int>(((u >> 1 | u << 15) & 0xFFFFu) >> (4 * (dim % 4)) & 15u);
+    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(rec[8 * D + (slot & 15) * (D / 16) + dim / 16] << 7)));
+    return static_cast<float>(code - 8) * s / kDecoded;
+  } else {
+    const int64_t at = ((static_cast<int64_t>(page) * c.page_tokens + slot) * kv_heads + head) * D + dim;
+    if constexpr (TYPE == SR_PAGE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(pages)[at]);
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pages)[at], __NV_E4M3)));
+  }
+}
 
 }  // namespace sr

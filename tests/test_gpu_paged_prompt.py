@@ -163,6 +163,48 @@ def test_numbers_that_are_none_stay_behind_the_mask(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,heads,kv,length", [(64, 4, 2, 200), (128, 6, 2, 63), (128, 4, 1, 1500), (64, 1, 1, 7)])
+def test_numbers_that_are_none_stay_behind_the_mask_of_a_few_rows(kind, d, heads, kv, length):
+    """The same for drafts of 4 tokens; an infinity too, where pages hold it."""
+    p = _pair(kind, heads, kv, d, 16, 2, 100, seed=9)
+    k, v, q = p.randn(length, kv, d), p.randn(length, kv, d), p.randn(4, heads, d)
+    v[length - 2] = float("nan")
+    k[length - 1] = float("nan")
+    v[length - 3, :, 5] = float("inf")
+    p.cache.append(k, v, counts=[length, 0])
+    o = p.cache.prompt_attention(q, [4, 0])
+    nan, inf = torch.isnan(o), torch.isinf(o)
+    assert not nan[:2].any() and nan[2:].all()
+    assert not inf[0].any()
+    if kind == "bf16":
+        assert (o[1, :, 5] == float("inf")).all() and inf[1].sum() == heads
+    else:
+        assert not inf[1].any()                    # these pages saturate
+    o = p.cache.prompt_attention(q, [4, 0], causal=False)
+    assert torch.isnan(o).all()
+    p.ok()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,kv,d,page,m", [(4, 4, 64, 16, 16), (32, 8, 128, 64, 4), (8, 1, 64, 48, 2), (5, 1, 128, 16, 3), (34, 2, 128, 32, 1),
+                                               (3, 1, 64, 32, 5), (10, 2, 128, 128, 3)])
+def test_a_few_rows_of_every_length(heads, kv, d, page, m, kind, causal):
+    """Drafts whose heads fit one product: every number of rows up to m, lengths of one tile and several, empty ones."""
+    n = len(LENGTHS)
+    p = _pair(kind, heads, kv, d, page, n + 1, -(-2100 // page), seed=heads + d)
+    seqs = p.rng.permutation(n + 1).tolist()
+    p.append(list(range(n + 1)), LENGTHS + [2000])
+    counts = [int(x) for x in p.rng.integers(0, m + 1, n + 1)]
+    counts[0] = m
+    prompt(p, kind, seqs, counts, causal)          # some sequences are shorter than their rows
+    p.append(seqs, counts)
+    prompt(p, kind, seqs, counts, causal)
+    prompt(p, kind, seqs[:1], [m], causal, qs=30.0)
+    p.ok()
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_large_scores_and_tiny_queries(kind):
     p = _pair(kind, 8, 2, 128, 32, 2, 20, seed=10, scale=0.7)
     p.append([0, 1], [600, 33])
