@@ -113,6 +113,7 @@ struct Bars {
   uint64_t kv_full[8], kv_empty[8];
   uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
   uint64_t x_full, x_empty, part_done, part_last, drain;
+  uint64_t fixed[kLoadWarps];          // bf16: values that a loading warp finishes have landed
   uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
   Tile tile[kTileSlots];
   Record rec[2];
@@ -319,7 +320,6 @@ struct Share {
   int32_t lim, watch, head, meta;         // lim, watch: of these 32
   __device__ __forceinline__ bool values() const { return meta & 1; }
   __device__ __forceinline__ bool watched() const { return values() && watch < 32; }
-  __device__ __forceinline__ bool whole() const { return (off[0] | off[1]) >= 0 && lim >= 32; }
 };
 
 // 16-byte pieces of a share that a lane holds. e4m3: four lanes take 64 bytes of a token's row, eight tokens at once;
@@ -387,40 +387,27 @@ __device__ __forceinline__ void store_raw(const Raw<D, TYPE>& v, int i, uint32_t
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
-// bf16, where a share is not whole: 16 (or 8) lanes copy a token's row, zeros past the limit
-template <int D>
-__device__ __forceinline__ void copy_share(const Share& r, const PagedView& c, int kv_heads, uint32_t tile, int w, int lane) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-  const __nv_bfloat16* pages = static_cast<const __nv_bfloat16*>(r.values() ? c.v_pages : c.k_pages);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int64_t row0 = max(r.off[x], static_cast<int64_t>(0));
-#pragma unroll 2
-    for (int y = 0; y < 16 / kRows; ++y) {
-      const int slot = y * kRows + lane / kLanes;
-      const bool there = r.off[x] >= 0 && x * 16 + slot < r.lim;
-      const __nv_bfloat16* src = pages + ((row0 + (there ? slot : 0)) * kv_heads + r.head) * D + lane % kLanes * 8;
-      copy16_or_zero(tile + piece_at<D>(w * 32 + x * 16 + slot, lane % kLanes), src, there);
-    }
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-}
-// What some rows do not see has to be finite; returns a bit per token of the 32 whose values were not (and are zeros now).
-template <int D, bool HALF>
+// Values as the products need them, row by row of a share: zeros where there is no token (ZERO), finite where some rows do
+// not see them; returns a bit per token of the 32 whose values were not (and are zeros now).
+template <int D, bool HALF, bool ZERO>
 __device__ __forceinline__ uint32_t clean_share(const Share& r, uint32_t tile, int chunk, int lane) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   uint32_t odd = 0;
   __syncwarp();
-#pragma unroll 1
-  for (int row = lane / kLanes; row < 32; row += kRows)
-    if (row >= r.watch) {
-      const uint32_t at = tile + piece_at<D>(chunk * 32 + row, lane % kLanes);
+#pragma unroll 4
+  for (int x = 0; x < 32 / kRows; ++x) {
+    const int row = x * kRows + lane / kLanes;
+    const uint32_t at = tile + piece_at<D>(chunk * 32 + row, lane % kLanes);
+    if (ZERO && (row >= r.lim || (row & 16 ? r.off[1] : r.off[0]) < 0)) {
+      store16(at, make_uint4(0, 0, 0, 0));
+    } else if (row >= r.watch) {
       uint4 y = load16(at);
       if (finite_only<HALF>(y)) {
         odd |= 1u << row;
         store16(at, y);
       }
     }
+  }
   return odd;
 }
 
@@ -590,6 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     mbar_init(&bars->part_done, 2 * BM);
     mbar_init(&bars->part_last, 1);
     mbar_init(&bars->drain, 1);
+    for (int s = 0; s < kLoadWarps; ++s) mbar_init(&bars->fixed[s], 1);
     for (int s = 0; s < kTileSlots; ++s) {
       mbar_init(&bars->tile_full[s], 1);
       mbar_init(&bars->tile_empty[s], C::kPerTile);
@@ -763,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
     if constexpr (TYPE == SR_PAGE_BF16) {
       const uint64_t policy = l2_policy_evict_last();
       const bool wide = c.page_tokens % 32 == 0;       // boxes of 32 rows, else of 16
+      uint32_t fixes = 0;
       for (;; n += C::kTeams) {
         const Tile& d = ready(n);
         if (!ok || d.meta < 0) break;
@@ -770,38 +759,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         if (!ok) break;
         uint64_t* full = &bars->kv_full[n % C::kStages];
         uint8_t* tile = sKV + n % C::kStages * C::kTileBytes;
-        uint32_t bytes = 0;
+        // Keys that no row sees may be anything: their scores are replaced. Values are finished here where some are no tokens,
+        // or not seen by all rows, once the copies have landed on a barrier of this warp's own.
+        const bool values = d.meta & 1;
+        bool fix = values && (d.lim < BN || d.watch < BN);
+        uint32_t held = 0;               // copies, by 32 tokens or by 16
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (d.off[x] >= 0) held |= 1u << x;
+        fix |= values && held != 0xFFu;
+        if (wide) held &= 0x55u;         // a copy of 32 tokens begins with its first 16
+        uint64_t* landed = fix ? &bars->fixed[team] : full;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(landed, __popc(held) * (wide ? 32 : 16) * D * 2);
+          const CUtensorMap* map = values ? &p.vmap : &p.kmap;
+          const int head = d.head * D;
 #pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          Share r;
-          share(r, d, x);
-          const bool copy = r.whole() && !r.watched();
-          uint32_t odd = 0;
-          if (copy) {
-            bytes += 32 * D * 2;
-          } else {
-            copy_share<D>(r, c, p.kv_heads, smem_u32(tile), x, lane);
-            if (r.watched()) odd = clean_share<D, false>(r, smem_u32(tile), x, lane);
-            fence_proxy_async_smem();
+          for (uint32_t left = held; left; left &= left - 1) {
+            const int x = __ffs(left) - 1;
+#pragma unroll
+            for (int a = 0; a < C::kAtoms; ++a)
+              tma_load_2d(tile + a * C::kAtomBytes + x * 16 * 128, map, landed, head + a * 64, static_cast<int>(d.off[x]), policy);
           }
-          note(r, x, odd);
         }
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_expect_tx(full, bytes);
+        if (fix) {
+          ok = __all_sync(0xffffffffu, wait_bounded(landed, fixes & 1u, wc, 13));
+          ++fixes;
+          if (!ok) break;
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
             Share r;
             share(r, d, x);
-            if (!r.whole() || r.watched()) continue;
-            const CUtensorMap* map = r.values() ? &p.vmap : &p.kmap;
-#pragma unroll
-            for (int a = 0; a < C::kAtoms; ++a) {
-              uint8_t* dst = tile + a * C::kAtomBytes + x * 32 * 128;
-              tma_load_2d(dst, map, full, r.head * D + a * 64, static_cast<int>(r.off[0]), policy);
-              if (!wide) tma_load_2d(dst + 16 * 128, map, full, r.head * D + a * 64, static_cast<int>(r.off[1]), policy);
-            }
+            note(r, x, clean_share<D, false, true>(r, smem_u32(tile), x, lane));
           }
+          publish(n);
         }
         release(n);
       }
@@ -810,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
         for (int k = 1; k <= C::kStages; ++k)
           if (n - k >= 0 && (n - k) % C::kTeams == team)
             wait_drain(&bars->kv_full[(n - k) % C::kStages], ((n - k) / C::kStages) & 1u, kTimeoutNs);
+      if ((!ok || bars->abort) && fixes > 0) wait_drain(&bars->fixed[team], (fixes - 1) & 1u, kTimeoutNs);
     } else {
       // a share's bytes are on their way in registers: as soon as one of them is stored the next share's follows it
       const DecodeMasks masks = decode_masks();
@@ -852,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
           store_raw<D, TYPE>(raw, i, tile, chunk, lane, masks);
           from.load(raw, i, p.kv_heads, lane);
         }
-        note(mine, chunk, mine.watched() ? clean_share<D, true>(mine, tile, chunk, lane) : 0);
+        note(mine, chunk, mine.watched() ? clean_share<D, true, false>(mine, tile, chunk, lane) : 0);
         if (++done == C::kSubs) {
           publish(at);
           done = 0;

@@ -261,11 +261,13 @@ class PagedCache:
         if counts is not None and n > 0 and min(counts) < 0:
             raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_read")
         shape = (n if counts is None else sum(counts), self.n_kv_heads, self.head_dim)
-        if k is None and v is None:
-            k, v = torch.empty((2, *shape), dtype=_BF16, device=self.device).unbind()
+        if k is None:
+            k = torch.empty(shape, dtype=_BF16, device=self.device)
         else:
-            k, v = (torch.empty(shape, dtype=_BF16, device=self.device) if t is None else t for t in (k, v))
             self._check("k", k, shape)
+        if v is None:
+            v = torch.empty(shape, dtype=_BF16, device=self.device)
+        else:
             self._check("v", v, shape)
         ids, at = self._ids(seqs)
         start, start_at = self._ids(first)
