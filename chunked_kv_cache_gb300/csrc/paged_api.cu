@@ -222,7 +222,7 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   v.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
-  if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type, v.group);
+  if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::paged_prompt_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::paged_evict_prepare();
   if (e == cudaSuccess && cfg->page_type == SR_PAGE_BF16) {
@@ -337,6 +337,7 @@ sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, cons
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  if (!sr::paged_prompt_plan(p)) return SR_ERR_INVALID_ARG;
   return sr::launch_paged_prompt(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
 }
 

@@ -3,15 +3,15 @@
 
 namespace sr {
 
-cudaError_t attn_prepare_bf16(int head_dim, int group);
+cudaError_t attn_prepare_bf16(int head_dim);
 cudaError_t attn_launch_bf16(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t rows_launch_bf16(const PagedRowsParams& p, cudaStream_t st);
 int attn_tile_tokens_bf16(int head_dim);
-cudaError_t attn_prepare_e4m3(int head_dim, int group);
+cudaError_t attn_prepare_e4m3(int head_dim);
 cudaError_t attn_launch_e4m3(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t rows_launch_e4m3(const PagedRowsParams& p, cudaStream_t st);
 int attn_tile_tokens_e4m3(int head_dim);
-cudaError_t attn_prepare_int4(int head_dim, int group);
+cudaError_t attn_prepare_int4(int head_dim);
 cudaError_t attn_launch_int4(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t rows_launch_int4(const PagedRowsParams& p, cudaStream_t st);
 int attn_tile_tokens_int4(int head_dim);
@@ -27,8 +27,8 @@ size_t paged_part_floats(int rows, int head_dim) { return (static_cast<size_t>(r
 int paged_tile_tokens(int head_dim, int page_type) {
   return by_type(page_type, &attn_tile_tokens_bf16, &attn_tile_tokens_e4m3, &attn_tile_tokens_int4)(head_dim);
 }
-cudaError_t paged_attn_prepare(int head_dim, int page_type, int group) {
-  return by_type(page_type, &attn_prepare_bf16, &attn_prepare_e4m3, &attn_prepare_int4)(head_dim, group);
+cudaError_t paged_attn_prepare(int head_dim, int page_type) {
+  return by_type(page_type, &attn_prepare_bf16, &attn_prepare_e4m3, &attn_prepare_int4)(head_dim);
 }
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens) {
   return (pool_tokens / tile_tokens + static_cast<int64_t>(n_seqs) * (1 + kPagedItemCost)) * n_kv;

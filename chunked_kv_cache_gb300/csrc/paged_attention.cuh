@@ -47,11 +47,24 @@
 // 537 MB (95 %); 32 of 4001 .. 32768, e4m3: 144 us for 935 MB (96 %); 64 of 1 .. 16384: 87 us for
 // 522 MB (89 %); 16 of 1000 .. 8192 with weights: 50 us for 232 MB (69 %).
 //
+// 4-bit pages: a warp's records come by bulk copies, one for each 16 tokens' keys or values, and their codes become fp16 in
+// registers: the matrix load that brings a word of eight codes (16-bit units of four, transposed for the values) leaves
+// just the pairs that five instructions of logic and four fused products and sums turn into eight operands, scale and all.
+// That decoding is what bounds it: 350 instructions for 16 tokens of 128 dims (the queue of the logic pipe half full), where the
+// stream would leave room for 390. 32 sequences of 4001 .. 32768 tokens, 8 key heads: 125 us for 526 MB (4.2 TB/s, 62 % of
+// the copy rate; e4m3, 935 MB: 144 us); one of 131071: 42 us for 151 MB; 64 of 1 .. 16384, 64 dims: 35 us for 75 MB, 51 us
+// with weights. Written with the masks and their bits as constants the compiler made two instructions of each: 149 us for
+// the first of these.
+//
+// A few new tokens per sequence (drafts to verify), whose heads fit the 16 columns: columns are (token, head) pairs, and the
+// last tokens' scores are masked by column. 4 tokens of 16 sequences of 1000 .. 8192, 32 heads, 8 key heads, 4 bits: 37 us,
+// where blocks of 128 rows (paged_prompt.cu) take 64 us.
+//
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: a weight meets the
 // values as two bf16 numbers, itself rounded and what that leaves (2^-15 of it at most is lost):
 // the second product costs under 1 % of the time (85.4 us and 84.8 us for 16 sequences of 8192
 // tokens), and without it outputs were 0.0023 off in the mean instead of 0.0017, of which 0.0017
-// is the rounding of the output itself. e4m3 pages: keys and values become fp16 exactly, the
+// is the rounding of the output itself. e4m3 and 4-bit pages: keys and values become fp16 exactly, the
 // weights are scaled by 2^6 and rounded to fp16 (2^-11), and a head's query is scaled by a
 // power of two to a largest element in [1, 2), so that fp16's ten fraction bits hold bf16's
 // seven exactly over 2^14 of range and to 2^-24 of the largest element below that.
@@ -1464,9 +1477,9 @@ cudaError_t launch(const Params<MODE>& p0, cudaStream_t st) {
 
 // The launchers of one page type, which has a translation unit to itself.
 template <int TYPE>
-cudaError_t attn_prepare(int head_dim, int group) {
+cudaError_t attn_prepare(int head_dim) {
   if (head_dim == 128) {
-    // new tokens may take both tiles of columns whatever the group
+    // a few new tokens may take both tiles of columns whatever the group
     const cudaError_t e = prepare<128, TYPE, 1>();
     return e == cudaSuccess ? prepare<128, TYPE, 2>() : e;
   }

@@ -3,7 +3,7 @@
 
 namespace sr {
 
-cudaError_t attn_prepare_int4(int head_dim, int group) { return attn_prepare<SR_PAGE_INT4>(head_dim, group); }
+cudaError_t attn_prepare_int4(int head_dim) { return attn_prepare<SR_PAGE_INT4>(head_dim); }
 cudaError_t attn_launch_int4(const PagedAttnParams& p, cudaStream_t st) { return attn_launch<SR_PAGE_INT4>(p, st); }
 cudaError_t rows_launch_int4(const PagedRowsParams& p, cudaStream_t st) { return rows_launch<SR_PAGE_INT4>(p, st); }
 int attn_tile_tokens_int4(int head_dim) { return attn_tile_tokens<SR_PAGE_INT4>(head_dim); }

@@ -62,7 +62,9 @@ __device__ __forceinline__ uint4 from_e4m3(const uint2& x, float scale) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// ---- 4-bit pages. A scale's byte b is the fp16 number with the bits b << 7; as fp32, b << 20 has its bits at an
+// ---- 4-bit pages: 42,684 rows of 1024 values, 56 us for 224 MB (4.0 TB/s, 59 %), bound by the arithmetic of the rounding
+// (60 instructions for eight values; 64 us with the values unpacked to floats and clamped each).
+// A scale's byte b is the fp16 number with the bits b << 7; as fp32, b << 20 has its bits at an
 // exponent that is 2^112 off, subnormal numbers among them, so that one product moves it to its place or back.
 constexpr uint32_t kScaleTop = 215;      // 3840: times the 16.25 of attention's decoding still an fp16 number
 constexpr uint32_t kScaleNan = 255;
@@ -288,7 +290,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 }
 
 // ------------------------------------------------------------------ read back
-// The way back of append: rows of the sequences' tokens as bf16, zeros where a sequence holds no such token.
+// The way back of append: rows of the sequences' tokens as bf16, zeros where a sequence holds no such token. HBM bound: from
+// 4-bit pages 8 histories of 2072 .. 11432 tokens, 40 heads of 128: 211 us for 1234 MB (5.8 TB/s, 86 % of the copy rate;
+// 322 us with one chunk at a time in flight), 42,684 rows of 1024 values 40 us for 224 MB.
 template <int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) paged_read_kernel(const __grid_constant__ ReadParams p) {
   grid_dep_wait();

@@ -162,7 +162,7 @@ struct alignas(64) PromptParams {
   int32_t causal;
   int32_t id[kMaxPagedSeqs];
   int32_t row0[kMaxPagedSeqs + 1]; // first row of each sequence
-  // set by the launcher
+  // set by paged_prompt_plan
   int32_t tpt;             // tokens of a tile of 128 query rows
   uint32_t group_magic;    // r / group = r * group_magic >> 16 for r < 128
   int32_t blocks;          // of query rows, over all sequences
@@ -183,14 +183,15 @@ cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStre
 cudaError_t launch_paged_append(const AppendParams& p, cudaStream_t st);
 cudaError_t launch_paged_rows(const PagedRowsParams& p, cudaStream_t st);
 cudaError_t launch_paged_read(const ReadParams& p, cudaStream_t st);
-cudaError_t launch_paged_prompt(PromptParams& p, cudaStream_t st);
+cudaError_t launch_paged_prompt(const PromptParams& p, cudaStream_t st);
 cudaError_t paged_prompt_prepare(int head_dim, int page_type);
+bool paged_prompt_plan(PromptParams& p);                              // blocks of query rows; false: more work than a launch takes
 size_t paged_prompt_floats(int head_dim);                            // floats of all partial results of a prompt's launch
 cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t st);
 cudaError_t launch_paged_evict(const EvictParams& p, cudaStream_t st);
 int paged_tile_tokens(int head_dim, int page_type);       // tokens of a tile
 cudaError_t paged_evict_prepare();
-cudaError_t paged_attn_prepare(int head_dim, int page_type, int group);
+cudaError_t paged_attn_prepare(int head_dim, int page_type);
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int group, int head_dim);                   // floats of one partial result
 int paged_append_rows_per_cta(const PagedView& c, int64_t rows);

@@ -260,7 +260,7 @@ class PagedCache:
                 raise ValueError(f"{len(given)} {name} for {n} sequences")
         if counts is not None and n > 0 and min(counts) < 0:
             raise N.SrError(N.SR_ERR_INVALID_ARG, "sr_paged_read")
-        shape = (n if counts is None else sum(counts), self.n_kv_heads, self.head_dim)
+        shape = (n if counts is None else int(sum(counts)), self.n_kv_heads, self.head_dim)
         if k is None:
             k = torch.empty(shape, dtype=_BF16, device=self.device)
         else:

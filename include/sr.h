@@ -566,6 +566,9 @@ SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int3
  * one each. o may be q. fp32 scores, softmax and sums; for their product with V weights are rounded to bf16
  * (bf16 pages: 2^-8 of themselves) or fp16 (2^-11). token_mass is neither read nor written. Pages that are none
  * of the pool are left out as above. The work is split over the lengths and joined; results do not depend on timing.
+ * Values that are no finite numbers reach the rows that see their token and no others. SR_ERR_INVALID_ARG also for a call of
+ * more than about 2^38 blocks of 256 rows times tiles of 128 tokens. Waits inside the kernel are bounded: should one run out
+ * (SR_ERR_TIMEOUT from err_word), the outputs are void and the cache is made again (sr_paged_init) before its next call.
  */
 SR_API sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, const int32_t* n_tokens, int32_t n,
                                            const void* q, void* o, float* lse, int32_t causal, void* stream);
