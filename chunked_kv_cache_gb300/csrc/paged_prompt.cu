@@ -26,9 +26,9 @@
 // group's chain (scores out, maximum, exponentials, weights in, second product, next scores) is longer than the other group's
 // products that run meanwhile, and the issuing warp waits in order. Instructions matter as much: one cache serves all
 // roles' loops, and unrolling the loading warps' took up to a quarter longer. 8192 tokens from nothing, 32 heads, 8 key heads
-// of 128, bf16: 497 us, 1107 TFLOP/s (58 % of the burst rate); 4096 after 4096: 305 us, 1354 TFLOP/s (70 %), e4m3 356 us, 4 bits
-// 369 us; four sequences, 131 .. 1021 tokens after 2003 .. 16384, 40 heads, 4 bits: 545 us, 1009 TFLOP/s; two
-// frames of 1560 that see 10920 tokens, 40 key heads, e4m3: 653 us, 1069 TFLOP/s. The first form of this kernel took 1323
+// of 128, bf16: 445 us, 1235 TFLOP/s (64 % of the burst rate); 4096 after 4096: 301 us, 1371 TFLOP/s (71 %), e4m3 351 us, 4 bits
+// 363 us; four sequences, 131 .. 1021 tokens after 2003 .. 16384, 40 heads, 4 bits: 544 us, 1011 TFLOP/s; two
+// frames of 1560 that see 10920 tokens, 40 key heads, e4m3: 651 us, 1073 TFLOP/s. The first form of this kernel took 1323
 // us for the first of these, with partial results joined row by row (55 us of it), queries copied 8 rows at a time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,7 +53,10 @@ constexpr int kLaunchRegs = 128;
 constexpr uint32_t kRegsSoftmax = 176;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int kItemCost = 1;           // steps that changing blocks costs
+// Steps that changing blocks costs (queries, a chain that starts anew, results): a long prompt's first CTAs have many short
+// blocks. 8192 tokens from nothing, bf16: 501 us with 1, 476, 450, 445 with 2, 3, 4, as with 6; 4096 after 4096 305, 306,
+// 301, 301, with 6 303.
+constexpr int kItemCost = 4;
 // A block's flags are kept for kFlagSlots blocks: who writes those of the eighth block behind one has had a stage back (of
 // 8 at most, two tiles a block) that the second block behind it used, whose weights softmax group 0 made after both
 // groups had read the first one's flags.
@@ -1488,7 +1491,7 @@ bool paged_prompt_plan(PromptParams& p) {
   p.blocks = static_cast<int32_t>(blocks);
   p.o_aligned = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   // a CTA's stretch of steps is counted in 32 bits (half an hour of work and more)
-  return blocks * p.c.n_kv <= (int64_t(1) << 31) / (p.c.cap / BN + 2) * std::min(sm_count(), kMaxPromptCtas);
+  return blocks * p.c.n_kv <= (int64_t(1) << 31) / (p.c.cap / BN + 1 + kItemCost) * std::min(sm_count(), kMaxPromptCtas);
 }
 
 cudaError_t launch_paged_prompt(const PromptParams& p, cudaStream_t st) {
