@@ -274,7 +274,7 @@ sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const int32_t*
   if (st != SR_OK) return st;
   if (rows == 0) return SR_OK;
   if (!k || !v) return SR_ERR_INVALID_ARG;
-  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, rows);
+  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, rows, false);
   share_rows(p.row0, n, p.rows_per_cta, p.cta0);
   p.c = c->view;
   p.k = static_cast<const __nv_bfloat16*>(k);
@@ -359,7 +359,7 @@ sr_status sr_paged_read(sr_paged_cache* c, const int32_t* seqs, const int32_t* f
   if (!k || !v) return SR_ERR_INVALID_ARG;
   p.n = n;
   p.c = c->view;
-  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, p.row0[n]);
+  p.rows_per_cta = sr::paged_append_rows_per_cta(c->view, p.row0[n], true);
   share_rows(p.row0, n, p.rows_per_cta, p.cta0);
   p.k = static_cast<__nv_bfloat16*>(k);
   p.v = static_cast<__nv_bfloat16*>(v);

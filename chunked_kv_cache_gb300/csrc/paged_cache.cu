@@ -62,7 +62,7 @@ __device__ __forceinline__ uint4 from_e4m3(const uint2& x, float scale) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// ---- 4-bit pages: 42,684 rows of 1024 values, 56 us for 224 MB (4.0 TB/s, 59 %), bound by the arithmetic of the rounding
+// ---- 4-bit pages: 42,684 rows of 1024 values, 55 us for 224 MB (4.1 TB/s, 60 %), bound by the arithmetic of the rounding
 // (60 instructions for eight values; 64 us with the values unpacked to floats and clamped each).
 // A scale's byte b is the fp16 number with the bits b << 7; as fp32, b << 20 has its bits at an
 // exponent that is 2^112 off, subnormal numbers among them, so that one product moves it to its place or back.
@@ -143,8 +143,10 @@ struct ChunkWalk {
   }
 };
 
+// (4 bits: four CTAs on an SM as the other types have anyway, 64 registers for 74: 12,000 rows of 1024 values 22.8 us with the
+// reset before it, 25.3 without the bound; 1,000 of 5120 13.4, 17.2)
 template <int TYPE>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, TYPE == SR_PAGE_INT4 ? 4 : 0) paged_append_kernel(const __grid_constant__ AppendParams p) {
   grid_dep_wait();
   grid_dep_launch_dependents();
   const PagedView& c = p.c;
@@ -291,8 +293,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __gr
 
 // ------------------------------------------------------------------ read back
 // The way back of append: rows of the sequences' tokens as bf16, zeros where a sequence holds no such token. HBM bound: from
-// 4-bit pages 8 histories of 2072 .. 11432 tokens, 40 heads of 128: 211 us for 1234 MB (5.8 TB/s, 86 % of the copy rate;
-// 322 us with one chunk at a time in flight), 42,684 rows of 1024 values 40 us for 224 MB.
+// 4-bit pages 8 histories of 2072 .. 11432 tokens, 40 heads of 128: 191 us for 1234 MB (6.5 TB/s, 95 % of the copy rate;
+// 322 us with one chunk at a time in flight), 42,684 rows of 1024 values 36.5 us for 224 MB.
 template <int TYPE>
 __global__ void __launch_bounds__(kAppendThreads) paged_read_kernel(const __grid_constant__ ReadParams p) {
   grid_dep_wait();
@@ -930,13 +932,23 @@ __global__ void __launch_bounds__(kEvictThreads, 2) paged_evict_kernel(const __g
 // One wave of the four CTAs that an SM holds, but at least a vector of each tensor per thread; two
 // waves where a thread would have more than 16 (42,700 rows of 1024 values: 61.3 us in one, 58.9 us in
 // two; 4,000 rows: 7.5 us, 9.1 us).
-int paged_append_rows_per_cta(const PagedView& c, int64_t rows) {
+// 4-bit pages, where a CTA would have more than 16 vectors a thread: several waves, so that the last one weighs little, as
+// long as a CTA has 2048 vectors of each tensor and whole steps of 8 tokens. Rows of 1024 values, reset and append
+// (4 waves) or reading back (16), against two waves: 42,684 rows 57.5 and 36.4 us against 58.3 and 40.0, 100,000 rows
+// 122.7 and 78.4 against 127.3 and 90.7. Fewer rows to a CTA were slower (21,000 rows, 4 to a CTA: 50.3 and 23.0 against 31.2
+// and 22.0). Below that one wave, of steps that no lane is idle in.
+int paged_append_rows_per_cta(const PagedView& c, int64_t rows, bool read) {
   const int64_t vectors = static_cast<int64_t>(c.n_kv) * c.head_dim / 8;     // of a row
   const int64_t wave = 4ll * sm_count();
-  const int64_t ctas = rows * vectors > 16 * wave * kAppendThreads ? 2 * wave : wave;
-  const int64_t per = std::max((kAppendThreads + vectors - 1) / vectors, (rows + ctas - 1) / ctas);
-  // records: whole steps of 8 tokens, where a CTA has as many
-  return static_cast<int>(c.page_type == SR_PAGE_INT4 && per > 8 ? (per + 7) / 8 * 8 : per);
+  const bool many = rows * vectors > 16 * wave * kAppendThreads;
+  const int64_t ctas = many ? 2 * wave : wave;
+  int64_t per = std::max((kAppendThreads + vectors - 1) / vectors, (rows + ctas - 1) / ctas);
+  if (c.page_type != SR_PAGE_INT4) return static_cast<int>(per);
+  if (many) {
+    const int64_t waves = read ? 16 : 4;
+    per = std::max(std::min(per, std::max<int64_t>(8, 2048 / vectors)), (rows + waves * wave - 1) / (waves * wave));
+  }
+  return static_cast<int>(per > 4 ? (per + 7) / 8 * 8 : per == 3 ? 4 : per);
 }
 
 cudaError_t launch_paged_reset(const PagedView& c, const PagedBatch& b, cudaStream_t st) {

@@ -194,6 +194,6 @@ cudaError_t paged_evict_prepare();
 cudaError_t paged_attn_prepare(int head_dim, int page_type);
 int64_t paged_score_tiles(int64_t pool_tokens, int n_seqs, int n_kv, int tile_tokens);   // tiles that scores are kept for
 size_t paged_part_floats(int group, int head_dim);                   // floats of one partial result
-int paged_append_rows_per_cta(const PagedView& c, int64_t rows);
+int paged_append_rows_per_cta(const PagedView& c, int64_t rows, bool read);
 
 }  // namespace sr
