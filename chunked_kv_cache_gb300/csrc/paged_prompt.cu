@@ -61,7 +61,7 @@ constexpr int kItemCost = 4;
 // 8 at most, two tiles a block) that the second block behind it used, whose weights softmax group 0 made after both
 // groups had read the first one's flags.
 constexpr int kFlagSlots = 8, kFlagTiles = 3;
-constexpr int kBarBytes = 3072;
+constexpr int kBarBytes = 3 * 1024;
 template <int D, int TYPE>
 struct Cfg {
   static constexpr bool kHalf = TYPE != SR_PAGE_BF16;       // products of fp16, else of bf16
