@@ -1329,9 +1329,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             tmem_ld32(tmem + lane_base + 256 + 128 + x * 32, o1);
             tmem_wait_ld();
             tmem_fix(o1);
+            // (a factor of zero, too: both groups' sums have been written, and a NaN among them is one that the row sees)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              of[i] = (f0 == 0.f ? 0.f : of[i] * f0) + (f1 == 0.f ? 0.f : __uint_as_float(o1[i]) * f1);
+            for (int i = 0; i < 32; ++i) of[i] = fmaf(__uint_as_float(o1[i]), f1, of[i] * f0);
           }
           float y[32];
 #pragma unroll

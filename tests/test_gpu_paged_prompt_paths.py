@@ -1,0 +1,115 @@
+"""Attention of several new tokens on the paths that few calls take, against a plain form in 64 bits: numbers that are
+none in whole, cut and merged blocks.
+
+The plain form computes from the tokens as the cache reads them back (exact, test_gpu_paged_int4). Tolerances are
+test_gpu_paged_prompt's. Which outputs are NaN or infinite has to agree element by element."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_common import device
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["bf16", "e4m3", "int4"]
+U, E = 2.0 ** -24, 2.0 ** -8
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from chunked_kv_cache_gb300 import build
+    build.build()
+    device()
+
+
+class Calls:
+    """A cache whose pages lie in no order, and what its attention should give."""
+
+    def __init__(self, kind, heads, kv, d, n, cap, page=16, seed=0):
+        import chunked_kv_cache_gb300 as sr
+        self.kind, self.heads, self.kv, self.d, self.n = kind, heads, kv, d, n
+        self.dev = device()
+        self.g = torch.Generator(device=self.dev).manual_seed(seed)
+        pages = -(-cap // page)
+        table = torch.randperm(n * pages, generator=self.g, device=self.dev).to(torch.int32).view(n, pages)
+        dtype = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int4": "int4"}[kind]
+        self.cache = sr.PagedCache(heads, kv, d, page_tokens=page, n_pages=n * pages, max_seqs=n, max_pages=pages,
+                                   page_dtype=dtype, device=self.dev, buffers=dict(block_table=table))
+        self.len = [0] * n
+
+    def randn(self, *shape, s=1.0):
+        return (torch.randn(shape, generator=self.g, device=self.dev) * s).to(torch.bfloat16)
+
+    def append(self, k, v, counts, seqs=None):
+        self.cache.append(k, v, counts=counts, seqs=seqs)
+        for i, c in enumerate(counts):
+            self.len[i if seqs is None else seqs[i]] += c
+
+    def plain(self, q, counts, seqs=None, causal=True):
+        """o, lse and the bounds of their errors, fp64: [rows][heads][d], [rows][heads]."""
+        out, r = [], 0
+        scale, g = self.d ** -0.5, self.heads // self.kv
+        for i, m in enumerate(counts):
+            s = i if seqs is None else seqs[i]
+            L = self.len[s]
+            k, v = (x.double() for x in self.cache.read([L], seqs=[s]))
+            x = q[r: r + m].double().view(m, self.kv, g, self.d)
+            r += m
+            t = torch.arange(L, device=self.dev)
+            sees = t[None] <= torch.arange(m, device=self.dev)[:, None] + (L - m) if causal else torch.ones(m, L, dtype=torch.bool, device=self.dev)
+            score = torch.einsum("rhgd,thd->rhgt", x, k) * scale
+            score = torch.where(sees[:, None, None], score, -INF)
+            lse = torch.logsumexp(score, -1) if L else torch.full(score.shape[:3], -INF, dtype=torch.float64, device=self.dev)
+            w = torch.where((lse == -INF)[..., None], 0.0, torch.exp(score - lse[..., None]))
+            vf = torch.where(torch.isfinite(v), v, 0.0)
+            o = torch.einsum("rhgt,thd->rhgd", w, vf)
+            wv = torch.einsum("rhgt,thd->rhgd", w, vf.abs())
+            for j in torch.nonzero(~torch.isfinite(v).all(2).all(1)).flatten().tolist():
+                odd = torch.where(torch.isfinite(v[j]), 0.0, v[j])[None, :, None]
+                there = sees[:, j, None, None, None] & (lse != -INF)[..., None] & (odd != 0)
+                o = o + torch.where(there, w[..., j, None] * odd, 0.0)
+            dot = torch.einsum("rhgd,thd->rhgt", x.abs(), torch.where(torch.isfinite(k), k, 0.0).abs()).amax(-1) if L else torch.zeros_like(lse)
+            dx = (self.d + 8) * U * scale * dot
+            W = 2.0 ** -8 if self.kind == "bf16" else 2.0 ** -11
+            bound = E * o.abs() + (W + 2 * dx + L * U + 2.0 ** -20)[..., None] * wv + L * 2.0 ** -31 * (vf.abs().max() if L else 0.0) + 1e-30
+            tol = dx + L * U + 2.0 ** -20 + 4 * U * lse.abs()
+            out.append([y.reshape(m, self.heads, *y.shape[3:]) for y in (o, lse, bound, tol)])
+        return [torch.cat(y) for y in zip(*out)]
+
+    def compare(self, q, counts, o, lse, seqs=None, causal=True):
+        ref, ref_lse, bound, tol = self.plain(q, counts, seqs, causal)
+        o = o.double()
+        assert torch.equal(torch.isnan(o), torch.isnan(ref)), "NaN elsewhere"
+        for inf in (INF, -INF):
+            assert torch.equal(o == inf, ref == inf), "infinite elsewhere"
+        fine = torch.isfinite(ref)
+        err = (o - ref).abs()
+        assert bool((err[fine] <= bound[fine]).all()), float((err / bound)[fine].max())
+        none = ref_lse == -INF
+        assert bool((lse.double() == ref_lse)[none].all()) and bool((o[none] == 0).all())
+        assert bool(((lse.double() - ref_lse).abs() <= tol)[~none].all())
+
+    def prompt(self, q, counts, seqs=None, causal=True):
+        o, lse = self.cache.prompt_attention(q, counts, seqs=seqs, lse=True, causal=causal)
+        self.compare(q, counts, o, lse, seqs, causal)
+        assert self.cache.error_status() == 0
+        return o, lse
+
+
+@pytest.mark.parametrize("low", [0, 1])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,kv,n", [(64, 1, 1), (128, 1, 1), (64, 16, 40), (128, 8, 40)])
+def test_nan_under_scores_that_leave_its_weight_at_zero(d, kv, n, kind, low):
+    """Rows of one query tile: the groups that share the key tiles merge sums of which one is lighter by far more than
+    2^-126. A NaN among its values is still one."""
+    p = Calls(kind, kv, kv, d, n, 320, seed=d + n)
+    length, m = 256 + 40, 40
+    k, v, q = p.randn(n * length, kv, d, s=0.1), p.randn(n * length, kv, d), p.randn(n * m, kv, d, s=0.1)
+    q[..., 0] = 256.0
+    tile = torch.arange(length, device=p.dev) // 128
+    k.view(n, length, kv, d)[..., 0] = torch.where(tile % 2 == low, -8.0, 8.0)[None, :, None]
+    v.view(n, length, kv, d)[::2, 128 * low + 10, :, 3] = NAN
+    p.append(k, v, [length] * n)
+    o, _ = p.prompt(q, [m] * n)
+    assert bool(torch.isnan(o[:m]).any(-1).all())
