@@ -373,8 +373,9 @@ __device__ __noinline__ void join_parts(const Params<MODE>& p, int first, int s0
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       const int64_t out = row_of<MODE>(p, item_i, item_h, r);
       uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * kCols);
-      o[0] = pack_bf16x2(a[0] * inv, a[1] * inv);
-      if constexpr (kCols == 4) o[1] = pack_bf16x2(a[2] * inv, a[3] * inv);
+      auto of = [&](int x) { return sum == 0.f ? 0.f : a[x] * inv; };      // no weight: 0, whatever the values are
+      o[0] = pack_bf16x2(of(0), of(1));
+      if constexpr (kCols == 4) o[1] = pack_bf16x2(of(2), of(3));
       if (lane == 0) {
         const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
         if (p.lse) p.lse[out] = lse2 * kLn2;
@@ -1177,6 +1178,7 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtasPerSm) paged_attn
         a.z *= scale;
         a.w *= scale;
         if (whole) {
+          if (sum == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);       // no weight: 0, whatever the values are
           const int64_t out = row_of<MODE>(p, item_i, item_h, row);
           *reinterpret_cast<uint2*>(p.o + out * D + 4 * quad) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
           if (quad == 0) {
@@ -1315,6 +1317,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
     y1 = fmaf(f, sums[w][2 * threadIdx.x + 1], y1);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  if (l == 0.f) y0 = y1 = 0.f;          // no weight: 0, whatever the values are
   reinterpret_cast<uint32_t*>(p.o + out * D)[threadIdx.x] = pack_bf16x2(y0 * inv, y1 * inv);
   if (threadIdx.x == 0) {
     const float lse2 = l == 0.f ? -INFINITY : all + log2f(l);

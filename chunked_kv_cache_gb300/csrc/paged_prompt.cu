@@ -547,8 +547,9 @@ __device__ __noinline__ void join_block(const PromptParams& p, const Block& k, i
       const float inv = sum[y] == 0.f ? 0.f : 1.f / sum[y];
       const int64_t out = (static_cast<int64_t>(p.row0[k.i]) + k.tok0 + tok) * p.c.n_heads + k.h * group + hh;
       uint32_t* o = reinterpret_cast<uint32_t*>(p.o + out * D + lane * N);
-      o[0] = pack_bf16x2(a[y][0] * inv, a[y][1] * inv);
-      if constexpr (N == 4) o[1] = pack_bf16x2(a[y][2] * inv, a[y][3] * inv);
+      auto of = [&](int z) { return sum[y] == 0.f ? 0.f : a[y][z] * inv; };     // no weight: 0, whatever the values are
+      o[0] = pack_bf16x2(of(0), of(1));
+      if constexpr (N == 4) o[1] = pack_bf16x2(of(2), of(3));
       if (lane == 0 && p.lse) p.lse[out] = sum[y] == 0.f ? -INFINITY : (top[y] + log2f(sum[y])) * kLn2;
     }
   }
@@ -1394,6 +1395,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_prompt_kernel(const __grid_
             for (int i = 0; i < D; i += 2)
               *reinterpret_cast<uint32_t*>(p.o + out * D + i) = pack_bf16x2(part[i], part[i + 1]);
         }
+        // no weight: the output is 0, whatever the values are (over what was written above, which keeps that short)
+        if (live && (join ? sum == 0.f : whole && l == 0.f))
+#pragma unroll 1
+          for (int i = 0; i < D; i += 8) *reinterpret_cast<uint4*>(p.o + out * D + i) = make_uint4(0, 0, 0, 0);
         if (live) {
           if (join) {
             if (p.lse) p.lse[out] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;

@@ -113,3 +113,24 @@ def test_nan_under_scores_that_leave_its_weight_at_zero(d, kv, n, kind, low):
     p.append(k, v, [length] * n)
     o, _ = p.prompt(q, [m] * n)
     assert bool(torch.isnan(o[:m]).any(-1).all())
+
+
+@pytest.mark.parametrize("length,m", [(40, 1), (40, 4), (40, 20), (3000, 1), (3000, 4), (3000, 40), (600, 300)])
+def test_rows_whose_scores_are_all_minus_infinity_over_values_that_are_none(length, m):
+    """o = 0 and lse = -inf whatever the values are, in sequences taken whole and in ones cut into parts; by prompt_attention
+    and, for one token, by attention."""
+    p = Calls("bf16", 4, 2, 64, 5, length, seed=length + m)
+    k, v, q = p.randn(5 * length, 2, 64), p.randn(5 * length, 2, 64), p.randn(5 * m, 4, 64)
+    k[:, 0, 0] = -INF
+    q[:, :, 0] = 1.0
+    v.view(5, length, 2, 64)[:, :, 0, 7] = NAN
+    v.view(5, length, 2, 64)[:, length // 2, 0, 9] = INF
+    p.append(k, v, [length] * 5)
+    calls = [lambda: p.cache.prompt_attention(q, [m] * 5, lse=True), lambda: p.cache.prompt_attention(q, [m] * 5, lse=True, causal=False)]
+    if m == 1:
+        calls += [lambda: p.cache.attention(q, lse=True), lambda: p.cache.attention(q, lse=True, mass_decay=1.0),
+                  lambda: p.cache.attention(q[:1], lse=True)]
+    for call in calls:
+        o, lse = call()
+        assert bool((o[:, :2] == 0).all()) and bool((lse[:, :2] == -INF).all())
+        assert bool(torch.isfinite(o[:, 2:]).all()) and bool(torch.isfinite(lse[:, 2:]).all())
