@@ -790,7 +790,16 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtasPerSm) paged_attn
     for (int32_t tile = first_tile; tile < end_tile; ++tile) {
       issue((stage + kStages - 1) % kStages);
       if constexpr (G::kRecords) {
-        wait_bounded(&sh.full[warp][stage], phases >> stage & 1u, wc, 0x21);
+        if (!__all_sync(0xffffffffu, wait_bounded(&sh.full[warp][stage], phases >> stage & 1u, wc, 0x21))) {
+          // A copy did not come in time: the outputs are void (err_word tells), and this warp leaves. Its shared memory is
+          // not given back before the copies of this tile and those ahead have come, or have had their time once more.
+          for (int x = 0; x < kStages && left > 0; ++x) {
+            const int s = (stage + x) % kStages;
+            wait_drain(&sh.full[warp][s], phases >> s & 1u, kCopyTimeoutNs);
+            cursor_next<G::CT>(comp, sh, n_kv, left);
+          }
+          return;
+        }
         phases ^= 1u << stage;
       } else {
         copy_wait<kStages - 1>();
@@ -1234,11 +1243,6 @@ __global__ void __launch_bounds__(kThreads, Geo<D, TYPE>::kCtasPerSm) paged_attn
         }
       }
     }
-  }
-  if constexpr (G::kRecords) {
-    // a copy that never came: shared memory is not given back before it has, or has had its time once more
-    if (sh.abort)
-      for (int x = 0; x < kStages; ++x) wait_drain(&sh.full[warp][x], (phases >> x & 1u) ^ 1u, kCopyTimeoutNs);
   }
 }
 

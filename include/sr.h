@@ -549,7 +549,9 @@ SR_API sr_status sr_paged_append(sr_paged_cache* c, const int32_t* seqs, const i
  * mass_decay < 0: weights are not accumulated. The workspace has room for the scores of every token of the pool
  * once; a batch whose sequences share pages and hold more leaves all weights as they were, with SR_DEVERR_WORKSPACE
  * in err_word (o and lse are written), and can be taken in smaller batches. The work is split over the length of the
- * sequences and joined, whatever their number; results do not depend on timing.
+ * sequences and joined, whatever their number; results do not depend on timing. 4-bit pages come by copies whose waits are
+ * bounded: should one run out (SR_ERR_TIMEOUT from err_word), the outputs are void and the cache is made again
+ * (sr_paged_init) before its next call.
  */
 SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int32_t n, const void* q, void* o,
                                     float* lse, float mass_decay, void* stream);
