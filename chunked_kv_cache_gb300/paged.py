@@ -29,7 +29,10 @@ class PagedCache:
     kv_exp [2][n_kv_heads] int32.
 
     buffers: a dict with any of these names, used in place and as found. Sequences
-    whose block table the caller does not fill get their pages from reserve().
+    whose block table the caller does not fill get their pages from reserve(). Also
+    "workspace", uint8, another cache's that is as long at least (sr_paged_workspace_bytes; most of
+    it is room for the parts of cut prompts, 21 MB for heads of 64 and 43 MB for heads of 128, whatever the
+    pool): caches whose calls never run at the same time, as a model's layers, may share one.
 
     Calls run on the current stream of the cache's device, which must be the current device, and
     two of one cache must not run at the same time (they share a workspace). The cache is
@@ -84,10 +87,11 @@ class PagedCache:
         self.token_pos = take("token_pos", per_token, i32, 0)
         self.token_mass = take("token_mass", per_token, torch.float32, 0.0) if mass else None
         self.kv_exp = take("kv_exp", (2, n_kv_heads), i32, 0)
+        space = self._workspace(given.pop("workspace", None), nbytes, dev)
         if given:
             raise ValueError(f"unknown buffers: {sorted(given)}")
         self.err_word = torch.zeros((1,), dtype=i32, device=dev)
-        self.workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        self.workspace = torch.empty((nbytes,), dtype=torch.uint8, device=dev) if space is None else space
         # pages not handed out yet (only when the cache owns its block table)
         self._free = list(range(n_pages - 1, -1, -1)) if own_table else None
         self._pages: list[list[int]] = [[] for _ in range(max_seqs)] if own_table else []
@@ -100,6 +104,18 @@ class PagedCache:
             self.handle = N.sr_paged_init(self.cfg, bufs, self._stream())
 
     # ---------------------------------------------------------------- helpers
+    @staticmethod
+    def _workspace(t, nbytes: int, dev):
+        """A given workspace, checked; None stays."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("workspace must be a torch.Tensor")
+        if t.dtype != torch.uint8 or t.dim() != 1 or t.numel() < nbytes or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"workspace: expected contiguous torch.uint8 of {nbytes} bytes or more on {dev}, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device} (contiguous={t.is_contiguous()})")
+        return t
+
     def _stream(self) -> int:
         # the handle itself: a Stream object costs two microseconds, as much as a launch
         return torch._C._cuda_getCurrentRawStream(self.device.index)

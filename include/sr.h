@@ -464,7 +464,9 @@ SR_API sr_status sr_layer_commit(sr_session* const* sessions, const sr_window* w
  * sr_paged_init clears them on its stream: a first call on another stream has to be ordered behind it, and the
  * buffers have to outlive the calls of every stream.
  * Caches that share pages need a workspace each and may run at the same time as long as
- * none writes what another reads. Sequences may share pages that are only read: the pages
+ * none writes what another reads. Caches whose calls never overlap, as those of a model's layers, may share one
+ * workspace of the longest one's size: a call leaves nothing in it that a later one reads but counters at zero.
+ * sr_paged_init counts as a call there. Sequences may share pages that are only read: the pages
  * that new tokens go to, and every page of a sequence that is evicted from, must be its own.
  * A cache is not thread-safe; distinct caches are independent.
  *

@@ -134,3 +134,57 @@ def test_rows_whose_scores_are_all_minus_infinity_over_values_that_are_none(leng
         o, lse = call()
         assert bool((o[:, :2] == 0).all()) and bool((lse[:, :2] == -INF).all())
         assert bool(torch.isfinite(o[:, 2:]).all()) and bool(torch.isfinite(lse[:, 2:]).all())
+
+
+def test_caches_whose_calls_do_not_overlap_share_a_workspace():
+    """Layers of several shapes and page types on one workspace, their calls in turn, captured ones among them: bit for bit what
+    each gives on its own."""
+    import chunked_kv_cache_gb300 as sr
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(1)
+    shapes = [(32, 8, 128, torch.bfloat16, 64), (4, 4, 64, "int4", 16), (8, 1, 128, torch.float8_e4m3fn, 32), (16, 2, 64, torch.bfloat16, 16)]
+
+    def layers(shared):
+        out = []
+        for heads, kv, d, dtype, page in shapes:
+            own = {} if not shared or not out else dict(workspace=out[0].workspace)
+            out.append(sr.PagedCache(heads, kv, d, page_tokens=page, n_pages=4 * (4096 // page), max_seqs=4, max_pages=4096 // page,
+                                     page_dtype=dtype, device=dev, buffers=own))
+            for s in range(4):
+                out[-1].reserve(s, 4096)
+        return out
+
+    both = [layers(False), layers(True)]
+    need = [c.workspace.numel() for c in both[0]]
+    assert need[0] == max(need) and all(c.workspace is both[1][0].workspace for c in both[1])
+    with pytest.raises(ValueError):
+        heads, kv, d, dtype, page = shapes[0]
+        sr.PagedCache(heads, kv, d, page_tokens=page, n_pages=4 * (4096 // page), max_seqs=4, max_pages=4096 // page,
+                      device=dev, buffers=dict(workspace=both[1][0].workspace[256:]))
+
+    def step(c, k, v, q, counts):
+        c.append(k, v, counts=counts)
+        out = list(c.prompt_attention(q, counts, lse=True))
+        out += c.attention(q[:4], lse=True, mass_decay=0.5)
+        c.evict(1500, n_sink=4, n_recent=64)
+        return out + [c.seq_len.clone(), c.token_mass.clone()]
+
+    for counts in ([1700, 33, 0, 600], [130, 1, 70, 900], [4, 4, 4, 4], [1, 1, 1, 1]):
+        for i, (heads, kv, d, _, _) in enumerate(shapes):
+            rows = sum(counts)
+            k, v, q = ((torch.randn(rows, h, d, generator=g, device=dev)).to(torch.bfloat16) for h in (kv, kv, heads))
+            for a, b in zip(step(both[0][i], k, v, q, counts), step(both[1][i], k, v, q, counts)):
+                assert torch.equal(a, b)
+    x = [torch.randn(4, h, d, generator=g, device=dev).to(torch.bfloat16) for h, d in [(8, 128), (32, 128), (4, 64), (4, 64)]]
+    side, graph = torch.cuda.Stream(dev), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        got = step(both[1][0], x[0], x[0], x[1], [1] * 4) + step(both[1][1], x[2], x[2], x[3], [1] * 4)
+    torch.cuda.current_stream().wait_stream(side)
+    graph.replay()
+    want = step(both[0][0], x[0], x[0], x[1], [1] * 4) + step(both[0][1], x[2], x[2], x[3], [1] * 4)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    for c in both[0] + both[1]:
+        assert c.error_status() == 0
+        c.close()

@@ -60,3 +60,14 @@ def test_pages_are_not_lost_where_the_table_cannot_be_written():
     assert c._free == [] and c._pages == [[2, 3, 4], [0, 1, 5], []]
     with pytest.raises(RuntimeError):
         c.reserve(2, 1)
+
+
+def test_a_given_workspace_is_checked():
+    cpu, ok = torch.device("cpu"), torch.empty(4096, dtype=torch.uint8)
+    assert PagedCache._workspace(None, 4096, cpu) is None
+    assert PagedCache._workspace(ok, 4096, cpu) is ok and PagedCache._workspace(ok, 100, cpu) is ok
+    for bad in (ok[:4095], ok[::2], ok.view(64, 64), ok.view(torch.int8), ok.to("meta")):
+        with pytest.raises(ValueError):
+            PagedCache._workspace(bad, 4096 if bad.numel() != 2048 else 2048, cpu)
+    with pytest.raises(TypeError):
+        PagedCache._workspace(bytes(4096), 4096, cpu)
