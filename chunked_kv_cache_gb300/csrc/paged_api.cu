@@ -19,6 +19,7 @@ struct sr_paged_cache {
   sr::PagedView view;
   sr::PagedLayout layout;
   CUtensorMap kmap, vmap;   // bf16 pages
+  bool prompts;             // the kernel of blocks of rows can be launched (a cache that never needs it does without)
   int device;
   int32_t* mark;         // [max_seqs] the last call that named a row (finds repeated rows)
   int32_t stamp;
@@ -223,13 +224,12 @@ sr_status sr_paged_init(const sr_paged_config* cfg, const sr_paged_buffers* bufs
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaGetDevice(&c->device);
   if (e == cudaSuccess) e = sr::paged_attn_prepare(cfg->head_dim, cfg->page_type);
-  if (e == cudaSuccess) e = sr::paged_prompt_prepare(cfg->head_dim, cfg->page_type);
   if (e == cudaSuccess) e = sr::paged_evict_prepare();
-  if (e == cudaSuccess && cfg->page_type == SR_PAGE_BF16) {
+  if (e == cudaSuccess) c->prompts = sr::paged_prompt_prepare(cfg->head_dim, cfg->page_type) == cudaSuccess;
+  if (c->prompts && cfg->page_type == SR_PAGE_BF16) {
     const int64_t rows = static_cast<int64_t>(cfg->n_pages) * cfg->page_tokens, row = static_cast<int64_t>(cfg->n_kv_heads) * cfg->head_dim;
     const int box = sr::paged_box_rows(cfg->page_tokens);
-    if (!sr::encode_rows(&c->kmap, b.k_pages, rows, row, box) || !sr::encode_rows(&c->vmap, b.v_pages, rows, row, box))
-      e = cudaErrorUnknown;
+    c->prompts = sr::encode_rows(&c->kmap, b.k_pages, rows, row, box) && sr::encode_rows(&c->vmap, b.v_pages, rows, row, box);
   }
   if (e == cudaSuccess) e = sr::launch_zero_words(b.err_word, 1, cs);
   if (e == cudaSuccess) e = sr::launch_zero_words(ws_at<int32_t>(c, c->layout.counters), sr::kPagedCounters, cs);
@@ -326,6 +326,7 @@ sr_status sr_paged_prompt_attention(sr_paged_cache* c, const int32_t* seqs, cons
     r.mass_decay = -1.f;
     return sr::launch_paged_rows(r, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SR_OK : SR_ERR_CUDA;
   }
+  if (!c->prompts) return SR_ERR_CUDA;
   p.n = n;
   p.causal = causal != 0;
   p.arrivals = ws_at<int32_t>(c, c->layout.counters) + sr::kMaxPagedSeqs;
