@@ -1,5 +1,6 @@
 """Attention of several new tokens on the paths that few calls take, against a plain form in 64 bits: numbers that are
-none in whole, cut and merged blocks.
+none in whole, cut and merged blocks, many blocks to a CTA, outputs on any 16 bytes, batches of every size, prompts among
+single tokens, one workspace for several caches.
 
 The plain form computes from the tokens as the cache reads them back (exact, test_gpu_paged_int4). Tolerances are
 test_gpu_paged_prompt's. Which outputs are NaN or infinite has to agree element by element."""
@@ -115,6 +116,57 @@ def test_nan_under_scores_that_leave_its_weight_at_zero(d, kv, n, kind, low):
     assert bool(torch.isnan(o[:m]).any(-1).all())
 
 
+# d, key heads, query heads of each, sequences, tokens before the new ones, new ones
+SHAPES = [
+    (64, 16, 1, 128, 60, 40),       # one query tile, 13 blocks to a CTA
+    (128, 16, 1, 128, 126, 256),    # two, and new tokens in three key tiles
+    (64, 16, 1, 96, 254, 256),
+    (128, 8, 4, 64, 100, 50),
+    (64, 2, 8, 256, 0, 33),         # as many sequences as a call takes
+    (128, 4, 3, 20, 300, 130),      # several blocks to a sequence
+    (128, 1, 2, 3, 1000, 200),      # cut blocks
+]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("shape", SHAPES)
+def test_numbers_that_are_none_among_the_new_tokens(shape, kind):
+    """NaN and infinities in some sequences' new values reach the rows that see them, and no row of a sequence without."""
+    d, kv, group, n, base, m = shape
+    p = Calls(kind, kv * group, kv, d, n, base + m, seed=base + m)
+    length = base + m
+    k, v, q = p.randn(n * length, kv, d), p.randn(n * length, kv, d), p.randn(n * m, kv * group, d)
+    each = v.view(n, length, kv, d)
+    rng = np.random.default_rng(n)
+    for s in range(n):
+        for j in rng.integers(1, m, 3 if s % 3 else 0).tolist() + ([m - 1, m - 2] if s % 3 == 2 else []):
+            each[s, base + j, int(rng.integers(kv)), int(rng.integers(d))] = [NAN, INF, -INF][int(rng.integers(3))]
+    p.append(k, v, [length] * n)
+    o, lse = p.prompt(q, [m] * n)
+    p.prompt(q, [m] * n, causal=False)
+    same = q.clone()                                  # in the queries' place
+    p.cache.prompt_attention(same, [m] * n, out=same)
+    assert torch.equal(same.view(torch.int16), o.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d,kv,group,m", [(64, 2, 4, 4), (128, 1, 1, 5), (128, 2, 8, 2)])
+def test_numbers_that_are_none_among_a_few_rows(d, kv, group, m, kind):
+    """The same where the rows are few enough for the kernel of single tokens; 256 sequences."""
+    n, length = 256, 70
+    p = Calls(kind, kv * group, kv, d, n, length, seed=d + m)
+    k, v, q = p.randn(n * length, kv, d), p.randn(n * length, kv, d), p.randn(n * m, kv * group, d)
+    each = v.view(n, length, kv, d)
+    for s in range(n):
+        if s % 2:
+            each[s, length - 1 - s // 2 % (m - 1), s % kv, s % d] = [NAN, INF, -INF][s % 3]
+    p.append(k, v, [length] * n)
+    o, _ = p.prompt(q, [m] * n)
+    same = q.clone()
+    p.cache.prompt_attention(same, [m] * n, out=same)
+    assert torch.equal(same.view(torch.int16), o.view(torch.int16))
+
+
 @pytest.mark.parametrize("length,m", [(40, 1), (40, 4), (40, 20), (3000, 1), (3000, 4), (3000, 40), (600, 300)])
 def test_rows_whose_scores_are_all_minus_infinity_over_values_that_are_none(length, m):
     """o = 0 and lse = -inf whatever the values are, in sequences taken whole and in ones cut into parts; by prompt_attention
@@ -134,6 +186,45 @@ def test_rows_whose_scores_are_all_minus_infinity_over_values_that_are_none(leng
         o, lse = call()
         assert bool((o[:, :2] == 0).all()) and bool((lse[:, :2] == -INF).all())
         assert bool(torch.isfinite(o[:, 2:]).all()) and bool(torch.isfinite(lse[:, 2:]).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("counts", [[200, 77, 33, 300], [4, 1, 0, 3]])
+def test_queries_and_outputs_on_any_16_bytes(counts, kind):
+    p = Calls(kind, 8, 2, 128, 4, 700, seed=3)
+    p.append(p.randn(4 * 400, 2, 128), p.randn(4 * 400, 2, 128), [400] * 4)
+    rows = sum(counts)
+    q = p.randn(rows, 8, 128)
+    want, want_lse = p.prompt(q, counts)
+    for shift in (8, 16, 24):
+        flat = [torch.full((rows * 1024 + 64,), -7.0, dtype=torch.bfloat16, device=p.dev) for _ in range(2)]
+        qs, out = (x[shift: shift + rows * 1024].view(rows, 8, 128) for x in flat)
+        lse = torch.full((rows * 8 + 3,), -7.0, device=p.dev)
+        qs.copy_(q)
+        p.cache.prompt_attention(qs, counts, out=out, lse=lse[1: 1 + rows * 8].view(rows, 8))
+        assert torch.equal(out, want) and torch.equal(lse[1: 1 + rows * 8].view(rows, 8), want_lse)
+        assert bool((flat[1][:shift] == -7).all()) and bool((flat[1][shift + rows * 1024:] == -7).all())
+        assert float(lse[0]) == -7 and bool((lse[1 + rows * 8:] == -7).all())
+    assert p.cache.error_status() == 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_prompt_among_single_tokens_and_drafts(kind, causal):
+    """What a server's step holds: one prompt, single tokens, drafts, a sequence that waits; the same rows alone agree to
+    the bounds of both kernels."""
+    p = Calls(kind, 16, 4, 128, 40, 1300, page=64, seed=6)
+    before = [int(x) for x in np.random.default_rng(6).integers(0, 700, 40)]
+    p.append(p.randn(sum(before), 4, 128), p.randn(sum(before), 4, 128), before)
+    counts = [1] * 40
+    counts[7], counts[8], counts[9], counts[21] = 513, 4, 0, 3
+    p.append(p.randn(sum(counts), 4, 128), p.randn(sum(counts), 4, 128), counts)
+    q = p.randn(sum(counts), 16, 128)
+    p.prompt(q, counts, causal=causal)
+    seqs = [s for s in range(40) if s != 7]
+    few = [counts[s] for s in seqs]
+    alone = torch.cat([q[:7], q[7 + 513:]])
+    p.prompt(alone, few, seqs, causal)
 
 
 def test_caches_whose_calls_do_not_overlap_share_a_workspace():
