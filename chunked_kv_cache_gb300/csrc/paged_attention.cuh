@@ -27,8 +27,8 @@
 // many parts are joined by a launch of their own (the rule stands at the launch).
 //
 // Inside a CTA each of four warps owns a quarter of every tile and runs by itself: it
-// copies its tokens' keys and values into its own three shared-memory stages
-// (cp.async, 16-byte chunks, rows past the length filled with zeros) and computes on
+// copies its tokens' keys and values into its own three shared-memory stages (4-bit pages of 128 dims: two)
+// (cp.async, 16-byte chunks, rows past the length filled with zeros; 4-bit pages: bulk copies) and computes on
 // the oldest stage. The copies run ahead across items, so that the stream does not pause
 // where one item ends.
 //
@@ -50,15 +50,16 @@
 // 4-bit pages: a warp's records come by bulk copies, one for each 16 tokens' keys or values, and their codes become fp16 in
 // registers: the matrix load that brings a word of eight codes (16-bit units of four, transposed for the values) leaves
 // just the pairs that five instructions of logic and four fused products and sums turn into eight operands, scale and all.
-// That decoding is what bounds it: 350 instructions for 16 tokens of 128 dims (the queue of the logic pipe half full), where the
-// stream would leave room for 390. 32 sequences of 4001 .. 32768 tokens, 8 key heads: 125 us for 526 MB (4.2 TB/s, 62 % of
-// the copy rate; e4m3, 935 MB: 144 us); one of 131071: 42 us for 151 MB; 64 of 1 .. 16384, 64 dims: 35 us for 75 MB, 51 us
-// with weights. Written with the masks and their bits as constants the compiler made two instructions of each: 149 us for
+// That decoding is what bounds it: 355 instructions for 16 tokens of 128 dims (255 of 64), of which two warps a scheduler issue
+// 2.2 a cycle and SM, waiting for one another's results (no pipe is above 52 %; at four a cycle the stream would bound). 32
+// sequences of 4001 .. 32768 tokens, 8 key heads: 124.7 us for 526 MB (4.2 TB/s, 62 % of the copy rate; e4m3, 935 MB: 144
+// us); one of 131071: 41 us for 151 MB; 64 of 1 .. 16384, 64 dims: 35 us for 75 MB, 49 us with weights, of which storing the
+// scores is 1 us and the second launch the rest. Written with the masks and their bits as constants the compiler made two instructions of each: 149 us for
 // the first of these.
 //
 // A few new tokens per sequence (drafts to verify), whose heads fit the 16 columns: columns are (token, head) pairs, and the
-// last tokens' scores are masked by column. 4 tokens of 16 sequences of 1000 .. 8192, 32 heads, 8 key heads, 4 bits: 37 us,
-// where blocks of 128 rows (paged_prompt.cu) take 64 us.
+// last tokens' scores are masked by column. 4 tokens of 16 sequences of 1000 .. 8192, 32 heads, 8 key heads, 4 bits: 35 us (e4m3
+// 37, bf16 50), where blocks of 128 rows (paged_prompt.cu) took 64 us; 8 tokens, which go there: 83, 70 and 59 us.
 //
 // Precision. Scores, softmax statistics and sums are fp32. bf16 pages: a weight meets the
 // values as two bf16 numbers, itself rounded and what that leaves (2^-15 of it at most is lost):

@@ -22,14 +22,21 @@
 // A weight of zero times a value that is no finite number is none either, so among new tokens that some rows do not see such
 // values leave the tile (a flag for each 32 tokens tells), and are added to the rows that do see them at the block's end.
 //
-// What bounds it. Two score tiles and their products are 2048 clocks of the tensor pipe; a step takes about 3100, since a
+// What bounds it. Two score tiles and their products are 2048 clocks of the tensor pipe at 128 dims; a step takes about 3100: a
 // group's chain (scores out, maximum, exponentials, weights in, second product, next scores) is longer than the other group's
-// products that run meanwhile, and the issuing warp waits in order. Instructions matter as much: one cache serves all
-// roles' loops, and unrolling the loading warps' took up to a quarter longer. 8192 tokens from nothing, 32 heads, 8 key heads
-// of 128, bf16: 445 us, 1235 TFLOP/s (64 % of the burst rate); 4096 after 4096: 301 us, 1371 TFLOP/s (71 %), e4m3 351 us, 4 bits
-// 363 us; four sequences, 131 .. 1021 tokens after 2003 .. 16384, 40 heads, 4 bits: 544 us, 1011 TFLOP/s; two
-// frames of 1560 that see 10920 tokens, 40 key heads, e4m3: 651 us, 1073 TFLOP/s. The first form of this kernel took 1323
+// products that run meanwhile, and the issuing warp waits in order. That is not a limit: attention.cu, of the same groups and
+// hand-overs, takes 2680 .. 2740, and where this kernel's other 400 go has not been measured. At 64 dims the products are
+// half and the chain is the same. Instructions matter as much: one cache serves all roles' loops, and unrolling the
+// loading warps' took up to a quarter longer. 8192 tokens from nothing, 32 heads, 8 key heads of 128, bf16: 455 us, 1208
+// TFLOP/s (63 % of the burst rate); 4096 after 4096: 300 us, 1375 TFLOP/s (72 %), e4m3 350 us, 4 bits 366 us (of 64 dims: 252,
+// 291, 292 us, 43, 37, 37 %); four sequences, 131 .. 1021 tokens after 2003 .. 16384, 40 heads, 4 bits: 545 us, 1010 TFLOP/s; two
+// frames of 1560 that see 10920 tokens, 40 key heads, e4m3: 653 us, 1069 TFLOP/s. The first form of this kernel took 1323
 // us for the first of these, with partial results joined row by row (55 us of it), queries copied 8 rows at a time.
+//
+// Precision. Scores, statistics and sums are fp32. For the second product weights are rounded once: to fp16 (2^-11), or, where
+// the values are bf16, to bf16 (2^-8), since both operands have one type. That is a choice for speed: with what the rounding
+// leaves as a second bf16 number (as in paged_attention.cuh, whose time is the stream) outputs are off by 0.0017 of
+// themselves in the mean square, their own rounding, instead of 0.0023, and 8192 tokens take 762 us instead of 457.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -54,8 +61,10 @@ constexpr uint32_t kRegsSoftmax = 176;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 // Steps that changing blocks costs (queries, a chain that starts anew, results): a long prompt's first CTAs have many short
-// blocks. 8192 tokens from nothing, bf16: 501 us with 1, 476, 450, 445 with 2, 3, 4, as with 6; 4096 after 4096 305, 306,
-// 301, 301, with 6 303.
+// blocks. With 1, 2, 3, 4, 6, in a captured graph: 8192 tokens from nothing, 128 dims, bf16 495, 467, 441, 440, 436 us, e4m3 573,
+// 534, 509, 494, 500, 4 bits 595, 554, 526, 526, 527; 64 dims 382, 369, 374, 376, 376, and 438, 409, 399, 405, 408 (e4m3), 443, 413,
+// 410, 414, 418. 4096 after 4096 and frames that see everything differ by 3 % at most (bf16 303, 303, 298, 300, 300; e4m3, 1560
+// of 10920 364, 364, 360, 359, 356).
 constexpr int kItemCost = 4;
 // A block's flags are kept for kFlagSlots blocks: who writes those of the eighth block behind one has had a stage back (of
 // 8 at most, two tiles a block) that the second block behind it used, whose weights softmax group 0 made after both

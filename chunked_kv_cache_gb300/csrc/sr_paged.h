@@ -104,7 +104,7 @@ struct PagedAttnParams {
   __nv_bfloat16* o;
   float* lse;
   int2* items;             // [n][n_kv] first part and number of parts, when a launch of its own joins them; else NULL
-  int64_t* unit0;          // [n + 1] first unit of each sequence on the line (see paged_attention.cu), and its end
+  int64_t* unit0;          // [n + 1] first unit of each sequence on the line (see paged_attention.cuh), and its end
   int32_t* arrivals;       // [kMaxPagedCtas] parts, or groups of parts, of an item that are done; left at zero
   int32_t* group_arrivals; // [2 * kMaxPagedCtas]
   float* parts;

@@ -242,7 +242,9 @@ class PagedCache:
                          out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = None, causal: bool = True):
         """Attention of the last counts[i] tokens of sequence seqs[i] (None: one each), appended before: q
         [rows][n_heads][head_dim], the sequences' rows back to back. causal: a row sees the tokens up to its own, else all
-        that its sequence holds. Returns out, or (out, lse) when lse is True or a tensor [rows][n_heads] fp32."""
+        that its sequence holds. Returns out, or (out, lse) when lse is True or a tensor [rows][n_heads] fp32. Calls of a
+        few rows to each sequence and calls with more take different kernels (sr_paged_prompt_attention in include/sr.h
+        has the rule and the times): over 4-bit pages single tokens are faster in a call without prompts."""
         rows = q.shape[0]
         shape = (rows, self.n_heads, self.head_dim)
         self._check("q", q, shape)

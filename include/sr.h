@@ -568,7 +568,12 @@ SR_API sr_status sr_paged_attention(sr_paged_cache* c, const int32_t* seqs, int3
  * causal == 0: all seq_len tokens. A row that sees no token (a sequence shorter than m has m - seq_len of them in
  * front), or whose scores are all -inf, gets o = 0 and lse = -inf. n_tokens: HOST array of n counts >= 0, NULL for
  * one each. o may be q. fp32 scores, softmax and sums; for their product with V weights are rounded to bf16
- * (bf16 pages: 2^-8 of themselves) or fp16 (2^-11). token_mass is neither read nor written. Pages that are none
+ * (bf16 pages: 2^-8 of themselves) or fp16 (2^-11). token_mass is neither read nor written.
+ * A call all of whose sequences have at most 16 rows to a key/value head (new tokens times the query heads that share it, or
+ * of one of their equal parts) is one read of the cache, with the weights held as sr_paged_attention holds them; any other
+ * fills tiles of 128 such rows for each sequence and head. So a sequence's bits, within these bounds, and its time depend on
+ * the longest one of its call: over 4-bit pages a prompt of 1024 and 31 single tokens after 1000 .. 8192 others take 200 us
+ * in one call and 121 us in two (bf16 pages: 114 and 155 us). Pages that are none
  * of the pool are left out as above. The work is split over the lengths and joined; results do not depend on timing.
  * Values that are no finite numbers reach the rows that see their token and no others. SR_ERR_INVALID_ARG also for a call of
  * more than about 2^38 blocks of 256 rows times tiles of 128 tokens. Waits inside the kernel are bounded: should one run out
